@@ -439,3 +439,9 @@ def gdn_prefill_chunked_static(dims: GdnDims, w: Weights, cu_seqlens_host, cu_se
         ctypes.byref(dims), ctypes.byref(w.struct()), N, cu.data_ptr(), _ptr(cu_seqlens_dev), _ptr(x), _ptr(z),
         _ptr(a_raw), _ptr(b_raw), _ptr(conv_state), _ptr(S), int(bool(zero_init)), _ptr(out),
         _ptr(prenorm_out), _ptr(dev_status), _stream(stream)))
+
+
+from . import _attn  # noqa: E402  (it needs the helpers above)
+from ._attn import *  # noqa: E402,F401,F403
+
+__all__ += _attn.__all__
