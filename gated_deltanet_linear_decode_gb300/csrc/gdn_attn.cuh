@@ -1,0 +1,685 @@
+// gdn_attn.cuh -- attention of the last K tokens of each sequence over the paged key-value cache
+// (include/gdn_attn.h, gdn_attn_decode): the kernel, instantiated per type in gdn_attn_bf16.cu and
+// gdn_attn_f32.cu.
+//
+// Mathematics.  A kv head's G query heads times K tokens are R = G*K rows that share its keys.  Over any set of
+// keys a row has m = max s, l = sum e^(s-m), o = sum e^(s-m) v; two sets join as m = max(m1, m2),
+// l = l1 e^(m1-m) + l2 e^(m2-m), o likewise, and o / l is the result once.  Scores are kept in base 2
+// (s log2 e).  One pass over the keys; every key and value is read from memory once per block of rows.
+//
+// What bounds it: the cache's bytes.  A bf16 key and value of head size d are 4 d bytes for 4 R d operations,
+// so up to about 64 rows (the tensor cores' mma.sync rate against the memory's) the stream is the time, and
+// the whole layout serves it:
+//   * one persistent CTA per SM; the keys of all (sequence, kv head, row block) groups, cut into tiles, are
+//     divided evenly over the CTAs whatever the lengths, from the lengths on the device (no host plan);
+//   * cp.async (16 bytes a lane, zero fill for keys that are not there) into rings of 16 KB stages that fill
+//     192 KB of shared memory, about 128 KB of it in flight; the loads run across group borders;
+//   * warps are key groups x row groups: KG key groups each walk their own tiles with their own ring, so
+//     their only meeting is the join of the triples (m, l, o) at a group's end; RG warps of a key group hold
+//     different rows and share its stages;
+//   * a group whose tiles span several CTAs is joined through the workspace by the CTA that arrives last.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include <type_traits>
+
+#include "gdn.h"
+#include "gdn_attn_internal.h"
+#include "gdn_common.cuh"
+
+namespace gdn {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kMaxCtas = 256;                     // counters at the start of the workspace
+constexpr size_t kCounterBytes = kMaxCtas * 4;
+
+// Shape of a kernel: Ta cache type, D head size, NT blocks of 8 rows a warp holds, RG row groups, KG key
+// groups, PIECES bf16 parts of a softmax weight (bf16 only).
+template <typename Ta_, int D_, int NT_, int RG_, int KG_, int PIECES_>
+struct Shape {
+    using Ta = Ta_;
+    static constexpr bool kBf16 = std::is_same<Ta_, __nv_bfloat16>::value;
+    static constexpr int D = D_, NT = NT_, RG = RG_, KG = KG_, PIECES = PIECES_;
+    static constexpr int kThreads = RG * KG * 32;
+    static constexpr int kRows = 8 * NT * RG;                          // rows of a block
+    static constexpr int kRowBytes = D * static_cast<int>(sizeof(Ta));
+    static constexpr int KT = kBf16 ? (D == 256 ? 16 : 32) : 2048 / D;   // keys of a stage
+    static constexpr int kHalfBytes = KT * kRowBytes;                  // the keys of a stage, then the values
+    static constexpr int kStageBytes = 2 * kHalfBytes;
+    static constexpr int kQBytes = kBf16 ? kRows * kRowBytes : 0;      // queries, bf16 kernels only
+    static constexpr int kRing = kQBytes > 32768 ? 131072 : kQBytes > 16384 ? 163840 : 196608;
+    static constexpr int kStages = kRing / kStageBytes / KG;           // of one key group
+    static constexpr int kTile = KG * KT;                              // keys of a tile
+    static constexpr int JC = D < 128 ? D : 128;                       // channels of a join pass
+    static constexpr int kJPitch = JC + 4;                             // 8t+g banks for the writes below
+    static constexpr int kJoinBytes = KG * 8 * kJPitch * 4;
+    static constexpr int kMlBytes = KG * kRows * 8;
+    static constexpr int kValidBytes = KG * kStages * RG * 4;
+    static constexpr int kSmem = KG * kStages * kStageBytes + kQBytes + kJoinBytes + kMlBytes + kValidBytes;
+    static_assert(kStages >= 3 && KT % RG == 0 && KT / RG <= 32 && kSmem + 512 <= 232448, "shape");
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// 16 bytes global -> shared; `n` = 16 or 0 (zero fill, nothing read).
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t movm(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+// c[16x8] += a[16x16] . b[16x8], bf16 operands
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Where a walk over the tiles stands: group (b, hk, rb), tile of the group.
+struct Cursor {
+    int b, hk, rb, tile, tiles, len;
+};
+
+__device__ __forceinline__ int seq_keys(const AttnParams& p, int b, bool* over) {
+    const long long cap = static_cast<long long>(p.max_pages) * p.cache.page_size;
+    const int n = p.seq_len[b];
+    *over = n > cap;
+    return static_cast<int>(min(static_cast<long long>(max(n, 0)), cap));
+}
+
+template <int kTile>
+__device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }   // an empty sequence has one
+
+template <int kTile>
+__device__ __forceinline__ void advance(const AttnParams& p, Cursor& c, int row_blocks) {
+    if (++c.tile < c.tiles) return;
+    c.tile = 0;
+    if (++c.rb < row_blocks) return;
+    c.rb = 0;
+    if (++c.hk < p.Hkv) return;
+    c.hk = 0;
+    if (++c.b < p.B) {
+        bool over;
+        c.len = seq_keys(p, c.b, &over);
+        c.tiles = tiles_of<kTile>(c.len);
+    }
+}
+
+struct Split {
+    int* counters;     // [kMaxCtas]
+    float* o;          // [2 * ctas][kRows][D]
+    float2* ml;        // [2 * ctas][kRows]
+};
+
+// The result of a row's channels c..c+3, gated, into out.
+template <typename Ta, int D>
+__device__ __forceinline__ void put(const AttnParams& p, bool out_bf16, int b, int hk, int row, int c, float4 y) {
+    const long long t = static_cast<long long>(b) * p.K + row / p.G;
+    const int h = hk * p.G + row % p.G;
+    if (p.gate) {
+        const Ta* g = static_cast<const Ta*>(p.gate) + t * p.ldg + static_cast<long long>(h) * D + c;
+        y.x *= sigmoidf_(ld_act(g));
+        y.y *= sigmoidf_(ld_act(g + 1));
+        y.z *= sigmoidf_(ld_act(g + 2));
+        y.w *= sigmoidf_(ld_act(g + 3));
+    }
+    const long long at = (t * p.Hq + h) * D + c;
+    if (out_bf16) StateIO<__nv_bfloat16>::st(static_cast<__nv_bfloat16*>(p.out) + at, y);
+    else StateIO<float>::st(static_cast<float*>(p.out) + at, y);
+}
+
+template <class S>
+__global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnParams p, const int out_bf16) {
+    using Ta = typename S::Ta;
+    constexpr int D = S::D, NT = S::NT, RG = S::RG, KG = S::KG, KT = S::KT, kTile = S::kTile;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t* const q_s = smem + KG * S::kStages * S::kStageBytes;
+    float* const join_s = reinterpret_cast<float*>(q_s + S::kQBytes);
+    float2* const ml_s = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join_s) + S::kJoinBytes);   // [KG][kRows]
+    volatile uint32_t* const valid_s = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(ml_s) + S::kMlBytes);
+    __shared__ long long sums_s[S::kThreads / 32 + 1];
+    __shared__ long long start_s[2];
+    __shared__ int flag_s, start_b_s;
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int kg = warp / RG, rg = warp % RG;
+    const int R = p.G * p.K, row_blocks = (R + S::kRows - 1) / S::kRows;
+    const int per_seq = p.Hkv * row_blocks;   // groups of a sequence
+
+    // ---------------------------------------------------------------- this CTA's share of the tiles
+    const int per = (p.B + S::kThreads - 1) / S::kThreads;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+    long long mine = 0;
+    bool over;
+    for (int b = b0; b < b1; ++b) mine += static_cast<long long>(tiles_of<kTile>(seq_keys(p, b, &over))) * per_seq;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sums_s[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < S::kThreads / 32; ++w) {
+        if (w < warp) before += sums_s[w];
+        total += sums_s[w];
+    }
+    before += incl - mine;
+    const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    const long long first = total * blockIdx.x / ctas, last = total * (blockIdx.x + 1) / ctas;   // tiles [first, last)
+    if (first >= before && first < before + mine) {   // one thread: its sequences hold the first tile
+        long long at = before;
+        int b = b0;
+        for (; b < b1; ++b) {
+            const long long n = static_cast<long long>(tiles_of<kTile>(seq_keys(p, b, &over))) * per_seq;
+            if (first < at + n) break;
+            at += n;
+        }
+        start_b_s = b;
+        start_s[0] = at;
+    }
+    __syncthreads();
+    Cursor cc;   // compute
+    cc.b = start_b_s;
+    cc.len = seq_keys(p, cc.b, &over);
+    cc.tiles = tiles_of<kTile>(cc.len);
+    {
+        const long long in_seq = first - start_s[0];
+        const int group = static_cast<int>(in_seq / cc.tiles);
+        cc.tile = static_cast<int>(in_seq % cc.tiles);
+        cc.hk = group / row_blocks;
+        cc.rb = group % row_blocks;
+    }
+    const int n_tiles = static_cast<int>(last - first);
+
+    // ---------------------------------------------------------------- loads
+    Cursor lc = cc;
+    constexpr int kKeys = KT / RG;   // keys of a stage that one warp loads; lane l knows key l's page
+    const uint32_t ring = smem_u32(smem) + kg * S::kStages * S::kStageBytes;
+    const int ps = p.cache.page_size;
+    int page = -1, page_off = 0;
+    auto look_up = [&]() {   // the page of this lane's key of the load cursor's tile
+        const int j = lc.tile * kTile + kg * KT + rg * kKeys + lane;
+        page = -1;
+        if (lane < kKeys && lc.b < p.B && j < lc.len) {
+            const int i = j / ps;
+            page_off = j - i * ps;
+            page = p.block_table[static_cast<size_t>(lc.b) * p.max_pages + i];
+            if (page < 0 || page >= p.cache.num_pages) {
+                page = -1;
+                if (p.status) atomicOr(p.status + lc.b, kKvBadIndex);
+            }
+        }
+    };
+    look_up();
+    int load_slot = 0;
+    auto load = [&](int i) {   // tile i of this CTA
+        if (i < n_tiles) {
+            const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
+            if (lane == 0) valid_s[(kg * S::kStages + load_slot) * RG + rg] = ok;
+            const long long off = page < 0 ? 0
+                                           : page * p.cache.page_stride + page_off * p.cache.token_stride +
+                                                 lc.hk * p.cache.head_stride;
+            constexpr int kChunks = S::kRowBytes / 16;   // of a row
+            const uint32_t st = ring + load_slot * S::kStageBytes;
+#pragma unroll
+            for (int it = 0; it < kKeys * kChunks / 32; ++it) {
+                const int flat = it * 32 + lane;
+                const int key = flat / kChunks, ch = flat % kChunks;
+                const long long o = __shfl_sync(0xffffffffu, off, key) + ch * (16 / static_cast<int>(sizeof(Ta)));
+                const int n = (ok >> key) & 1 ? 16 : 0;
+                const int row = rg * kKeys + key;
+                const uint32_t dst = st + row * S::kRowBytes + (S::kBf16 ? (ch ^ (row & 7)) : ch) * 16;
+                cp16(dst, static_cast<const Ta*>(p.cache.k) + o, n);
+                cp16(dst + S::kHalfBytes, static_cast<const Ta*>(p.cache.v) + o, n);
+            }
+            advance<kTile>(p, lc, row_blocks);
+            look_up();
+            if (++load_slot == S::kStages) load_slot = 0;
+        }
+        cp_commit();
+    };
+    for (int i = 0; i < S::kStages - 1; ++i) load(i);
+
+    // ---------------------------------------------------------------- state of a row set
+    // bf16: o[mt][nt] is the 16 x 8 fragment (channels 16 mt.., rows 8 nt..) of o transposed; this thread has rows
+    // 8 nt + 2 (lane%4) + {0,1}.  fp32: lane l has rows 0..7, the channels of qf.
+    constexpr int kCols = S::kBf16 ? NT * 2 : 8;
+    constexpr int kC = D / 32;
+    float o[S::kBf16 ? D / 16 * NT : 8][S::kBf16 ? 4 : kC];
+    float m[kCols], l[kCols];
+    float qf[S::kBf16 ? 1 : 8][kC];
+    int limit[kCols];   // keys that a row sees
+    // the fp32 kernel's channels of a lane: kV consecutive ones every 32 kV
+    constexpr int kV = kC < 4 ? kC : 4;
+
+    auto begin_segment = [&]() {
+        const Ta* q = static_cast<const Ta*>(p.q) + static_cast<long long>(cc.b) * p.K * p.ldq + static_cast<long long>(cc.hk) * p.G * D;
+        const int row0 = cc.rb * S::kRows;
+        if constexpr (S::kBf16) {
+            constexpr int kChunks = S::kRowBytes / 16;
+            for (int i = threadIdx.x; i < S::kRows * kChunks; i += S::kThreads) {
+                const int r = i / kChunks, ch = i % kChunks, row = row0 + r;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row < R) v = *reinterpret_cast<const uint4*>(q + (row / p.G) * p.ldq + (row % p.G) * D + ch * 8);
+                *reinterpret_cast<uint4*>(q_s + r * S::kRowBytes + (ch ^ (r & 7)) * 16) = v;
+            }
+            __syncthreads();
+        } else {
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int row = row0 + rg * 8 + r;
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                    qf[r][c] = row < R ? q[(row / p.G) * p.ldq + (row % p.G) * D + (c / kV) * 32 * kV + lane * kV + c % kV] *
+                                             (p.scale * kLog2e)
+                                       : 0.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+            const int row = row0 + (S::kBf16 ? rg * 8 * NT + (i / 2) * 8 + (lane & 3) * 2 + (i & 1) : rg * 8 + i);
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            limit[i] = row < R ? cc.len - p.K + row / p.G + 1 : 0;
+        }
+#pragma unroll
+        for (auto& x : o)
+#pragma unroll
+            for (float& y : x) y = 0.f;
+    };
+
+    // ---------------------------------------------------------------- one stage
+    int slot = 0;
+    auto compute = [&]() {
+        const uint32_t st = ring + slot * S::kStageBytes;
+        const int j0 = cc.tile * kTile + kg * KT;   // the stage's first key
+        uint32_t ok = 0;
+#pragma unroll
+        for (int w = 0; w < RG; ++w) ok |= valid_s[(kg * S::kStages + slot) * RG + w] << (w * kKeys);
+        constexpr uint32_t kFull = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1;
+        if (ok == 0) return;
+        const bool masked = ok != kFull || j0 + KT > cc.len - p.K + 1;
+        if constexpr (S::kBf16) {
+            constexpr int SUB = KT / 16;
+            float s[SUB][NT][4];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u][n][e] = 0.f;
+            // s transposed: keys x rows = K . Q^T
+            const int key = lane & 15;
+            const uint32_t qa = smem_u32(q_s) + (rg * 8 * NT + (lane & 7)) * S::kRowBytes;
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ks += 2) {
+                uint32_t qb[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    ldsm4(qa + n * 8 * S::kRowBytes + ((2 * ks + (lane >> 3)) ^ (lane & 7)) * 16, qb[n]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+                        uint32_t a[4];
+                        ldsm4(st + (u * 16 + key) * S::kRowBytes + ((2 * (ks + h) + (lane >> 4)) ^ (key & 7)) * 16, a);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16816(s[u][n], a, qb[n][2 * h], qb[n][2 * h + 1]);
+                    }
+            }
+            const float c = p.scale * kLog2e;
+            float mx[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mx[n][0] = mx[n][1] = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = s[u][n][e] * c;
+                        if (masked) {
+                            const int k = u * 16 + (lane >> 2) + (e & 2) * 4;
+                            if (!((ok >> k) & 1) || j0 + k >= limit[n * 2 + (e & 1)]) x = -INFINITY;
+                        }
+                        s[u][n][e] = x;
+                        mx[n][e & 1] = fmaxf(mx[n][e & 1], x);
+                    }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], d));
+            }
+            bool up = false;
+            float f[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float m2 = fmaxf(m[n * 2 + e], mx[n][e]);
+                    up |= m2 > m[n * 2 + e];
+                    const float base = m2 == -INFINITY ? 0.f : m2;   // a row that has seen no key
+                    f[n][e] = exp2f(m[n * 2 + e] - base);
+                    m[n * 2 + e] = m2;
+                    mx[n][e] = base;
+                }
+            if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    l[n * 2] *= f[n][0];
+                    l[n * 2 + 1] *= f[n][1];
+#pragma unroll
+                    for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[mt * NT + n][e] *= f[n][e & 1];
+                }
+            }
+            // The weights go to the tensor cores as PIECES bf16 parts, each the rounding of what the ones before
+            // leave: two give 2^-17, below a bf16 result's own rounding; three all of an fp32 weight's bits.
+            uint32_t pb[SUB][NT][S::PIECES][2];
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = exp2f(s[u][n][e] - mx[n][e & 1]);
+                        l[n * 2 + (e & 1)] += w[e];
+                    }
+#pragma unroll
+                    for (int i = 0; i < S::PIECES; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x = StateIO<__nv_bfloat16>::pack(w[2 * h], w[2 * h + 1]);
+                            if (i + 1 < S::PIECES) {
+                                w[2 * h] -= __uint_as_float(x << 16);
+                                w[2 * h + 1] -= __uint_as_float(x & 0xffff0000u);
+                            }
+                            pb[u][n][i][h] = movm(x);
+                        }
+                }
+            // o transposed: channels x rows += V^T . P^T
+            const uint32_t va = st + S::kHalfBytes + ((lane & 7) + (lane >> 4) * 8) * S::kRowBytes;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t a[4];
+                    ldsm4t(va + u * 16 * S::kRowBytes + ((2 * mt + ((lane >> 3) & 1)) ^ (lane & 7)) * 16, a);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < S::PIECES; ++i) mma16816(o[mt * NT + n], a, pb[u][n][i][0], pb[u][n][i][1]);
+                }
+        } else {
+            // fp32 products and sums on the CUDA cores: 4 keys x 8 rows at a time, the channels over the lanes
+            const float* ks = reinterpret_cast<const float*>(smem + (kg * S::kStages + slot) * S::kStageBytes) + lane * kV;
+            const float* vs = ks + S::kHalfBytes / 4;
+#pragma unroll 1
+            for (int k0 = 0; k0 < KT; k0 += 4) {
+                float part[32];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float kv[kC];
+#pragma unroll
+                    for (int c = 0; c < kC; c += kV)
+#pragma unroll
+                        for (int i = 0; i < kV; ++i) kv[c + i] = ks[(k0 + k) * D + c / kV * 32 * kV + i];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r) {
+                        float x = 0.f;
+#pragma unroll
+                        for (int c = 0; c < kC; ++c) x = fmaf(kv[c], qf[r][c], x);
+                        part[k * 8 + r] = x;
+                    }
+                }
+                float s = reduce32_transposed(part);   // key k0 + lane/8, row lane%8
+                const int r = lane & 7, kk = k0 + (lane >> 3);
+                int lim = limit[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) lim = r == i ? limit[i] : lim;
+                if (masked && (!((ok >> kk) & 1) || j0 + kk >= lim)) s = -INFINITY;
+                float mx = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                float mine_m = m[0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) mine_m = r == i ? m[i] : mine_m;
+                const float m2 = fmaxf(mine_m, mx), base = m2 == -INFINITY ? 0.f : m2;
+                const float w = exp2f(s - base), f = exp2f(mine_m - base);
+                float lsum = w + __shfl_xor_sync(0xffffffffu, w, 8);
+                lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
+                const bool up = __any_sync(0xffffffffu, m2 > mine_m);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    m[i] = __shfl_sync(0xffffffffu, m2, i);
+                    const float ls = __shfl_sync(0xffffffffu, lsum, i);
+                    if (up) {
+                        const float fi = __shfl_sync(0xffffffffu, f, i);
+                        l[i] *= fi;
+#pragma unroll
+                        for (int c = 0; c < kC; ++c) o[i][c] *= fi;
+                    }
+                    l[i] += ls;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float kv[kC];
+#pragma unroll
+                    for (int c = 0; c < kC; c += kV)
+#pragma unroll
+                        for (int i = 0; i < kV; ++i) kv[c + i] = vs[(k0 + k) * D + c / kV * 32 * kV + i];
+#pragma unroll
+                    for (int r2 = 0; r2 < 8; ++r2) {
+                        const float wr = __shfl_sync(0xffffffffu, w, k * 8 + r2);
+#pragma unroll
+                        for (int c = 0; c < kC; ++c) o[r2][c] = fmaf(wr, kv[c], o[r2][c]);
+                    }
+                }
+            }
+        }
+    };
+
+    // ---------------------------------------------------------------- the end of a group, or of this CTA's part of it
+    const Split sp = {static_cast<int*>(p.workspace), reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kCounterBytes),
+                      reinterpret_cast<float2*>(static_cast<uint8_t*>(p.workspace) + kCounterBytes +
+                                                static_cast<size_t>(2) * gridDim.x * S::kRows * D * 4)};
+    long long seg_first = first;   // this CTA's first tile of the group
+    auto end_segment = [&](long long next) {   // tiles [seg_first, next) of the group are done
+        const long long g_first = next - 1 - cc.tile, g_last = g_first + cc.tiles;   // the group's tiles
+        const bool whole = seg_first == g_first && next == g_last;
+        const int part = 2 * blockIdx.x + (seg_first == first ? 0 : 1);
+        if constexpr (S::kBf16) {
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+        }
+#pragma unroll
+        for (int i = 0; i < kCols; ++i) {
+            if constexpr (S::kBf16) {
+                if (lane < 4) ml_s[kg * S::kRows + rg * 8 * NT + (i / 2) * 8 + lane * 2 + (i & 1)] = make_float2(m[i], l[i]);
+            } else {
+                if (lane == i) ml_s[kg * S::kRows + rg * 8 + i] = make_float2(m[i], l[i]);
+            }
+        }
+        const int rows = min(S::kRows, R - cc.rb * S::kRows);
+#pragma unroll
+        for (int pass = 0; pass < RG * NT * (D / S::JC); ++pass) {
+            const int ch0 = pass % (D / S::JC) * S::JC, nt = pass / (D / S::JC) % NT, prg = pass / (D / S::JC) / NT;
+            const int r0 = (prg * NT + nt) * 8;
+            if (r0 >= rows) break;
+            if (rg == prg) {
+                if constexpr (S::kBf16) {
+                    float* w = join_s + (kg * 8 + (lane & 3) * 2) * S::kJPitch + (lane >> 2);
+#pragma unroll
+                    for (int mt = 0; mt < S::JC / 16; ++mt) {
+                        // every index of o is a constant once the passes and tiles are unrolled
+                        const float(&x)[4] = o[(ch0 / 16 + mt) * NT + nt];
+                        w[mt * 16] = x[0];
+                        w[mt * 16 + S::kJPitch] = x[1];
+                        w[mt * 16 + 8] = x[2];
+                        w[mt * 16 + 8 + S::kJPitch] = x[3];
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+#pragma unroll
+                        for (int c = 0; c < kC; ++c)
+                            if (c / kV * 32 * kV >= ch0 && c / kV * 32 * kV < ch0 + S::JC)
+                                join_s[(kg * 8 + r) * S::kJPitch + c / kV * 32 * kV - ch0 + lane * kV + c % kV] = o[r][c];
+                }
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < 8 * S::JC / 4; i += S::kThreads) {
+                const int r = i / (S::JC / 4), ch = i % (S::JC / 4) * 4, row = r0 + r;
+                if (row >= rows) break;
+                float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+                for (int g = 0; g < KG; ++g) mm = fmaxf(mm, ml_s[g * S::kRows + row].x);
+                const float base = mm == -INFINITY ? 0.f : mm;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int g = 0; g < KG; ++g) {
+                    const float2 t = ml_s[g * S::kRows + row];
+                    const float f = exp2f(t.x - base);
+                    const float4 x = *reinterpret_cast<const float4*>(join_s + (g * 8 + r) * S::kJPitch + ch);
+                    ll = fmaf(f, t.y, ll);
+                    y.x = fmaf(f, x.x, y.x);
+                    y.y = fmaf(f, x.y, y.y);
+                    y.z = fmaf(f, x.z, y.z);
+                    y.w = fmaf(f, x.w, y.w);
+                }
+                if (whole) {
+                    const float inv = ll == 0.f ? 0.f : 1.0f / ll;
+                    put<Ta, D>(p, out_bf16, cc.b, cc.hk, cc.rb * S::kRows + row, ch0 + ch,
+                               make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+                } else {
+                    *reinterpret_cast<float4*>(sp.o + (static_cast<size_t>(part) * S::kRows + row) * D + ch0 + ch) = y;
+                    if (ch0 + ch == 0) sp.ml[static_cast<size_t>(part) * S::kRows + row] = make_float2(mm, ll);
+                }
+            }
+            __syncthreads();
+        }
+        if (whole) return;
+        // the CTAs of this group, and the part that the first of them wrote
+        const int c0 = static_cast<int>(((g_first + 1) * ctas - 1) / total), c1 = static_cast<int>((g_last * ctas - 1) / total);
+        const int n = c1 - c0 + 1;
+        const int part0 = 2 * c0 + (total * c0 / ctas == g_first ? 0 : 1);
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            // counts to n - 1 and back to zero: ready for the next call
+            flag_s = atomicInc(reinterpret_cast<unsigned*>(sp.counters) + c0, static_cast<unsigned>(n - 1)) == static_cast<unsigned>(n - 1);
+            __threadfence();
+        }
+        __syncthreads();
+        if (!flag_s) return;
+        for (int i = threadIdx.x; i < rows * (D / 4); i += S::kThreads) {
+            const int row = i / (D / 4), ch = i % (D / 4) * 4;
+            float mm = -INFINITY, ll = 0.f;
+            for (int k = 0; k < n; ++k) {
+                const int q = k == 0 ? part0 : 2 * (c0 + k);
+                mm = fmaxf(mm, __ldcg(sp.ml + static_cast<size_t>(q) * S::kRows + row).x);
+            }
+            const float base = mm == -INFINITY ? 0.f : mm;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (int k = 0; k < n; ++k) {
+                const int q = k == 0 ? part0 : 2 * (c0 + k);
+                const float2 t = __ldcg(sp.ml + static_cast<size_t>(q) * S::kRows + row);
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(sp.o + (static_cast<size_t>(q) * S::kRows + row) * D + ch));
+                const float f = exp2f(t.x - base);
+                ll = fmaf(f, t.y, ll);
+                y.x = fmaf(f, x.x, y.x);
+                y.y = fmaf(f, x.y, y.y);
+                y.z = fmaf(f, x.z, y.z);
+                y.w = fmaf(f, x.w, y.w);
+            }
+            const float inv = ll == 0.f ? 0.f : 1.0f / ll;
+            put<Ta, D>(p, out_bf16, cc.b, cc.hk, cc.rb * S::kRows + row, ch,
+                       make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+        }
+    };
+
+    // ---------------------------------------------------------------- the walk
+    if (threadIdx.x == 0 && p.status && cc.tile == 0 && cc.hk == 0 && cc.rb == 0) {
+        seq_keys(p, cc.b, &over);
+        if (over) atomicOr(p.status + cc.b, kKvBadIndex);
+    }
+    begin_segment();
+    for (int i = 0; i < n_tiles; ++i) {
+        cp_wait<S::kStages - 2>();
+        if constexpr (RG == 1) __syncwarp();
+        else asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(RG * 32) : "memory");
+        load(i + S::kStages - 1);
+        compute();
+        if (++slot == S::kStages) slot = 0;
+        const bool group_done = cc.tile + 1 == cc.tiles;
+        if (group_done || i + 1 == n_tiles) {
+            end_segment(first + i + 1);
+            seg_first = first + i + 1;
+        }
+        if (group_done && i + 1 < n_tiles) {
+            const int b = cc.b;
+            advance<kTile>(p, cc, row_blocks);
+            if (threadIdx.x == 0 && p.status && cc.b != b) {
+                seq_keys(p, cc.b, &over);
+                if (over) atomicOr(p.status + cc.b, kKvBadIndex);
+            }
+            begin_segment();
+        } else {
+            ++cc.tile;
+        }
+    }
+    cp_wait<0>();
+}
+
+template <class S>
+cudaError_t launch(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    attn_decode_kernel<S><<<sms, S::kThreads, S::kSmem, stream>>>(p, out_bf16 ? 1 : 0);
+    return cudaGetLastError();
+}
+
+// CTAs of a launch: one per SM (0 if the device cannot be asked).
+inline int grid_ctas() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms < kMaxCtas ? sms : kMaxCtas;
+}
+
+cudaError_t launch_bf16(const AttnParams& p, int head_dim, bool out_bf16, int sms, cudaStream_t stream);
+cudaError_t launch_f32(const AttnParams& p, int head_dim, bool out_bf16, int sms, cudaStream_t stream);
+
+// Rows of a block for R rows a kv head.
+inline int block_rows(int R, bool bf16) {
+    const int most = bf16 ? 128 : 64;
+    int n = 8;
+    while (n < R && n < most) n *= 2;
+    return n;
+}
+
+}  // namespace attn
+}  // namespace gdn

@@ -1,0 +1,43 @@
+// gdn_attn_f32.cu -- gdn_attn_decode over an fp32 cache: fp32 products and sums on the CUDA cores, 8 rows a
+// warp; see gdn_attn.cuh.
+#include "gdn_attn.cuh"
+
+namespace gdn {
+namespace attn {
+
+namespace {
+
+template <int D>
+cudaError_t by_rows(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
+    switch (block_rows(p.G * p.K, false)) {
+        case 8: return launch<Shape<float, D, 1, 1, 4, 1>>(p, out_bf16, sms, stream);
+        case 16: return launch<Shape<float, D, 1, 2, 4, 1>>(p, out_bf16, sms, stream);
+        case 32: return launch<Shape<float, D, 1, 4, 2, 1>>(p, out_bf16, sms, stream);
+        default: return launch<Shape<float, D, 1, 8, 1, 1>>(p, out_bf16, sms, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_f32(const AttnParams& p, int head_dim, bool out_bf16, int sms, cudaStream_t stream) {
+    if (head_dim == 64) return by_rows<64>(p, out_bf16, sms, stream);
+    if (head_dim == 128) return by_rows<128>(p, out_bf16, sms, stream);
+    return by_rows<256>(p, out_bf16, sms, stream);
+}
+
+}  // namespace attn
+
+size_t attn_workspace_bytes(int, int K, int Hq, int Hkv, int head_dim, int act_dtype) {
+    const size_t parts = 2 * static_cast<size_t>(attn::kMaxCtas);   // two of each CTA
+    const size_t rows = attn::block_rows(Hq / Hkv * K, act_dtype == GDN_BF16);
+    return attn::kCounterBytes + parts * rows * (head_dim * 4 + 8);
+}
+
+cudaError_t launch_attn_decode(const AttnParams& p, int head_dim, int act_dtype, int out_dtype, cudaStream_t stream) {
+    const int sms = attn::grid_ctas();
+    if (sms == 0) return cudaErrorInvalidDevice;
+    return act_dtype == GDN_BF16 ? attn::launch_bf16(p, head_dim, out_dtype == GDN_BF16, sms, stream)
+                                 : attn::launch_f32(p, head_dim, out_dtype == GDN_BF16, sms, stream);
+}
+
+}  // namespace gdn
