@@ -6,43 +6,78 @@
 #include "gdn.h"
 #include "gdn_attn_internal.h"
 #include "gdn_common.cuh"
+#include "gdn_vec.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 1024;
+// Page bookkeeping.  Integer work on a few kilobytes to a few megabytes: bound by the latency of a launch and of a
+// handful of dependent loads, and for prompts by how many threads write the rows.  Every CTA of one cluster
+// scans all of the sequences for itself (prefix sums over what they ask for, kept in shared memory), then the
+// rows and pages -- not the sequences -- are spread over all threads, each finding its sequence by bisection
+// (a prompt of 60,000 tokens beside a hundred of one keeps every thread busy).  The inputs may be the
+// outputs, so lengths and counts are written only after a cluster barrier behind the last read.
+constexpr int kMaxThreads = 1024;
+constexpr int kManyRows = 4096, kManyPages = 4096;   // above: 8 CTAs
 
-// Exclusive prefix sum of one value a thread over the block; *total = the sum of all.
-// Every thread of the block calls it; `warp_sums` is shared, 33 entries.
-__device__ __forceinline__ long long block_prefix(long long v, long long* warp_sums, long long* total) {
+struct Pair {
+    long long rows, pages;
+};
+
+// Exclusive prefix sums of one Pair a thread over the block; *total = the sums of all.
+// Every thread of the block calls it; `sums` is shared, 33 entries.
+__device__ __forceinline__ Pair block_prefix(Pair v, Pair* sums, Pair* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
-    long long x = v;
+    Pair x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const long long r = __shfl_up_sync(0xffffffffu, x.rows, o), g = __shfl_up_sync(0xffffffffu, x.pages, o);
+        if (lane >= o) {
+            x.rows += r;
+            x.pages += g;
+        }
     }
-    __syncthreads();   // the last use of warp_sums is over
-    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();   // the last use of sums is over
+    if (lane == 31) sums[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        const long long s = lane < n_warps ? warp_sums[lane] : 0;
-        long long t = s;
+        const Pair s = lane < n_warps ? sums[lane] : Pair{0, 0};
+        Pair t = s;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += y;
+            const long long r = __shfl_up_sync(0xffffffffu, t.rows, o), g = __shfl_up_sync(0xffffffffu, t.pages, o);
+            if (lane >= o) {
+                t.rows += r;
+                t.pages += g;
+            }
         }
-        if (lane < n_warps) warp_sums[lane] = t - s;
-        if (lane == 31) warp_sums[32] = t;
+        if (lane < n_warps) sums[lane] = Pair{t.rows - s.rows, t.pages - s.pages};
+        if (lane == 31) sums[32] = t;
     }
     __syncthreads();
-    *total = warp_sums[32];
-    return warp_sums[warp] + x - v;
+    *total = sums[32];
+    return Pair{sums[warp].rows + x.rows - v.rows, sums[warp].pages + x.pages - v.pages};
 }
 
-// What one sequence asks for: rows (tokens) and pages; -1 rows where the request is refused by itself.
+// The last i in 0..n-1 with a[i] <= x (a[0] <= x, a not decreasing).
+__device__ __forceinline__ int find(const int* a, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ uint32_t cluster_ctas() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return n;
+}
+
+// What one sequence asks for; rows = -1 where the request is refused by itself.
 struct Ask {
     int len, held, rows, pages;
 };
@@ -63,231 +98,314 @@ __device__ __forceinline__ Ask extend_ask(const KvExtendParams& p, int b) {
     return a;
 }
 
-// One CTA; a thread owns a run of consecutive sequences.  Prefix sums over the asked pages and rows
-// decide what is served, a third one over the served rows gives cu_seqlens; then the rows.
-__global__ void __launch_bounds__(kThreads) kv_extend_kernel(const KvExtendParams p) {
-    __shared__ long long sums[33];
-    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+__global__ void __launch_bounds__(kMaxThreads) kv_extend_kernel(const KvExtendParams p) {
+    extern __shared__ int smem[];
+    int* const row_s = smem;               // [B + 1] first row of each sequence
+    int* const page_s = smem + p.B + 1;    // [B + 1] pages served before it
+    __shared__ Pair sums[33];
+    const int per = (p.B + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
     const int free_n = min(max(*p.free_count, 0), p.num_pages);
-    long long pages = 0, rows = 0, total;
+    Pair ask{0, 0}, total;
     for (int b = b0; b < b1; ++b) {
         const Ask a = extend_ask(p, b);
-        pages += a.pages;
-        rows += max(a.rows, 0);
+        ask.rows += max(a.rows, 0);
+        ask.pages += a.pages;
     }
-    const long long pages0 = block_prefix(pages, sums, &total), rows0 = block_prefix(rows, sums, &total);
-    long long served_rows = 0, served_pages = 0;
-    {
-        long long pg = pages0, rw = rows0;
+    const Pair before = block_prefix(ask, sums, &total);
+    // Where a request that would fit by itself is refused for want of pages or rows, so is every later one that
+    // asks for any: what is served is a prefix of the asked pages, and of the asked rows.
+    auto serve = [&](auto&& f) {
+        Pair at = before;
         for (int b = b0; b < b1; ++b) {
             const Ask a = extend_ask(p, b);
-            if (a.rows >= 0 && (a.pages == 0 || pg + a.pages <= free_n) && (a.rows == 0 || rw + a.rows <= p.T)) {
-                served_rows += a.rows;
-                served_pages += a.pages;
-            }
-            pg += a.pages;
-            rw += max(a.rows, 0);
+            const bool ok = a.rows >= 0 && (a.pages == 0 || at.pages + a.pages <= free_n) &&
+                            (a.rows == 0 || at.rows + a.rows <= p.T);
+            f(b, a, ok);
+            at.rows += max(a.rows, 0);
+            at.pages += a.pages;
         }
+    };
+    Pair at = before;
+    if (total.rows > p.T || total.pages > free_n) {   // some are refused: sums over the others
+        Pair got{0, 0};
+        serve([&](int, const Ask& a, bool ok) {
+            got.rows += ok ? a.rows : 0;
+            got.pages += ok ? a.pages : 0;
+        });
+        at = block_prefix(got, sums, &total);
     }
-    long long total_rows, total_pages;
-    long long row = block_prefix(served_rows, sums, &total_rows);
-    block_prefix(served_pages, sums, &total_pages);
-    long long pg = pages0, rw = rows0;
-    for (int b = b0; b < b1; ++b) {
-        const Ask a = extend_ask(p, b);
-        const bool ok = a.rows >= 0 && (a.pages == 0 || pg + a.pages <= free_n) && (a.rows == 0 || rw + a.rows <= p.T);
-        const int n = ok ? a.rows : 0, got = ok ? a.pages : 0;
-        int* table = p.block_table + static_cast<size_t>(b) * p.max_pages;
-        for (int j = 0; j < got; ++j) table[a.held + j] = p.free_list[free_n - 1 - static_cast<int>(pg) - j];
-        for (int i = 0; i < n; ++i) {
-            const int pos = a.len + i;
-            p.positions[row + i] = pos;
-            p.slot_map[row + i] = table[pos / p.page_size] * p.page_size + pos % p.page_size;
+    const bool first_cta = cluster_ctarank() == 0;
+    serve([&](int b, const Ask& a, bool ok) {
+        row_s[b] = static_cast<int>(at.rows);
+        page_s[b] = static_cast<int>(at.pages);
+        at.rows += ok ? a.rows : 0;
+        at.pages += ok ? a.pages : 0;
+        if (!ok && first_cta && p.status) atomicOr(p.status + b, kKvRefused);
+    });
+    if (threadIdx.x == 0) {
+        row_s[p.B] = static_cast<int>(total.rows);
+        page_s[p.B] = static_cast<int>(total.pages);
+    }
+    __syncthreads();
+    const int rows = row_s[p.B], pages = page_s[p.B];
+    const int me = cluster_ctarank() * blockDim.x + threadIdx.x, all = cluster_ctas() * blockDim.x;
+    for (int g = me; g < pages; g += all) {
+        const int b = find(page_s, p.B, g);
+        p.block_table[static_cast<size_t>(b) * p.max_pages + p.n_pages[b] + g - page_s[b]] = p.free_list[free_n - 1 - g];
+    }
+    for (int t = me; t < p.T; t += all) {
+        int slot = -1, pos = 0;
+        if (t < rows) {
+            const int b = find(row_s, p.B, t);
+            pos = p.seq_len[b] + t - row_s[b];
+            const int i = pos / p.page_size, held = p.n_pages[b];
+            // a page of this call is read where it comes from, not where another thread is writing it
+            const int page = i < held ? p.block_table[static_cast<size_t>(b) * p.max_pages + i]
+                                      : p.free_list[free_n - 1 - page_s[b] - (i - held)];
+            slot = page * p.page_size + (pos - i * p.page_size);
         }
-        p.cu_seqlens[b] = static_cast<int>(row);
-        p.seq_len_out[b] = a.len + n;
-        p.n_pages_out[b] = a.held + got;
-        if (!ok && p.status) atomicOr(p.status + b, kKvRefused);
-        pg += a.pages;
-        rw += max(a.rows, 0);
-        row += n;
+        p.slot_map[t] = slot;
+        p.positions[t] = pos;
+    }
+    cluster_sync_all();
+    if (!first_cta) return;
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        p.cu_seqlens[b] = row_s[b];
+        p.seq_len_out[b] = p.seq_len[b] + row_s[b + 1] - row_s[b];
+        p.n_pages_out[b] = p.n_pages[b] + page_s[b + 1] - page_s[b];
     }
     if (threadIdx.x == 0) {
-        p.cu_seqlens[p.B] = static_cast<int>(total_rows);
-        *p.free_count_out = free_n - static_cast<int>(total_pages);
-    }
-    for (int t = static_cast<int>(total_rows) + threadIdx.x; t < p.T; t += kThreads) {
-        p.slot_map[t] = -1;
-        p.positions[t] = 0;
+        p.cu_seqlens[p.B] = rows;
+        *p.free_count_out = free_n - pages;
     }
 }
 
-__device__ __forceinline__ bool truncate_ask(const KvTruncateParams& p, int b, int* len, int* held, int* keep) {
-    *len = p.seq_len[b];
-    *held = p.n_pages[b];
-    const int n = p.new_len[b];
-    if (n < 0 || n > *len || *held < 0 || *held > p.max_pages) {
-        *keep = *held;
-        return false;
-    }
-    *keep = static_cast<int>(min((static_cast<long long>(n) + p.page_size - 1) / p.page_size, static_cast<long long>(*held)));
-    *len = n;
-    return true;
-}
-
-// One CTA; a thread owns a run of consecutive sequences.  The page that is given back as number g of n
-// goes to free_list[free_count + n - 1 - g].
-__global__ void __launch_bounds__(kThreads) kv_truncate_kernel(const KvTruncateParams p) {
-    __shared__ long long sums[33];
-    const int per = (p.B + kThreads - 1) / kThreads, b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-    const int free_n = min(max(*p.free_count, 0), p.num_pages);
-    long long back = 0, total, asked;
+// What a sequence gives back: pages keep..held-1, or nothing where it is refused by itself (ok false).
+struct Back {
     int len, held, keep;
-    for (int b = b0; b < b1; ++b) {
-        truncate_ask(p, b, &len, &held, &keep);
-        back += held - keep;
+    bool ok;
+};
+
+__device__ __forceinline__ Back truncate_ask(const KvTruncateParams& p, int b) {
+    Back r;
+    r.len = p.seq_len[b];
+    r.held = p.n_pages[b];
+    r.keep = r.held;
+    const int n = p.new_len[b];
+    r.ok = n >= 0 && n <= r.len && r.held >= 0 && r.held <= p.max_pages;
+    if (r.ok) {
+        r.len = n;
+        r.keep = static_cast<int>(min((static_cast<long long>(n) + p.page_size - 1) / p.page_size, static_cast<long long>(r.held)));
     }
-    const long long before = block_prefix(back, sums, &asked);
+    return r;
+}
+
+// The page that is given back as number g of n goes to free_list[free_count + n - 1 - g].
+__global__ void __launch_bounds__(kMaxThreads) kv_truncate_kernel(const KvTruncateParams p) {
+    extern __shared__ int smem[];
+    int* const page_s = smem;   // [B + 1] pages given back before each sequence
+    __shared__ Pair sums[33];
+    const int per = (p.B + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+    const int free_n = min(max(*p.free_count, 0), p.num_pages), room = p.num_pages - free_n;
+    Pair ask{0, 0}, total;
+    for (int b = b0; b < b1; ++b) {
+        const Back r = truncate_ask(p, b);
+        ask.pages += r.held - r.keep;
+    }
+    Pair at = block_prefix(ask, sums, &total);
+    const long long before = at.pages;
     // a sequence whose pages would not fit the stack is refused, as are all after it that give any back
-    long long g = before, served = 0;
-    for (int b = b0; b < b1; ++b) {
-        truncate_ask(p, b, &len, &held, &keep);
-        if (g + held - keep <= p.num_pages - free_n) served += held - keep;
-        g += held - keep;
+    if (total.pages > room) {
+        Pair got{0, 0};
+        long long g = before;
+        for (int b = b0; b < b1; ++b) {
+            const Back r = truncate_ask(p, b);
+            const int n = r.held - r.keep;
+            if (g + n <= room) got.pages += n;
+            g += n;
+        }
+        at = block_prefix(got, sums, &total);
     }
-    block_prefix(served, sums, &total);
-    g = before;
+    const bool first_cta = cluster_ctarank() == 0;
+    long long g = before;
     for (int b = b0; b < b1; ++b) {
-        const int old = p.seq_len[b];
-        bool ok = truncate_ask(p, b, &len, &held, &keep);
-        const int n = held - keep;
-        const bool fits = n == 0 || g + n <= p.num_pages - free_n;
-        const int* table = p.block_table + static_cast<size_t>(b) * p.max_pages;
-        if (ok && fits)
-            for (int j = 0; j < n; ++j) p.free_list[free_n + total - 1 - g - j] = table[keep + j];
-        ok = ok && fits;
-        p.seq_len_out[b] = ok ? len : old;
-        p.n_pages_out[b] = ok ? keep : held;
-        if (!ok && p.status) atomicOr(p.status + b, kKvRefused);
+        const Back r = truncate_ask(p, b);
+        const int n = r.held - r.keep;
+        const bool fits = n == 0 || g + n <= room;
+        page_s[b] = static_cast<int>(at.pages);
+        if (fits) at.pages += n;
+        if (first_cta && p.status && !(r.ok && fits)) atomicOr(p.status + b, kKvRefused);
         g += n;
     }
-    if (threadIdx.x == 0) *p.free_count_out = free_n + static_cast<int>(total);
+    if (threadIdx.x == 0) page_s[p.B] = static_cast<int>(total.pages);
+    __syncthreads();
+    const int pages = page_s[p.B];
+    // a warp takes 128 consecutive pages at a time: one bisection serves those of one sequence
+    const int lane = threadIdx.x & 31;
+    const int me = (cluster_ctarank() * blockDim.x + threadIdx.x) >> 5, all = (cluster_ctas() * blockDim.x) >> 5;
+    for (int c = me * 128; c < pages; c += all * 128) {
+        const int bc = find(page_s, p.B, c), end = page_s[bc + 1];
+        const Back rc = truncate_ask(p, bc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int gg = c + i * 32 + lane;
+            if (gg < pages) {
+                int b = bc, keep = rc.keep;
+                if (gg >= end) {
+                    b = find(page_s, p.B, gg);
+                    keep = truncate_ask(p, b).keep;
+                }
+                p.free_list[free_n + pages - 1 - gg] = p.block_table[static_cast<size_t>(b) * p.max_pages + keep + gg - page_s[b]];
+            }
+        }
+    }
+    cluster_sync_all();
+    if (!first_cta) return;
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        const Back r = truncate_ask(p, b);
+        const int n = page_s[b + 1] - page_s[b];
+        const bool done = r.ok && n == r.held - r.keep;
+        const int old = p.seq_len[b];
+        p.seq_len_out[b] = done ? r.len : old;
+        p.n_pages_out[b] = r.held - n;
+    }
+    if (threadIdx.x == 0) *p.free_count_out = free_n + pages;
 }
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p + i);
-        v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+// One cluster of `ctas` CTAs with room for `ints` words.
+template <typename P>
+cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, int threads, size_t ints, cudaStream_t stream) {
+    const size_t smem = ints * 4;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
     }
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 x = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-    uint4 x;
-    x.x = StateIO<__nv_bfloat16>::pack(v[0], v[1]);
-    x.y = StateIO<__nv_bfloat16>::pack(v[2], v[3]);
-    x.z = StateIO<__nv_bfloat16>::pack(v[4], v[5]);
-    x.w = StateIO<__nv_bfloat16>::pack(v[6], v[7]);
-    *reinterpret_cast<uint4*>(p) = x;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// D/8 lanes hold one head of one token, 8 consecutive channels each (a 16-byte access, two for
-// fp32).  The norm's sum is a butterfly over those lanes; the two halves of a rotary pair are
-// rope_dim/2 channels, i.e. rope_dim/16 lanes, apart, so the partner's channels come by shuffle.
+// The append.  Elementwise over (2 H_q + 4 H_kv) head_dim elements a token, read and written once: bound by the
+// memory for prompts, by latency for a decode batch.  D/8 lanes hold one head, 8 consecutive channels each (a
+// 16-byte access, two for fp32); a warp takes kPass of its token's head sets at a time, all loads first.  The
+// norm's sum is a butterfly over the lanes of a head; the two halves of a rotary pair are rope_dim/2 channels,
+// i.e. rope_dim/16 lanes, apart, so the partner's channels come by shuffle.
+constexpr int kPass = 4;
+
 template <typename Ta, int D>
-__global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p) {
-    constexpr int kLanes = D / 8;
+__global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p, const int warps_per_token) {
+    constexpr int kLanes = D / 8, kSet = 32 / kLanes;   // lanes of a head, heads of a warp
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int i = lane % kLanes, sub = lane / kLanes;
+    const int t = blockIdx.x * (8 / warps_per_token) + warp / warps_per_token;
+    if (t >= p.T) return;   // a whole warp
     const int n_heads = p.Hq + 2 * p.Hkv;
-    const long long item = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) / kLanes;
-    const int i = threadIdx.x % kLanes;   // lane of the head
-    const bool live = item < static_cast<long long>(p.T) * n_heads;
-    const long long t = live ? item / n_heads : 0;
-    const int h = live ? static_cast<int>(item % n_heads) : 0;
-    const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;   // q, k, v
-    const int hh = kind == 0 ? h : kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
-    const Ta* src = kind == 0   ? static_cast<const Ta*>(p.q) + t * p.ldq
-                    : kind == 1 ? static_cast<const Ta*>(p.k) + t * p.ldk
-                                : static_cast<const Ta*>(p.v) + t * p.ldv;
-    float u[8];
-    load8(src + static_cast<size_t>(hh) * D + i * 8, u);
     const int slot = p.slot_map[t], pos = p.positions[t];
     const bool pos_ok = p.rope_dim == 0 || (pos >= 0 && pos < p.n_pos);
     const bool ok = pos_ok && slot < static_cast<long long>(p.cache.num_pages) * p.cache.page_size;
-    const float* w = kind == 0 ? p.q_norm_w : p.k_norm_w;
-    // every lane of the warp takes part in the shuffles, whatever its head is
-    float ss = 0.f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) ss = fmaf(u[c], u[c], ss);
-#pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (kind != 2 && w) {
-        const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-        float wv[8];
-        load8(w + i * 8, wv);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) u[c] = u[c] * r * wv[c];
-    }
-    if (p.rope_dim > 0) {
-        const int half = p.rope_dim / 16;   // lanes in one half of the pairs
-        const bool lo = i < half, in = i < 2 * half;
-        const int from = (threadIdx.x & 31) - i + (lo ? i + half : in ? i - half : i);
-        float co[8], si[8];
-        if (in && pos_ok && kind != 2) {
-            const size_t at = static_cast<size_t>(pos) * (p.rope_dim / 2) + (lo ? i : i - half) * 8;
-            load8(p.rope_cos + at, co);
-            load8(p.rope_sin + at, si);
-        }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const float o = __shfl_sync(0xffffffffu, u[c], from);
-            if (in && pos_ok && kind != 2) u[c] = lo ? u[c] * co[c] - o * si[c] : u[c] * co[c] + o * si[c];
-        }
-    }
-    if (!live) return;
     if (!ok) {
-        if (p.status && h == 0 && i == 0) atomicOr(p.status, kKvBadIndex);
+        if (p.status && lane == 0 && warp % warps_per_token == 0) atomicOr(p.status, kKvBadIndex);
         return;
     }
-    if (kind == 0) {
-        store8(static_cast<Ta*>(p.q_out) + (t * p.Hq + hh) * D + i * 8, u);
-    } else if (slot >= 0) {
-        const long long at = static_cast<long long>(slot / p.cache.page_size) * p.cache.page_stride +
-                             static_cast<long long>(slot % p.cache.page_size) * p.cache.token_stride +
-                             static_cast<long long>(hh) * p.cache.head_stride + i * 8;
-        store8(static_cast<Ta*>(kind == 1 ? p.cache.k : p.cache.v) + at, u);
+    const Ta* const q = static_cast<const Ta*>(p.q) + t * p.ldq;
+    const Ta* const k = static_cast<const Ta*>(p.k) + t * p.ldk;
+    const Ta* const v = static_cast<const Ta*>(p.v) + t * p.ldv;
+    const int page = slot < 0 ? 0 : slot / p.cache.page_size;
+    const long long at = page * p.cache.page_stride + (slot - page * p.cache.page_size) * p.cache.token_stride + i * 8;
+    const int half = p.rope_dim / 16;   // lanes in one half of the pairs
+    const bool lo = i < half, in = i < 2 * half;
+    const int from = lane - i + (lo ? i + half : in ? i - half : i);
+    for (int h0 = warp % warps_per_token * kSet * kPass + sub; h0 - sub < n_heads; h0 += warps_per_token * kSet * kPass) {
+        Raw8<Ta> raw[kPass];
+#pragma unroll
+        for (int s = 0; s < kPass; ++s) {
+            const int h = h0 + s * kSet;
+            if (h < n_heads)
+                raw[s].load((h < p.Hq ? q + h * D : h < p.Hq + p.Hkv ? k + (h - p.Hq) * D : v + (h - p.Hq - p.Hkv) * D) + i * 8);
+        }
+#pragma unroll
+        for (int s = 0; s < kPass; ++s) {
+            const int h = h0 + s * kSet;
+            if (h - sub >= n_heads) break;   // the same for the whole warp
+            const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;   // q, k, v
+            float u[8];
+            raw[s].get(u);
+            // every lane of the warp takes part in the shuffles, whatever its head is
+            float ss = 0.f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) ss = fmaf(u[c], u[c], ss);
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float* const w = kind == 0 ? p.q_norm_w : p.k_norm_w;
+            if (kind != 2 && w) {
+                const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
+                float wv[8];
+                load8(w + i * 8, wv);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) u[c] = u[c] * r * wv[c];
+            }
+            if (half > 0) {
+                float co[8], si[8];
+                const bool turn = in && kind != 2;
+                if (turn) {
+                    const size_t tab = static_cast<size_t>(pos) * (p.rope_dim / 2) + (lo ? i : i - half) * 8;
+                    load8(p.rope_cos + tab, co);
+                    load8(p.rope_sin + tab, si);
+                }
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float o = __shfl_sync(0xffffffffu, u[c], from);
+                    if (turn) u[c] = lo ? u[c] * co[c] - o * si[c] : u[c] * co[c] + o * si[c];
+                }
+            }
+            if (h >= n_heads) continue;
+            if (kind == 0) {
+                store8(static_cast<Ta*>(p.q_out) + (static_cast<long long>(t) * p.Hq + h) * D + i * 8, u);
+            } else if (slot >= 0) {
+                const long long hh = kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
+                Ta* const dst = static_cast<Ta*>(kind == 1 ? p.cache.k : p.cache.v) + at + hh * p.cache.head_stride;
+                if (kind == 1) store8(dst, u);
+                else raw[s].store(dst);   // a copy, bit for bit
+            }
+        }
     }
 }
 
 template <typename Ta, int D>
 cudaError_t append(const KvAppendParams& p, cudaStream_t stream) {
-    const long long threads = static_cast<long long>(p.T) * (p.Hq + 2 * p.Hkv) * (D / 8);
-    const long long blocks = (threads + 255) / 256;
-    kv_append_kernel<Ta, D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p);
+    // warps of a token: enough for one pass over its heads, at most 8
+    const int sets = (p.Hq + 2 * p.Hkv + 32 * 8 / D - 1) / (32 * 8 / D);
+    int wpt = 1;
+    while (wpt < 8 && wpt * kPass < sets) wpt *= 2;
+    const int tokens = 8 / wpt;
+    kv_append_kernel<Ta, D><<<(p.T + tokens - 1) / tokens, 256, 0, stream>>>(p, wpt);
     return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_kv_extend(const KvExtendParams& p, cudaStream_t stream) {
-    kv_extend_kernel<<<1, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    const int ctas = p.T > kManyRows ? 8 : 1;
+    const int threads = p.T <= 256 && p.B <= 256 ? 256 : kMaxThreads;
+    return launch_cluster(kv_extend_kernel, p, ctas, threads, 2 * (static_cast<size_t>(p.B) + 1), stream);
 }
 
 cudaError_t launch_kv_truncate(const KvTruncateParams& p, cudaStream_t stream) {
-    kv_truncate_kernel<<<1, kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    const int ctas = p.num_pages > kManyPages ? 8 : 1;
+    const int threads = p.B <= 256 && ctas == 1 ? 256 : kMaxThreads;
+    return launch_cluster(kv_truncate_kernel, p, ctas, threads, static_cast<size_t>(p.B) + 1, stream);
 }
 
 cudaError_t launch_kv_append(const KvAppendParams& p, int head_dim, int act_dtype, cudaStream_t stream) {

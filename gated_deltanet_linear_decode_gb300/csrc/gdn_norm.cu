@@ -6,12 +6,15 @@
 #include "gdn.h"
 #include "gdn_attn_internal.h"
 #include "gdn_common.cuh"
+#include "gdn_vec.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Elementwise but for one or two sums over a row, every element read and written once: bound by the memory.  A row
+// is held in registers between its passes: with 16-byte accesses (8 channels a thread and chunk) by a CTA, or
+// by 1 to 32 lanes of one where it has at most 256 channels.  The fp32 weights come from L1 after the first row of an SM.
 
 __device__ __forceinline__ float block_sum(float v, float* s) {
     v = warp_sum(v);
@@ -19,31 +22,117 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
     if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
     __syncthreads();
     float t = 0.f;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) t += s[w];
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) t += s[w];
     return t;
 }
 
-// One CTA per row, the row in shared memory between the passes.
+// N chunks a thread.  lanes > 0: that many lanes (a power of two <= 32) share a row, several rows a CTA; lanes == 0: a CTA a row.
+template <typename Ta, typename Tr, int N>
+__global__ void __launch_bounds__(512) norm_residual_kernel(const NormParams p, const int lanes) {
+    __shared__ float sums[16];
+    const long long t = lanes ? static_cast<long long>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes : blockIdx.x;
+    const int i0 = lanes ? threadIdx.x % lanes : threadIdx.x, step = blockDim.x;
+    const int chunks = p.H / 8;
+    const bool live = t < p.T;
+    auto sum = [&](float v) {
+        if (!lanes) return block_sum(v, sums);
+        for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
+    Raw8<Ta> y[N], g[N];
+    Raw8<Tr> h[N];
+    float g1 = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        const int i = i0 + c * step;
+        if (live && i < chunks) {
+            h[c].load(static_cast<const Tr*>(p.h) + t * p.H + i * 8);
+            if (p.y) y[c].load(static_cast<const Ta*>(p.y) + t * p.ldy + i * 8);
+            if (p.gate_cols > 1) g[c].load(static_cast<const Ta*>(p.gate) + t * p.ldg + i * 8);
+        }
+    }
+    if (live && p.gate_cols == 1) g1 = sigmoidf_(ld_act(static_cast<const Ta*>(p.gate) + t * p.ldg));
+    float r = 1.f;
+    if (p.post_w) {
+        float ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < N; ++c)
+            if (live && i0 + c * step < chunks) {
+                float u[8];
+                y[c].get(u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(u[e], u[e], ss);
+            }
+        r = 1.0f / sqrtf(sum(ss) / p.H + p.eps);
+    }
+    float v[N][8], ss = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        const int i = i0 + c * step;
+        if (!live || i >= chunks) continue;
+        h[c].get(v[c]);
+        if (p.y) {
+            float u[8], w[8];
+            y[c].get(u);
+            if (p.post_w) {
+                load8(p.post_w + i * 8, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = u[e] * r * w[e];
+            }
+            if (p.gate_cols == 1) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] *= g1;
+            } else if (p.gate_cols) {
+                g[c].get(w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] *= sigmoidf_(w[e]);
+            }
+            if (p.chan_scale) {
+                load8(p.chan_scale + i * 8, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] *= w[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[c][e] = fmaf(p.alpha, u[e], v[c][e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) ss = fmaf(v[c][e], v[c][e], ss);
+        if (p.h_out) store8(static_cast<Tr*>(p.h_out) + t * p.H + i * 8, v[c]);
+    }
+    if (!p.x) return;
+    r = 1.0f / sqrtf(sum(ss) / p.H + p.eps);
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+        const int i = i0 + c * step;
+        if (!live || i >= chunks) continue;
+        float w[8];
+        load8(p.pre_w + i * 8, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[c][e] = v[c][e] * r * w[e];
+        store8(static_cast<Ta*>(p.x) + t * p.H + i * 8, v[c]);
+    }
+}
+
+// Rows that do not start on 16 bytes: one element a thread at a time, the row in shared memory between the passes.
 template <typename Ta, typename Tr>
-__global__ void __launch_bounds__(kThreads) norm_residual_kernel(const NormParams p) {
+__global__ void __launch_bounds__(512) norm_residual_any_kernel(const NormParams p) {
     extern __shared__ float row[];
-    __shared__ float sums[kThreads / 32];
+    __shared__ float sums[16];
     const long long t = blockIdx.x;
     const Ta* y = static_cast<const Ta*>(p.y) + t * p.ldy;
     const Ta* gate = static_cast<const Ta*>(p.gate) + t * p.ldg;
     const Tr* h = static_cast<const Tr*>(p.h) + t * p.H;
     float r = 1.f;
-    if (p.y && p.post_w) {
+    if (p.post_w) {
         float ss = 0.f;
-        for (int i = threadIdx.x; i < p.H; i += kThreads) {
+        for (int i = threadIdx.x; i < p.H; i += blockDim.x) {
             const float v = ld_act(y + i);
             ss = fmaf(v, v, ss);
         }
         r = 1.0f / sqrtf(block_sum(ss, sums) / p.H + p.eps);
     }
     float ss = 0.f;
-    for (int i = threadIdx.x; i < p.H; i += kThreads) {
+    for (int i = threadIdx.x; i < p.H; i += blockDim.x) {
         float v = ld_act(h + i);
         if (p.y) {
             float u = ld_act(y + i) * r;
@@ -58,17 +147,36 @@ __global__ void __launch_bounds__(kThreads) norm_residual_kernel(const NormParam
     }
     if (!p.x) return;
     r = 1.0f / sqrtf(block_sum(ss, sums) / p.H + p.eps);
-    for (int i = threadIdx.x; i < p.H; i += kThreads) st_out(static_cast<Ta*>(p.x) + t * p.H + i, row[i] * r * p.pre_w[i]);
+    for (int i = threadIdx.x; i < p.H; i += blockDim.x) st_out(static_cast<Ta*>(p.x) + t * p.H + i, row[i] * r * p.pre_w[i]);
 }
 
 template <typename Ta, typename Tr>
 cudaError_t norm(const NormParams& p, cudaStream_t stream) {
-    const int smem = p.H * 4;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(norm_residual_kernel<Ta, Tr>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
+    const int vec = 16 / static_cast<int>(sizeof(Ta));
+    const bool wide = p.H % 8 == 0 && (!p.y || p.ldy % vec == 0) && (p.gate_cols < 2 || p.ldg % vec == 0);
+    if (!wide) {
+        const int threads = p.H >= 1024 ? 512 : p.H >= 256 ? 128 : 32;
+        const int smem = p.H * 4;
+        if (smem > 40 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(norm_residual_any_kernel<Ta, Tr>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
+        norm_residual_any_kernel<Ta, Tr><<<p.T, threads, smem, stream>>>(p);
+        return cudaGetLastError();
     }
-    norm_residual_kernel<Ta, Tr><<<p.T, kThreads, smem, stream>>>(p);
+    const int chunks = p.H / 8;
+    if (chunks <= 32) {
+        int lanes = 1;
+        while (lanes < chunks) lanes *= 2;
+        const int rows = 128 / lanes;
+        norm_residual_kernel<Ta, Tr, 1><<<(p.T + rows - 1) / rows, 128, 0, stream>>>(p, lanes);
+    } else if (chunks <= 256) {
+        norm_residual_kernel<Ta, Tr, 1><<<p.T, (chunks + 31) / 32 * 32, 0, stream>>>(p, 0);
+    } else if (chunks <= 1024) {
+        norm_residual_kernel<Ta, Tr, 2><<<p.T, (chunks + 63) / 64 * 32, 0, stream>>>(p, 0);
+    } else {
+        norm_residual_kernel<Ta, Tr, 4><<<p.T, (chunks + 127) / 128 * 32, 0, stream>>>(p, 0);
+    }
     return cudaGetLastError();
 }
 

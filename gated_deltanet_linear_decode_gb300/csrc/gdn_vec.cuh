@@ -1,0 +1,75 @@
+// gdn_vec.cuh -- eight consecutive elements of fp32 or bf16 at a time, in 16-byte accesses.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "gdn_common.cuh"
+
+namespace gdn {
+
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p + i);
+        v[i] = x.x; v[i + 1] = x.y; v[i + 2] = x.z; v[i + 3] = x.w;
+    }
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+    uint4 x;
+    x.x = StateIO<__nv_bfloat16>::pack(v[0], v[1]);
+    x.y = StateIO<__nv_bfloat16>::pack(v[2], v[3]);
+    x.z = StateIO<__nv_bfloat16>::pack(v[4], v[5]);
+    x.w = StateIO<__nv_bfloat16>::pack(v[6], v[7]);
+    *reinterpret_cast<uint4*>(p) = x;
+}
+
+// Eight elements as they lie in memory, for loads that are issued ahead of their use.
+template <typename T>
+struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+
+    __device__ __forceinline__ void load(const T* p) {   // read once: not kept in L1
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            asm volatile("ld.global.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w) : "l"(reinterpret_cast<const uint4*>(p) + i));
+    }
+    __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                v[4 * i] = __uint_as_float(w[i].x);
+                v[4 * i + 1] = __uint_as_float(w[i].y);
+                v[4 * i + 2] = __uint_as_float(w[i].z);
+                v[4 * i + 3] = __uint_as_float(w[i].w);
+            }
+        } else {
+            const uint32_t x[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(x[i] << 16);
+                v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+
+}  // namespace gdn
