@@ -305,7 +305,7 @@ cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, int threads,
 constexpr int kPass = 4;
 
 template <typename Ta, int D>
-__global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p, const int warps_per_token) {
+__global__ void __launch_bounds__(256, sizeof(Ta) == 2 ? 4 : 3) kv_append_kernel(const KvAppendParams p, const int warps_per_token) {
     constexpr int kLanes = D / 8, kSet = 32 / kLanes;   // lanes of a head, heads of a warp
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int i = lane % kLanes, sub = lane / kLanes;
@@ -322,62 +322,67 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const KvAppendParams p, 
     const Ta* const q = static_cast<const Ta*>(p.q) + t * p.ldq;
     const Ta* const k = static_cast<const Ta*>(p.k) + t * p.ldk;
     const Ta* const v = static_cast<const Ta*>(p.v) + t * p.ldv;
+    Ta* const q_out = static_cast<Ta*>(p.q_out) + static_cast<long long>(t) * p.Hq * D + i * 8;
     const int page = slot < 0 ? 0 : slot / p.cache.page_size;
     const long long at = page * p.cache.page_stride + (slot - page * p.cache.page_size) * p.cache.token_stride + i * 8;
+    // This lane's rotation, the same for every head of the token: u' = u co + partner si, si negative in the first
+    // half of the pairs; co = 1, si = 0 past the rotated channels.
     const int half = p.rope_dim / 16;   // lanes in one half of the pairs
-    const bool lo = i < half, in = i < 2 * half;
-    const int from = lane - i + (lo ? i + half : in ? i - half : i);
-    for (int h0 = warp % warps_per_token * kSet * kPass + sub; h0 - sub < n_heads; h0 += warps_per_token * kSet * kPass) {
+    int from = lane;
+    float co[8], si[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        co[c] = 1.f;
+        si[c] = 0.f;
+    }
+    if (i < 2 * half) {
+        const bool lo = i < half;
+        from = lo ? lane + half : lane - half;
+        const size_t tab = static_cast<size_t>(pos) * (p.rope_dim / 2) + (lo ? i : i - half) * 8;
+        load8(p.rope_cos + tab, co);
+        load8(p.rope_sin + tab, si);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) si[c] = lo ? -si[c] : si[c];
+    }
+    const int n_qk = p.Hq + p.Hkv;
+    for (int h0 = warp % warps_per_token * kSet * kPass; h0 < n_heads; h0 += warps_per_token * kSet * kPass) {
         Raw8<Ta> raw[kPass];
 #pragma unroll
         for (int s = 0; s < kPass; ++s) {
-            const int h = h0 + s * kSet;
-            if (h < n_heads)
-                raw[s].load((h < p.Hq ? q + h * D : h < p.Hq + p.Hkv ? k + (h - p.Hq) * D : v + (h - p.Hq - p.Hkv) * D) + i * 8);
+            const int h = h0 + s * kSet + sub;
+            if (h < n_heads) raw[s].load((h < p.Hq ? q + h * D : h < n_qk ? k + (h - p.Hq) * D : v + (h - n_qk) * D) + i * 8);
         }
 #pragma unroll
         for (int s = 0; s < kPass; ++s) {
-            const int h = h0 + s * kSet;
-            if (h - sub >= n_heads) break;   // the same for the whole warp
-            const int kind = h < p.Hq ? 0 : h < p.Hq + p.Hkv ? 1 : 2;   // q, k, v
+            const int hs = h0 + s * kSet, h = hs + sub;   // hs: the same for the whole warp
+            if (hs >= n_heads) break;
             float u[8];
-            raw[s].get(u);
-            // every lane of the warp takes part in the shuffles, whatever its head is
-            float ss = 0.f;
+            if (hs < n_qk) {
+                raw[s].get(u);
+                // every lane of the warp takes part in the shuffles, whatever its head is
+                const float* const w = h < p.Hq ? p.q_norm_w : p.k_norm_w;
+                float ss = 0.f;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) ss = fmaf(u[c], u[c], ss);
+                for (int c = 0; c < 8; ++c) ss = fmaf(u[c], u[c], ss);
 #pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float* const w = kind == 0 ? p.q_norm_w : p.k_norm_w;
-            if (kind != 2 && w) {
-                const float r = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-                float wv[8];
-                load8(w + i * 8, wv);
+                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                if (w) {
+                    const float r = rsqrtf(ss * (1.0f / D) + p.eps);   // within 2 units in the last place
+                    float wv[8];
+                    load8(w + i * 8, wv);
 #pragma unroll
-                for (int c = 0; c < 8; ++c) u[c] = u[c] * r * wv[c];
-            }
-            if (half > 0) {
-                float co[8], si[8];
-                const bool turn = in && kind != 2;
-                if (turn) {
-                    const size_t tab = static_cast<size_t>(pos) * (p.rope_dim / 2) + (lo ? i : i - half) * 8;
-                    load8(p.rope_cos + tab, co);
-                    load8(p.rope_sin + tab, si);
+                    for (int c = 0; c < 8; ++c) u[c] = u[c] * r * wv[c];
                 }
+                if (half > 0) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float o = __shfl_sync(0xffffffffu, u[c], from);
-                    if (turn) u[c] = lo ? u[c] * co[c] - o * si[c] : u[c] * co[c] + o * si[c];
+                    for (int c = 0; c < 8; ++c) u[c] = fmaf(__shfl_sync(0xffffffffu, u[c], from), si[c], u[c] * co[c]);
                 }
             }
-            if (h >= n_heads) continue;
-            if (kind == 0) {
-                store8(static_cast<Ta*>(p.q_out) + (static_cast<long long>(t) * p.Hq + h) * D + i * 8, u);
-            } else if (slot >= 0) {
-                const long long hh = kind == 1 ? h - p.Hq : h - p.Hq - p.Hkv;
-                Ta* const dst = static_cast<Ta*>(kind == 1 ? p.cache.k : p.cache.v) + at + hh * p.cache.head_stride;
-                if (kind == 1) store8(dst, u);
-                else raw[s].store(dst);   // a copy, bit for bit
+            if (h < p.Hq) {
+                store8(q_out + h * D, u);
+            } else if (h < n_heads && slot >= 0) {
+                if (h < n_qk) store8(static_cast<Ta*>(p.cache.k) + at + (h - p.Hq) * p.cache.head_stride, u);
+                else raw[s].store(static_cast<Ta*>(p.cache.v) + at + (h - n_qk) * p.cache.head_stride);   // a copy, bit for bit
             }
         }
     }
