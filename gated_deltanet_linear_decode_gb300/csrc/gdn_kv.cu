@@ -298,104 +298,123 @@ cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, int threads,
 }
 
 // The append.  Elementwise over (2 H_q + 4 H_kv) head_dim elements a token, read and written once: bound by the
-// memory for prompts, by latency for a decode batch.  D/8 lanes hold one head, 8 consecutive channels each (a
-// 16-byte access, two for fp32); a warp takes kPass of its token's head sets at a time, all loads first.  The
-// norm's sum is a butterfly over the lanes of a head; the two halves of a rotary pair are rope_dim/2 channels,
-// i.e. rope_dim/16 lanes, apart, so the partner's channels come by shuffle.
+// memory for prompts -- where the instructions a head takes and the registers that hold back other warps
+// matter -- and by latency for a decode batch.  A warp takes one job: up to kPass head sets of one token, all q
+// or all k or all v, so that where they come from, where they go and what is done to them is settled once; all
+// loads first.  D/8 lanes hold one head, 8 consecutive channels each (a 16-byte access, two for fp32).  The norm's sum is
+// a butterfly over the lanes of a head.  The two halves of a rotary pair are rope_dim/2 channels, i.e. rope_dim/16
+// lanes, apart: the partner's channels come by shuffle, as they lie in memory, and norm weight and rotation are
+// one pair of factors a channel, u' = r (u A + partner B), the same for all heads of the job.
 constexpr int kPass = 4;
 
 template <typename Ta, int D>
-__global__ void __launch_bounds__(256, sizeof(Ta) == 2 ? 4 : 3) kv_append_kernel(const KvAppendParams p, const int warps_per_token) {
-    constexpr int kLanes = D / 8, kSet = 32 / kLanes;   // lanes of a head, heads of a warp
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int i = lane % kLanes, sub = lane / kLanes;
-    const int t = blockIdx.x * (8 / warps_per_token) + warp / warps_per_token;
+__global__ void __launch_bounds__(256, sizeof(Ta) == 2 ? 4 : 3) kv_append_kernel(const KvAppendParams p, const int q_jobs, const int kv_jobs) {
+    constexpr int kLanes = D / 8, kSet = 32 / kLanes;   // lanes of a head, heads of a set
+    const int lane = threadIdx.x & 31, i = lane % kLanes, sub = lane / kLanes;
+    const int jobs = q_jobs + 2 * kv_jobs;
+    const unsigned id = blockIdx.x * 8u + (threadIdx.x >> 5);
+    const int t = static_cast<int>(id / jobs);
+    int job = static_cast<int>(id - static_cast<unsigned>(t) * jobs);
     if (t >= p.T) return;   // a whole warp
-    const int n_heads = p.Hq + 2 * p.Hkv;
+    const int kind = job < q_jobs ? 0 : job < q_jobs + kv_jobs ? 1 : 2;   // q, k, v
+    if (kind) job -= kind == 1 ? q_jobs : q_jobs + kv_jobs;
+    const int heads = kind == 0 ? p.Hq : p.Hkv, h0 = job * kPass * kSet + sub;
+    const Ta* const src = (kind == 0   ? static_cast<const Ta*>(p.q) + t * p.ldq
+                           : kind == 1 ? static_cast<const Ta*>(p.k) + t * p.ldk
+                                       : static_cast<const Ta*>(p.v) + t * p.ldv) +
+                          h0 * D + i * 8;
+    Raw8<Ta> raw[kPass];
+#pragma unroll
+    for (int s = 0; s < kPass; ++s)
+        if (h0 + s * kSet < heads) raw[s].load(src + s * kSet * D);
     const int slot = p.slot_map[t], pos = p.positions[t];
-    const bool pos_ok = p.rope_dim == 0 || (pos >= 0 && pos < p.n_pos);
-    const bool ok = pos_ok && slot < static_cast<long long>(p.cache.num_pages) * p.cache.page_size;
-    if (!ok) {
-        if (p.status && lane == 0 && warp % warps_per_token == 0) atomicOr(p.status, kKvBadIndex);
+    if ((p.rope_dim != 0 && (pos < 0 || pos >= p.n_pos)) || slot >= p.cache.num_pages * p.cache.page_size) {
+        if (p.status && lane == 0 && id == static_cast<unsigned>(t) * jobs) atomicOr(p.status, kKvBadIndex);
         return;
     }
-    const Ta* const q = static_cast<const Ta*>(p.q) + t * p.ldq;
-    const Ta* const k = static_cast<const Ta*>(p.k) + t * p.ldk;
-    const Ta* const v = static_cast<const Ta*>(p.v) + t * p.ldv;
-    Ta* const q_out = static_cast<Ta*>(p.q_out) + static_cast<long long>(t) * p.Hq * D + i * 8;
-    const int page = slot < 0 ? 0 : slot / p.cache.page_size;
-    const long long at = page * p.cache.page_stride + (slot - page * p.cache.page_size) * p.cache.token_stride + i * 8;
-    // This lane's rotation, the same for every head of the token: u' = u co + partner si, si negative in the first
-    // half of the pairs; co = 1, si = 0 past the rotated channels.
+    Ta* dst;
+    long long step = D;   // elements from head to head
+    if (kind == 0) {
+        dst = static_cast<Ta*>(p.q_out) + (static_cast<long long>(t) * p.Hq + h0) * D;
+    } else {
+        if (slot < 0) return;
+        const int page = slot / p.cache.page_size;
+        step = p.cache.head_stride;
+        dst = static_cast<Ta*>(kind == 1 ? p.cache.k : p.cache.v) + page * p.cache.page_stride +
+              (slot - page * p.cache.page_size) * p.cache.token_stride + h0 * step;
+    }
+    dst += i * 8;
+    step *= kSet;
+    if (kind == 2) {   // copies, bit for bit
+#pragma unroll
+        for (int s = 0; s < kPass; ++s)
+            if (h0 + s * kSet < heads) raw[s].store(dst + s * step);
+        return;
+    }
+    const float* const w = kind == 0 ? p.q_norm_w : p.k_norm_w;
     const int half = p.rope_dim / 16;   // lanes in one half of the pairs
     int from = lane;
-    float co[8], si[8];
+    float A[8], B[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-        co[c] = 1.f;
-        si[c] = 0.f;
+        A[c] = 1.f;
+        B[c] = 0.f;
     }
+    if (w) load8(w + i * 8, A);
     if (i < 2 * half) {
-        const bool lo = i < half;
-        from = lo ? lane + half : lane - half;
-        const size_t tab = static_cast<size_t>(pos) * (p.rope_dim / 2) + (lo ? i : i - half) * 8;
-        load8(p.rope_cos + tab, co);
-        load8(p.rope_sin + tab, si);
+        const int d = i < half ? half : -half;   // to the partner's lane
+        from += d;
+        const size_t tab = static_cast<size_t>(pos) * (p.rope_dim / 2) + (d > 0 ? i : i - half) * 8;
+        float x[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) si[c] = lo ? -si[c] : si[c];
+        for (int c = 0; c < 8; ++c) B[c] = 1.f;
+        if (w) load8(w + (i + d) * 8, B);
+        load8(p.rope_cos + tab, x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) A[c] *= x[c];
+        load8(p.rope_sin + tab, x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) B[c] *= d > 0 ? -x[c] : x[c];
     }
-    const int n_qk = p.Hq + p.Hkv;
-    for (int h0 = warp % warps_per_token * kSet * kPass; h0 < n_heads; h0 += warps_per_token * kSet * kPass) {
-        Raw8<Ta> raw[kPass];
 #pragma unroll
-        for (int s = 0; s < kPass; ++s) {
-            const int h = h0 + s * kSet + sub;
-            if (h < n_heads) raw[s].load((h < p.Hq ? q + h * D : h < n_qk ? k + (h - p.Hq) * D : v + (h - n_qk) * D) + i * 8);
+    for (int s = 0; s < kPass; ++s) {
+        if (h0 - sub + s * kSet >= heads) break;   // the same for the whole warp; its lanes shuffle together
+        float u[8], r = 1.f;
+        raw[s].get(u);
+        if (w) {
+            float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) ss = fma2(make_float2(u[c], u[c + 1]), make_float2(u[c], u[c + 1]), ss);
+            r = ss.x + ss.y;
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+            r = rsqrtf(r * (1.0f / D) + p.eps);   // within 2 units in the last place
         }
+        if (half > 0) {
+            float x[8];
+            raw[s].shuffled(from).get(x);
 #pragma unroll
-        for (int s = 0; s < kPass; ++s) {
-            const int hs = h0 + s * kSet, h = hs + sub;   // hs: the same for the whole warp
-            if (hs >= n_heads) break;
-            float u[8];
-            if (hs < n_qk) {
-                raw[s].get(u);
-                // every lane of the warp takes part in the shuffles, whatever its head is
-                const float* const w = h < p.Hq ? p.q_norm_w : p.k_norm_w;
-                float ss = 0.f;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) ss = fmaf(u[c], u[c], ss);
-#pragma unroll
-                for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                if (w) {
-                    const float r = rsqrtf(ss * (1.0f / D) + p.eps);   // within 2 units in the last place
-                    float wv[8];
-                    load8(w + i * 8, wv);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) u[c] = u[c] * r * wv[c];
-                }
-                if (half > 0) {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) u[c] = fmaf(__shfl_sync(0xffffffffu, u[c], from), si[c], u[c] * co[c]);
-                }
+            for (int c = 0; c < 8; c += 2) {
+                const float2 y = mul2(make_float2(r, r), fma2(make_float2(x[c], x[c + 1]), make_float2(B[c], B[c + 1]),
+                                                              mul2(make_float2(u[c], u[c + 1]), make_float2(A[c], A[c + 1]))));
+                u[c] = y.x;
+                u[c + 1] = y.y;
             }
-            if (h < p.Hq) {
-                store8(q_out + h * D, u);
-            } else if (h < n_heads && slot >= 0) {
-                if (h < n_qk) store8(static_cast<Ta*>(p.cache.k) + at + (h - p.Hq) * p.cache.head_stride, u);
-                else raw[s].store(static_cast<Ta*>(p.cache.v) + at + (h - n_qk) * p.cache.head_stride);   // a copy, bit for bit
-            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) u[c] *= r * A[c];
         }
+        if (h0 + s * kSet < heads) store8(dst + s * step, u);
     }
 }
 
 template <typename Ta, int D>
 cudaError_t append(const KvAppendParams& p, cudaStream_t stream) {
-    // warps of a token: enough for one pass over its heads, at most 8
-    const int sets = (p.Hq + 2 * p.Hkv + 32 * 8 / D - 1) / (32 * 8 / D);
-    int wpt = 1;
-    while (wpt < 8 && wpt * kPass < sets) wpt *= 2;
-    const int tokens = 8 / wpt;
-    kv_append_kernel<Ta, D><<<(p.T + tokens - 1) / tokens, 256, 0, stream>>>(p, wpt);
+    constexpr int kHeads = kPass * 256 / D;   // of a job
+    const int q_jobs = (p.Hq + kHeads - 1) / kHeads, kv_jobs = (p.Hkv + kHeads - 1) / kHeads;
+    const long long blocks = (static_cast<long long>(p.T) * (q_jobs + 2 * kv_jobs) + 7) / 8;
+    if (blocks > 1 << 28) return cudaErrorInvalidConfiguration;   // a warp's number has 31 bits
+    kv_append_kernel<Ta, D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, q_jobs, kv_jobs);
     return cudaGetLastError();
 }
 

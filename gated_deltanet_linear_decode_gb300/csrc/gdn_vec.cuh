@@ -8,6 +8,23 @@
 
 namespace gdn {
 
+// Two fp32 operations in one instruction (each rounds as the single one does).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+          "l"(reinterpret_cast<unsigned long long&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<unsigned long long&>(d))
+        : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+    return d;
+}
+
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; i += 4) {
@@ -51,6 +68,18 @@ struct Raw8 {
     __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+    }
+    // The elements of lane `from`.
+    __device__ __forceinline__ Raw8 shuffled(int from) const {
+        Raw8 r;
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) {
+            r.w[i].x = __shfl_sync(0xffffffffu, w[i].x, from);
+            r.w[i].y = __shfl_sync(0xffffffffu, w[i].y, from);
+            r.w[i].z = __shfl_sync(0xffffffffu, w[i].z, from);
+            r.w[i].w = __shfl_sync(0xffffffffu, w[i].w, from);
+        }
+        return r;
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         if constexpr (sizeof(T) == 4) {
