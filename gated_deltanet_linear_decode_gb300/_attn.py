@@ -8,7 +8,7 @@ import math
 
 import torch
 
-from . import GDN_BF16, GdnError, _dt, _need, _ptr, _stream, gdn_status_string, library
+from . import GDN_BF16, GdnError, _dt, _need, gdn_status_string, library
 
 __all__ = [
     "GdnAttnDims", "GdnKvCache", "GdnNormDims", "KvCache", "make_attn_dims", "make_norm_dims", "gdn_kv_extend",
@@ -72,26 +72,49 @@ def _done(fn: str, status: int) -> None:
         raise GdnError(fn, status, gdn_status_string(status))
 
 
-def _rows(t, dtype, T: int, n: int, optional=False):
-    """A [T][n] tensor whose rows are dense (a column slice of a wider one will do); its pitch."""
+# A decode step makes a handful of these calls a layer, each a few microseconds on the device, so the checks
+# are kept to one expression a tensor; what fails it goes to _need for the message.
+_BF16 = torch.bfloat16
+
+
+def _p(t, dtype, shape):
+    """The pointer of a dense tensor of this type and shape."""
+    if t is not None and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
+    _need(t, dtype, shape)
+    raise ValueError("bad tensor")
+
+
+def _opt(t, dtype, shape):
+    return None if t is None else _p(t, dtype, shape)
+
+
+def _rows(t, dtype, T: int, n: int):
+    """Pointer and pitch of a [T][n] tensor whose rows are dense (a column slice of a wider one will do)."""
     if t is None:
-        if optional:
-            return 0
         raise ValueError("missing tensor")
     if not t.is_cuda:
         raise ValueError("tensors must live on a CUDA device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"expected {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != n:
+    if t.shape != (T, n):
         raise ValueError(f"expected shape {(T, n)}, got {tuple(t.shape)}")
-    s0, s1 = t.stride()
-    if s1 != 1 and n > 1:
+    ld, one = t.stride()
+    if one != 1 and n > 1:
         raise ValueError("rows must be contiguous")
-    return s0 if T > 1 else max(s0, n)
+    return t.data_ptr(), ld if T > 1 else max(ld, n)
+
+
+def _stream(stream):
+    """The CUDA stream to launch on: the given one, or torch's current one (its handle alone; building the stream
+    object costs 3 us)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _act(dims):
-    return torch.bfloat16 if dims.act_dtype == GDN_BF16 else torch.float32
+    return _BF16 if dims.act_dtype == GDN_BF16 else _F32
 
 
 def make_attn_dims(Hq: int, Hkv: int, head_dim: int, act_dtype=torch.bfloat16, out_dtype=torch.float32,
@@ -123,7 +146,6 @@ class KvCache:
         self.k, self.v = k, v
         self.dtype, self.page_size, self.heads, self.head_dim = k.dtype, k.shape[1], k.shape[2], k.shape[3]
         self.struct = GdnKvCache(k.data_ptr(), v.data_ptr(), k.shape[0], k.shape[1], *k.stride()[:3])
-        self.ref = ctypes.byref(self.struct)
 
 
 def _cache(dims: GdnAttnDims, cache: KvCache):
@@ -131,7 +153,7 @@ def _cache(dims: GdnAttnDims, cache: KvCache):
         raise TypeError(f"expected a cache of {_act(dims)}, got {cache.dtype}")
     if cache.heads != dims.H_kv or cache.head_dim != dims.head_dim:
         raise ValueError(f"expected a cache of {dims.H_kv} heads of {dims.head_dim}, got {cache.heads} of {cache.head_dim}")
-    return cache.ref
+    return cache.struct
 
 
 def gdn_kv_extend(page_size: int, n_new, seq_len, n_pages, block_table, free_list, free_count, slot_map, positions,
@@ -141,19 +163,14 @@ def gdn_kv_extend(page_size: int, n_new, seq_len, n_pages, block_table, free_lis
     [B][max_pages], slot and position of every new token, cu_seqlens [B+1].  The lengths, held pages and
     free count are updated in place unless *_out are given."""
     B, P = block_table.shape
-    T = slot_map.shape[0]
-    sl = seq_len if seq_len_out is None else seq_len_out
-    np_ = n_pages if n_pages_out is None else n_pages_out
-    fc = free_count if free_count_out is None else free_count_out
-    _need(block_table, _I32); _need(free_list, _I32, (free_list.numel(),))
-    for t in (n_new, seq_len, n_pages, sl, np_):
-        _need(t, _I32, (B,))
-    _need(free_count, _I32, (1,)); _need(fc, _I32, (1,)); _need(slot_map, _I32, (T,)); _need(positions, _I32, (T,))
-    _need(cu_seqlens, _I32, (B + 1,)); _need(dev_status, _I32, (B,), optional=True)
+    T, N, nb = slot_map.shape[0], free_list.shape[0], (B,)
+    sl, np_, fc = _p(seq_len, _I32, nb), _p(n_pages, _I32, nb), _p(free_count, _I32, (1,))
     _done("gdn_kv_extend", _fn("gdn_kv_extend")(
-        page_size, free_list.numel(), B, P, T, _ptr(n_new), _ptr(seq_len), _ptr(n_pages), _ptr(block_table),
-        _ptr(free_list), _ptr(free_count), _ptr(sl), _ptr(np_), _ptr(fc), _ptr(slot_map), _ptr(positions),
-        _ptr(cu_seqlens), _ptr(dev_status), _stream(stream)))
+        page_size, N, B, P, T, _p(n_new, _I32, nb), sl, np_, _p(block_table, _I32, (B, P)), _p(free_list, _I32, (N,)),
+        fc, sl if seq_len_out is None else _p(seq_len_out, _I32, nb),
+        np_ if n_pages_out is None else _p(n_pages_out, _I32, nb),
+        fc if free_count_out is None else _p(free_count_out, _I32, (1,)), _p(slot_map, _I32, (T,)),
+        _p(positions, _I32, (T,)), _p(cu_seqlens, _I32, (B + 1,)), _opt(dev_status, _I32, nb), _stream(stream)))
 
 
 def gdn_kv_truncate(page_size: int, new_len, seq_len, n_pages, block_table, free_list, free_count, seq_len_out=None,
@@ -161,42 +178,38 @@ def gdn_kv_truncate(page_size: int, new_len, seq_len, n_pages, block_table, free
     """Shorten every sequence to new_len[b] tokens (0: finished) and put the pages past them back on the
     free stack; in place unless *_out are given."""
     B, P = block_table.shape
-    sl = seq_len if seq_len_out is None else seq_len_out
-    np_ = n_pages if n_pages_out is None else n_pages_out
-    fc = free_count if free_count_out is None else free_count_out
-    _need(block_table, _I32); _need(free_list, _I32, (free_list.numel(),))
-    for t in (new_len, seq_len, n_pages, sl, np_):
-        _need(t, _I32, (B,))
-    _need(free_count, _I32, (1,)); _need(fc, _I32, (1,)); _need(dev_status, _I32, (B,), optional=True)
+    N, nb = free_list.shape[0], (B,)
+    sl, np_, fc = _p(seq_len, _I32, nb), _p(n_pages, _I32, nb), _p(free_count, _I32, (1,))
     _done("gdn_kv_truncate", _fn("gdn_kv_truncate")(
-        page_size, free_list.numel(), B, P, _ptr(new_len), _ptr(seq_len), _ptr(n_pages), _ptr(block_table),
-        _ptr(free_list), _ptr(free_count), _ptr(sl), _ptr(np_), _ptr(fc), _ptr(dev_status), _stream(stream)))
+        page_size, N, B, P, _p(new_len, _I32, nb), sl, np_, _p(block_table, _I32, (B, P)), _p(free_list, _I32, (N,)), fc,
+        sl if seq_len_out is None else _p(seq_len_out, _I32, nb),
+        np_ if n_pages_out is None else _p(n_pages_out, _I32, nb),
+        fc if free_count_out is None else _p(free_count_out, _I32, (1,)), _opt(dev_status, _I32, nb), _stream(stream)))
 
 
 def gdn_kv_append(dims: GdnAttnDims, cache: KvCache, q, k, v, positions, slot_map, q_out, q_norm_w=None,
                   k_norm_w=None, rope_cos=None, rope_sin=None, dev_status=None, stream=None) -> None:
     """Norm and rotate the q and k heads of T tokens (rows of a fused projection, column slices allowed),
     store k and v in the cache at slot_map, q in q_out."""
-    T, D, a = positions.shape[0], dims.head_dim, _act(dims)
+    T, D, a, r = positions.shape[0], dims.head_dim, _act(dims), dims.rope_dim
+    nq, nk = dims.H_q * D, dims.H_kv * D
     c = _cache(dims, cache)
-    ldq, ldk = _rows(q, a, T, dims.H_q * D), _rows(k, a, T, dims.H_kv * D)
-    ldv = _rows(v, a, T, dims.H_kv * D)
-    _need(positions, _I32, (T,)); _need(slot_map, _I32, (T,)); _need(q_out, a, (T, dims.H_q * D))
-    _need(q_norm_w, _F32, (D,), optional=True); _need(k_norm_w, _F32, (D,), optional=True)
+    (xq, ldq), (xk, ldk), (xv, ldv) = _rows(q, a, T, nq), _rows(k, a, T, nk), _rows(v, a, T, nk)
+    cos = sin = None
     n_pos = 0
-    if dims.rope_dim:
-        _need(rope_cos, _F32)
+    if r:
+        if rope_cos is None:
+            raise ValueError("missing tensor")
         n_pos = rope_cos.shape[0]
-        _need(rope_cos, _F32, (n_pos, dims.rope_dim // 2)); _need(rope_sin, _F32, (n_pos, dims.rope_dim // 2))
-    _need(dev_status, _I32, (1,), optional=True)
+        cos, sin = _p(rope_cos, _F32, (n_pos, r // 2)), _p(rope_sin, _F32, (n_pos, r // 2))
     _done("gdn_kv_append", _fn("gdn_kv_append")(
-        ctypes.byref(dims), c, T, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(positions), _ptr(slot_map),
-        _ptr(q_norm_w), _ptr(k_norm_w), _ptr(rope_cos), _ptr(rope_sin), n_pos, _ptr(q_out), _ptr(dev_status),
-        _stream(stream)))
+        dims, c, T, xq, ldq, xk, ldk, xv, ldv, _p(positions, _I32, (T,)), _p(slot_map, _I32, (T,)),
+        _opt(q_norm_w, _F32, (D,)), _opt(k_norm_w, _F32, (D,)), cos, sin, n_pos, _p(q_out, a, (T, nq)),
+        _opt(dev_status, _I32, (1,)), _stream(stream)))
 
 
 def gdn_attn_decode_workspace_bytes(dims: GdnAttnDims, B: int, K: int) -> int:
-    return int(_fn("gdn_attn_decode_workspace_bytes")(ctypes.byref(dims), B, K))
+    return int(_fn("gdn_attn_decode_workspace_bytes")(dims, B, K))
 
 
 def gdn_attn_decode(dims: GdnAttnDims, cache: KvCache, K: int, q, block_table, seq_len, out, gate=None,
@@ -206,17 +219,16 @@ def gdn_attn_decode(dims: GdnAttnDims, cache: KvCache, K: int, q, block_table, s
     B, P = block_table.shape
     T, n, a = B * K, dims.H_q * dims.head_dim, _act(dims)
     c = _cache(dims, cache)
-    ldq, ldg = _rows(q, a, T, n), _rows(gate, a, T, n, optional=True)
-    _need(block_table, _I32); _need(seq_len, _I32, (B,))
-    _need(out, torch.bfloat16 if dims.out_dtype == GDN_BF16 else torch.float32, (T, n))
-    _need(dev_status, _I32, (B,), optional=True)
-    ws_bytes = 0
+    xq, ldq = _rows(q, a, T, n)
+    xg, ldg = (None, 0) if gate is None else _rows(gate, a, T, n)
+    ws, ws_bytes = None, 0
     if workspace is not None:
         _need(workspace)
-        ws_bytes = workspace.numel() * workspace.element_size()
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _done("gdn_attn_decode", _fn("gdn_attn_decode")(
-        ctypes.byref(dims), c, B, K, P, _ptr(q), ldq, _ptr(gate), ldg, _ptr(block_table), _ptr(seq_len), _ptr(out),
-        _ptr(workspace) if ws_bytes else None, ws_bytes, _ptr(dev_status), _stream(stream)))
+        dims, c, B, K, P, xq, ldq, xg, ldg, _p(block_table, _I32, (B, P)), _p(seq_len, _I32, (B,)),
+        _p(out, _BF16 if dims.out_dtype == GDN_BF16 else _F32, (T, n)), ws, ws_bytes, _opt(dev_status, _I32, (B,)),
+        _stream(stream)))
 
 
 def gdn_norm_residual(dims: GdnNormDims, h, h_out=None, y=None, gate=None, post_w=None, chan_scale=None, pre_w=None,
@@ -224,13 +236,10 @@ def gdn_norm_residual(dims: GdnNormDims, h, h_out=None, y=None, gate=None, post_
     """h_out = h + alpha * chan_scale * sigmoid(gate) * RMSNorm(y) post_w and x = RMSNorm(h_out) pre_w, every
     part but h optional; gate [T][1] or [T][H]; h_out may be h."""
     T, H, a = h.shape[0], dims.H, _act(dims)
-    r = torch.bfloat16 if dims.res_dtype == GDN_BF16 else torch.float32
-    _need(h, r, (T, H)); _need(h_out, r, (T, H), optional=True); _need(x, a, (T, H), optional=True)
-    ldy = _rows(y, a, T, H, optional=True)
+    r, th, w = _BF16 if dims.res_dtype == GDN_BF16 else _F32, (T, H), (H,)
+    xy, ldy = (None, 0) if y is None else _rows(y, a, T, H)
     cols = 0 if gate is None else gate.shape[1]
-    ldg = _rows(gate, a, T, cols, optional=True)
-    for t in (post_w, chan_scale, pre_w):
-        _need(t, _F32, (H,), optional=True)
+    xg, ldg = (None, 0) if gate is None else _rows(gate, a, T, cols)
     _done("gdn_norm_residual", _fn("gdn_norm_residual")(
-        ctypes.byref(dims), T, _ptr(y), ldy, _ptr(gate), ldg, cols, _ptr(h), _ptr(post_w), _ptr(chan_scale),
-        _ptr(pre_w), _ptr(h_out), _ptr(x), _stream(stream)))
+        dims, T, xy, ldy, xg, ldg, cols, _p(h, r, th), _opt(post_w, _F32, w), _opt(chan_scale, _F32, w),
+        _opt(pre_w, _F32, w), _opt(h_out, r, th), _opt(x, a, th), _stream(stream)))
