@@ -34,8 +34,12 @@ namespace gdn {
 namespace attn {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kMaxCtas = 256;                     // counters at the start of the workspace
-constexpr size_t kCounterBytes = kMaxCtas * 4;
+constexpr int kMaxCtas = 256;
+constexpr int kFanOne = 16, kMaxFan = 32;         // parts joined at once: all of up to kFanOne, at most kMaxFan
+template <int D>
+constexpr int kJoinMin = kMaxFan * 32 + 64 + 32 * D;   // weights and totals of 8 rows, the rows
+constexpr size_t kCounterBytes = 3 * kMaxCtas * 4;   // at the start of the workspace
+static_assert(kMaxCtas / 12 < kMaxFan, "parts of the second step");
 
 // Shape of a kernel: Ta cache type, D head size, NT blocks of 8 rows a warp holds, RG row groups, KG key
 // groups, PIECES bf16 parts of a softmax weight (bf16 only).
@@ -56,7 +60,7 @@ struct Shape {
     static constexpr int kTile = KG * KT;                              // keys of a tile
     static constexpr int JC = D < 128 ? D : 128;                       // channels of a join pass
     static constexpr int kJPitch = JC + 4;                             // 8t+g banks for the writes below
-    static constexpr int kJoinBytes = KG * 8 * kJPitch * 4;
+    static constexpr int kJoinBytes = KG * 8 * kJPitch * 4 > kJoinMin<D> ? KG * 8 * kJPitch * 4 : kJoinMin<D>;
     static constexpr int kMlBytes = KG * kRows * 8;
     static constexpr int kValidBytes = KG * kStages * RG * 4;
     static constexpr int kSmem = KG * kStages * kStageBytes + kQBytes + kJoinBytes + kMlBytes + kValidBytes;
@@ -86,9 +90,15 @@ __device__ __forceinline__ uint32_t movm(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
+// 2^x, a relative error of 2^-22; results under 2^-126 are 0
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // c[16x8] += a[16x16] . b[16x8], bf16 operands
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -124,26 +134,129 @@ __device__ __forceinline__ void advance(const AttnParams& p, Cursor& c, int row_
 }
 
 struct Split {
-    int* counters;     // [kMaxCtas]
+    int* counters;     // [2 kMaxCtas] by a part's place, [kMaxCtas] by CTA
     float* o;          // [2 * ctas][kRows][D]
     float2* ml;        // [2 * ctas][kRows]
 };
 
+// row / G for rows under 4096 and G <= 16 (g_inv = 65536 / G rounded up).
+__device__ __forceinline__ int token_of(const AttnParams& p, int row) { return static_cast<int>((static_cast<unsigned>(row) * p.g_inv) >> 16); }
+
+// sigmoid(x) with the approximate 2^x and 1/x: a relative error of 2^-21, |x| 2^-23 more
+__device__ __forceinline__ float gate_of(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2(-x * kLog2e)));
+    return y;
+}
+
 // The result of a row's channels c..c+3, gated, into out.
 template <typename Ta, int D>
 __device__ __forceinline__ void put(const AttnParams& p, bool out_bf16, int b, int hk, int row, int c, float4 y) {
-    const long long t = static_cast<long long>(b) * p.K + row / p.G;
-    const int h = hk * p.G + row % p.G;
+    const int tok = token_of(p, row), h = hk * p.G + row - tok * p.G;
+    const long long t = static_cast<long long>(b) * p.K + tok;
     if (p.gate) {
-        const Ta* g = static_cast<const Ta*>(p.gate) + t * p.ldg + static_cast<long long>(h) * D + c;
-        y.x *= sigmoidf_(ld_act(g));
-        y.y *= sigmoidf_(ld_act(g + 1));
-        y.z *= sigmoidf_(ld_act(g + 2));
-        y.w *= sigmoidf_(ld_act(g + 3));
+        const float4 g = StateIO<Ta>::ld(static_cast<const Ta*>(p.gate) + t * p.ldg + static_cast<long long>(h) * D + c);
+        y.x *= gate_of(g.x);
+        y.y *= gate_of(g.y);
+        y.z *= gate_of(g.z);
+        y.w *= gate_of(g.w);
     }
     const long long at = (t * p.Hq + h) * D + c;
     if (out_bf16) StateIO<__nv_bfloat16>::st(static_cast<__nv_bfloat16*>(p.out) + at, y);
     else StateIO<float>::st(static_cast<float*>(p.out) + at, y);
+}
+
+// a / b with the short division where it will do.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+// Join `count` parts of a group's rows (part k's rows begin at row_at(k)): into the result if `final`, else into place
+// `to`.  All loads of a step are issued together: 8 rows cost a round trip for the statistics and one for every eight
+// parts.  Parts have all kRows rows; those past `rows` hold nothing and go nowhere.  `w_s`: kJoinMin<D> bytes.
+template <class S, class F>
+__device__ __forceinline__ void join_parts(const AttnParams& p, bool out_bf16, const Split& sp, int rows, int b, int hk, int row0,
+                                           float* w_s, int count, bool final, int to, F row_at) {
+    using Ta = typename S::Ta;
+    constexpr int D = S::D, kItems = 8 * D / 4, kBatch = kItems > S::kThreads ? kItems / S::kThreads : 1;
+    constexpr int kTpr = 16;   // threads a row; the first 128 threads
+    float2* const t_s = reinterpret_cast<float2*>(w_s + kMaxFan * 8);
+    float4* const y_s = reinterpret_cast<float4*>(t_s + 8);
+#pragma unroll 1
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+        if (threadIdx.x < 8 * kTpr) {
+            const int r = threadIdx.x / kTpr, sub = threadIdx.x % kTpr;
+            float2 t[kMaxFan / kTpr];
+            float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+            for (int i = 0; i < kMaxFan / kTpr; ++i) {
+                const int k = i * kTpr + sub;
+                t[i] = make_float2(-INFINITY, 0.f);
+                if (k < count) t[i] = __ldcg(sp.ml + row_at(k) + r0 + r);
+            }
+#pragma unroll
+            for (int i = 0; i < kMaxFan / kTpr; ++i) mm = fmaxf(mm, t[i].x);
+#pragma unroll
+            for (int d = 1; d < kTpr; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+            const float base = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+            for (int i = 0; i < kMaxFan / kTpr; ++i) {
+                const float f = ex2(t[i].x - base);
+                ll = fmaf(f, t[i].y, ll);
+                w_s[(i * kTpr + sub) * 8 + r] = f;
+            }
+#pragma unroll
+            for (int d = 1; d < kTpr; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+            if (sub == 0) t_s[r] = make_float2(mm, ll);
+        }
+        __syncthreads();
+        if (kItems >= S::kThreads || threadIdx.x < kItems) {
+            float4 y[kBatch];
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const float* const w = w_s + threadIdx.x / (D / 4);
+#pragma unroll 1
+            for (int k0 = 0; k0 < count; k0 += 8) {   // 8 loads at a time; past the last part it again, with the weight 0
+                float4 v[8][kBatch];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const float4* const x = reinterpret_cast<const float4*>(sp.o + (row_at(min(k0 + u, count - 1)) + r0) * D) + threadIdx.x;
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) v[u][j] = __ldcg(x + j * S::kThreads);
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+                        const float f = w[(k0 + u) * 8 + j * (S::kThreads / (D / 4))];
+                        y[j].x = fmaf(f, v[u][j].x, y[j].x);
+                        y[j].y = fmaf(f, v[u][j].y, y[j].y);
+                        y[j].z = fmaf(f, v[u][j].z, y[j].z);
+                        y[j].w = fmaf(f, v[u][j].w, y[j].w);
+                    }
+            }
+            if (final) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) y_s[threadIdx.x + j * S::kThreads] = y[j];
+            } else {
+                float4* const dst = reinterpret_cast<float4*>(sp.o + (static_cast<size_t>(to) * S::kRows + r0) * D) + threadIdx.x;
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) dst[j * S::kThreads] = y[j];
+                if (threadIdx.x < 8) sp.ml[static_cast<size_t>(to) * S::kRows + r0 + threadIdx.x] = t_s[threadIdx.x];
+            }
+        }
+        if (final) {
+            // each thread its own values again, in a loop that is not unrolled: code that runs once costs its fetch
+#pragma unroll 1
+            for (int i = threadIdx.x; i < min(8, rows - r0) * (D / 4); i += S::kThreads) {
+                const int r = i / (D / 4);
+                const float ll = t_s[r].y, inv = ll == 0.f ? 0.f : 1.0f / ll;
+                const float4 y = y_s[i];
+                put<Ta, D>(p, out_bf16, b, hk, row0 + r0 + r, i % (D / 4) * 4, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+            }
+        }
+        __syncthreads();
+    }
 }
 
 template <class S>
@@ -186,7 +299,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
     before += incl - mine;
     const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
     if (static_cast<int>(blockIdx.x) >= ctas) return;
-    const long long first = total * blockIdx.x / ctas, last = total * (blockIdx.x + 1) / ctas;   // tiles [first, last)
+    const long long first = quot(total * blockIdx.x, ctas), last = quot(total * (blockIdx.x + 1), ctas);   // tiles [first, last)
     if (first >= before && first < before + mine) {   // one thread: its sequences hold the first tile
         long long at = before;
         int b = b0;
@@ -205,8 +318,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
     cc.tiles = tiles_of<kTile>(cc.len);
     {
         const long long in_seq = first - start_s[0];
-        const int group = static_cast<int>(in_seq / cc.tiles);
-        cc.tile = static_cast<int>(in_seq % cc.tiles);
+        const int group = static_cast<int>(quot(in_seq, cc.tiles));
+        cc.tile = static_cast<int>(in_seq - static_cast<long long>(group) * cc.tiles);
         cc.hk = group / row_blocks;
         cc.rb = group % row_blocks;
     }
@@ -217,29 +330,34 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
     constexpr int kKeys = KT / RG;   // keys of a stage that one warp loads; lane l knows key l's page
     const uint32_t ring = smem_u32(smem) + kg * S::kStages * S::kStageBytes;
     const int ps = p.cache.page_size;
-    int page = -1, page_off = 0;
-    auto look_up = [&]() {   // the page of this lane's key of the load cursor's tile
-        const int j = lc.tile * kTile + kg * KT + rg * kKeys + lane;
-        page = -1;
-        if (lane < kKeys && lc.b < p.B && j < lc.len) {
-            const int i = j / ps;
-            page_off = j - i * ps;
-            page = p.block_table[static_cast<size_t>(lc.b) * p.max_pages + i];
-            if (page < 0 || page >= p.cache.num_pages) {
-                page = -1;
-                if (p.status) atomicOr(p.status + lc.b, kKvBadIndex);
+    // pages are looked up two tiles ahead of their keys' loads
+    int page[2] = {-1, -1}, in_page[2] = {0, 0}, head[2] = {0, 0};
+    int looked = 0, load_slot = 0;
+    auto load = [&](int i) {   // look up tile i + 2 of this CTA, load tile i
+        const int pg = page[0];
+        const long long off = pg * p.cache.page_stride + in_page[0] * p.cache.token_stride + head[0] * p.cache.head_stride;
+        page[0] = page[1];
+        in_page[0] = in_page[1];
+        head[0] = head[1];
+        page[1] = -1;
+        if (looked < n_tiles) {
+            const int j = lc.tile * kTile + kg * KT + rg * kKeys + lane;
+            if (lane < kKeys && j < lc.len) {
+                const int k = j / ps;
+                in_page[1] = j - k * ps;
+                head[1] = lc.hk;
+                page[1] = p.block_table[static_cast<size_t>(lc.b) * p.max_pages + k];
+                if (page[1] < 0 || page[1] >= p.cache.num_pages) {
+                    page[1] = -1;
+                    if (p.status) atomicOr(p.status + lc.b, kKvBadIndex);
+                }
             }
+            advance<kTile>(p, lc, row_blocks);
+            ++looked;
         }
-    };
-    look_up();
-    int load_slot = 0;
-    auto load = [&](int i) {   // tile i of this CTA
-        if (i < n_tiles) {
-            const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
+        if (i >= 0 && i < n_tiles) {
+            const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
             if (lane == 0) valid_s[(kg * S::kStages + load_slot) * RG + rg] = ok;
-            const long long off = page < 0 ? 0
-                                           : page * p.cache.page_stride + page_off * p.cache.token_stride +
-                                                 lc.hk * p.cache.head_stride;
             constexpr int kChunks = S::kRowBytes / 16;   // of a row
             const uint32_t st = ring + load_slot * S::kStageBytes;
 #pragma unroll
@@ -250,16 +368,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                 const int n = (ok >> key) & 1 ? 16 : 0;
                 const int row = rg * kKeys + key;
                 const uint32_t dst = st + row * S::kRowBytes + (S::kBf16 ? (ch ^ (row & 7)) : ch) * 16;
-                cp16(dst, static_cast<const Ta*>(p.cache.k) + o, n);
-                cp16(dst + S::kHalfBytes, static_cast<const Ta*>(p.cache.v) + o, n);
+                cp16(dst, static_cast<const Ta*>(p.cache.k) + (n ? o : 0), n);
+                cp16(dst + S::kHalfBytes, static_cast<const Ta*>(p.cache.v) + (n ? o : 0), n);
             }
-            advance<kTile>(p, lc, row_blocks);
-            look_up();
             if (++load_slot == S::kStages) load_slot = 0;
         }
         cp_commit();
     };
-    for (int i = 0; i < S::kStages - 1; ++i) load(i);
 
     // ---------------------------------------------------------------- state of a row set
     // bf16: o[mt][nt] is the 16 x 8 fragment (channels 16 mt.., rows 8 nt..) of o transposed; this thread has rows
@@ -269,7 +384,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
     float o[S::kBf16 ? D / 16 * NT : 8][S::kBf16 ? 4 : kC];
     float m[kCols], l[kCols];
     float qf[S::kBf16 ? 1 : 8][kC];
-    int limit[kCols];   // keys that a row sees
+    // keys that row i of this warp's rows sees
+    auto limit = [&](int i) {
+        const int row = cc.rb * S::kRows + rg * 8 * NT + i;
+        return row < R ? cc.len - p.K + token_of(p, row) + 1 : 0;
+    };
     // the fp32 kernel's channels of a lane: kV consecutive ones every 32 kV
     constexpr int kV = kC < 4 ? kC : 4;
 
@@ -281,27 +400,26 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
             for (int i = threadIdx.x; i < S::kRows * kChunks; i += S::kThreads) {
                 const int r = i / kChunks, ch = i % kChunks, row = row0 + r;
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (row < R) v = *reinterpret_cast<const uint4*>(q + (row / p.G) * p.ldq + (row % p.G) * D + ch * 8);
+                const int tok = token_of(p, row);
+                if (row < R) v = *reinterpret_cast<const uint4*>(q + tok * p.ldq + (row - tok * p.G) * D + ch * 8);
                 *reinterpret_cast<uint4*>(q_s + r * S::kRowBytes + (ch ^ (r & 7)) * 16) = v;
             }
             __syncthreads();
         } else {
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
-                const int row = row0 + rg * 8 + r;
+                const int row = row0 + rg * 8 + r, tok = token_of(p, row);
 #pragma unroll
                 for (int c = 0; c < kC; ++c)
-                    qf[r][c] = row < R ? q[(row / p.G) * p.ldq + (row % p.G) * D + (c / kV) * 32 * kV + lane * kV + c % kV] *
+                    qf[r][c] = row < R ? q[tok * p.ldq + (row - tok * p.G) * D + (c / kV) * 32 * kV + lane * kV + c % kV] *
                                              (p.scale * kLog2e)
                                        : 0.f;
             }
         }
 #pragma unroll
         for (int i = 0; i < kCols; ++i) {
-            const int row = row0 + (S::kBf16 ? rg * 8 * NT + (i / 2) * 8 + (lane & 3) * 2 + (i & 1) : rg * 8 + i);
             m[i] = -INFINITY;
             l[i] = 0.f;
-            limit[i] = row < R ? cc.len - p.K + row / p.G + 1 : 0;
         }
 #pragma unroll
         for (auto& x : o)
@@ -323,31 +441,35 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
         if constexpr (S::kBf16) {
             constexpr int SUB = KT / 16;
             float s[SUB][NT][4];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[u][n][e] = 0.f;
-            // s transposed: keys x rows = K . Q^T
+            // s transposed: keys x rows = K . Q^T.  A 16-byte chunk c of row r lies at c ^ (r % 8): with c = c0 + c1, c0 a
+            // constant whose bits c1 (of the lane) lacks, that is the lane's (c1 ^ r%8) with c0's low bits flipped, so four
+            // addresses and constant offsets reach all chunks.
             const int key = lane & 15;
-            const uint32_t qa = smem_u32(q_s) + (rg * 8 * NT + (lane & 7)) * S::kRowBytes;
+            const uint32_t qa = smem_u32(q_s) + (rg * 8 * NT + (lane & 7)) * S::kRowBytes + ((lane >> 3) ^ (lane & 7)) * 16;
+            const uint32_t ka = st + key * S::kRowBytes + ((lane >> 4) ^ (key & 7)) * 16;
+            constexpr int kSplit = SUB * NT >= 4 ? 1 : 2;   // independent sums, for the latency of a product
+            float s2[kSplit][SUB][NT][4] = {};
 #pragma unroll
             for (int ks = 0; ks < D / 16; ks += 2) {
                 uint32_t qb[NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                    ldsm4(qa + n * 8 * S::kRowBytes + ((2 * ks + (lane >> 3)) ^ (lane & 7)) * 16, qb[n]);
+                for (int n = 0; n < NT; ++n) ldsm4((qa ^ ((2 * ks & 4) * 16)) + (2 * ks & ~7) * 16 + n * 8 * S::kRowBytes, qb[n]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int u = 0; u < SUB; ++u) {
                         uint32_t a[4];
-                        ldsm4(st + (u * 16 + key) * S::kRowBytes + ((2 * (ks + h) + (lane >> 4)) ^ (key & 7)) * 16, a);
+                        ldsm4((ka ^ ((2 * (ks + h) & 6) * 16)) + (2 * (ks + h) & ~7) * 16 + u * 16 * S::kRowBytes, a);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(s[u][n], a, qb[n][2 * h], qb[n][2 * h + 1]);
+                        for (int n = 0; n < NT; ++n) mma16816(s2[h % kSplit][u][n], a, qb[n][2 * h], qb[n][2 * h + 1]);
                     }
             }
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[u][n][e] = kSplit == 2 ? s2[0][u][n][e] + s2[kSplit - 1][u][n][e] : s2[0][u][n][e];
             const float c = p.scale * kLog2e;
             float mx[NT][2];
 #pragma unroll
@@ -360,7 +482,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                         float x = s[u][n][e] * c;
                         if (masked) {
                             const int k = u * 16 + (lane >> 2) + (e & 2) * 4;
-                            if (!((ok >> k) & 1) || j0 + k >= limit[n * 2 + (e & 1)]) x = -INFINITY;
+                            if (!((ok >> k) & 1) || j0 + k >= limit(n * 8 + (lane & 3) * 2 + (e & 1))) x = -INFINITY;
                         }
                         s[u][n][e] = x;
                         mx[n][e & 1] = fmaxf(mx[n][e & 1], x);
@@ -379,7 +501,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                     const float m2 = fmaxf(m[n * 2 + e], mx[n][e]);
                     up |= m2 > m[n * 2 + e];
                     const float base = m2 == -INFINITY ? 0.f : m2;   // a row that has seen no key
-                    f[n][e] = exp2f(m[n * 2 + e] - base);
+                    f[n][e] = ex2(m[n * 2 + e] - base);
                     m[n * 2 + e] = m2;
                     mx[n][e] = base;
                 }
@@ -404,7 +526,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                     float w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        w[e] = exp2f(s[u][n][e] - mx[n][e & 1]);
+                        w[e] = ex2(s[u][n][e] - mx[n][e & 1]);
                         l[n * 2 + (e & 1)] += w[e];
                     }
 #pragma unroll
@@ -420,17 +542,17 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                         }
                 }
             // o transposed: channels x rows += V^T . P^T
-            const uint32_t va = st + S::kHalfBytes + ((lane & 7) + (lane >> 4) * 8) * S::kRowBytes;
+            const uint32_t va = st + S::kHalfBytes + ((lane & 7) + (lane >> 4) * 8) * S::kRowBytes + (((lane >> 3) & 1) ^ (lane & 7)) * 16;
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt)
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
                     uint32_t a[4];
-                    ldsm4t(va + u * 16 * S::kRowBytes + ((2 * mt + ((lane >> 3) & 1)) ^ (lane & 7)) * 16, a);
+                    ldsm4t((va ^ ((2 * mt & 6) * 16)) + (2 * mt & ~7) * 16 + u * 16 * S::kRowBytes, a);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int i = 0; i < S::PIECES; ++i)
 #pragma unroll
-                        for (int i = 0; i < S::PIECES; ++i) mma16816(o[mt * NT + n], a, pb[u][n][i][0], pb[u][n][i][1]);
+                        for (int n = 0; n < NT; ++n) mma16816(o[mt * NT + n], a, pb[u][n][i][0], pb[u][n][i][1]);
                 }
         } else {
             // fp32 products and sums on the CUDA cores: 4 keys x 8 rows at a time, the channels over the lanes
@@ -456,17 +578,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                 }
                 float s = reduce32_transposed(part);   // key k0 + lane/8, row lane%8
                 const int r = lane & 7, kk = k0 + (lane >> 3);
-                int lim = limit[0];
-#pragma unroll
-                for (int i = 1; i < 8; ++i) lim = r == i ? limit[i] : lim;
-                if (masked && (!((ok >> kk) & 1) || j0 + kk >= lim)) s = -INFINITY;
+                if (masked && (!((ok >> kk) & 1) || j0 + kk >= limit(r))) s = -INFINITY;
                 float mx = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                 float mine_m = m[0];
 #pragma unroll
                 for (int i = 1; i < 8; ++i) mine_m = r == i ? m[i] : mine_m;
                 const float m2 = fmaxf(mine_m, mx), base = m2 == -INFINITY ? 0.f : m2;
-                const float w = exp2f(s - base), f = exp2f(mine_m - base);
+                const float w = ex2(s - base), f = ex2(mine_m - base);
                 float lsum = w + __shfl_xor_sync(0xffffffffu, w, 8);
                 lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
                 const bool up = __any_sync(0xffffffffu, m2 > mine_m);
@@ -524,46 +643,50 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
             }
         }
         const int rows = min(S::kRows, R - cc.rb * S::kRows);
-#pragma unroll
-        for (int pass = 0; pass < RG * NT * (D / S::JC); ++pass) {
-            const int ch0 = pass % (D / S::JC) * S::JC, nt = pass / (D / S::JC) % NT, prg = pass / (D / S::JC) / NT;
-            const int r0 = (prg * NT + nt) * 8;
+        constexpr int kHalves = D / S::JC;
+#pragma unroll 1
+        for (int pass = 0; pass < RG * NT * kHalves; ++pass) {
+            const int ch0 = pass % kHalves * S::JC, r0 = pass / kHalves * 8;
             if (r0 >= rows) break;
-            if (rg == prg) {
+            if (pass / (NT * kHalves) == rg) {
+                const int mine_pass = pass % (NT * kHalves);
                 if constexpr (S::kBf16) {
                     float* w = join_s + (kg * 8 + (lane & 3) * 2) * S::kJPitch + (lane >> 2);
 #pragma unroll
-                    for (int mt = 0; mt < S::JC / 16; ++mt) {
-                        // every index of o is a constant once the passes and tiles are unrolled
-                        const float(&x)[4] = o[(ch0 / 16 + mt) * NT + nt];
-                        w[mt * 16] = x[0];
-                        w[mt * 16 + S::kJPitch] = x[1];
-                        w[mt * 16 + 8] = x[2];
-                        w[mt * 16 + 8 + S::kJPitch] = x[3];
-                    }
+                    for (int q = 0; q < NT * kHalves; ++q)   // every index of o is a constant
+                        if (q == mine_pass)
+#pragma unroll
+                            for (int mt = 0; mt < S::JC / 16; ++mt) {
+                                const float(&x)[4] = o[(q % kHalves * (S::JC / 16) + mt) * NT + q / kHalves];
+                                w[mt * 16] = x[0];
+                                w[mt * 16 + S::kJPitch] = x[1];
+                                w[mt * 16 + 8] = x[2];
+                                w[mt * 16 + 8 + S::kJPitch] = x[3];
+                            }
                 } else {
 #pragma unroll
                     for (int r = 0; r < 8; ++r)
 #pragma unroll
                         for (int c = 0; c < kC; ++c)
-                            if (c / kV * 32 * kV >= ch0 && c / kV * 32 * kV < ch0 + S::JC)
-                                join_s[(kg * 8 + r) * S::kJPitch + c / kV * 32 * kV - ch0 + lane * kV + c % kV] = o[r][c];
+                            if (c / kV * 32 * kV / S::JC == mine_pass)
+                                join_s[(kg * 8 + r) * S::kJPitch + c / kV * 32 * kV % S::JC + lane * kV + c % kV] = o[r][c];
                 }
             }
             __syncthreads();
+#pragma unroll 1
             for (int i = threadIdx.x; i < 8 * S::JC / 4; i += S::kThreads) {
                 const int r = i / (S::JC / 4), ch = i % (S::JC / 4) * 4, row = r0 + r;
                 if (row >= rows) break;
                 float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-                for (int g = 0; g < KG; ++g) mm = fmaxf(mm, ml_s[g * S::kRows + row].x);
+                for (int k = 0; k < KG; ++k) mm = fmaxf(mm, ml_s[k * S::kRows + row].x);
                 const float base = mm == -INFINITY ? 0.f : mm;
                 float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int g = 0; g < KG; ++g) {
-                    const float2 t = ml_s[g * S::kRows + row];
-                    const float f = exp2f(t.x - base);
-                    const float4 x = *reinterpret_cast<const float4*>(join_s + (g * 8 + r) * S::kJPitch + ch);
+                for (int k = 0; k < KG; ++k) {
+                    const float2 t = ml_s[k * S::kRows + row];
+                    const float f = ex2(t.x - base);
+                    const float4 x = *reinterpret_cast<const float4*>(join_s + (k * 8 + r) * S::kJPitch + ch);
                     ll = fmaf(f, t.y, ll);
                     y.x = fmaf(f, x.x, y.x);
                     y.y = fmaf(f, x.y, y.y);
@@ -582,57 +705,60 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
             __syncthreads();
         }
         if (whole) return;
-        // the CTAs of this group, and the part that the first of them wrote
-        const int c0 = static_cast<int>(((g_first + 1) * ctas - 1) / total), c1 = static_cast<int>((g_last * ctas - 1) / total);
-        const int n = c1 - c0 + 1;
-        const int part0 = 2 * c0 + (total * c0 / ctas == g_first ? 0 : 1);
-        __threadfence();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            // counts to n - 1 and back to zero: ready for the next call
-            flag_s = atomicInc(reinterpret_cast<unsigned*>(sp.counters) + c0, static_cast<unsigned>(n - 1)) == static_cast<unsigned>(n - 1);
-            __threadfence();
-        }
-        __syncthreads();
-        if (!flag_s) return;
-        for (int i = threadIdx.x; i < rows * (D / 4); i += S::kThreads) {
-            const int row = i / (D / 4), ch = i % (D / 4) * 4;
-            float mm = -INFINITY, ll = 0.f;
-            for (int k = 0; k < n; ++k) {
-                const int q = k == 0 ? part0 : 2 * (c0 + k);
-                mm = fmaxf(mm, __ldcg(sp.ml + static_cast<size_t>(q) * S::kRows + row).x);
+        // The CTAs c0.. of this group hold its n parts; the first one's lies in either of that CTA's two places.  Up to
+        // kFanOne parts are joined by the CTA that arrives last; of more, `fan` neighbours each are joined that way into
+        // the first one's place, and the results of those again: few parts for one CTA to read, and no CTA waits.
+        // What is joined with what, and in which order, does not depend on who arrives last.
+        const int c0 = static_cast<int>(quot((g_first + 1) * ctas - 1, total)), c1 = static_cast<int>(quot(g_last * ctas - 1, total));
+        const int n = c1 - c0 + 1, fan = n <= kFanOne ? kFanOne : n <= 64 ? 8 : 12;
+        const int k0 = (static_cast<int>(blockIdx.x) - c0) / fan * fan;   // this CTA's neighbours are k0..
+        const int part0 = 2 * c0 + (quot(total * c0, ctas) == g_first ? 0 : 1);
+        auto place = [&](int k) { return k == 0 ? part0 : 2 * (c0 + k); };
+#pragma unroll 1
+        for (int level = 0; level < 2; ++level) {
+            const int from = level == 0 ? k0 : 0, stride = level == 0 ? 1 : fan;
+            const int count = level == 0 ? min(fan, n - k0) : (n + fan - 1) / fan;
+            const bool final = level == 1 || n <= fan;
+            if (level == 0 && count == 1) continue;   // already where level 1 reads it
+            __syncthreads();   // this CTA's part is written
+            if (threadIdx.x == 0) {
+                int* const counter = level == 0 ? sp.counters + place(k0) : sp.counters + 2 * kMaxCtas + c0;
+                // releases what the CTA wrote, acquires what the others did; counts to count - 1 and back to zero, ready
+                // for the next call
+                unsigned old;
+                asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(count - 1) : "memory");
+                flag_s = old == static_cast<unsigned>(count - 1);
             }
-            const float base = mm == -INFINITY ? 0.f : mm;
-            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int k = 0; k < n; ++k) {
-                const int q = k == 0 ? part0 : 2 * (c0 + k);
-                const float2 t = __ldcg(sp.ml + static_cast<size_t>(q) * S::kRows + row);
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(sp.o + (static_cast<size_t>(q) * S::kRows + row) * D + ch));
-                const float f = exp2f(t.x - base);
-                ll = fmaf(f, t.y, ll);
-                y.x = fmaf(f, x.x, y.x);
-                y.y = fmaf(f, x.y, y.y);
-                y.z = fmaf(f, x.z, y.z);
-                y.w = fmaf(f, x.w, y.w);
-            }
-            const float inv = ll == 0.f ? 0.f : 1.0f / ll;
-            put<Ta, D>(p, out_bf16, cc.b, cc.hk, cc.rb * S::kRows + row, ch,
-                       make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+            __syncthreads();
+            if (!flag_s) return;
+            const int to = place(k0);
+            join_parts<S>(p, out_bf16, sp, rows, cc.b, cc.hk, cc.rb * S::kRows, join_s, count, final, to,
+                          [&](int k) { return static_cast<size_t>(place(from + k * stride)) * S::kRows; });
+            if (final) return;
         }
     };
 
     // ---------------------------------------------------------------- the walk
-    if (threadIdx.x == 0 && p.status && cc.tile == 0 && cc.hk == 0 && cc.rb == 0) {
-        seq_keys(p, cc.b, &over);
-        if (over) atomicOr(p.status + cc.b, kKvBadIndex);
-    }
-    begin_segment();
-    for (int i = 0; i < n_tiles; ++i) {
-        cp_wait<S::kStages - 2>();
-        if constexpr (RG == 1) __syncwarp();
-        else asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(RG * 32) : "memory");
+    // One copy of each part (the code is fetched anew by every launch): the first two turns only look up pages, the next
+    // kStages - 1 only load.
+    bool fresh = true, new_seq = cc.tile == 0 && cc.hk == 0 && cc.rb == 0;
+#pragma unroll 1
+    for (int i = -1 - S::kStages; i < n_tiles; ++i) {
+        if (i >= 0) {
+            if (fresh) {
+                begin_segment();
+                if (new_seq && threadIdx.x == 0 && p.status) {
+                    seq_keys(p, cc.b, &over);
+                    if (over) atomicOr(p.status + cc.b, kKvBadIndex);
+                }
+                fresh = false;
+            }
+            cp_wait<S::kStages - 2>();
+            if constexpr (RG == 1) __syncwarp();
+            else asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(RG * 32) : "memory");
+        }
         load(i + S::kStages - 1);
+        if (i < 0) continue;
         compute();
         if (++slot == S::kStages) slot = 0;
         const bool group_done = cc.tile + 1 == cc.tiles;
@@ -643,11 +769,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
         if (group_done && i + 1 < n_tiles) {
             const int b = cc.b;
             advance<kTile>(p, cc, row_blocks);
-            if (threadIdx.x == 0 && p.status && cc.b != b) {
-                seq_keys(p, cc.b, &over);
-                if (over) atomicOr(p.status + cc.b, kKvBadIndex);
-            }
-            begin_segment();
+            new_seq = cc.b != b;
+            fresh = true;
         } else {
             ++cc.tile;
         }

@@ -244,7 +244,8 @@ gdn_status gdn_attn_decode(const gdn_attn_dims* dims, const gdn_kv_cache* cache,
                     {{kc.k, kv_bytes}, {kc.v, kv_bytes}, {q, rows_bytes(T, n, ldq, es)},
                      {gate, rows_bytes(T, n, ldg, es)}, {block_table, nb * max_pages}, {seq_len, nb}}))
         return GDN_E_INVALID_ARG;
-    gdn::AttnParams p{kc, B, K, dims->H_q, dims->H_kv, dims->H_q / dims->H_kv, max_pages, dims->scale, q, gate, ldq,
+    const int G = dims->H_q / dims->H_kv;
+    gdn::AttnParams p{kc, B, K, dims->H_q, dims->H_kv, G, max_pages, (65536u + G - 1) / G, dims->scale, q, gate, ldq,
                       ldg, block_table, seq_len, out, workspace, dev_status};
     return cuda_status(gdn::launch_attn_decode(p, dims->head_dim, dims->act_dtype, dims->out_dtype,
                                                reinterpret_cast<cudaStream_t>(stream)));

@@ -73,6 +73,7 @@ struct KvAppendParams {
 struct AttnParams {
     KvCache cache;
     int B, K, Hq, Hkv, G, max_pages;
+    unsigned g_inv;       // 65536 / G rounded up
     float scale;
     const void* q;
     const void* gate;     // optional
