@@ -8,7 +8,7 @@ import math
 
 import torch
 
-from . import GDN_BF16, GdnError, _dt, _need, gdn_status_string, library
+from . import GDN_BF16, GDN_FLAG_TEST_STALL, GdnError, _dt, _need, gdn_status_string, library
 
 __all__ = [
     "GdnAttnDims", "GdnKvCache", "GdnNormDims", "KvCache", "make_attn_dims", "make_norm_dims", "gdn_kv_extend",
@@ -28,7 +28,7 @@ _F32 = torch.float32
 class GdnAttnDims(ctypes.Structure):
     _fields_ = [("H_q", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("rope_dim", ctypes.c_int32), ("scale", ctypes.c_float), ("eps", ctypes.c_float),
-                ("act_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+                ("act_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
 class GdnKvCache(ctypes.Structure):
@@ -118,10 +118,12 @@ def _act(dims):
 
 
 def make_attn_dims(Hq: int, Hkv: int, head_dim: int, act_dtype=torch.bfloat16, out_dtype=torch.float32,
-                   rope_dim: int = 0, scale: float | None = None, eps: float = 1e-6) -> GdnAttnDims:
-    """Head counts, head size and types of a full-attention layer; scale defaults to 1/sqrt(head_dim)."""
+                   rope_dim: int = 0, scale: float | None = None, eps: float = 1e-6,
+                   test_stall: bool = False) -> GdnAttnDims:
+    """Head counts, head size and types of a full-attention layer; scale defaults to 1/sqrt(head_dim);
+    test_stall selects GDN_FLAG_TEST_STALL (the give-up path of the kernel's waits)."""
     return GdnAttnDims(Hq, Hkv, head_dim, rope_dim, 1.0 / math.sqrt(head_dim) if scale is None else scale, eps,
-                       _dt(act_dtype), _dt(out_dtype))
+                       _dt(act_dtype), _dt(out_dtype), GDN_FLAG_TEST_STALL if test_stall else 0)
 
 
 def make_norm_dims(H: int, act_dtype=torch.bfloat16, res_dtype=torch.bfloat16, alpha: float = 1.0,

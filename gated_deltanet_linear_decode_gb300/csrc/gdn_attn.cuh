@@ -11,13 +11,20 @@
 // so up to about 64 rows (the tensor cores' mma.sync rate against the memory's) the stream is the time, and
 // the whole layout serves it:
 //   * one persistent CTA per SM; the keys of all (sequence, kv head, row block) groups, cut into tiles, are
-//     divided evenly over the CTAs whatever the lengths, from the lengths on the device (no host plan);
-//   * cp.async (16 bytes a lane, zero fill for keys that are not there) into rings of 16 KB stages that fill
-//     192 KB of shared memory, about 128 KB of it in flight; the loads run across group borders;
-//   * warps are key groups x row groups: KG key groups each walk their own tiles with their own ring, so
+//     divided evenly over the CTAs whatever the lengths, from the lengths on the device (no host plan).  A group
+//     counts kGroupCost tiles more than it has, for its begin and end;
+//   * four producer warps issue cp.async (16 bytes a lane, zero fill for keys that are not there) into rings of 16 KB
+//     stages that fill 192 KB of shared memory, most of it in flight; the loads run across group borders.  They have
+//     warps of their own because a warp stands still while the memory takes its requests: with the loads in the computing
+//     warps, those spent 175 of 305 us there (64 ragged sequences, 2.2 GB) and the two times added up;
+//   * the other warps are key groups x row groups: KG key groups each walk their own tiles with their own ring, so
 //     their only meeting is the join of the triples (m, l, o) at a group's end; RG warps of a key group hold
 //     different rows and share its stages;
 //   * a group whose tiles span several CTAs is joined through the workspace by the CTA that arrives last.
+//
+// Waits.  Producers and consumers meet at an mbarrier pair a stage.  Every wait has a limit; a warp whose wait gives up
+// sets a flag that ends all waits of the CTA, nothing more is written, and the sequences concerned get bit 4 of
+// their status words.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -29,6 +36,7 @@
 #include "gdn.h"
 #include "gdn_attn_internal.h"
 #include "gdn_common.cuh"
+#include "gdn_tc.cuh"
 
 namespace gdn {
 namespace attn {
@@ -48,7 +56,9 @@ struct Shape {
     using Ta = Ta_;
     static constexpr bool kBf16 = std::is_same<Ta_, __nv_bfloat16>::value;
     static constexpr int D = D_, NT = NT_, RG = RG_, KG = KG_, PIECES = PIECES_;
-    static constexpr int kThreads = RG * KG * 32;
+    static constexpr int kThreads = RG * KG * 32;                      // that compute
+    static constexpr int kAll = kThreads + 128;                        // and four warps that load
+    static constexpr int PW = 4 / KG;                                  // of them, a key group's
     static constexpr int kRows = 8 * NT * RG;                          // rows of a block
     static constexpr int kRowBytes = D * static_cast<int>(sizeof(Ta));
     static constexpr int KT = kBf16 ? (D == 256 ? 16 : 32) : 2048 / D;   // keys of a stage
@@ -58,24 +68,42 @@ struct Shape {
     static constexpr int kRing = kQBytes > 32768 ? 131072 : kQBytes > 16384 ? 163840 : 196608;
     static constexpr int kStages = kRing / kStageBytes / KG;           // of one key group
     static constexpr int kTile = KG * KT;                              // keys of a tile
+    static constexpr int kGroupCost = 3;                               // a group's begin and end, in tiles
     static constexpr int JC = D < 128 ? D : 128;                       // channels of a join pass
     static constexpr int kJPitch = JC + 4;                             // 8t+g banks for the writes below
     static constexpr int kJoinBytes = KG * 8 * kJPitch * 4 > kJoinMin<D> ? KG * 8 * kJPitch * 4 : kJoinMin<D>;
     static constexpr int kMlBytes = KG * kRows * 8;
-    static constexpr int kValidBytes = KG * kStages * RG * 4;
-    static constexpr int kSmem = KG * kStages * kStageBytes + kQBytes + kJoinBytes + kMlBytes + kValidBytes;
-    static_assert(kStages >= 3 && KT % RG == 0 && KT / RG <= 32 && kSmem + 512 <= 232448, "shape");
+    static constexpr int kBarBytes = (2 * KG * kStages + 1) * 8;       // full and empty of each stage, and one that nothing arrives on
+    static constexpr int kValidBytes = KG * kStages * PW * 4;
+    static constexpr int kSmem = KG * kStages * kStageBytes + kQBytes + kJoinBytes + kMlBytes + kBarBytes + kValidBytes;
+    // With 12 warps the computing ones take over registers of the loading ones: 168 a thread at launch = 2/3 of 224 + 1/3 of 56.
+    static constexpr bool kMoveRegs = kAll > 256;
+    static_assert(kStages >= 3 && KT % PW == 0 && KT / PW <= 32 && kSmem + 512 <= 232448, "shape");
 };
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+using tc::smem_u32;
 
 // 16 bytes global -> shared; `n` = 16 or 0 (zero fill, nothing read).
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int n) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// One arrival on `bar` when all cp.async of this thread so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+constexpr int kWaitLimit = 1 << 22;   // polls of a wait before it gives up
+
+// Wait for phase `parity` of `bar`; false when it gives up or another warp has.
+__device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int limit = kWaitLimit) {
+    for (int it = 0; it < limit; it += 16) {
+        if (tc::mbar_wait(bar, parity, 16)) return true;
+        if (*abort) return false;
+    }
+    *abort = 1;
+    return false;
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -103,9 +131,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Where a walk over the tiles stands: group (b, hk, rb), tile of the group.
+// Where a walk over the tiles stands: group (b, hk, rb), tile of the group.  `at` numbers the tiles of all groups one
+// after another, each group's followed by cost numbers that no tile has.
 struct Cursor {
     int b, hk, rb, tile, tiles, len;
+    long long at;
 };
 
 __device__ __forceinline__ int seq_keys(const AttnParams& p, int b, bool* over) {
@@ -118,9 +148,8 @@ __device__ __forceinline__ int seq_keys(const AttnParams& p, int b, bool* over) 
 template <int kTile>
 __device__ __forceinline__ int tiles_of(int len) { return max(1, (len + kTile - 1) / kTile); }   // an empty sequence has one
 
-template <int kTile>
-__device__ __forceinline__ void advance(const AttnParams& p, Cursor& c, int row_blocks) {
-    if (++c.tile < c.tiles) return;
+template <class S>
+__device__ __forceinline__ void next_group(const AttnParams& p, Cursor& c, int row_blocks) {
     c.tile = 0;
     if (++c.rb < row_blocks) return;
     c.rb = 0;
@@ -129,8 +158,16 @@ __device__ __forceinline__ void advance(const AttnParams& p, Cursor& c, int row_
     if (++c.b < p.B) {
         bool over;
         c.len = seq_keys(p, c.b, &over);
-        c.tiles = tiles_of<kTile>(c.len);
+        c.tiles = tiles_of<S::kTile>(c.len);
     }
+}
+
+template <class S>
+__device__ __forceinline__ void advance(const AttnParams& p, Cursor& c, int row_blocks) {
+    ++c.at;
+    if (++c.tile < c.tiles) return;
+    c.at += S::kGroupCost;
+    next_group<S>(p, c, row_blocks);
 }
 
 struct Split {
@@ -164,6 +201,12 @@ __device__ __forceinline__ void put(const AttnParams& p, bool out_bf16, int b, i
     const long long at = (t * p.Hq + h) * D + c;
     if (out_bf16) StateIO<__nv_bfloat16>::st(static_cast<__nv_bfloat16*>(p.out) + at, y);
     else StateIO<float>::st(static_cast<float*>(p.out) + at, y);
+}
+
+// The barrier of the computing warps.
+template <class S>
+__device__ __forceinline__ void sync_computing() {
+    asm volatile("bar.sync 1, %0;" ::"n"(S::kThreads) : "memory");
 }
 
 // a / b with the short division where it will do.
@@ -209,7 +252,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, bool out_bf16, c
             for (int d = 1; d < kTpr; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
             if (sub == 0) t_s[r] = make_float2(mm, ll);
         }
-        __syncthreads();
+        sync_computing<S>();
         if (kItems >= S::kThreads || threadIdx.x < kItems) {
             float4 y[kBatch];
 #pragma unroll
@@ -255,34 +298,49 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, bool out_bf16, c
                 put<Ta, D>(p, out_bf16, b, hk, row0 + r0 + r, i % (D / 4) * 4, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
             }
         }
-        __syncthreads();
+        sync_computing<S>();
     }
 }
 
 template <class S>
-__global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnParams p, const int out_bf16) {
+__global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParams p, const int out_bf16) {
     using Ta = typename S::Ta;
-    constexpr int D = S::D, NT = S::NT, RG = S::RG, KG = S::KG, KT = S::KT, kTile = S::kTile;
+    constexpr int D = S::D, NT = S::NT, RG = S::RG, KG = S::KG, KT = S::KT, PW = S::PW, kTile = S::kTile;
+    constexpr int kStages = S::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* const q_s = smem + KG * S::kStages * S::kStageBytes;
+    uint8_t* const q_s = smem + KG * kStages * S::kStageBytes;
     float* const join_s = reinterpret_cast<float*>(q_s + S::kQBytes);
     float2* const ml_s = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(join_s) + S::kJoinBytes);   // [KG][kRows]
-    volatile uint32_t* const valid_s = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(ml_s) + S::kMlBytes);
-    __shared__ long long sums_s[S::kThreads / 32 + 1];
-    __shared__ long long start_s[2];
-    __shared__ int flag_s, start_b_s;
+    uint64_t* const full_s = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(ml_s) + S::kMlBytes);   // [KG][kStages]
+    uint64_t* const empty_s = full_s + KG * kStages;
+    uint64_t* const never_s = empty_s + KG * kStages;
+    volatile uint32_t* const valid_s = reinterpret_cast<uint32_t*>(never_s + 1);   // [KG][kStages][PW]
+    __shared__ long long sums_s[S::kAll / 32];
+    __shared__ long long start_s;
+    __shared__ int flag_s, stop_s, start_b_s;
+    __shared__ volatile int abort_s;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int kg = warp / RG, rg = warp % RG;
     const int R = p.G * p.K, row_blocks = (R + S::kRows - 1) / S::kRows;
     const int per_seq = p.Hkv * row_blocks;   // groups of a sequence
 
     // ---------------------------------------------------------------- this CTA's share of the tiles
-    const int per = (p.B + S::kThreads - 1) / S::kThreads;
+    if (threadIdx.x < KG * kStages) {
+        tc::mbar_init(full_s + threadIdx.x, PW * 33);   // each loading lane's copies, and one arrival a warp for the valid word
+        tc::mbar_init(empty_s + threadIdx.x, RG);
+    }
+    if (threadIdx.x == 0) {
+        tc::mbar_init(never_s, 1);
+        abort_s = 0;
+    }
+    const int per = (p.B + S::kAll - 1) / S::kAll;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-    long long mine = 0;
     bool over;
-    for (int b = b0; b < b1; ++b) mine += static_cast<long long>(tiles_of<kTile>(seq_keys(p, b, &over))) * per_seq;
+    auto numbers_of = [&](int b) {   // of a sequence's groups
+        return static_cast<long long>(tiles_of<kTile>(seq_keys(p, b, &over)) + S::kGroupCost) * per_seq;
+    };
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += numbers_of(b);
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -292,89 +350,111 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
     if (lane == 31) sums_s[warp] = incl;
     __syncthreads();
     long long before = 0, total = 0;
-    for (int w = 0; w < S::kThreads / 32; ++w) {
+    for (int w = 0; w < S::kAll / 32; ++w) {
         if (w < warp) before += sums_s[w];
         total += sums_s[w];
     }
     before += incl - mine;
     const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
     if (static_cast<int>(blockIdx.x) >= ctas) return;
-    const long long first = quot(total * blockIdx.x, ctas), last = quot(total * (blockIdx.x + 1), ctas);   // tiles [first, last)
-    if (first >= before && first < before + mine) {   // one thread: its sequences hold the first tile
+    const long long first = quot(total * blockIdx.x, ctas), last = quot(total * (blockIdx.x + 1), ctas);   // numbers [first, last)
+    if (first >= before && first < before + mine) {   // one thread: its sequences hold the first number
         long long at = before;
         int b = b0;
         for (; b < b1; ++b) {
-            const long long n = static_cast<long long>(tiles_of<kTile>(seq_keys(p, b, &over))) * per_seq;
+            const long long n = numbers_of(b);
             if (first < at + n) break;
             at += n;
         }
         start_b_s = b;
-        start_s[0] = at;
+        start_s = at;
     }
     __syncthreads();
-    Cursor cc;   // compute
+    Cursor cc;
     cc.b = start_b_s;
     cc.len = seq_keys(p, cc.b, &over);
     cc.tiles = tiles_of<kTile>(cc.len);
     {
-        const long long in_seq = first - start_s[0];
-        const int group = static_cast<int>(quot(in_seq, cc.tiles));
-        cc.tile = static_cast<int>(in_seq - static_cast<long long>(group) * cc.tiles);
+        const int size = cc.tiles + S::kGroupCost;
+        const long long in_seq = first - start_s;
+        const int group = static_cast<int>(quot(in_seq, size));
+        cc.tile = static_cast<int>(in_seq - static_cast<long long>(group) * size);
         cc.hk = group / row_blocks;
-        cc.rb = group % row_blocks;
-    }
-    const int n_tiles = static_cast<int>(last - first);
-
-    // ---------------------------------------------------------------- loads
-    Cursor lc = cc;
-    constexpr int kKeys = KT / RG;   // keys of a stage that one warp loads; lane l knows key l's page
-    const uint32_t ring = smem_u32(smem) + kg * S::kStages * S::kStageBytes;
-    const int ps = p.cache.page_size;
-    // pages are looked up two tiles ahead of their keys' loads
-    int page[2] = {-1, -1}, in_page[2] = {0, 0}, head[2] = {0, 0};
-    int looked = 0, load_slot = 0;
-    auto load = [&](int i) {   // look up tile i + 2 of this CTA, load tile i
-        const int pg = page[0];
-        const long long off = pg * p.cache.page_stride + in_page[0] * p.cache.token_stride + head[0] * p.cache.head_stride;
-        page[0] = page[1];
-        in_page[0] = in_page[1];
-        head[0] = head[1];
-        page[1] = -1;
-        if (looked < n_tiles) {
-            const int j = lc.tile * kTile + kg * KT + rg * kKeys + lane;
-            if (lane < kKeys && j < lc.len) {
-                const int k = j / ps;
-                in_page[1] = j - k * ps;
-                head[1] = lc.hk;
-                page[1] = p.block_table[static_cast<size_t>(lc.b) * p.max_pages + k];
-                if (page[1] < 0 || page[1] >= p.cache.num_pages) {
-                    page[1] = -1;
-                    if (p.status) atomicOr(p.status + lc.b, kKvBadIndex);
-                }
-            }
-            advance<kTile>(p, lc, row_blocks);
-            ++looked;
+        cc.rb = group - cc.hk * row_blocks;
+        cc.at = first;
+        if (cc.tile >= cc.tiles) {   // among the numbers without a tile: the next group is the first
+            cc.at += size - cc.tile;
+            next_group<S>(p, cc, row_blocks);
         }
-        if (i >= 0 && i < n_tiles) {
+    }
+
+    // ---------------------------------------------------------------- the loading warps
+    if (warp >= RG * KG) {
+        if constexpr (S::kMoveRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        constexpr int kKeys = KT / PW;   // keys of a stage that one warp loads; lane l knows key l's page
+        const int kg = (warp - RG * KG) / PW, pw = (warp - RG * KG) % PW;
+        const uint32_t ring = smem_u32(smem) + kg * kStages * S::kStageBytes;
+        const int ps = p.cache.page_size;
+        // pages are looked up two tiles ahead of their keys' loads: turn t looks up tile t and loads tile t - 2
+        int page[2] = {-1, -1}, in_page[2] = {0, 0}, head[2] = {0, 0};
+        int tiles = 0, slot = 0;   // tiles: looked up so far
+        uint32_t round = 0;
+#pragma unroll 1
+        for (int t = 0;; ++t) {
+            const int pg = page[0];
+            const long long off = pg * p.cache.page_stride + in_page[0] * p.cache.token_stride + head[0] * p.cache.head_stride;
+            page[0] = page[1];
+            in_page[0] = in_page[1];
+            head[0] = head[1];
+            page[1] = -1;
+            if (cc.at < last) {
+                const int j = cc.tile * kTile + kg * KT + pw * kKeys + lane;
+                if (lane < kKeys && j < cc.len) {
+                    const int k = j / ps;
+                    in_page[1] = j - k * ps;
+                    head[1] = cc.hk;
+                    page[1] = p.block_table[static_cast<size_t>(cc.b) * p.max_pages + k];
+                    if (page[1] < 0 || page[1] >= p.cache.num_pages) {
+                        page[1] = -1;
+                        if (p.status) atomicOr(p.status + cc.b, kKvBadIndex);
+                    }
+                }
+                advance<S>(p, cc, row_blocks);
+                ++tiles;
+            }
+            if (t < 2) continue;
+            if (t - 2 >= tiles) break;
+            if (round > 0 && !stage_wait(empty_s + kg * kStages + slot, (round - 1) & 1, &abort_s)) break;
             const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
-            if (lane == 0) valid_s[(kg * S::kStages + load_slot) * RG + rg] = ok;
+            if (lane == 0) valid_s[(kg * kStages + slot) * PW + pw] = ok;
             constexpr int kChunks = S::kRowBytes / 16;   // of a row
-            const uint32_t st = ring + load_slot * S::kStageBytes;
+            const uint32_t st = ring + slot * S::kStageBytes;
 #pragma unroll
             for (int it = 0; it < kKeys * kChunks / 32; ++it) {
                 const int flat = it * 32 + lane;
                 const int key = flat / kChunks, ch = flat % kChunks;
                 const long long o = __shfl_sync(0xffffffffu, off, key) + ch * (16 / static_cast<int>(sizeof(Ta)));
                 const int n = (ok >> key) & 1 ? 16 : 0;
-                const int row = rg * kKeys + key;
+                const int row = pw * kKeys + key;
                 const uint32_t dst = st + row * S::kRowBytes + (S::kBf16 ? (ch ^ (row & 7)) : ch) * 16;
                 cp16(dst, static_cast<const Ta*>(p.cache.k) + (n ? o : 0), n);
                 cp16(dst + S::kHalfBytes, static_cast<const Ta*>(p.cache.v) + (n ? o : 0), n);
             }
-            if (++load_slot == S::kStages) load_slot = 0;
+            cp_arrive(full_s + kg * kStages + slot);
+            if (lane == 0) tc::mbar_arrive(full_s + kg * kStages + slot);
+            if (++slot == kStages) {
+                slot = 0;
+                ++round;
+            }
         }
-        cp_commit();
-    };
+        cp_wait_all();   // nothing of a call that gives up is in flight when the CTA ends
+        return;
+    }
+
+    // ---------------------------------------------------------------- the computing warps
+    if constexpr (S::kMoveRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int kg = warp / RG, rg = warp % RG;
+    const uint32_t ring = smem_u32(smem) + kg * kStages * S::kStageBytes;
 
     // ---------------------------------------------------------------- state of a row set
     // bf16: o[mt][nt] is the 16 x 8 fragment (channels 16 mt.., rows 8 nt..) of o transposed; this thread has rows
@@ -404,7 +484,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                 if (row < R) v = *reinterpret_cast<const uint4*>(q + tok * p.ldq + (row - tok * p.G) * D + ch * 8);
                 *reinterpret_cast<uint4*>(q_s + r * S::kRowBytes + (ch ^ (r & 7)) * 16) = v;
             }
-            __syncthreads();
+            sync_computing<S>();
         } else {
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
@@ -434,7 +514,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
         const int j0 = cc.tile * kTile + kg * KT;   // the stage's first key
         uint32_t ok = 0;
 #pragma unroll
-        for (int w = 0; w < RG; ++w) ok |= valid_s[(kg * S::kStages + slot) * RG + w] << (w * kKeys);
+        for (int w = 0; w < PW; ++w) ok |= valid_s[(kg * kStages + slot) * PW + w] << (w * (KT / PW));
         constexpr uint32_t kFull = KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1;
         if (ok == 0) return;
         const bool masked = ok != kFull || j0 + KT > cc.len - p.K + 1;
@@ -556,7 +636,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                 }
         } else {
             // fp32 products and sums on the CUDA cores: 4 keys x 8 rows at a time, the channels over the lanes
-            const float* ks = reinterpret_cast<const float*>(smem + (kg * S::kStages + slot) * S::kStageBytes) + lane * kV;
+            const float* ks = reinterpret_cast<const float*>(smem + (kg * kStages + slot) * S::kStageBytes) + lane * kV;
             const float* vs = ks + S::kHalfBytes / 4;
 #pragma unroll 1
             for (int k0 = 0; k0 < KT; k0 += 4) {
@@ -623,11 +703,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
     const Split sp = {static_cast<int*>(p.workspace), reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kCounterBytes),
                       reinterpret_cast<float2*>(static_cast<uint8_t*>(p.workspace) + kCounterBytes +
                                                 static_cast<size_t>(2) * gridDim.x * S::kRows * D * 4)};
-    long long seg_first = first;   // this CTA's first tile of the group
-    auto end_segment = [&](long long next) {   // tiles [seg_first, next) of the group are done
-        const long long g_first = next - 1 - cc.tile, g_last = g_first + cc.tiles;   // the group's tiles
-        const bool whole = seg_first == g_first && next == g_last;
-        const int part = 2 * blockIdx.x + (seg_first == first ? 0 : 1);
+    long long seg_first = cc.at;   // this CTA's first tile of the group
+    bool first_seg = true;         // of this CTA
+    auto end_segment = [&]() {     // the tiles from seg_first up to and with cc's are done
+        const long long g_first = cc.at - cc.tile, g_last = g_first + cc.tiles;   // the group's tiles
+        const bool whole = seg_first == g_first && cc.at + 1 == g_last;
+        const int part = 2 * blockIdx.x + (first_seg ? 0 : 1);
+        if (threadIdx.x == 0) stop_s = abort_s;
         if constexpr (S::kBf16) {
 #pragma unroll
             for (int i = 0; i < kCols; ++i)
@@ -672,7 +754,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                                 join_s[(kg * 8 + r) * S::kJPitch + c / kV * 32 * kV % S::JC + lane * kV + c % kV] = o[r][c];
                 }
             }
-            __syncthreads();
+            sync_computing<S>();
+            if (stop_s) {   // a wait gave up: nothing of this group is written
+                if (threadIdx.x == 0 && p.status) atomicOr(p.status + cc.b, 16);
+                return;
+            }
 #pragma unroll 1
             for (int i = threadIdx.x; i < 8 * S::JC / 4; i += S::kThreads) {
                 const int r = i / (S::JC / 4), ch = i % (S::JC / 4) * 4, row = r0 + r;
@@ -702,7 +788,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                     if (ch0 + ch == 0) sp.ml[static_cast<size_t>(part) * S::kRows + row] = make_float2(mm, ll);
                 }
             }
-            __syncthreads();
+            sync_computing<S>();
         }
         if (whole) return;
         // The CTAs c0.. of this group hold its n parts; the first one's lies in either of that CTA's two places.  Up to
@@ -712,7 +798,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
         const int c0 = static_cast<int>(quot((g_first + 1) * ctas - 1, total)), c1 = static_cast<int>(quot(g_last * ctas - 1, total));
         const int n = c1 - c0 + 1, fan = n <= kFanOne ? kFanOne : n <= 64 ? 8 : 12;
         const int k0 = (static_cast<int>(blockIdx.x) - c0) / fan * fan;   // this CTA's neighbours are k0..
-        const int part0 = 2 * c0 + (quot(total * c0, ctas) == g_first ? 0 : 1);
+        const int part0 = 2 * c0 + (quot(total * c0, ctas) >= g_first - S::kGroupCost ? 0 : 1);   // no tile of the group before in that CTA
         auto place = [&](int k) { return k == 0 ? part0 : 2 * (c0 + k); };
 #pragma unroll 1
         for (int level = 0; level < 2; ++level) {
@@ -720,7 +806,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
             const int count = level == 0 ? min(fan, n - k0) : (n + fan - 1) / fan;
             const bool final = level == 1 || n <= fan;
             if (level == 0 && count == 1) continue;   // already where level 1 reads it
-            __syncthreads();   // this CTA's part is written
+            sync_computing<S>();   // this CTA's part is written
             if (threadIdx.x == 0) {
                 int* const counter = level == 0 ? sp.counters + place(k0) : sp.counters + 2 * kMaxCtas + c0;
                 // releases what the CTA wrote, acquires what the others did; counts to count - 1 and back to zero, ready
@@ -729,7 +815,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
                 asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(count - 1) : "memory");
                 flag_s = old == static_cast<unsigned>(count - 1);
             }
-            __syncthreads();
+            sync_computing<S>();
             if (!flag_s) return;
             const int to = place(k0);
             join_parts<S>(p, out_bf16, sp, rows, cc.b, cc.hk, cc.rb * S::kRows, join_s, count, final, to,
@@ -738,51 +824,48 @@ __global__ void __launch_bounds__(S::kThreads, 1) attn_decode_kernel(const AttnP
         }
     };
 
-    // ---------------------------------------------------------------- the walk
-    // One copy of each part (the code is fetched anew by every launch): the first two turns only look up pages, the next
-    // kStages - 1 only load.
+    // ---------------------------------------------------------------- the walk (one copy of each part: the code is fetched
+    // anew by every launch)
+    if (p.test_stall) stage_wait(never_s, 0, &abort_s, 256);
     bool fresh = true, new_seq = cc.tile == 0 && cc.hk == 0 && cc.rb == 0;
+    uint32_t phase = 0;
 #pragma unroll 1
-    for (int i = -1 - S::kStages; i < n_tiles; ++i) {
-        if (i >= 0) {
-            if (fresh) {
-                begin_segment();
-                if (new_seq && threadIdx.x == 0 && p.status) {
-                    seq_keys(p, cc.b, &over);
-                    if (over) atomicOr(p.status + cc.b, kKvBadIndex);
-                }
-                fresh = false;
+    while (cc.at < last) {
+        if (fresh) {
+            begin_segment();
+            if (new_seq && threadIdx.x == 0 && p.status) {
+                seq_keys(p, cc.b, &over);
+                if (over) atomicOr(p.status + cc.b, kKvBadIndex);
             }
-            cp_wait<S::kStages - 2>();
-            if constexpr (RG == 1) __syncwarp();
-            else asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(RG * 32) : "memory");
+            fresh = false;
         }
-        load(i + S::kStages - 1);
-        if (i < 0) continue;
-        compute();
-        if (++slot == S::kStages) slot = 0;
+        if (stage_wait(full_s + kg * kStages + slot, phase, &abort_s)) compute();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(empty_s + kg * kStages + slot);
+        if (++slot == kStages) {
+            slot = 0;
+            phase ^= 1;
+        }
         const bool group_done = cc.tile + 1 == cc.tiles;
-        if (group_done || i + 1 == n_tiles) {
-            end_segment(first + i + 1);
-            seg_first = first + i + 1;
+        if (group_done || cc.at + 1 == last) {
+            end_segment();
+            first_seg = false;
         }
-        if (group_done && i + 1 < n_tiles) {
-            const int b = cc.b;
-            advance<kTile>(p, cc, row_blocks);
+        const int b = cc.b;
+        advance<S>(p, cc, row_blocks);
+        if (group_done) {
             new_seq = cc.b != b;
             fresh = true;
-        } else {
-            ++cc.tile;
+            seg_first = cc.at;
         }
     }
-    cp_wait<0>();
 }
 
 template <class S>
 cudaError_t launch(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    attn_decode_kernel<S><<<sms, S::kThreads, S::kSmem, stream>>>(p, out_bf16 ? 1 : 0);
+    attn_decode_kernel<S><<<sms, S::kAll, S::kSmem, stream>>>(p, out_bf16 ? 1 : 0);
     return cudaGetLastError();
 }
 

@@ -64,7 +64,7 @@ gdn_status check_attn_dims(const gdn_attn_dims* d) {
         return GDN_E_INVALID_ARG;
     if (!is_dtype(d->act_dtype) || !is_dtype(d->out_dtype)) return GDN_E_INVALID_ARG;
     if (!std::isfinite(d->scale) || !(d->eps > 0.0f) || !std::isfinite(d->eps)) return GDN_E_INVALID_ARG;
-    if (d->rope_dim < 0 || d->rope_dim > d->head_dim) return GDN_E_INVALID_ARG;
+    if (d->rope_dim < 0 || d->rope_dim > d->head_dim || (d->flags & ~GDN_FLAG_TEST_STALL)) return GDN_E_INVALID_ARG;
     if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256) return GDN_E_UNSUPPORTED;
     if (d->H_q / d->H_kv > 16 || d->rope_dim % 16 != 0) return GDN_E_UNSUPPORTED;
     return GDN_OK;
@@ -246,7 +246,8 @@ gdn_status gdn_attn_decode(const gdn_attn_dims* dims, const gdn_kv_cache* cache,
         return GDN_E_INVALID_ARG;
     const int G = dims->H_q / dims->H_kv;
     gdn::AttnParams p{kc, B, K, dims->H_q, dims->H_kv, G, max_pages, (65536u + G - 1) / G, dims->scale, q, gate, ldq,
-                      ldg, block_table, seq_len, out, workspace, dev_status};
+                      ldg, block_table, seq_len, out, workspace, dev_status,
+                      (dims->flags & GDN_FLAG_TEST_STALL) ? 1 : 0};
     return cuda_status(gdn::launch_attn_decode(p, dims->head_dim, dims->act_dtype, dims->out_dtype,
                                                reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -83,6 +83,7 @@ struct AttnParams {
     void* out;
     void* workspace;
     int* status;          // optional [B]
+    int test_stall;       // GDN_FLAG_TEST_STALL
 };
 
 struct NormParams {

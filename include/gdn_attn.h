@@ -32,6 +32,9 @@
  *   GDN_KV_REFUSED   the page bookkeeping left the sequence as it was
  *   GDN_KV_BAD_INDEX a length, page, slot or position outside its range; the
  *                    keys or tokens concerned were left out
+ *   16 (bit 4)       a bounded wait inside gdn_attn_decode gave up: outputs of
+ *                    the sequence were not (fully) written, and the workspace
+ *                    has to be zeroed before its next use
  */
 #ifndef GDN_ATTN_H
 #define GDN_ATTN_H
@@ -56,6 +59,7 @@ typedef struct {
     float eps;          /* RMSNorm eps                                          */
     int32_t act_dtype;  /* gdn_dtype of q, k, v, gate and the cache             */
     int32_t out_dtype;  /* gdn_dtype of the attention's out                     */
+    uint32_t flags;     /* 0, or GDN_FLAG_TEST_STALL (gdn.h; gdn_attn_decode)   */
 } gdn_attn_dims;
 
 /*

@@ -36,8 +36,8 @@ def test_headers_compile_as_c_and_match_the_bindings():
     assert r.returncode == 0, r.stderr
 
 
-def adims(Hq=16, Hkv=2, d=256, rope=0, scale=0.0625, eps=1e-6, act=1, out=1):
-    return gdn.GdnAttnDims(Hq, Hkv, d, rope, scale, eps, act, out)
+def adims(Hq=16, Hkv=2, d=256, rope=0, scale=0.0625, eps=1e-6, act=1, out=1, flags=0):
+    return gdn.GdnAttnDims(Hq, Hkv, d, rope, scale, eps, act, out, flags)
 
 
 def cache(k=A(0), v=A(1), pages=100, ps=16, s=None, dims=None):
@@ -60,7 +60,7 @@ BAD_DIMS = [
     (dict(Hq=0), INVALID), (dict(Hkv=0), INVALID), (dict(Hq=5, Hkv=2), INVALID), (dict(act=2), INVALID),
     (dict(out=-1), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(eps=0.0), INVALID),
     (dict(rope=-16), INVALID), (dict(rope=272), INVALID), (dict(d=96), UNSUPPORTED), (dict(d=512), UNSUPPORTED),
-    (dict(Hq=34, Hkv=2), UNSUPPORTED), (dict(rope=24), UNSUPPORTED)]
+    (dict(Hq=34, Hkv=2), UNSUPPORTED), (dict(rope=24), UNSUPPORTED), (dict(flags=1), INVALID), (dict(flags=8), INVALID)]
 
 
 @pytest.mark.parametrize("kw,status", BAD_DIMS)

@@ -231,3 +231,20 @@ def test_graph_replay_follows_the_lengths():
         g.replay()
         torch.cuda.synchronize()
         c.close(out)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_wait_that_gives_up_writes_nothing(dtype):
+    """GDN_FLAG_TEST_STALL: the computing warps first wait on a barrier that nothing arrives on.  Every sequence
+    reports bit 4, no output byte changes, and with a zeroed workspace the next call is right."""
+    c = Case([300, 0, 40, 4000, 17], 2, 8, 2, 128, 16, dtype, seed=16)
+    d = gdn.make_attn_dims(c.Hq, c.Hkv, c.d, dtype, F32, test_stall=True)
+    ws = torch.zeros(gdn.gdn_attn_decode_workspace_bytes(d, 5, 2), dtype=torch.uint8, device="cuda")
+    out = torch.full((10, c.Hq * c.d), 7.0, device="cuda")
+    st = torch.zeros(5, dtype=torch.int32, device="cuda")
+    gdn.gdn_attn_decode(d, gdn.KvCache(c.k, c.v), 2, c.q, c.table.cuda(), c.seq_len, out, gate=c.gate, workspace=ws,
+                        dev_status=st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [16] * 5 and (out == 7.0).all()
+    ws.zero_()
+    c.close(c.run(F32, ws=ws))
