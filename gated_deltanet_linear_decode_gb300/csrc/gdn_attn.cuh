@@ -36,6 +36,7 @@
 #include "gdn.h"
 #include "gdn_attn_internal.h"
 #include "gdn_common.cuh"
+#include "gdn_launch.h"
 #include "gdn_tc.cuh"
 
 namespace gdn {
@@ -44,8 +45,6 @@ namespace attn {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kMaxCtas = 256;
 constexpr int kFanOne = 16, kMaxFan = 32;         // parts joined at once: all of up to kFanOne, at most kMaxFan
-template <int D>
-constexpr int kJoinMin = kMaxFan * 32 + 64 + 32 * D;   // weights and totals of 8 rows, the rows
 constexpr size_t kCounterBytes = 3 * kMaxCtas * 4;   // at the start of the workspace
 static_assert(kMaxCtas / 12 < kMaxFan, "parts of the second step");
 
@@ -65,13 +64,14 @@ struct Shape {
     static constexpr int kHalfBytes = KT * kRowBytes;                  // the keys of a stage, then the values
     static constexpr int kStageBytes = 2 * kHalfBytes;
     static constexpr int kQBytes = kBf16 ? kRows * kRowBytes : 0;      // queries, bf16 kernels only
-    static constexpr int kRing = kQBytes > 32768 ? 131072 : kQBytes > 16384 ? 163840 : 196608;
+    static constexpr int kRing = kQBytes > 32768 ? 131072 : kQBytes > 16384 || kRows == 128 ? 163840 : 196608;
     static constexpr int kStages = kRing / kStageBytes / KG;           // of one key group
     static constexpr int kTile = KG * KT;                              // keys of a tile
     static constexpr int kGroupCost = 3;                               // a group's begin and end, in tiles
     static constexpr int JC = D < 128 ? D : 128;                       // channels of a join pass
     static constexpr int kJPitch = JC + 4;                             // 8t+g banks for the writes below
-    static constexpr int kJoinBytes = KG * 8 * kJPitch * 4 > kJoinMin<D> ? KG * 8 * kJPitch * 4 : kJoinMin<D>;
+    static constexpr int kPartBytes = (kMaxFan * 4 + 8) * kRows;       // weights and totals of a join of parts
+    static constexpr int kJoinBytes = KG * 8 * kJPitch * 4 > kPartBytes ? KG * 8 * kJPitch * 4 : kPartBytes;
     static constexpr int kMlBytes = KG * kRows * 8;
     static constexpr int kBarBytes = (2 * KG * kStages + 1) * 8;       // full and empty of each stage, and one that nothing arrives on
     static constexpr int kValidBytes = KG * kStages * PW * 4;
@@ -215,91 +215,84 @@ __device__ __forceinline__ long long quot(long long a, long long b) {
 }
 
 // Join `count` parts of a group's rows (part k's rows begin at row_at(k)): into the result if `final`, else into place
-// `to`.  All loads of a step are issued together: 8 rows cost a round trip for the statistics and one for every eight
-// parts.  Parts have all kRows rows; those past `rows` hold nothing and go nowhere.  `w_s`: kJoinMin<D> bytes.
+// `to`.  The loads of a step are issued together: a round trip for the statistics, then one for every eight parts of
+// kBatch * kThreads float4s.  Parts have all kRows rows; those past `rows` hold nothing and go nowhere.
 template <class S, class F>
 __device__ __forceinline__ void join_parts(const AttnParams& p, bool out_bf16, const Split& sp, int rows, int b, int hk, int row0,
                                            float* w_s, int count, bool final, int to, F row_at) {
     using Ta = typename S::Ta;
-    constexpr int D = S::D, kItems = 8 * D / 4, kBatch = kItems > S::kThreads ? kItems / S::kThreads : 1;
-    constexpr int kTpr = 16;   // threads a row; the first 128 threads
-    float2* const t_s = reinterpret_cast<float2*>(w_s + kMaxFan * 8);
-    float4* const y_s = reinterpret_cast<float4*>(t_s + 8);
+    constexpr int D = S::D, kItems = S::kRows * D / 4, kBatch = kItems / S::kThreads < 4 ? kItems / S::kThreads : 4;
+    constexpr int kTpr = 8;   // threads a row for the statistics
+    static_assert(kItems % (S::kThreads * kBatch) == 0 && kBatch > 0, "every thread has a share");
+    float2* const t_s = reinterpret_cast<float2*>(w_s + kMaxFan * S::kRows);   // [kRows]; w_s [kMaxFan][kRows]
 #pragma unroll 1
-    for (int r0 = 0; r0 < rows; r0 += 8) {
-        if (threadIdx.x < 8 * kTpr) {
-            const int r = threadIdx.x / kTpr, sub = threadIdx.x % kTpr;
-            float2 t[kMaxFan / kTpr];
-            float mm = -INFINITY, ll = 0.f;
+    for (int r = threadIdx.x / kTpr; r < rows; r += S::kThreads / kTpr) {
+        const int sub = threadIdx.x % kTpr;
+        const uint32_t group = 0xffu << (threadIdx.x & 24);
+        float2 t[kMaxFan / kTpr];
+        float mm = -INFINITY, ll = 0.f;
 #pragma unroll
-            for (int i = 0; i < kMaxFan / kTpr; ++i) {
-                const int k = i * kTpr + sub;
-                t[i] = make_float2(-INFINITY, 0.f);
-                if (k < count) t[i] = __ldcg(sp.ml + row_at(k) + r0 + r);
-            }
-#pragma unroll
-            for (int i = 0; i < kMaxFan / kTpr; ++i) mm = fmaxf(mm, t[i].x);
-#pragma unroll
-            for (int d = 1; d < kTpr; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
-            const float base = mm == -INFINITY ? 0.f : mm;
-#pragma unroll
-            for (int i = 0; i < kMaxFan / kTpr; ++i) {
-                const float f = ex2(t[i].x - base);
-                ll = fmaf(f, t[i].y, ll);
-                w_s[(i * kTpr + sub) * 8 + r] = f;
-            }
-#pragma unroll
-            for (int d = 1; d < kTpr; d <<= 1) ll += __shfl_xor_sync(0xffffffffu, ll, d);
-            if (sub == 0) t_s[r] = make_float2(mm, ll);
+        for (int i = 0; i < kMaxFan / kTpr; ++i) {
+            const int k = i * kTpr + sub;
+            t[i] = make_float2(-INFINITY, 0.f);
+            if (k < count) t[i] = __ldcg(sp.ml + row_at(k) + r);
         }
-        sync_computing<S>();
-        if (kItems >= S::kThreads || threadIdx.x < kItems) {
-            float4 y[kBatch];
 #pragma unroll
-            for (int j = 0; j < kBatch; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const float* const w = w_s + threadIdx.x / (D / 4);
-#pragma unroll 1
-            for (int k0 = 0; k0 < count; k0 += 8) {   // 8 loads at a time; past the last part it again, with the weight 0
-                float4 v[8][kBatch];
+        for (int i = 0; i < kMaxFan / kTpr; ++i) mm = fmaxf(mm, t[i].x);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const float4* const x = reinterpret_cast<const float4*>(sp.o + (row_at(min(k0 + u, count - 1)) + r0) * D) + threadIdx.x;
+        for (int d = 1; d < kTpr; d <<= 1) mm = fmaxf(mm, __shfl_xor_sync(group, mm, d));
+        const float base = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-                    for (int j = 0; j < kBatch; ++j) v[u][j] = __ldcg(x + j * S::kThreads);
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-#pragma unroll
-                    for (int j = 0; j < kBatch; ++j) {
-                        const float f = w[(k0 + u) * 8 + j * (S::kThreads / (D / 4))];
-                        y[j].x = fmaf(f, v[u][j].x, y[j].x);
-                        y[j].y = fmaf(f, v[u][j].y, y[j].y);
-                        y[j].z = fmaf(f, v[u][j].z, y[j].z);
-                        y[j].w = fmaf(f, v[u][j].w, y[j].w);
-                    }
-            }
-            if (final) {
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) y_s[threadIdx.x + j * S::kThreads] = y[j];
-            } else {
-                float4* const dst = reinterpret_cast<float4*>(sp.o + (static_cast<size_t>(to) * S::kRows + r0) * D) + threadIdx.x;
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) dst[j * S::kThreads] = y[j];
-                if (threadIdx.x < 8) sp.ml[static_cast<size_t>(to) * S::kRows + r0 + threadIdx.x] = t_s[threadIdx.x];
-            }
+        for (int i = 0; i < kMaxFan / kTpr; ++i) {
+            const float f = ex2(t[i].x - base);
+            ll = fmaf(f, t[i].y, ll);
+            w_s[(i * kTpr + sub) * S::kRows + r] = f;
         }
-        if (final) {
-            // each thread its own values again, in a loop that is not unrolled: code that runs once costs its fetch
-#pragma unroll 1
-            for (int i = threadIdx.x; i < min(8, rows - r0) * (D / 4); i += S::kThreads) {
-                const int r = i / (D / 4);
-                const float ll = t_s[r].y, inv = ll == 0.f ? 0.f : 1.0f / ll;
-                const float4 y = y_s[i];
-                put<Ta, D>(p, out_bf16, b, hk, row0 + r0 + r, i % (D / 4) * 4, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-            }
+#pragma unroll
+        for (int d = 1; d < kTpr; d <<= 1) ll += __shfl_xor_sync(group, ll, d);
+        if (sub == 0) {
+            t_s[r] = make_float2(mm, ll);
+            if (!final) sp.ml[static_cast<size_t>(to) * S::kRows + r] = make_float2(mm, ll);
         }
-        sync_computing<S>();
     }
+    sync_computing<S>();
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < rows * (D / 4); i0 += S::kThreads * kBatch) {
+        float4 y[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) y[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k0 = 0; k0 < count; k0 += 8) {   // past the last part it again, with the weight 0
+            float4 v[8][kBatch];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float4* const x = reinterpret_cast<const float4*>(sp.o + row_at(min(k0 + u, count - 1)) * D) + i0;
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) v[u][j] = __ldcg(x + j * S::kThreads);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const float f = w_s[(k0 + u) * S::kRows + (i0 + j * S::kThreads) / (D / 4)];
+                    y[j].x = fmaf(f, v[u][j].x, y[j].x);
+                    y[j].y = fmaf(f, v[u][j].y, y[j].y);
+                    y[j].z = fmaf(f, v[u][j].z, y[j].z);
+                    y[j].w = fmaf(f, v[u][j].w, y[j].w);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int i = i0 + j * S::kThreads, r = i / (D / 4);
+            if (!final) {
+                reinterpret_cast<float4*>(sp.o + static_cast<size_t>(to) * S::kRows * D)[i] = y[j];
+            } else if (r < rows) {
+                const float ll = t_s[r].y, inv = ll == 0.f ? 0.f : 1.0f / ll;
+                put<Ta, D>(p, out_bf16, b, hk, row0 + r, i % (D / 4) * 4, make_float4(y[j].x * inv, y[j].y * inv, y[j].z * inv, y[j].w * inv));
+            }
+        }
+    }
+    sync_computing<S>();
 }
 
 template <class S>
@@ -333,6 +326,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
         tc::mbar_init(never_s, 1);
         abort_s = 0;
     }
+    grid_dependency_wait();   // launched as a programmatic dependent: nothing global is touched before the previous kernel is done
     const int per = (p.B + S::kAll - 1) / S::kAll;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
     bool over;
@@ -356,7 +350,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
     }
     before += incl - mine;
     const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-    if (static_cast<int>(blockIdx.x) >= ctas) return;
+    if (static_cast<int>(blockIdx.x) >= ctas) return;   // (an exit lets the next kernel start, too)
     const long long first = quot(total * blockIdx.x, ctas), last = quot(total * (blockIdx.x + 1), ctas);   // numbers [first, last)
     if (first >= before && first < before + mine) {   // one thread: its sequences hold the first number
         long long at = before;
@@ -370,6 +364,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
         start_s = at;
     }
     __syncthreads();
+    grid_launch_dependents();
     Cursor cc;
     cc.b = start_b_s;
     cc.len = seq_keys(p, cc.b, &over);
@@ -529,20 +524,26 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             const uint32_t ka = st + key * S::kRowBytes + ((lane >> 4) ^ (key & 7)) * 16;
             constexpr int kSplit = SUB * NT >= 4 ? 1 : 2;   // independent sums, for the latency of a product
             float s2[kSplit][SUB][NT][4] = {};
+            constexpr int kKs = SUB == 1 ? 4 : 2;   // steps whose operands are loaded together
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ks += 2) {
-                uint32_t qb[NT][4];
+            for (int k0 = 0; k0 < D / 16; k0 += kKs) {
+                uint32_t qb[kKs / 2][NT][4], a[kKs][SUB][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) ldsm4((qa ^ ((2 * ks & 4) * 16)) + (2 * ks & ~7) * 16 + n * 8 * S::kRowBytes, qb[n]);
+                for (int i = 0; i < kKs; ++i) {
+                    const int ks = k0 + i;
+                    if (i % 2 == 0)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                        for (int n = 0; n < NT; ++n)
+                            ldsm4((qa ^ ((2 * ks & 4) * 16)) + (2 * ks & ~7) * 16 + n * 8 * S::kRowBytes, qb[i / 2][n]);
 #pragma unroll
-                    for (int u = 0; u < SUB; ++u) {
-                        uint32_t a[4];
-                        ldsm4((ka ^ ((2 * (ks + h) & 6) * 16)) + (2 * (ks + h) & ~7) * 16 + u * 16 * S::kRowBytes, a);
+                    for (int u = 0; u < SUB; ++u) ldsm4((ka ^ ((2 * ks & 6) * 16)) + (2 * ks & ~7) * 16 + u * 16 * S::kRowBytes, a[i][u]);
+                }
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(s2[h % kSplit][u][n], a, qb[n][2 * h], qb[n][2 * h + 1]);
-                    }
+                for (int i = 0; i < kKs; ++i)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16816(s2[i % kSplit][u][n], a[i][u], qb[i / 2][n][i % 2 * 2], qb[i / 2][n][i % 2 * 2 + 1]);
             }
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
@@ -623,17 +624,24 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 }
             // o transposed: channels x rows += V^T . P^T
             const uint32_t va = st + S::kHalfBytes + ((lane & 7) + (lane >> 4) * 8) * S::kRowBytes + (((lane >> 3) & 1) ^ (lane & 7)) * 16;
+            constexpr int kMt = SUB == 1 ? 4 : 2;   // as kKs above
 #pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt)
+            for (int m0 = 0; m0 < D / 16; m0 += kMt) {
+                uint32_t a[kMt][SUB][4];
 #pragma unroll
-                for (int u = 0; u < SUB; ++u) {
-                    uint32_t a[4];
-                    ldsm4t((va ^ ((2 * mt & 6) * 16)) + (2 * mt & ~7) * 16 + u * 16 * S::kRowBytes, a);
+                for (int i = 0; i < kMt; ++i)
 #pragma unroll
-                    for (int i = 0; i < S::PIECES; ++i)
+                    for (int u = 0; u < SUB; ++u)
+                        ldsm4t((va ^ ((2 * (m0 + i) & 6) * 16)) + (2 * (m0 + i) & ~7) * 16 + u * 16 * S::kRowBytes, a[i][u]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16816(o[mt * NT + n], a, pb[u][n][i][0], pb[u][n][i][1]);
-                }
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int q = 0; q < S::PIECES; ++q)
+#pragma unroll
+                        for (int i = 0; i < kMt; ++i)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma16816(o[(m0 + i) * NT + n], a[i][u], pb[u][n][q][0], pb[u][n][q][1]);
+            }
         } else {
             // fp32 products and sums on the CUDA cores: 4 keys x 8 rows at a time, the channels over the lanes
             const float* ks = reinterpret_cast<const float*>(smem + (kg * kStages + slot) * S::kStageBytes) + lane * kV;
@@ -865,8 +873,7 @@ template <class S>
 cudaError_t launch(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
     const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    attn_decode_kernel<S><<<sms, S::kAll, S::kSmem, stream>>>(p, out_bf16 ? 1 : 0);
-    return cudaGetLastError();
+    return launch_dependent(attn_decode_kernel<S>, dim3(sms), dim3(S::kAll), S::kSmem, stream, p, out_bf16 ? 1 : 0);
 }
 
 // CTAs of a launch: one per SM (0 if the device cannot be asked).

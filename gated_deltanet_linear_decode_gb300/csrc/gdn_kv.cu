@@ -6,6 +6,7 @@
 #include "gdn.h"
 #include "gdn_attn_internal.h"
 #include "gdn_common.cuh"
+#include "gdn_launch.h"
 #include "gdn_vec.cuh"
 
 namespace gdn {
@@ -103,6 +104,8 @@ __global__ void __launch_bounds__(kMaxThreads) kv_extend_kernel(const KvExtendPa
     int* const row_s = smem;               // [B + 1] first row of each sequence
     int* const page_s = smem + p.B + 1;    // [B + 1] pages served before it
     __shared__ Pair sums[33];
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int per = (p.B + blockDim.x - 1) / blockDim.x;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
     const int free_n = min(max(*p.free_count, 0), p.num_pages);
@@ -206,6 +209,8 @@ __global__ void __launch_bounds__(kMaxThreads) kv_truncate_kernel(const KvTrunca
     extern __shared__ int smem[];
     int* const page_s = smem;   // [B + 1] pages given back before each sequence
     __shared__ Pair sums[33];
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int per = (p.B + blockDim.x - 1) / blockDim.x;
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
     const int free_n = min(max(*p.free_count, 0), p.num_pages), room = p.num_pages - free_n;
@@ -282,19 +287,7 @@ cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, int threads,
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return launch_dependent_cluster(kernel, ctas, dim3(ctas), dim3(threads), smem, stream, p);
 }
 
 // The append.  Elementwise over (2 H_q + 4 H_kv) head_dim elements a token, read and written once: bound by the
@@ -310,6 +303,8 @@ constexpr int kPass = 4;
 template <typename Ta, int D>
 __global__ void __launch_bounds__(256, sizeof(Ta) == 2 ? 4 : 3) kv_append_kernel(const KvAppendParams p, const int q_jobs, const int kv_jobs) {
     constexpr int kLanes = D / 8, kSet = 32 / kLanes;   // lanes of a head, heads of a set
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int lane = threadIdx.x & 31, i = lane % kLanes, sub = lane / kLanes;
     const int jobs = q_jobs + 2 * kv_jobs;
     const unsigned id = blockIdx.x * 8u + (threadIdx.x >> 5);
@@ -414,8 +409,7 @@ cudaError_t append(const KvAppendParams& p, cudaStream_t stream) {
     const int q_jobs = (p.Hq + kHeads - 1) / kHeads, kv_jobs = (p.Hkv + kHeads - 1) / kHeads;
     const long long blocks = (static_cast<long long>(p.T) * (q_jobs + 2 * kv_jobs) + 7) / 8;
     if (blocks > 1 << 28) return cudaErrorInvalidConfiguration;   // a warp's number has 31 bits
-    kv_append_kernel<Ta, D><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(p, q_jobs, kv_jobs);
-    return cudaGetLastError();
+    return launch_dependent(kv_append_kernel<Ta, D>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p, q_jobs, kv_jobs);
 }
 
 }  // namespace

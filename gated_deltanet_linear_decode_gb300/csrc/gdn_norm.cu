@@ -6,6 +6,7 @@
 #include "gdn.h"
 #include "gdn_attn_internal.h"
 #include "gdn_common.cuh"
+#include "gdn_launch.h"
 #include "gdn_vec.cuh"
 
 namespace gdn {
@@ -28,8 +29,10 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
 
 // N chunks a thread.  lanes > 0: that many lanes (a power of two <= 32) share a row, several rows a CTA; lanes == 0: a CTA a row.
 template <typename Ta, typename Tr, int N>
-__global__ void __launch_bounds__(512) norm_residual_kernel(const NormParams p, const int lanes) {
+__global__ void __launch_bounds__(512) norm_residual_kernel(NormParams p, int lanes) {
     __shared__ float sums[16];
+    grid_dependency_wait();
+    grid_launch_dependents();
     const long long t = lanes ? static_cast<long long>(blockIdx.x) * (blockDim.x / lanes) + threadIdx.x / lanes : blockIdx.x;
     const int i0 = lanes ? threadIdx.x % lanes : threadIdx.x, step = blockDim.x;
     const int chunks = p.H / 8;
@@ -118,6 +121,8 @@ template <typename Ta, typename Tr>
 __global__ void __launch_bounds__(512) norm_residual_any_kernel(const NormParams p) {
     extern __shared__ float row[];
     __shared__ float sums[16];
+    grid_dependency_wait();
+    grid_launch_dependents();
     const long long t = blockIdx.x;
     const Ta* y = static_cast<const Ta*>(p.y) + t * p.ldy;
     const Ta* gate = static_cast<const Ta*>(p.gate) + t * p.ldg;
@@ -161,23 +166,21 @@ cudaError_t norm(const NormParams& p, cudaStream_t stream) {
             const cudaError_t e = cudaFuncSetAttribute(norm_residual_any_kernel<Ta, Tr>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
             if (e != cudaSuccess) return e;
         }
-        norm_residual_any_kernel<Ta, Tr><<<p.T, threads, smem, stream>>>(p);
-        return cudaGetLastError();
+        return launch_dependent(norm_residual_any_kernel<Ta, Tr>, dim3(p.T), dim3(threads), smem, stream, p);
     }
     const int chunks = p.H / 8;
     if (chunks <= 32) {
         int lanes = 1;
         while (lanes < chunks) lanes *= 2;
         const int rows = 128 / lanes;
-        norm_residual_kernel<Ta, Tr, 1><<<(p.T + rows - 1) / rows, 128, 0, stream>>>(p, lanes);
-    } else if (chunks <= 256) {
-        norm_residual_kernel<Ta, Tr, 1><<<p.T, (chunks + 31) / 32 * 32, 0, stream>>>(p, 0);
-    } else if (chunks <= 1024) {
-        norm_residual_kernel<Ta, Tr, 2><<<p.T, (chunks + 63) / 64 * 32, 0, stream>>>(p, 0);
-    } else {
-        norm_residual_kernel<Ta, Tr, 4><<<p.T, (chunks + 127) / 128 * 32, 0, stream>>>(p, 0);
+        return launch_dependent(norm_residual_kernel<Ta, Tr, 1>, dim3((p.T + rows - 1) / rows), dim3(128), 0, stream, p, lanes);
     }
-    return cudaGetLastError();
+    const auto a_row = [&](void (*kernel)(NormParams, int), int n) {   // a CTA a row, n chunks a thread
+        return launch_dependent(kernel, dim3(p.T), dim3((chunks + 32 * n - 1) / (32 * n) * 32), 0, stream, p, 0);
+    };
+    if (chunks <= 256) return a_row(norm_residual_kernel<Ta, Tr, 1>, 1);
+    if (chunks <= 1024) return a_row(norm_residual_kernel<Ta, Tr, 2>, 2);
+    return a_row(norm_residual_kernel<Ta, Tr, 4>, 4);
 }
 
 }  // namespace
