@@ -1,6 +1,6 @@
 // gdn_attn.cuh -- attention of the last K tokens of each sequence over the paged key-value cache
 // (include/gdn_attn.h, gdn_attn_decode): the kernel, instantiated per type in gdn_attn_bf16.cu and
-// gdn_attn_f32.cu.
+// gdn_attn_f32.cu; gdn_attn_tc.cu builds on it for many rows.
 //
 // Mathematics.  A kv head's G query heads times K tokens are R = G*K rows that share its keys.  Over any set of
 // keys a row has m = max s, l = sum e^(s-m), o = sum e^(s-m) v; two sets join as m = max(m1, m2),
@@ -91,18 +91,29 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int n) {
 __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 constexpr int kWaitLimit = 1 << 22;   // polls of a wait before it gives up
 
 // Wait for phase `parity` of `bar`; false when it gives up or another warp has.
 __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int limit = kWaitLimit) {
+    uint32_t done;   // the usual case by itself
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+    if (done) return true;
     for (int it = 0; it < limit; it += 16) {
         if (tc::mbar_wait(bar, parity, 16)) return true;
         if (*abort) return false;
     }
     *abort = 1;
     return false;
+}
+// The same by a whole warp, with one answer for all of it.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, stage_wait(bar, parity, abort));
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -203,6 +214,8 @@ __device__ __forceinline__ void put(const AttnParams& p, bool out_bf16, int b, i
     else StateIO<float>::st(static_cast<float*>(p.out) + at, y);
 }
 
+__device__ __forceinline__ float4 times(float4 y, float f) { return make_float4(y.x * f, y.y * f, y.z * f, y.w * f); }
+
 // The barrier of the computing warps.
 template <class S>
 __device__ __forceinline__ void sync_computing() {
@@ -288,11 +301,127 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, bool out_bf16, c
                 reinterpret_cast<float4*>(sp.o + static_cast<size_t>(to) * S::kRows * D)[i] = y[j];
             } else if (r < rows) {
                 const float ll = t_s[r].y, inv = ll == 0.f ? 0.f : 1.0f / ll;
-                put<Ta, D>(p, out_bf16, b, hk, row0 + r, i % (D / 4) * 4, make_float4(y[j].x * inv, y[j].y * inv, y[j].z * inv, y[j].w * inv));
+                put<Ta, D>(p, out_bf16, b, hk, row0 + r, i % (D / 4) * 4, times(y[j], inv));
             }
         }
     }
     sync_computing<S>();
+}
+
+template <class S>
+__device__ __forceinline__ Split split_of(const AttnParams& p) {
+    uint8_t* const w = static_cast<uint8_t*>(p.workspace);
+    return {reinterpret_cast<int*>(w), reinterpret_cast<float*>(w + kCounterBytes),
+            reinterpret_cast<float2*>(w + kCounterBytes + static_cast<size_t>(2) * gridDim.x * S::kRows * S::D * 4)};
+}
+
+// A CTA's share: numbers [first, last) of the `total` of all groups, which `ctas` CTAs divide.
+struct Share {
+    long long first, last, total;
+    int ctas;
+};
+struct PlanSmem {
+    long long sums[16], start;   // by warp
+    int start_b;
+};
+
+// This CTA's share and where it begins (c.at >= last where it holds no tile); false if it has none.  All threads call it.
+template <class S>
+__device__ __forceinline__ bool my_share(const AttnParams& p, int row_blocks, PlanSmem& sm, Cursor& c, Share& sh) {
+    grid_dependency_wait();   // launched as a programmatic dependent: nothing global is touched before the previous kernel is done
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per_seq = p.Hkv * row_blocks;   // groups of a sequence
+    const int per = (p.B + S::kAll - 1) / S::kAll;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+    bool over;
+    auto numbers_of = [&](int b) {   // of a sequence's groups
+        return static_cast<long long>(tiles_of<S::kTile>(seq_keys(p, b, &over)) + S::kGroupCost) * per_seq;
+    };
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += numbers_of(b);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sm.sums[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < S::kAll / 32; ++w) {
+        if (w < warp) before += sm.sums[w];
+        total += sm.sums[w];
+    }
+    before += incl - mine;
+    sh.total = total;
+    sh.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+    if (static_cast<int>(blockIdx.x) >= sh.ctas) return false;
+    sh.first = quot(total * blockIdx.x, sh.ctas);
+    sh.last = quot(total * (blockIdx.x + 1), sh.ctas);
+    if (sh.first >= before && sh.first < before + mine) {   // one thread: its sequences hold the first number
+        long long at = before;
+        int b = b0;
+        for (; b < b1; ++b) {
+            const long long n = numbers_of(b);
+            if (sh.first < at + n) break;
+            at += n;
+        }
+        sm.start_b = b;
+        sm.start = at;
+    }
+    __syncthreads();
+    grid_launch_dependents();
+    c.b = sm.start_b;
+    c.len = seq_keys(p, c.b, &over);
+    c.tiles = tiles_of<S::kTile>(c.len);
+    const int size = c.tiles + S::kGroupCost;
+    const long long in_seq = sh.first - sm.start;
+    const int group = static_cast<int>(quot(in_seq, size));
+    c.tile = static_cast<int>(in_seq - static_cast<long long>(group) * size);
+    c.hk = group / row_blocks;
+    c.rb = group - c.hk * row_blocks;
+    c.at = sh.first;
+    if (c.tile >= c.tiles) {   // among the numbers without a tile: the next group is the first
+        c.at += size - c.tile;
+        next_group<S>(p, c, row_blocks);
+    }
+    return true;
+}
+
+// After this CTA's part of a split group is written: join what is complete.  The CTAs c0.. of the group hold its n parts;
+// the first one's lies in either of that CTA's two places.  Up to kFanOne parts are joined by the CTA that arrives
+// last; of more, `fan` neighbours each are joined that way into the first one's place, and the results of those
+// again: few parts for one CTA to read, and no CTA waits.  What is joined with what, and in which order, does not
+// depend on who arrives last.
+template <class S>
+__device__ __forceinline__ void join_group(const AttnParams& p, bool out_bf16, const Split& sp, const Share& sh, const Cursor& cc,
+                                           long long g_first, long long g_last, int rows, float* join_s, int* flag_s) {
+    const int c0 = static_cast<int>(quot((g_first + 1) * sh.ctas - 1, sh.total)), c1 = static_cast<int>(quot(g_last * sh.ctas - 1, sh.total));
+    const int n = c1 - c0 + 1, fan = n <= kFanOne ? kFanOne : n <= 64 ? 8 : 12;
+    const int k0 = (static_cast<int>(blockIdx.x) - c0) / fan * fan;   // this CTA's neighbours are k0..
+    const int part0 = 2 * c0 + (quot(sh.total * c0, sh.ctas) >= g_first - S::kGroupCost ? 0 : 1);   // no tile of the group before in that CTA
+    auto place = [&](int k) { return k == 0 ? part0 : 2 * (c0 + k); };
+#pragma unroll 1
+    for (int level = 0; level < 2; ++level) {
+        const int from = level == 0 ? k0 : 0, stride = level == 0 ? 1 : fan;
+        const int count = level == 0 ? min(fan, n - k0) : (n + fan - 1) / fan;
+        const bool final = level == 1 || n <= fan;
+        if (level == 0 && count == 1) continue;   // already where level 1 reads it
+        sync_computing<S>();   // this CTA's part is written
+        if (threadIdx.x == 0) {
+            int* const counter = level == 0 ? sp.counters + place(k0) : sp.counters + 2 * kMaxCtas + c0;
+            // releases what the CTA wrote, acquires what the others did; counts to count - 1 and back to zero, ready
+            // for the next call
+            unsigned old;
+            asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(count - 1) : "memory");
+            *flag_s = old == static_cast<unsigned>(count - 1);
+        }
+        sync_computing<S>();
+        if (!*flag_s) return;
+        join_parts<S>(p, out_bf16, sp, rows, cc.b, cc.hk, cc.rb * S::kRows, join_s, count, final, place(k0),
+                      [&](int k) { return static_cast<size_t>(place(from + k * stride)) * S::kRows; });
+        if (final) return;
+    }
 }
 
 template <class S>
@@ -308,16 +437,13 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
     uint64_t* const empty_s = full_s + KG * kStages;
     uint64_t* const never_s = empty_s + KG * kStages;
     volatile uint32_t* const valid_s = reinterpret_cast<uint32_t*>(never_s + 1);   // [KG][kStages][PW]
-    __shared__ long long sums_s[S::kAll / 32];
-    __shared__ long long start_s;
-    __shared__ int flag_s, stop_s, start_b_s;
+    __shared__ PlanSmem plan_s;
+    __shared__ int flag_s, stop_s;
     __shared__ volatile int abort_s;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int R = p.G * p.K, row_blocks = (R + S::kRows - 1) / S::kRows;
-    const int per_seq = p.Hkv * row_blocks;   // groups of a sequence
 
-    // ---------------------------------------------------------------- this CTA's share of the tiles
     if (threadIdx.x < KG * kStages) {
         tc::mbar_init(full_s + threadIdx.x, PW * 33);   // each loading lane's copies, and one arrival a warp for the valid word
         tc::mbar_init(empty_s + threadIdx.x, RG);
@@ -326,62 +452,11 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
         tc::mbar_init(never_s, 1);
         abort_s = 0;
     }
-    grid_dependency_wait();   // launched as a programmatic dependent: nothing global is touched before the previous kernel is done
-    const int per = (p.B + S::kAll - 1) / S::kAll;
-    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-    bool over;
-    auto numbers_of = [&](int b) {   // of a sequence's groups
-        return static_cast<long long>(tiles_of<kTile>(seq_keys(p, b, &over)) + S::kGroupCost) * per_seq;
-    };
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += numbers_of(b);
-    long long incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) sums_s[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < S::kAll / 32; ++w) {
-        if (w < warp) before += sums_s[w];
-        total += sums_s[w];
-    }
-    before += incl - mine;
-    const int ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-    if (static_cast<int>(blockIdx.x) >= ctas) return;   // (an exit lets the next kernel start, too)
-    const long long first = quot(total * blockIdx.x, ctas), last = quot(total * (blockIdx.x + 1), ctas);   // numbers [first, last)
-    if (first >= before && first < before + mine) {   // one thread: its sequences hold the first number
-        long long at = before;
-        int b = b0;
-        for (; b < b1; ++b) {
-            const long long n = numbers_of(b);
-            if (first < at + n) break;
-            at += n;
-        }
-        start_b_s = b;
-        start_s = at;
-    }
-    __syncthreads();
-    grid_launch_dependents();
     Cursor cc;
-    cc.b = start_b_s;
-    cc.len = seq_keys(p, cc.b, &over);
-    cc.tiles = tiles_of<kTile>(cc.len);
-    {
-        const int size = cc.tiles + S::kGroupCost;
-        const long long in_seq = first - start_s;
-        const int group = static_cast<int>(quot(in_seq, size));
-        cc.tile = static_cast<int>(in_seq - static_cast<long long>(group) * size);
-        cc.hk = group / row_blocks;
-        cc.rb = group - cc.hk * row_blocks;
-        cc.at = first;
-        if (cc.tile >= cc.tiles) {   // among the numbers without a tile: the next group is the first
-            cc.at += size - cc.tile;
-            next_group<S>(p, cc, row_blocks);
-        }
-    }
+    Share sh;
+    if (!my_share<S>(p, row_blocks, plan_s, cc, sh)) return;   // (an exit lets the next kernel start, too)
+    const long long last = sh.last;
+    bool over;
 
     // ---------------------------------------------------------------- the loading warps
     if (warp >= RG * KG) {
@@ -391,36 +466,36 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
         const uint32_t ring = smem_u32(smem) + kg * kStages * S::kStageBytes;
         const int ps = p.cache.page_size;
         // pages are looked up two tiles ahead of their keys' loads: turn t looks up tile t and loads tile t - 2
-        int page[2] = {-1, -1}, in_page[2] = {0, 0}, head[2] = {0, 0};
+        int page[2] = {0, 0}, in_page[2] = {0, 0}, head[2] = {0, 0}, seq[2] = {-1, -1};   // seq -1: no key
         int tiles = 0, slot = 0;   // tiles: looked up so far
         uint32_t round = 0;
 #pragma unroll 1
         for (int t = 0;; ++t) {
-            const int pg = page[0];
+            const int pg = page[0], pg_seq = seq[0];
             const long long off = pg * p.cache.page_stride + in_page[0] * p.cache.token_stride + head[0] * p.cache.head_stride;
             page[0] = page[1];
             in_page[0] = in_page[1];
             head[0] = head[1];
-            page[1] = -1;
+            seq[0] = seq[1];
+            seq[1] = -1;
             if (cc.at < last) {
                 const int j = cc.tile * kTile + kg * KT + pw * kKeys + lane;
                 if (lane < kKeys && j < cc.len) {
                     const int k = j / ps;
                     in_page[1] = j - k * ps;
                     head[1] = cc.hk;
-                    page[1] = p.block_table[static_cast<size_t>(cc.b) * p.max_pages + k];
-                    if (page[1] < 0 || page[1] >= p.cache.num_pages) {
-                        page[1] = -1;
-                        if (p.status) atomicOr(p.status + cc.b, kKvBadIndex);
-                    }
+                    seq[1] = cc.b;
+                    page[1] = p.block_table[static_cast<size_t>(cc.b) * p.max_pages + k];   // looked at when it is used
                 }
                 advance<S>(p, cc, row_blocks);
                 ++tiles;
             }
             if (t < 2) continue;
             if (t - 2 >= tiles) break;
-            if (round > 0 && !stage_wait(empty_s + kg * kStages + slot, (round - 1) & 1, &abort_s)) break;
-            const uint32_t ok = __ballot_sync(0xffffffffu, pg >= 0);
+            if (round > 0 && !warp_wait(empty_s + kg * kStages + slot, (round - 1) & 1, &abort_s)) break;
+            const bool in_cache = pg >= 0 && pg < p.cache.num_pages;
+            const uint32_t ok = __ballot_sync(0xffffffffu, pg_seq >= 0 && in_cache);
+            if (pg_seq >= 0 && !in_cache && p.status) atomicOr(p.status + pg_seq, kKvBadIndex);
             if (lane == 0) valid_s[(kg * kStages + slot) * PW + pw] = ok;
             constexpr int kChunks = S::kRowBytes / 16;   // of a row
             const uint32_t st = ring + slot * S::kStageBytes;
@@ -708,9 +783,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
     };
 
     // ---------------------------------------------------------------- the end of a group, or of this CTA's part of it
-    const Split sp = {static_cast<int*>(p.workspace), reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) + kCounterBytes),
-                      reinterpret_cast<float2*>(static_cast<uint8_t*>(p.workspace) + kCounterBytes +
-                                                static_cast<size_t>(2) * gridDim.x * S::kRows * D * 4)};
+    const Split sp = split_of<S>(p);
     long long seg_first = cc.at;   // this CTA's first tile of the group
     bool first_seg = true;         // of this CTA
     auto end_segment = [&]() {     // the tiles from seg_first up to and with cc's are done
@@ -767,7 +840,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 if (threadIdx.x == 0 && p.status) atomicOr(p.status + cc.b, 16);
                 return;
             }
-#pragma unroll 1
+#pragma unroll 1   // code that runs once costs its fetch
             for (int i = threadIdx.x; i < 8 * S::JC / 4; i += S::kThreads) {
                 const int r = i / (S::JC / 4), ch = i % (S::JC / 4) * 4, row = r0 + r;
                 if (row >= rows) break;
@@ -788,9 +861,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                     y.w = fmaf(f, x.w, y.w);
                 }
                 if (whole) {
-                    const float inv = ll == 0.f ? 0.f : 1.0f / ll;
-                    put<Ta, D>(p, out_bf16, cc.b, cc.hk, cc.rb * S::kRows + row, ch0 + ch,
-                               make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+                    put<Ta, D>(p, out_bf16, cc.b, cc.hk, cc.rb * S::kRows + row, ch0 + ch, times(y, ll == 0.f ? 0.f : 1.0f / ll));
                 } else {
                     *reinterpret_cast<float4*>(sp.o + (static_cast<size_t>(part) * S::kRows + row) * D + ch0 + ch) = y;
                     if (ch0 + ch == 0) sp.ml[static_cast<size_t>(part) * S::kRows + row] = make_float2(mm, ll);
@@ -799,37 +870,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             sync_computing<S>();
         }
         if (whole) return;
-        // The CTAs c0.. of this group hold its n parts; the first one's lies in either of that CTA's two places.  Up to
-        // kFanOne parts are joined by the CTA that arrives last; of more, `fan` neighbours each are joined that way into
-        // the first one's place, and the results of those again: few parts for one CTA to read, and no CTA waits.
-        // What is joined with what, and in which order, does not depend on who arrives last.
-        const int c0 = static_cast<int>(quot((g_first + 1) * ctas - 1, total)), c1 = static_cast<int>(quot(g_last * ctas - 1, total));
-        const int n = c1 - c0 + 1, fan = n <= kFanOne ? kFanOne : n <= 64 ? 8 : 12;
-        const int k0 = (static_cast<int>(blockIdx.x) - c0) / fan * fan;   // this CTA's neighbours are k0..
-        const int part0 = 2 * c0 + (quot(total * c0, ctas) >= g_first - S::kGroupCost ? 0 : 1);   // no tile of the group before in that CTA
-        auto place = [&](int k) { return k == 0 ? part0 : 2 * (c0 + k); };
-#pragma unroll 1
-        for (int level = 0; level < 2; ++level) {
-            const int from = level == 0 ? k0 : 0, stride = level == 0 ? 1 : fan;
-            const int count = level == 0 ? min(fan, n - k0) : (n + fan - 1) / fan;
-            const bool final = level == 1 || n <= fan;
-            if (level == 0 && count == 1) continue;   // already where level 1 reads it
-            sync_computing<S>();   // this CTA's part is written
-            if (threadIdx.x == 0) {
-                int* const counter = level == 0 ? sp.counters + place(k0) : sp.counters + 2 * kMaxCtas + c0;
-                // releases what the CTA wrote, acquires what the others did; counts to count - 1 and back to zero, ready
-                // for the next call
-                unsigned old;
-                asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(count - 1) : "memory");
-                flag_s = old == static_cast<unsigned>(count - 1);
-            }
-            sync_computing<S>();
-            if (!flag_s) return;
-            const int to = place(k0);
-            join_parts<S>(p, out_bf16, sp, rows, cc.b, cc.hk, cc.rb * S::kRows, join_s, count, final, to,
-                          [&](int k) { return static_cast<size_t>(place(from + k * stride)) * S::kRows; });
-            if (final) return;
-        }
+        join_group<S>(p, out_bf16, sp, sh, cc, g_first, g_last, rows, join_s, &flag_s);
     };
 
     // ---------------------------------------------------------------- the walk (one copy of each part: the code is fetched
@@ -847,7 +888,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             }
             fresh = false;
         }
-        if (stage_wait(full_s + kg * kStages + slot, phase, &abort_s)) compute();
+        if (warp_wait(full_s + kg * kStages + slot, phase, &abort_s)) compute();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(empty_s + kg * kStages + slot);
         if (++slot == kStages) {
@@ -884,6 +925,7 @@ inline int grid_ctas() {
 }
 
 cudaError_t launch_bf16(const AttnParams& p, int head_dim, bool out_bf16, int sms, cudaStream_t stream);
+cudaError_t launch_tc(const AttnParams& p, int head_dim, bool out_bf16, int sms, cudaStream_t stream);
 cudaError_t launch_f32(const AttnParams& p, int head_dim, bool out_bf16, int sms, cudaStream_t stream);
 
 // Rows of a block for R rows a kv head.
