@@ -38,6 +38,7 @@
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
 #include "gdn_tc.cuh"
+#include "gdn_vec.cuh"
 
 namespace gdn {
 namespace attn {
@@ -129,12 +130,6 @@ __device__ __forceinline__ uint32_t movm(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-// 2^x, a relative error of 2^-22; results under 2^-126 are 0
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // c[16x8] += a[16x16] . b[16x8], bf16 operands
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -189,13 +184,6 @@ struct Split {
 
 // row / G for rows under 4096 and G <= 16 (g_inv = 65536 / G rounded up).
 __device__ __forceinline__ int token_of(const AttnParams& p, int row) { return static_cast<int>((static_cast<unsigned>(row) * p.g_inv) >> 16); }
-
-// sigmoid(x) with the approximate 2^x and 1/x: a relative error of 2^-21, |x| 2^-23 more
-__device__ __forceinline__ float gate_of(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2(-x * kLog2e)));
-    return y;
-}
 
 // The result of a row's channels c..c+3, gated, into out.
 template <typename Ta, int D>

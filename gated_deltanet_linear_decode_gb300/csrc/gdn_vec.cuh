@@ -8,6 +8,20 @@
 
 namespace gdn {
 
+// 2^x, a relative error of 2^-22; results under 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// sigmoid(x) with the approximate 2^x and 1/x, a fifth of the instructions: a relative error of 2^-21, and |x| 2^-24 more
+// from the exponent's rounding.
+__device__ __forceinline__ float gate_of(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.0f + ex2(-x * 1.4426950408889634f)));
+    return y;
+}
+
 // Two fp32 operations in one instruction (each rounds as the single one does).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
