@@ -27,9 +27,11 @@ __device__ __forceinline__ float block_sum(float v, float* s) {
     return t;
 }
 
+constexpr int kAhead = 304;   // rows: two for each of the 152 SMs
+
 // N chunks a thread.  lanes > 0: that many lanes (a power of two <= 32) share a row, several rows a CTA; lanes == 0: a CTA a row.
 template <typename Ta, typename Tr, int N>
-__global__ void __launch_bounds__(512) norm_residual_kernel(NormParams p, int lanes) {
+__global__ void __launch_bounds__(512, N <= 2 ? 2 : 1) norm_residual_kernel(NormParams p, int lanes) {
     __shared__ float sums[16];
     grid_dependency_wait();
     grid_launch_dependents();
@@ -52,6 +54,19 @@ __global__ void __launch_bounds__(512) norm_residual_kernel(NormParams p, int la
             h[c].load(static_cast<const Tr*>(p.h) + t * p.H + i * 8);
             if (p.y) y[c].load(static_cast<const Ta*>(p.y) + t * p.ldy + i * 8);
             if (p.gate_cols > 1) g[c].load(static_cast<const Ta*>(p.gate) + t * p.ldg + i * 8);
+        }
+    }
+    // A row waits for its sums twice, and the rows that fit an SM meanwhile do not keep the memory busy: the row that a later
+    // CTA will take is brought into L2 (8192 x 5120: 106.6 -> 95.7 us; 456 rows ahead 96.5, 1000 rows 106).
+    if (!lanes && t + kAhead < p.T) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            const int i = i0 + c * step;
+            if (i < chunks && i % (16 / static_cast<int>(sizeof(Tr))) == 0) prefetch_l2(static_cast<const Tr*>(p.h) + (t + kAhead) * p.H + i * 8);
+            if (i < chunks && i % (16 / static_cast<int>(sizeof(Ta))) == 0) {
+                if (p.y) prefetch_l2(static_cast<const Ta*>(p.y) + (t + kAhead) * p.ldy + i * 8);
+                if (p.gate_cols > 1) prefetch_l2(static_cast<const Ta*>(p.gate) + (t + kAhead) * p.ldg + i * 8);
+            }
         }
     }
     if (live && p.gate_cols == 1) g1 = gate_of(ld_act(static_cast<const Ta*>(p.gate) + t * p.ldg));

@@ -22,6 +22,9 @@ __device__ __forceinline__ float gate_of(float x) {
     return y;
 }
 
+// Hint: bring the 128-byte line of p into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Two fp32 operations in one instruction (each rounds as the single one does).
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     float2 d;
