@@ -706,64 +706,80 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                             for (int n = 0; n < NT; ++n) mma16816(o[(m0 + i) * NT + n], a[i][u], pb[u][n][q][0], pb[u][n][q][1]);
             }
         } else {
-            // fp32 products and sums on the CUDA cores: 4 keys x 8 rows at a time, the channels over the lanes
+            // fp32 products and sums on the CUDA cores: 4 keys x 8 rows at a time, the channels over the lanes; two such sets
+            // side by side where the registers allow, since a warp has its scheduler to itself
+            constexpr int U = D <= 128 ? 2 : 1;
             const float* ks = reinterpret_cast<const float*>(smem + (kg * kStages + slot) * S::kStageBytes) + lane * kV;
             const float* vs = ks + S::kHalfBytes / 4;
+            const int r = lane & 7;
 #pragma unroll 1
-            for (int k0 = 0; k0 < KT; k0 += 4) {
-                float part[32];
+            for (int k0 = 0; k0 < KT; k0 += 4 * U) {
+                float s[U], mx = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float kv[kC];
+                for (int u = 0; u < U; ++u) {
+                    float part[32];
 #pragma unroll
-                    for (int c = 0; c < kC; c += kV)
+                    for (int k = 0; k < 4; ++k) {
+                        float kv[kC];
 #pragma unroll
-                        for (int i = 0; i < kV; ++i) kv[c + i] = ks[(k0 + k) * D + c / kV * 32 * kV + i];
+                        for (int c = 0; c < kC; c += kV)
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        float x = 0.f;
+                            for (int i = 0; i < kV; ++i) kv[c + i] = ks[(k0 + 4 * u + k) * D + c / kV * 32 * kV + i];
 #pragma unroll
-                        for (int c = 0; c < kC; ++c) x = fmaf(kv[c], qf[r][c], x);
-                        part[k * 8 + r] = x;
+                        for (int rr = 0; rr < 8; ++rr) {
+                            float x = 0.f;
+#pragma unroll
+                            for (int c = 0; c < kC; ++c) x = fmaf(kv[c], qf[rr][c], x);
+                            part[k * 8 + rr] = x;
+                        }
                     }
+                    s[u] = reduce32_transposed(part);   // key k0 + 4u + lane/8, row lane%8
                 }
-                float s = reduce32_transposed(part);   // key k0 + lane/8, row lane%8
-                const int r = lane & 7, kk = k0 + (lane >> 3);
-                if (masked && (!((ok >> kk) & 1) || j0 + kk >= limit(r))) s = -INFINITY;
-                float mx = fmaxf(s, __shfl_xor_sync(0xffffffffu, s, 8));
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int kk = k0 + 4 * u + (lane >> 3);
+                    if (masked && (!((ok >> kk) & 1) || j0 + kk >= limit(r))) s[u] = -INFINITY;
+                    mx = fmaxf(mx, s[u]);
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                 float mine_m = m[0];
 #pragma unroll
                 for (int i = 1; i < 8; ++i) mine_m = r == i ? m[i] : mine_m;
                 const float m2 = fmaxf(mine_m, mx), base = m2 == -INFINITY ? 0.f : m2;
-                const float w = ex2(s - base), f = ex2(mine_m - base);
-                float lsum = w + __shfl_xor_sync(0xffffffffu, w, 8);
-                lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
-                const bool up = __any_sync(0xffffffffu, m2 > mine_m);
+                float w[U], lsum = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    m[i] = __shfl_sync(0xffffffffu, m2, i);
-                    const float ls = __shfl_sync(0xffffffffu, lsum, i);
-                    if (up) {
+                for (int u = 0; u < U; ++u) {
+                    w[u] = ex2(s[u] - base);
+                    lsum += w[u];
+                }
+                lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
+                lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
+                if (__any_sync(0xffffffffu, m2 > mine_m)) {
+                    const float f = ex2(mine_m - base);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        m[i] = __shfl_sync(0xffffffffu, m2, i);
                         const float fi = __shfl_sync(0xffffffffu, f, i);
                         l[i] *= fi;
 #pragma unroll
                         for (int c = 0; c < kC; ++c) o[i][c] *= fi;
                     }
-                    l[i] += ls;
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int i = 0; i < 8; ++i) l[i] += __shfl_sync(0xffffffffu, lsum, i);
+#pragma unroll
+                for (int k = 0; k < 4 * U; ++k) {
                     float kv[kC];
 #pragma unroll
                     for (int c = 0; c < kC; c += kV)
 #pragma unroll
                         for (int i = 0; i < kV; ++i) kv[c + i] = vs[(k0 + k) * D + c / kV * 32 * kV + i];
 #pragma unroll
-                    for (int r2 = 0; r2 < 8; ++r2) {
-                        const float wr = __shfl_sync(0xffffffffu, w, k * 8 + r2);
+                    for (int rr = 0; rr < 8; ++rr) {
+                        const float wr = __shfl_sync(0xffffffffu, w[k / 4], k % 4 * 8 + rr);
 #pragma unroll
-                        for (int c = 0; c < kC; ++c) o[r2][c] = fmaf(wr, kv[c], o[r2][c]);
+                        for (int c = 0; c < kC; ++c) o[rr][c] = fmaf(wr, kv[c], o[rr][c]);
                     }
                 }
             }
