@@ -727,10 +727,11 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                             for (int i = 0; i < kV; ++i) kv[c + i] = ks[(k0 + 4 * u + k) * D + c / kV * 32 * kV + i];
 #pragma unroll
                         for (int rr = 0; rr < 8; ++rr) {
-                            float x = 0.f;
+                            float2 x = mul2(make_float2(kv[0], kv[1]), make_float2(qf[rr][0], qf[rr][1]));
 #pragma unroll
-                            for (int c = 0; c < kC; ++c) x = fmaf(kv[c], qf[rr][c], x);
-                            part[k * 8 + rr] = x;
+                            for (int c = 2; c < kC; c += 2)
+                                x = fma2(make_float2(kv[c], kv[c + 1]), make_float2(qf[rr][c], qf[rr][c + 1]), x);
+                            part[k * 8 + rr] = x.x + x.y;   // (two sums a row, of even and odd channels)
                         }
                     }
                     s[u] = reduce32_transposed(part);   // key k0 + 4u + lane/8, row lane%8
@@ -779,7 +780,11 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                     for (int rr = 0; rr < 8; ++rr) {
                         const float wr = __shfl_sync(0xffffffffu, w[k / 4], k % 4 * 8 + rr);
 #pragma unroll
-                        for (int c = 0; c < kC; ++c) o[rr][c] = fmaf(wr, kv[c], o[rr][c]);
+                        for (int c = 0; c < kC; c += 2) {
+                            const float2 x = fma2(make_float2(wr, wr), make_float2(kv[c], kv[c + 1]), make_float2(o[rr][c], o[rr][c + 1]));
+                            o[rr][c] = x.x;
+                            o[rr][c + 1] = x.y;
+                        }
                     }
                 }
             }
