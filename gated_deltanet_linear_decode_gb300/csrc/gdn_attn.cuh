@@ -687,15 +687,28 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 }
             // o transposed: channels x rows += V^T . P^T
             const uint32_t va = st + S::kHalfBytes + ((lane & 7) + (lane >> 4) * 8) * S::kRowBytes + (((lane >> 3) & 1) ^ (lane & 7)) * 16;
-            constexpr int kMt = SUB == 1 ? 4 : 2;   // as kKs above
+            // The tensor cores' sums drop what is below the last bit, always downwards in magnitude: over a long sequence that
+            // adds up (16,000 keys: 1.3e-5 of the result).  Where the result is fp32 a stage is summed by itself and
+            // then added with a rounding that goes both ways.
+            constexpr bool kApart = S::PIECES == 3;
+            constexpr int kMt = SUB == 1 && !kApart ? 4 : 2;   // as kKs above
 #pragma unroll
             for (int m0 = 0; m0 < D / 16; m0 += kMt) {
                 uint32_t a[kMt][SUB][4];
+                float sum[kMt][NT][4];
 #pragma unroll
                 for (int i = 0; i < kMt; ++i)
 #pragma unroll
                     for (int u = 0; u < SUB; ++u)
                         ldsm4t((va ^ ((2 * (m0 + i) & 6) * 16)) + (2 * (m0 + i) & ~7) * 16 + u * 16 * S::kRowBytes, a[i][u]);
+                if constexpr (kApart) {
+#pragma unroll
+                    for (int i = 0; i < kMt; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sum[i][n][e] = 0.f;
+                }
 #pragma unroll
                 for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -703,7 +716,16 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
 #pragma unroll
                         for (int i = 0; i < kMt; ++i)
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) mma16816(o[(m0 + i) * NT + n], a[i][u], pb[u][n][q][0], pb[u][n][q][1]);
+                            for (int n = 0; n < NT; ++n)
+                                mma16816(kApart ? sum[i][n] : o[(m0 + i) * NT + n], a[i][u], pb[u][n][q][0], pb[u][n][q][1]);
+                if constexpr (kApart) {
+#pragma unroll
+                    for (int i = 0; i < kMt; ++i)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[(m0 + i) * NT + n][e] += sum[i][n][e];
+                }
             }
         } else {
             // fp32 products and sums on the CUDA cores: 4 keys x 8 rows at a time, the channels over the lanes; two such sets
@@ -934,7 +956,7 @@ inline int grid_ctas() {
 }
 
 cudaError_t launch_bf16(const AttnParams& p, int head_dim, bool out_bf16, int sms, cudaStream_t stream);
-cudaError_t launch_tc(const AttnParams& p, int head_dim, bool out_bf16, int sms, cudaStream_t stream);
+cudaError_t launch_tc(const AttnParams& p, int head_dim, int sms, cudaStream_t stream);
 cudaError_t launch_f32(const AttnParams& p, int head_dim, bool out_bf16, int sms, cudaStream_t stream);
 
 // Rows of a block for R rows a kv head.

@@ -10,13 +10,18 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
+// Warps by rows: 4 key groups as long as the rows fit two warps of 16, then 2 and 1 (8 warps hold 224 registers each).
+// More than 32 rows only come here with an fp32 result.
 template <int D, int PIECES>
 cudaError_t by_rows(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
-    switch (block_rows(p.G * p.K, true)) {
-        case 8: return launch<Shape<bf16, D, 1, 1, 4, PIECES>>(p, out_bf16, sms, stream);
-        case 16: return launch<Shape<bf16, D, 2, 1, 4, PIECES>>(p, out_bf16, sms, stream);
-        default: return launch<Shape<bf16, D, 2, 2, 4, PIECES>>(p, out_bf16, sms, stream);
+    const int n = block_rows(p.G * p.K, true);
+    if (n == 8) return launch<Shape<bf16, D, 1, 1, 4, PIECES>>(p, out_bf16, sms, stream);
+    if (n == 16) return launch<Shape<bf16, D, 2, 1, 4, PIECES>>(p, out_bf16, sms, stream);
+    if constexpr (PIECES == 3) {
+        if (n == 64) return launch<Shape<bf16, D, 2, 4, 2, PIECES>>(p, out_bf16, sms, stream);
+        if (n == 128) return launch<Shape<bf16, D, 2, 8, 1, PIECES>>(p, out_bf16, sms, stream);
     }
+    return launch<Shape<bf16, D, 2, 2, 4, PIECES>>(p, out_bf16, sms, stream);
 }
 
 template <int D>

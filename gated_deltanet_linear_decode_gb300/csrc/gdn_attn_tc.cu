@@ -1,5 +1,5 @@
-// gdn_attn_tc.cu -- gdn_attn_decode over a bf16 cache for more than 32 rows a kv head (a speculative verify of wide
-// groups): the products on the 5th-generation tensor cores.  The division of the keys over the CTAs, the page look-ups
+// gdn_attn_tc.cu -- gdn_attn_decode over a bf16 cache, with a bf16 result, for more than 32 rows a kv head (a speculative
+// verify of wide groups): the products on the 5th-generation tensor cores.  The division of the keys over the CTAs, the page look-ups
 // and the join of split groups are those of gdn_attn.cuh.
 //
 // With R rows the products take 4 R d operations a key of 4 d bytes.  On mma.sync every 16 rows read the keys and
@@ -18,14 +18,15 @@
 // TFLOP/s).  What bounds it: 128 rows the softmax (a thread's 128 keys a tile, 8,300 cycles); 64 rows a group's end,
 // 24,000 cycles twice a CTA, most of it the fetch of code that runs twice.
 // Roles, one persistent CTA per SM:
-//   warps 0-3   a thread a lane: S from tensor memory, weights e^(s - base) as two or three bf16 parts back into its place;
+//   warps 0-3   a thread a lane: S from tensor memory, weights e^(s - base) as two bf16 parts back into its place;
 //   warps 4-11  load: cp.async into a ring of 16 KB units, 128 keys x 64 channels each in the 128-byte swizzle
 //               layout, in the order of their use, with zero fill for keys that are not there;
 //   warp 12     one thread issues S (both operands K-major in shared memory) two tiles ahead of O (P in tensor memory, V as
 //               it lies in the ring, MN-major); a commit hands each unit back.
 // The base of a lane is its running maximum, but it is raised (and its O and l scaled) only when a score passes it by
 // more than 8 in base 2: then all weights stay under 2^8, the sums in 32 bits are as exact as with the maximum
-// itself, and O is hardly ever read before the end.
+// itself, and O is hardly ever read before the end.  (The tensor cores' sums drop what is below the last bit: 4.5e-5 of the
+// result at 16,000 keys a CTA, a fortieth of a bf16 result's own rounding.)
 #include "gdn_attn.cuh"
 
 namespace gdn {
@@ -37,10 +38,10 @@ using bf16 = __nv_bfloat16;
 constexpr int kUnit = 16384;      // 128 keys x 64 channels
 constexpr float kSlack = 8.0f;    // how far a score may pass its row's base
 
-template <int D_, int NR_, int PIECES_>
+template <int D_, int NR_>
 struct TcShape {
     using Ta = bf16;
-    static constexpr int D = D_, NR = NR_, PIECES = PIECES_;
+    static constexpr int D = D_, NR = NR_;
     static constexpr int kRows = NR;          // rows of a block
     static constexpr int kThreads = 128;      // softmax
     static constexpr int kLoaders = 8;        // warps that load, 16 keys of a tile each
@@ -55,11 +56,9 @@ struct TcShape {
     static constexpr int kFit = (232448 - 3072 - kQBytes) / kUnit;
     static constexpr int kUnits = kFit > 12 ? 12 : kFit / 2 * 2;        // even: two units of values lie side by side
     static constexpr int kSmem = kUnits * kUnit + kQBytes + 3072;
-    // Tensor memory: kBufs times 128 columns where a tile's S and then the first two parts of its P lie, kBufs times 64 for
-    // a third part, and O.  At d = 256 a third part leaves room for one, so that the next tile's S has to wait for this one's O.
-    static constexpr int kBufs = D == 256 && PIECES == 3 ? 1 : 2;
-    static constexpr int kColP3 = 128 * kBufs, kColO = 512 - (D == 64 ? 64 : D);
-    static_assert(kUnits >= 6 && kSmem <= 232448 && kColP3 + (PIECES == 3 ? 64 * kBufs : 0) <= kColO, "shape");
+    // Tensor memory: twice 128 columns where a tile's S and then its P lie, and O.
+    static constexpr int kColO = 256;
+    static_assert(kUnits >= 6 && kSmem <= 232448 && kColO + D <= 512, "shape");
 };
 
 // What follows the operands in shared memory.
@@ -100,7 +99,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
 }
 
 template <class S>
-__global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p, const int out_bf16) {
+__global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p) {
     constexpr int D = S::D, NR = S::NR, kUnits = S::kUnits;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const q_s = smem + kUnits * kUnit;
@@ -122,7 +121,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
         tc::mbar_init(&sm.o_done, 1);
         tc::mbar_init(&sm.drained, 1);
         tc::mbar_init(&sm.never, 1);
-        sm.abort = 0;
+        sm.abort = (tc::smem_u32(smem) & 1023) != 0;   // the swizzle goes by address bits 7-9
     }
     Cursor cc;
     Share sh;
@@ -213,13 +212,13 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
             if (t < 3) continue;
             const int i = t - 3;
             if (i >= tiles) break;
-            // in the order of their use: S is kBufs tiles ahead of O
+            // in the order of their use: S is two tiles ahead of O
             if (begins & 1) {
                 load(p.cache.k, 0, i);
-                if (S::kBufs == 2 && !(ends & 1) && ok) load(p.cache.k, 1, i + 1);
+                if (!(ends & 1) && ok) load(p.cache.k, 1, i + 1);
             }
             if (ok) load(p.cache.v, 0, -1);
-            if (ok && !(ends & 1) && (S::kBufs == 1 || !(ends & 2))) load(p.cache.k, S::kBufs, i + S::kBufs);
+            if (ok && !(ends & 3)) load(p.cache.k, 2, i + 2);
         }
         cp_wait_all();   // nothing is in flight when the CTA ends
     } else if (warp == kIssuer) {
@@ -243,7 +242,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
                 return u;
             };
             auto issue_s = [&](int i) {   // of tile i, the next one
-                const uint32_t d = t_s + i % S::kBufs * 128;
+                const uint32_t d = t_s + (i & 1) * 128;
                 int u = landed();
                 if (!ok) return;
 #pragma unroll
@@ -254,9 +253,9 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
                     tc::mma_commit(sm.empty + u);
                     if (++u == kUnits) u = 0;
                 }
-                tc::mma_commit(&sm.s_full[i % S::kBufs]);
+                tc::mma_commit(&sm.s_full[(i & 1)]);
             };
-            // S is issued kBufs tiles ahead of O, within a group: it runs while the threads compute, and they do not wait for O.
+            // S is issued two tiles ahead of O, within a group: it runs while the threads compute, and they do not wait for O.
             bool first_of_group = true;
 #pragma unroll 1
             while (cc.at < last && ok) {
@@ -267,32 +266,32 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
                     ok = stage_wait(&sm.q_ready, q_phase, &sm.abort);
                     q_phase ^= 1;
                     issue_s(done);
-                    if (S::kBufs == 2 && more >= 1) issue_s(done + 1);
+                    if (more >= 1) issue_s(done + 1);
                 }
-                ok = ok && stage_wait(&sm.p_ready[done % S::kBufs], done / S::kBufs & 1, &sm.abort);
+                ok = ok && stage_wait(&sm.p_ready[(done & 1)], (done >> 1) & 1, &sm.abort);
                 if (!ok) break;
                 tc::fence_after_sync();
-                const uint32_t t_p = t_s + done % S::kBufs * 128, t_p3 = t_s + S::kColP3 + done % S::kBufs * 64;
+                const uint32_t t_p = t_s + (done & 1) * 128;
                 int u = landed();
                 if (!ok) break;
 #pragma unroll
                 for (int h = 0; h < D / S::NV; ++h) {
                     const uint32_t v_lo = ring_lo + u * (kUnit >> 4) + kDescLoN;
 #pragma unroll
-                    for (int q = 0; q < S::PIECES; ++q)
+                    for (int q = 0; q < 2; ++q)
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_ts(t_o + h * S::NV, q < 2 ? t_p + ks / 2 * 32 + q * 16 + ks % 2 * 8 : t_p3 + ks * 8, v_lo + ks * (2048 >> 4), id_o,
+                            mma_ts(t_o + h * S::NV, t_p + ks / 2 * 32 + q * 16 + ks % 2 * 8, v_lo + ks * (2048 >> 4), id_o,
                                    !first_of_group || (q | ks) != 0);
                     tc::mma_commit(sm.empty + u);
                     if (S::kPerV == 2) tc::mma_commit(sm.empty + u + 1);
                     if ((u += S::kPerV) == kUnits) u = 0;
                 }
                 tc::mma_commit(&sm.o_done);
-                if (more >= S::kBufs) {   // into the place that O's product has read P from
+                if (more >= 2) {   // into the place that O's product has read P from
                     ok = stage_wait(&sm.o_done, done & 1, &sm.abort);
                     tc::fence_after_sync();
-                    issue_s(done + S::kBufs);
+                    issue_s(done + 2);
                 }
                 ++done;
                 advance<S>(p, cc, row_blocks);
@@ -338,8 +337,8 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
                     if (over) atomicOr(p.status + cc.b, kKvBadIndex);
                 }
             }
-            if (warp_wait(&sm.s_full[count % S::kBufs], count / S::kBufs & 1, &sm.abort)) {
-                const uint32_t my_s = t_s + my_lanes + count % S::kBufs * 128, my_p3 = t_s + my_lanes + S::kColP3 + count % S::kBufs * 64;
+            if (warp_wait(&sm.s_full[(count & 1)], (count >> 1) & 1, &sm.abort)) {
+                const uint32_t my_s = t_s + my_lanes + (count & 1) * 128;
                 tc::fence_after_sync();
                 // this row sees the keys of the tile before `sees` that are there
                 const int sees = cc.len - p.K + token_of(p, row0 + r) + 1 - cc.tile * 128 - key0;
@@ -391,9 +390,8 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
                         }
                     }
                 }
-                // Weights: PIECES bf16 parts, each the rounding of what the ones before leave (two: 2^-17, below a bf16
-                // result's own rounding; three: all of an fp32 weight's bits), two keys a column; the first two parts of 32
-                // keys take the columns of their scores.
+                // Weights: two bf16 parts, the second the rounding of what the first leaves (2^-17 together, below a bf16
+                // result's own rounding), two keys a column: those of 32 keys take the columns of their scores.
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
                     float(&w)[32] = s[kHold ? i : 0];
@@ -404,18 +402,18 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
                         l += w[e];
                     }
 #pragma unroll
-                    for (int q = 0; q < S::PIECES; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         float x[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const uint32_t u = StateIO<bf16>::pack(w[2 * e], w[2 * e + 1]);
-                            if (q + 1 < S::PIECES) {
+                            if (q == 0) {
                                 w[2 * e] -= __uint_as_float(u << 16);
                                 w[2 * e + 1] -= __uint_as_float(u & 0xffff0000u);
                             }
                             x[e] = __uint_as_float(u);
                         }
-                        tc::tmem_st16(q < 2 ? my_s + key0 + i * 32 + q * 16 : my_p3 + key0 / 2 + i * 16, x);
+                        tc::tmem_st16(my_s + key0 + i * 32 + q * 16, x);
                     }
                 }
                 if (NR < 128) {   // zeros for the keys that are other lanes'
@@ -426,15 +424,14 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
                     for (int i = 0; i < 4; ++i)
                         if (i / kChunks != key0 / NR)
 #pragma unroll
-                            for (int q = 0; q < S::PIECES; ++q)
-                                tc::tmem_st16(q < 2 ? my_s + i * 32 + q * 16 : my_p3 + i * 16, z);
+                            for (int q = 0; q < 2; ++q) tc::tmem_st16(my_s + i * 32 + q * 16, z);
                 }
                 tc::tmem_wait_st();
                 // Before the last tile of a group goes off: the one before it has been added, so that the wait for the last
                 // one cannot take the wrong phase for its own.
                 if (!fresh && (cc.tile + 1 == cc.tiles || cc.at + 1 == last)) warp_wait(&sm.o_done, (count - 1) & 1, &sm.abort);
                 tc::fence_before_sync();
-                tc::mbar_arrive(&sm.p_ready[count % S::kBufs]);
+                tc::mbar_arrive(&sm.p_ready[(count & 1)]);
             }
             ++count;
             const bool group_done = cc.tile + 1 == cc.tiles;
@@ -483,12 +480,12 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
                                 const float4 v = *reinterpret_cast<const float4*>(buf + (x + row) * kPitch + ch);
                                 y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
                             }
-                            if (whole) put<bf16, D>(p, out_bf16, cc.b, cc.hk, row0 + row, h * CH + ch, times(y, sm.f[row]));
+                            if (whole) put<bf16, D>(p, true, cc.b, cc.hk, row0 + row, h * CH + ch, times(y, sm.f[row]));
                             else *reinterpret_cast<float4*>(sp.o + (static_cast<size_t>(part) * NR + row) * D + h * CH + ch) = y;
                         }
                         sync_computing<S>();
                     }
-                    if (!whole) join_group<S>(p, out_bf16, sp, sh, cc, g_first, g_last, rows, buf, &sm.flag);
+                    if (!whole) join_group<S>(p, true, sp, sh, cc, g_first, g_last, rows, buf, &sm.flag);
                 }
                 first_seg = false;
             }
@@ -507,30 +504,25 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p,
     if (warp == kIssuer) tc::tmem_dealloc(sm.tmem, 512);
 }
 
-template <int D, int NR, int PIECES>
-cudaError_t launch_shape(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
-    using S = TcShape<D, NR, PIECES>;
+template <int D, int NR>
+cudaError_t launch_shape(const AttnParams& p, int sms, cudaStream_t stream) {
+    using S = TcShape<D, NR>;
     const cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(attn_tc_kernel<S>, dim3(sms), dim3(S::kAll), S::kSmem, stream, p, out_bf16 ? 1 : 0);
-}
-
-template <int D, int PIECES>
-cudaError_t by_rows(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
-    return block_rows(p.G * p.K, true) == 64 ? launch_shape<D, 64, PIECES>(p, out_bf16, sms, stream) : launch_shape<D, 128, PIECES>(p, out_bf16, sms, stream);
+    return launch_dependent(attn_tc_kernel<S>, dim3(sms), dim3(S::kAll), S::kSmem, stream, p);
 }
 
 template <int D>
-cudaError_t by_out(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
-    return out_bf16 ? by_rows<D, 2>(p, true, sms, stream) : by_rows<D, 3>(p, false, sms, stream);
+cudaError_t by_rows(const AttnParams& p, int sms, cudaStream_t stream) {
+    return block_rows(p.G * p.K, true) == 64 ? launch_shape<D, 64>(p, sms, stream) : launch_shape<D, 128>(p, sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_tc(const AttnParams& p, int head_dim, bool out_bf16, int sms, cudaStream_t stream) {
-    if (head_dim == 64) return by_out<64>(p, out_bf16, sms, stream);
-    if (head_dim == 128) return by_out<128>(p, out_bf16, sms, stream);
-    return by_out<256>(p, out_bf16, sms, stream);
+cudaError_t launch_tc(const AttnParams& p, int head_dim, int sms, cudaStream_t stream) {
+    if (head_dim == 64) return by_rows<64>(p, sms, stream);
+    if (head_dim == 128) return by_rows<128>(p, sms, stream);
+    return by_rows<256>(p, sms, stream);
 }
 
 }  // namespace attn

@@ -248,3 +248,45 @@ def test_a_wait_that_gives_up_writes_nothing(dtype):
     assert st.tolist() == [16] * 5 and (out == 7.0).all()
     ws.zero_()
     c.close(c.run(F32, ws=ws))
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+@pytest.mark.parametrize("d,Hq,K", [(256, 8, 10), (64, 16, 16), (128, 12, 16)])
+def test_many_rows_give_up_and_repeat(d, Hq, K, out_dtype):
+    """The same for more than 32 rows a kv head, and such calls give the same bits each time, also split over many CTAs."""
+    c = Case([300, 0, 40, 9000, 17], K, Hq, 2, d, 16, BF, seed=17)
+    st = torch.zeros(5, dtype=torch.int32, device="cuda")
+    dims = gdn.make_attn_dims(Hq, 2, d, BF, out_dtype, test_stall=True)
+    n = gdn.gdn_attn_decode_workspace_bytes(dims, 5, K)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    out = torch.full((5 * K, Hq * d), 7.0, dtype=out_dtype, device="cuda")
+    gdn.gdn_attn_decode(dims, gdn.KvCache(c.k, c.v), K, c.q, c.table.cuda(), c.seq_len, out, gate=c.gate, workspace=ws,
+                        dev_status=st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [16] * 5 and (out == 7.0).all()
+    ws.zero_()
+    first = c.run(out_dtype, ws=ws)
+    c.close(first)
+    for _ in range(5):
+        assert torch.equal(c.run(out_dtype, ws=ws), first)
+
+
+@pytest.mark.parametrize("dtype,Hq,K", [(BF, 8, 1), (BF, 8, 2), (BF, 8, 3), (BF, 8, 8), (F32, 8, 1)])
+def test_long_sums_keep_their_bits(dtype, Hq, K):
+    """Sequences that one SM walks by itself (more of them than SMs, all on the same pages): values of one sign, so that
+    a sum that always rounds one way would drift by 2^-25 a step; the fp32 contract holds all the same."""
+    n, ps, d, B = 16000, 16, 64, 160
+    c = Case([n], K, Hq, 1, d, ps, dtype, seed=18, gate=False)
+    c.v.abs_()
+    g = torch.Generator().manual_seed(19)
+    q = torch.randn(B * K, Hq * d, generator=g).to(dtype).cuda()
+    dims = gdn.make_attn_dims(Hq, 1, d, dtype, F32)
+    ws = torch.zeros(gdn.gdn_attn_decode_workspace_bytes(dims, B, K), dtype=torch.uint8, device="cuda")
+    out = torch.empty(B * K, Hq * d, device="cuda")
+    gdn.gdn_attn_decode(dims, gdn.KvCache(c.k, c.v), K, q, c.table.repeat(B, 1).cuda(), torch.full((B,), n, dtype=torch.int32, device="cuda"),
+                        out, workspace=ws)
+    k, v = R.f64(c.k), R.f64(c.v)
+    for b in (0, 77, B - 1):
+        rows = slice(b * K, b * K + K)
+        ref = R.attn(R.f64(q[rows]), k, v, c.table.numpy(), [n], K, Hq, 1, d)
+        assert np.abs(R.f64(out[rows]) - ref).max() <= 1e-5 * np.nanmax(np.abs(v))
