@@ -68,7 +68,9 @@ struct Shape {
     static constexpr int kRing = kQBytes > 32768 ? 131072 : kQBytes > 16384 || kRows == 128 ? 163840 : 196608;
     static constexpr int kStages = kRing / kStageBytes / KG;           // of one key group
     static constexpr int kTile = KG * KT;                              // keys of a tile
-    static constexpr int kGroupCost = 3;                               // a group's begin and end, in tiles
+    // A group's begin and end, in tiles (64 KB each).  64 ragged sequences, heads of 256, 24 rows: 3 tiles 118 us, 5 tiles 108,
+    // 8 tiles 106; heads of 128, 24 rows: 3 tiles 121, 8 tiles 132; fp32, heads of 64: 2 tiles 112, 8 tiles 136.
+    static constexpr int kGroupCost = !kBf16 || D == 64 ? 3 : D == 128 ? 4 : RG > 1 ? 8 : 6;
     static constexpr int JC = D < 128 ? D : 128;                       // channels of a join pass
     static constexpr int kJPitch = JC + 4;                             // 8t+g banks for the writes below
     static constexpr int kPartBytes = (kMaxFan * 4 + 8) * kRows;       // weights and totals of a join of parts
@@ -77,8 +79,11 @@ struct Shape {
     static constexpr int kBarBytes = (2 * KG * kStages + 1) * 8;       // full and empty of each stage, and one that nothing arrives on
     static constexpr int kValidBytes = KG * kStages * PW * 4;
     static constexpr int kSmem = KG * kStages * kStageBytes + kQBytes + kJoinBytes + kMlBytes + kBarBytes + kValidBytes;
-    // With 12 warps the computing ones take over registers of the loading ones: 168 a thread at launch = 2/3 of 224 + 1/3 of 56.
+    // With more than 8 warps the computing ones take over registers of the loading ones: 168 a thread at launch for 12
+    // warps are 2/3 of 224 and 1/3 of 56, 128 for 16 are 3/4 of 152 and 1/4 of 56.
     static constexpr bool kMoveRegs = kAll > 256;
+    static constexpr int kRegs = kAll == 384 ? 224 : 152;
+    static_assert(!kMoveRegs || kAll == 384 || kAll == 512, "registers");
     static_assert(kStages >= 3 && KT % PW == 0 && KT / PW <= 32 && kSmem + 512 <= 232448, "shape");
 };
 
@@ -510,7 +515,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
     }
 
     // ---------------------------------------------------------------- the computing warps
-    if constexpr (S::kMoveRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    if constexpr (S::kMoveRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::kRegs));
     const int kg = warp / RG, rg = warp % RG;
     const uint32_t ring = smem_u32(smem) + kg * kStages * S::kStageBytes;
 

@@ -1,6 +1,12 @@
 // gdn_attn_bf16.cu -- gdn_attn_decode over a bf16 cache: mma.sync with the keys (and the channels of the values)
-// on the 16-row side and 8 or 16 query rows a warp on the other, so that the few rows of a decode step
-// fill the instruction; see gdn_attn.cuh.
+// on the 16-row side and 8 query rows a warp (16 where more would not fit the registers) on the other, so that the
+// few rows of a decode step fill the instruction; see gdn_attn.cuh.
+//
+// Measured, 64 ragged sequences of up to 8192 keys (0.54 GB), 16/2 heads of 256: 8 rows 94 us, 16 rows 96, 24 rows 106, 32 rows
+// 124; of up to 16384 keys, 24/4 heads (2.2 GB): 333 us (6.5 TB/s).  Eight rows a warp and more warps hide the
+// products' latencies better than 16 rows a warp, which read the keys and values from shared memory once for twice the
+// rows: 16 rows took 123 us that way against 103, 24 rows 131 against 117 (before the groups' cost was weighed as it is
+// now); at 32 rows the registers of 16 computing warps no longer suffice.
 #include "gdn_attn.cuh"
 
 namespace gdn {
@@ -10,16 +16,16 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-// Warps by rows: 4 key groups as long as the rows fit two warps of 16, then 2 and 1 (8 warps hold 224 registers each).
-// More than 32 rows only come here with an fp32 result.
+// 4 key groups as long as the rows fit, then 2 and 1.  More than 32 rows only come here with an fp32 result.
 template <int D, int PIECES>
 cudaError_t by_rows(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
-    const int n = block_rows(p.G * p.K, true);
-    if (n == 8) return launch<Shape<bf16, D, 1, 1, 4, PIECES>>(p, out_bf16, sms, stream);
-    if (n == 16) return launch<Shape<bf16, D, 2, 1, 4, PIECES>>(p, out_bf16, sms, stream);
+    const int R = p.G * p.K;
+    if (R <= 8) return launch<Shape<bf16, D, 1, 1, 4, PIECES>>(p, out_bf16, sms, stream);
+    if (R <= 16) return launch<Shape<bf16, D, 1, 2, 4, PIECES>>(p, out_bf16, sms, stream);
+    if (R <= 24) return launch<Shape<bf16, D, 1, 3, 4, PIECES>>(p, out_bf16, sms, stream);
     if constexpr (PIECES == 3) {
-        if (n == 64) return launch<Shape<bf16, D, 2, 4, 2, PIECES>>(p, out_bf16, sms, stream);
-        if (n == 128) return launch<Shape<bf16, D, 2, 8, 1, PIECES>>(p, out_bf16, sms, stream);
+        if (R > 64) return launch<Shape<bf16, D, 2, 8, 1, PIECES>>(p, out_bf16, sms, stream);
+        if (R > 32) return launch<Shape<bf16, D, 2, 4, 2, PIECES>>(p, out_bf16, sms, stream);
     }
     return launch<Shape<bf16, D, 2, 2, 4, PIECES>>(p, out_bf16, sms, stream);
 }

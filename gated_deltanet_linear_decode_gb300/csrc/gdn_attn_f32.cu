@@ -38,8 +38,9 @@ cudaError_t launch_attn_decode(const AttnParams& p, int head_dim, int act_dtype,
     if (sms == 0) return cudaErrorInvalidDevice;
     const bool out_bf16 = out_dtype == GDN_BF16;
     if (act_dtype != GDN_BF16) return attn::launch_f32(p, head_dim, out_bf16, sms, stream);
-    // 64 ragged sequences of up to 8192 keys, 16/2 heads of 256: 24 rows 131 us on mma.sync and 137 on tcgen05, 64 rows 253
-    // and 205, 128 rows 465 and 324; heads of 64: 32 rows 173 and 231, 64 rows 352 and 323.
+    // 64 ragged sequences of up to 8192 keys, 16/2 heads of 256, both with a group's cost at 3 tiles: 24 rows 131 us on
+    // mma.sync and 137 on tcgen05, 64 rows 253 and 204, 128 rows 465 and 324; heads of 64: 32 rows 173 and 231, 64 rows
+    // 352 and 305.
     // (fp32 results stay on mma.sync: the sums in tensor memory lose bits over a long sequence, see gdn_attn.cuh.)
     return p.G * p.K > 32 && out_bf16 ? attn::launch_tc(p, head_dim, sms, stream) : attn::launch_bf16(p, head_dim, out_bf16, sms, stream);
 }

@@ -14,7 +14,7 @@
 // its 128 KB take.  (With the keys or channels on the M side and R on the N side, a product of N = 32 took as long as one
 // of N = 128, and the softmax needed its maximum over lanes.)
 //
-// Measured, 64 ragged sequences of up to 8192 keys (0.54 GB), 16/2 heads of 256: 64 rows 205 us, 128 rows 324 us (214
+// Measured, 64 ragged sequences of up to 8192 keys (0.54 GB), 16/2 heads of 256: 64 rows 174 us, 128 rows 275 us (252
 // TFLOP/s).  What bounds it: 128 rows the softmax (a thread's 128 keys a tile, 8,300 cycles); 64 rows a group's end,
 // 24,000 cycles twice a CTA, most of it the fetch of code that runs twice.
 // Roles, one persistent CTA per SM:
@@ -47,7 +47,8 @@ struct TcShape {
     static constexpr int kLoaders = 8;        // warps that load, 16 keys of a tile each
     static constexpr int kAll = 32 * (4 + kLoaders + 1);
     static constexpr int kTile = 128;         // keys
-    static constexpr int kGroupCost = 2;
+    // at d = 256: 64 rows 2 tiles 204 us, 8 tiles 174, 16 tiles 187; 128 rows 8 tiles 288 us, 12 tiles 275
+    static constexpr int kGroupCost = D == 256 ? (NR == 64 ? 8 : 12) : D == 128 ? 6 : 4;
     static constexpr int kCols = D / 64;      // units of a tile's keys, and of its values
     static constexpr int NV = D > 64 ? 128 : 64;   // channels of one product with V: two units side by side, or one
     static constexpr int kPerV = NV / 64;
