@@ -15,7 +15,9 @@ namespace {
 
 // Elementwise but for one or two sums over a row, every element read and written once: bound by the memory.  A row
 // is held in registers between its passes: with 16-byte accesses (8 channels a thread and chunk) by a CTA, or
-// by 1 to 32 lanes of one where it has at most 256 channels.  The fp32 weights come from L1 after the first row of an SM.
+// by 1 to 32 lanes of one where it has at most 256 channels (32768 rows of 256, bf16: 18 us against 34 by a CTA a row).
+// The fp32 weights come from L1 after the first row of an SM.  Measured: 8192 rows of 5120, fp32 stream, gate and scale
+// (587 MB): 96 us, 6.1 TB/s; 64 rows of 2048: 2.8 us, the latency of a launch, its loads and two sums.
 
 __device__ __forceinline__ float block_sum(float v, float* s) {
     v = warp_sum(v);
@@ -193,7 +195,12 @@ cudaError_t norm(const NormParams& p, cudaStream_t stream) {
     const auto a_row = [&](void (*kernel)(NormParams, int), int n) {   // a CTA a row, n chunks a thread
         return launch_dependent(kernel, dim3(p.T), dim3((chunks + 32 * n - 1) / (32 * n) * 32), 0, stream, p, 0);
     };
-    if (chunks <= 256) return a_row(norm_residual_kernel<Ta, Tr, 1>, 1);
+    // One chunk a thread is quickest to its sums, two keep more loads in flight: one while the call's threads are at most half of
+    // what the SMs hold (bf16, 2048 channels: 64 rows 2.7 us against 3.1, 304 rows 3.1 against 3.5, 608 rows 4.8 against 3.9,
+    // 8192 rows 33 against 30).  A chunk of fp32 is two loads already: one up to 2048 channels (8192 rows of 1024: 25 us
+    // against 28; of 4096: 104 against 89).
+    const bool few = static_cast<long long>(p.T) * chunks <= 152 * 512 && chunks <= 512;
+    if (few || (sizeof(Ta) == 4 && chunks <= 256)) return a_row(norm_residual_kernel<Ta, Tr, 1>, 1);
     if (chunks <= 1024) return a_row(norm_residual_kernel<Ta, Tr, 2>, 2);
     return a_row(norm_residual_kernel<Ta, Tr, 4>, 4);
 }

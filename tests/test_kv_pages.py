@@ -83,6 +83,17 @@ def test_steps_of_decode_verify_and_truncate(B, ps, max_len, in_place):
         s.truncate(keep, in_place)
 
 
+@pytest.mark.parametrize("B,ps,max_len", [(40, 2, 400), (300, 2, 60), (512, 2, 60), (513, 2, 60)])
+def test_many_pages(B, ps, max_len):
+    """Caches of more than 4096 pages, a few to a thread and more sequences than threads."""
+    rng = random.Random(B)
+    s = State(rng, B, ps, max_len, 4200, width=-(-max_len // ps) + 12)
+    for step in range(3):
+        new = [rng.randint(0, 8) for _ in range(B)]
+        s.extend(new, sum(new) + 5)
+        s.truncate([rng.randint(0, x) for x in s.model.lens])
+
+
 @pytest.mark.parametrize("lens", [[8000, 1, 0, 500], [65536], [1] * 9, [4097, 4095, 4096]])
 def test_prompts_into_an_empty_cache(lens):
     ps = 16

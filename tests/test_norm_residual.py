@@ -47,6 +47,13 @@ def test_sizes(T, H, dtype, res):
     run(T, H, dtype, res, gate=[0, 1, H][T % 3], chan=T % 2 == 0, seed=T * 7 + H)
 
 
+@pytest.mark.parametrize("dtype,res", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("T,H", [(608, 1024), (609, 1024), (2100, 264), (311, 4096), (400, 4104), (700, 1992), (305, 8192)])
+def test_many_rows(T, H, dtype, res):
+    """Either side of one and two chunks a thread, rows enough for a look-ahead, widths that leave threads without a chunk."""
+    run(T, H, dtype, res, gate=[0, 1, H][T % 3], chan=T % 2 == 0, pitch=8 * (T % 2), seed=T + H)
+
+
 @pytest.mark.parametrize("H", [256, 255])
 @pytest.mark.parametrize("kw", [
     dict(y=False), dict(y=False, store=False), dict(post=False), dict(pre=False), dict(store=False),
