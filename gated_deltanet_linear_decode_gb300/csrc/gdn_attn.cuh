@@ -50,16 +50,17 @@ constexpr size_t kCounterBytes = 3 * kMaxCtas * 4;   // at the start of the work
 static_assert(kMaxCtas / 12 < kMaxFan, "parts of the second step");
 
 // Shape of a kernel: Ta cache type, D head size, NT blocks of 8 rows a warp holds, RG row groups, KG key
-// groups, PIECES bf16 parts of a softmax weight (bf16 only).
-template <typename Ta_, int D_, int NT_, int RG_, int KG_, int PIECES_>
+// groups, PIECES bf16 parts of a softmax weight (bf16 only), FR rows a warp holds (fp32; NT is 1).
+template <typename Ta_, int D_, int NT_, int RG_, int KG_, int PIECES_, int FR_ = 8>
 struct Shape {
     using Ta = Ta_;
     static constexpr bool kBf16 = std::is_same<Ta_, __nv_bfloat16>::value;
     static constexpr int D = D_, NT = NT_, RG = RG_, KG = KG_, PIECES = PIECES_;
+    static constexpr int kWarpRows = kBf16 ? 8 * NT : FR_, kPassRows = kBf16 ? 8 : FR_;   // of a warp, of a join pass
     static constexpr int kThreads = RG * KG * 32;                      // that compute
     static constexpr int kAll = kThreads + 128;                        // and four warps that load
     static constexpr int PW = 4 / KG;                                  // of them, a key group's
-    static constexpr int kRows = 8 * NT * RG;                          // rows of a block
+    static constexpr int kRows = kWarpRows * RG < 8 ? 8 : kWarpRows * RG;   // rows of a block (of 8, some are not used by fewer)
     static constexpr int kRowBytes = D * static_cast<int>(sizeof(Ta));
     static constexpr int KT = kBf16 ? (D == 256 ? 16 : 32) : 2048 / D;   // keys of a stage
     static constexpr int kHalfBytes = KT * kRowBytes;                  // the keys of a stage, then the values
@@ -227,9 +228,10 @@ template <class S, class F>
 __device__ __forceinline__ void join_parts(const AttnParams& p, bool out_bf16, const Split& sp, int rows, int b, int hk, int row0,
                                            float* w_s, int count, bool final, int to, F row_at) {
     using Ta = typename S::Ta;
-    constexpr int D = S::D, kItems = S::kRows * D / 4, kBatch = kItems / S::kThreads < 4 ? kItems / S::kThreads : 4;
+    constexpr int D = S::D, kItems = S::kRows * D / 4, kShare = kItems / S::kThreads;
+    constexpr int kBatch = kShare < 1 ? 1 : kShare < 4 ? kShare : 4;
     constexpr int kTpr = 8;   // threads a row for the statistics
-    static_assert(kItems % (S::kThreads * kBatch) == 0 && kBatch > 0, "every thread has a share");
+    static_assert(kBatch == 1 || kItems % (S::kThreads * kBatch) == 0, "a batch ends with the rows of a part");
     float2* const t_s = reinterpret_cast<float2*>(w_s + kMaxFan * S::kRows);   // [kRows]; w_s [kMaxFan][kRows]
 #pragma unroll 1
     for (int r = threadIdx.x / kTpr; r < rows; r += S::kThreads / kTpr) {
@@ -521,15 +523,15 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
 
     // ---------------------------------------------------------------- state of a row set
     // bf16: o[mt][nt] is the 16 x 8 fragment (channels 16 mt.., rows 8 nt..) of o transposed; this thread has rows
-    // 8 nt + 2 (lane%4) + {0,1}.  fp32: lane l has rows 0..7, the channels of qf.
-    constexpr int kCols = S::kBf16 ? NT * 2 : 8;
+    // 8 nt + 2 (lane%4) + {0,1}.  fp32: lane l has all FR rows, the channels of qf.
+    constexpr int FR = S::kWarpRows, kCols = S::kBf16 ? NT * 2 : FR;
     constexpr int kC = D / 32;
-    float o[S::kBf16 ? D / 16 * NT : 8][S::kBf16 ? 4 : kC];
+    float o[S::kBf16 ? D / 16 * NT : FR][S::kBf16 ? 4 : kC];
     float m[kCols], l[kCols];
-    float qf[S::kBf16 ? 1 : 8][kC];
+    float qf[S::kBf16 ? 1 : FR][kC];
     // keys that row i of this warp's rows sees
     auto limit = [&](int i) {
-        const int row = cc.rb * S::kRows + rg * 8 * NT + i;
+        const int row = cc.rb * S::kRows + rg * S::kWarpRows + i;
         return row < R ? cc.len - p.K + token_of(p, row) + 1 : 0;
     };
     // the fp32 kernel's channels of a lane: kV consecutive ones every 32 kV
@@ -550,8 +552,8 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             sync_computing<S>();
         } else {
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const int row = row0 + rg * 8 + r, tok = token_of(p, row);
+            for (int r = 0; r < FR; ++r) {
+                const int row = row0 + rg * FR + r, tok = token_of(p, row);
 #pragma unroll
                 for (int c = 0; c < kC; ++c)
                     qf[r][c] = row < R ? q[tok * p.ldq + (row - tok * p.G) * D + (c / kV) * 32 * kV + lane * kV + c % kV] *
@@ -733,47 +735,47 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 }
             }
         } else {
-            // fp32 products and sums on the CUDA cores: 4 keys x 8 rows at a time, the channels over the lanes; two such sets
+            // fp32 products and sums on the CUDA cores: 4 keys x 8 rows (8 x 4, 16 x 2) at a time, the channels over the lanes; two such sets
             // side by side where the registers allow, since a warp has its scheduler to itself
-            constexpr int U = D <= 128 ? 2 : 1;
+            constexpr int SK = 32 / FR, U = D <= 128 && KT >= 2 * SK ? 2 : 1;   // keys of a set, sets
             const float* ks = reinterpret_cast<const float*>(smem + (kg * kStages + slot) * S::kStageBytes) + lane * kV;
             const float* vs = ks + S::kHalfBytes / 4;
-            const int r = lane & 7;
+            const int r = lane % FR;
 #pragma unroll 1
-            for (int k0 = 0; k0 < KT; k0 += 4 * U) {
+            for (int k0 = 0; k0 < KT; k0 += SK * U) {
                 float s[U], mx = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     float part[32];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < SK; ++k) {
                         float kv[kC];
 #pragma unroll
                         for (int c = 0; c < kC; c += kV)
 #pragma unroll
-                            for (int i = 0; i < kV; ++i) kv[c + i] = ks[(k0 + 4 * u + k) * D + c / kV * 32 * kV + i];
+                            for (int i = 0; i < kV; ++i) kv[c + i] = ks[(k0 + SK * u + k) * D + c / kV * 32 * kV + i];
 #pragma unroll
-                        for (int rr = 0; rr < 8; ++rr) {
+                        for (int rr = 0; rr < FR; ++rr) {
                             float2 x = mul2(make_float2(kv[0], kv[1]), make_float2(qf[rr][0], qf[rr][1]));
 #pragma unroll
                             for (int c = 2; c < kC; c += 2)
                                 x = fma2(make_float2(kv[c], kv[c + 1]), make_float2(qf[rr][c], qf[rr][c + 1]), x);
-                            part[k * 8 + rr] = x.x + x.y;   // (two sums a row, of even and odd channels)
+                            part[k * FR + rr] = x.x + x.y;   // (two sums a row, of even and odd channels)
                         }
                     }
-                    s[u] = reduce32_transposed(part);   // key k0 + 4u + lane/8, row lane%8
+                    s[u] = reduce32_transposed(part);   // key k0 + SK u + lane / FR, row lane % FR
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int kk = k0 + 4 * u + (lane >> 3);
+                    const int kk = k0 + SK * u + lane / FR;
                     if (masked && (!((ok >> kk) & 1) || j0 + kk >= limit(r))) s[u] = -INFINITY;
                     mx = fmaxf(mx, s[u]);
                 }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+#pragma unroll
+                for (int d = FR; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                 float mine_m = m[0];
 #pragma unroll
-                for (int i = 1; i < 8; ++i) mine_m = r == i ? m[i] : mine_m;
+                for (int i = 1; i < FR; ++i) mine_m = r == i ? m[i] : mine_m;
                 const float m2 = fmaxf(mine_m, mx), base = m2 == -INFINITY ? 0.f : m2;
                 float w[U], lsum = 0.f;
 #pragma unroll
@@ -781,12 +783,12 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                     w[u] = ex2(s[u] - base);
                     lsum += w[u];
                 }
-                lsum += __shfl_xor_sync(0xffffffffu, lsum, 8);
-                lsum += __shfl_xor_sync(0xffffffffu, lsum, 16);
+#pragma unroll
+                for (int d = FR; d < 32; d <<= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, d);
                 if (__any_sync(0xffffffffu, m2 > mine_m)) {
                     const float f = ex2(mine_m - base);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < FR; ++i) {
                         m[i] = __shfl_sync(0xffffffffu, m2, i);
                         const float fi = __shfl_sync(0xffffffffu, f, i);
                         l[i] *= fi;
@@ -795,17 +797,17 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) l[i] += __shfl_sync(0xffffffffu, lsum, i);
+                for (int i = 0; i < FR; ++i) l[i] += __shfl_sync(0xffffffffu, lsum, i);
 #pragma unroll
-                for (int k = 0; k < 4 * U; ++k) {
+                for (int k = 0; k < SK * U; ++k) {
                     float kv[kC];
 #pragma unroll
                     for (int c = 0; c < kC; c += kV)
 #pragma unroll
                         for (int i = 0; i < kV; ++i) kv[c + i] = vs[(k0 + k) * D + c / kV * 32 * kV + i];
 #pragma unroll
-                    for (int rr = 0; rr < 8; ++rr) {
-                        const float wr = __shfl_sync(0xffffffffu, w[k / 4], k % 4 * 8 + rr);
+                    for (int rr = 0; rr < FR; ++rr) {
+                        const float wr = __shfl_sync(0xffffffffu, w[k / SK], k % SK * FR + rr);
 #pragma unroll
                         for (int c = 0; c < kC; c += 2) {
                             const float2 x = fma2(make_float2(wr, wr), make_float2(kv[c], kv[c + 1]), make_float2(o[rr][c], o[rr][c + 1]));
@@ -838,14 +840,14 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             if constexpr (S::kBf16) {
                 if (lane < 4) ml_s[kg * S::kRows + rg * 8 * NT + (i / 2) * 8 + lane * 2 + (i & 1)] = make_float2(m[i], l[i]);
             } else {
-                if (lane == i) ml_s[kg * S::kRows + rg * 8 + i] = make_float2(m[i], l[i]);
+                if (lane == i) ml_s[kg * S::kRows + rg * FR + i] = make_float2(m[i], l[i]);
             }
         }
         const int rows = min(S::kRows, R - cc.rb * S::kRows);
-        constexpr int kHalves = D / S::JC;
+        constexpr int kHalves = D / S::JC, PR = S::kPassRows;
 #pragma unroll 1
         for (int pass = 0; pass < RG * NT * kHalves; ++pass) {
-            const int ch0 = pass % kHalves * S::JC, r0 = pass / kHalves * 8;
+            const int ch0 = pass % kHalves * S::JC, r0 = pass / kHalves * PR;
             if (r0 >= rows) break;
             if (pass / (NT * kHalves) == rg) {
                 const int mine_pass = pass % (NT * kHalves);
@@ -864,11 +866,11 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                             }
                 } else {
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
+                    for (int r = 0; r < PR; ++r)
 #pragma unroll
                         for (int c = 0; c < kC; ++c)
                             if (c / kV * 32 * kV / S::JC == mine_pass)
-                                join_s[(kg * 8 + r) * S::kJPitch + c / kV * 32 * kV % S::JC + lane * kV + c % kV] = o[r][c];
+                                join_s[(kg * PR + r) * S::kJPitch + c / kV * 32 * kV % S::JC + lane * kV + c % kV] = o[r][c];
                 }
             }
             sync_computing<S>();
@@ -877,7 +879,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 return;
             }
 #pragma unroll 1   // code that runs once costs its fetch
-            for (int i = threadIdx.x; i < 8 * S::JC / 4; i += S::kThreads) {
+            for (int i = threadIdx.x; i < PR * S::JC / 4; i += S::kThreads) {
                 const int r = i / (S::JC / 4), ch = i % (S::JC / 4) * 4, row = r0 + r;
                 if (row >= rows) break;
                 float mm = -INFINITY, ll = 0.f;
@@ -889,7 +891,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 for (int k = 0; k < KG; ++k) {
                     const float2 t = ml_s[k * S::kRows + row];
                     const float f = ex2(t.x - base);
-                    const float4 x = *reinterpret_cast<const float4*>(join_s + (k * 8 + r) * S::kJPitch + ch);
+                    const float4 x = *reinterpret_cast<const float4*>(join_s + (k * PR + r) * S::kJPitch + ch);
                     ll = fmaf(f, t.y, ll);
                     y.x = fmaf(f, x.x, y.x);
                     y.y = fmaf(f, x.y, y.y);

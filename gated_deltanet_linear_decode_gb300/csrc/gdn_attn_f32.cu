@@ -1,5 +1,12 @@
-// gdn_attn_f32.cu -- gdn_attn_decode over an fp32 cache: fp32 products and sums on the CUDA cores, 8 rows a
+// gdn_attn_f32.cu -- gdn_attn_decode over an fp32 cache: fp32 products and sums on the CUDA cores, 2 to 8 rows a
 // warp; see gdn_attn.cuh.
+//
+// But for heads of 256 with up to 4 rows, the products bind and not the memory: every row that a warp has costs its products, the
+// reduction over the lanes and the weights' way to them whether a query stands in it or not, and a second warp a scheduler
+// hides their latencies.  16 ragged sequences of up to 4096 keys, 8 kv heads, us (floors 21, 43, 86 for heads of 64,
+// 128, 256): up to 4 rows by one warp of 8 rows 63, 72, 115, of 4 rows 41, 53, 96, by two of 2 rows 36, 52; 5 to 8 rows
+// by one warp of 8 64, 73, 124, by two of 4 rows 52, 64, 112.  9 sequences, 2 tokens, up to 5001 keys, 6/3 heads of 64: 16.2 us
+// (floor 5.2).  Heads of 256 and up to 4 rows: 6.1 TB/s.
 #include "gdn_attn.cuh"
 
 namespace gdn {
@@ -9,8 +16,10 @@ namespace {
 
 template <int D>
 cudaError_t by_rows(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
-    switch (block_rows(p.G * p.K, false)) {
-        case 8: return launch<Shape<float, D, 1, 1, 4, 1>>(p, out_bf16, sms, stream);
+    const int R = p.G * p.K;
+    if (R <= 4) return launch<Shape<float, D, 1, D == 64 ? 2 : 1, 4, 1, D == 64 ? 2 : 4>>(p, out_bf16, sms, stream);
+    if (R <= 8) return launch<Shape<float, D, 1, 2, 4, 1, 4>>(p, out_bf16, sms, stream);
+    switch (block_rows(R, false)) {
         case 16: return launch<Shape<float, D, 1, 2, 4, 1>>(p, out_bf16, sms, stream);
         case 32: return launch<Shape<float, D, 1, 4, 2, 1>>(p, out_bf16, sms, stream);
         default: return launch<Shape<float, D, 1, 8, 1, 1>>(p, out_bf16, sms, stream);

@@ -103,6 +103,14 @@ def test_against_the_definition(i, dtype, out_dtype):
     c.close(c.run(out_dtype))
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("K,G_", [(1, 1), (2, 1), (1, 3), (2, 2), (1, 5), (3, 2), (2, 4), (3, 3), (1, 16)])
+def test_few_rows_in_fp32(K, G_, d):
+    """Every number of rows a warp may hold or leave empty: a group of many parts, one of one, one without keys."""
+    c = Case([9000, 0, 1, 31, 2500], K, 2 * G_, 2, d, 11, F32, seed=K * 100 + G_ * 10 + d)
+    c.close(c.run(F32))
+
+
 @pytest.mark.parametrize("layout", ["htd", "pair", "pth"])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_cache_layouts(layout, dtype):
