@@ -304,22 +304,26 @@ cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, int threads,
 // a butterfly over the lanes of a head.  The two halves of a rotary pair are rope_dim/2 channels, i.e. rope_dim/16
 // lanes, apart: the partner's channels come by shuffle, as they lie in memory, and norm weight and rotation are
 // one pair of factors a channel, u' = r (u A + partner B), the same for all heads of the job.
-// Measured, heads of 256, 64 channels rotated: 8192 tokens of 24/4 heads (271 MB) 54.6 us, 5.0 TB/s; 64 tokens of 16/2 heads
-// 2.5 us.  Two head sets a job and five CTAs an SM: 64 and 2.1 us; eight sets and three CTAs: 64 and 3.5; four sets and
-// five CTAs: 52.8 and 2.7, with spills.
+// Small CTAs, so that a finished warp's place is soon another's, and the registers of four head sets without spills.
+// Measured, heads of 256, 64 channels rotated: 8192 tokens of 24/4 heads (271 MB) 49.6 us, 5.5 TB/s; 64 tokens of 16/2 heads
+// 2.4 us.  8192 tokens by CTAs of 8 warps, four an SM 54.7 us; 4 warps, eight 52.5, nine 50.1, ten 49.7 (with spills; heads
+// of 64 39 us against 34); 2 warps, sixteen 52.1, eighteen 49.6; 1 warp 66.  By CTAs of 8 warps two and eight head sets a
+// job both 64 us.
+constexpr unsigned kAppendWarps = 2;
 constexpr int kPass = 4;
 
 template <typename Ta, int D>
-__global__ void __launch_bounds__(256, sizeof(Ta) == 2 ? 4 : 3) kv_append_kernel(const KvAppendParams p, const int q_jobs, const int kv_jobs) {
+__global__ void __launch_bounds__(32 * kAppendWarps, sizeof(Ta) == 2 ? 18 : 12) kv_append_kernel(const KvAppendParams p, const int q_jobs, const int kv_jobs) {
     constexpr int kLanes = D / 8, kSet = 32 / kLanes;   // lanes of a head, heads of a set
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, i = lane % kLanes, sub = lane / kLanes;
     const int jobs = q_jobs + 2 * kv_jobs;
-    const unsigned id = blockIdx.x * 8u + (threadIdx.x >> 5);
+    const unsigned id = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     const int t = static_cast<int>(id / jobs);
     int job = static_cast<int>(id - static_cast<unsigned>(t) * jobs);
     if (t >= p.T) return;   // a whole warp
+    const int slot = p.slot_map[t], pos = p.positions[t];
     const int kind = job < q_jobs ? 0 : job < q_jobs + kv_jobs ? 1 : 2;   // q, k, v
     if (kind) job -= kind == 1 ? q_jobs : q_jobs + kv_jobs;
     const int heads = kind == 0 ? p.Hq : p.Hkv, h0 = job * kPass * kSet + sub;
@@ -331,7 +335,6 @@ __global__ void __launch_bounds__(256, sizeof(Ta) == 2 ? 4 : 3) kv_append_kernel
 #pragma unroll
     for (int s = 0; s < kPass; ++s)
         if (h0 + s * kSet < heads) raw[s].load(src + s * kSet * D);
-    const int slot = p.slot_map[t], pos = p.positions[t];
     if ((p.rope_dim != 0 && (pos < 0 || pos >= p.n_pos)) || slot >= p.cache.num_pages * p.cache.page_size) {
         if (p.status && lane == 0 && id == static_cast<unsigned>(t) * jobs) atomicOr(p.status, kKvBadIndex);
         return;
@@ -416,9 +419,9 @@ template <typename Ta, int D>
 cudaError_t append(const KvAppendParams& p, cudaStream_t stream) {
     constexpr int kHeads = kPass * 256 / D;   // of a job
     const int q_jobs = (p.Hq + kHeads - 1) / kHeads, kv_jobs = (p.Hkv + kHeads - 1) / kHeads;
-    const long long blocks = (static_cast<long long>(p.T) * (q_jobs + 2 * kv_jobs) + 7) / 8;
-    if (blocks > 1 << 28) return cudaErrorInvalidConfiguration;   // a warp's number has 31 bits
-    return launch_dependent(kv_append_kernel<Ta, D>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p, q_jobs, kv_jobs);
+    const long long blocks = (static_cast<long long>(p.T) * (q_jobs + 2 * kv_jobs) + kAppendWarps - 1) / kAppendWarps;
+    if (blocks > (1ll << 31) / kAppendWarps - 1) return cudaErrorInvalidConfiguration;   // a warp's number has 31 bits
+    return launch_dependent(kv_append_kernel<Ta, D>, dim3(static_cast<unsigned>(blocks)), dim3(32 * kAppendWarps), 0, stream, p, q_jobs, kv_jobs);
 }
 
 }  // namespace
