@@ -70,8 +70,10 @@ struct Shape {
     static constexpr int kStages = kRing / kStageBytes / KG;           // of one key group
     static constexpr int kTile = KG * KT;                              // keys of a tile
     // A group's begin and end, in tiles (64 KB each).  64 ragged sequences, heads of 256, 24 rows: 3 tiles 118 us, 5 tiles 108,
-    // 8 tiles 106; heads of 128, 24 rows: 3 tiles 121, 8 tiles 132; fp32, heads of 64: 2 tiles 112, 8 tiles 136.
-    static constexpr int kGroupCost = !kBf16 || D == 64 ? 3 : D == 128 ? 4 : RG > 1 ? 8 : 6;
+    // 8 tiles 106; heads of 128, 24 rows: 3 tiles 121, 8 tiles 132.  fp32, 16 sequences, 8 rows: heads of 64 1 tile 48.7,
+    // 2 tiles 49.9, 5 tiles 56 (9 sequences in pages of 11: 15.8, 15.0, 16.4); of 128 1 tile 68, 2 and 3 tiles 64, 5 tiles 68; of
+    // 256 2 tiles 119, 3 tiles 110, 5 tiles 102, 8 tiles 107.
+    static constexpr int kGroupCost = kBf16 ? (D == 64 ? 3 : D == 128 ? 4 : RG > 1 ? 8 : 6) : D == 64 ? 2 : D == 128 ? 3 : 5;
     static constexpr int JC = D < 128 ? D : 128;                       // channels of a join pass
     static constexpr int kJPitch = JC + 4;                             // 8t+g banks for the writes below
     static constexpr int kPartBytes = (kMaxFan * 4 + 8) * kRows;       // weights and totals of a join of parts
