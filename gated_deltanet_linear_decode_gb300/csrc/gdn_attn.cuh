@@ -697,9 +697,13 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             // o transposed: channels x rows += V^T . P^T
             const uint32_t va = st + S::kHalfBytes + ((lane & 7) + (lane >> 4) * 8) * S::kRowBytes + (((lane >> 3) & 1) ^ (lane & 7)) * 16;
             // The tensor cores' sums drop what is below the last bit, always downwards in magnitude: over a long sequence that
-            // adds up (16,000 keys: 1.3e-5 of the result).  Where the result is fp32 a stage is summed by itself and
-            // then added with a rounding that goes both ways.
-            constexpr bool kApart = S::PIECES == 3;
+            // adds up (16,000 keys: 1.3e-5 of the result, and 0.29% of bf16 results not the nearest ones, against 0.19% with sums
+            // apart and 0.11% in fp32 throughout; 64 sequences of up to 16,384 keys).  So a stage is summed by itself and then
+            // added with a rounding that goes both ways, where the result is fp32, and where up to 8 rows make it free (heads of
+            // 256, 64 ragged sequences, 91.1 us against 91.3).  bf16 results of more rows keep the one running sum, whose drift
+            // is a hundredth of their own rounding: 16 rows would take 94.8 us against 94.6 (heads of 64 118 against 114), 24
+            // rows 110.8 against 105.6, 32 rows 144 against 124.
+            constexpr bool kApart = S::PIECES == 3 || RG * NT == 1;
             constexpr int kMt = SUB == 1 && !kApart ? 4 : 2;   // as kKs above
 #pragma unroll
             for (int m0 = 0; m0 < D / 16; m0 += kMt) {
