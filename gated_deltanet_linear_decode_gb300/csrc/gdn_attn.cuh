@@ -24,7 +24,8 @@
 //
 // Waits.  Producers and consumers meet at an mbarrier pair a stage.  Every wait has a limit; a warp whose wait gives up
 // sets a flag that ends all waits of the CTA, nothing more is written, and the sequences concerned get bit 4 of
-// their status words.
+// their status words.  What a computing warp missed is told by the warp itself (stop) before the barrier at its group's end,
+// behind which all of them look: a copy of the flag taken before that barrier misses a warp that gives up later.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
     uint64_t* const never_s = empty_s + KG * kStages;
     volatile uint32_t* const valid_s = reinterpret_cast<uint32_t*>(never_s + 1);   // [KG][kStages][PW]
     __shared__ PlanSmem plan_s;
-    __shared__ int flag_s, stop_s;
+    __shared__ int flag_s, stop_s;   // stop: a computing warp has missed a stage; never taken back
     __shared__ volatile int abort_s;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -448,6 +449,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
     if (threadIdx.x == 0) {
         tc::mbar_init(never_s, 1);
         abort_s = 0;
+        stop_s = 0;
     }
     Cursor cc;
     Share sh;
@@ -540,6 +542,9 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
     constexpr int kV = kC < 4 ? kC : 4;
 
     auto begin_segment = [&]() {
+        auto stall = [&]() {   // here, where few registers are in use
+            if (p.test_stall && warp == RG * KG - 1 && !stage_wait(never_s, 0, &abort_s, 256)) stop_s = 1;
+        };
         const Ta* q = static_cast<const Ta*>(p.q) + static_cast<long long>(cc.b) * p.K * p.ldq + static_cast<long long>(cc.hk) * p.G * D;
         const int row0 = cc.rb * S::kRows;
         if constexpr (S::kBf16) {
@@ -552,7 +557,9 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 *reinterpret_cast<uint4*>(q_s + r * S::kRowBytes + (ch ^ (r & 7)) * 16) = v;
             }
             sync_computing<S>();
+            stall();
         } else {
+            stall();
 #pragma unroll
             for (int r = 0; r < FR; ++r) {
                 const int row = row0 + rg * FR + r, tok = token_of(p, row);
@@ -834,7 +841,6 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
         const long long g_first = cc.at - cc.tile, g_last = g_first + cc.tiles;   // the group's tiles
         const bool whole = seg_first == g_first && cc.at + 1 == g_last;
         const int part = 2 * blockIdx.x + (first_seg ? 0 : 1);
-        if (threadIdx.x == 0) stop_s = abort_s;
         if constexpr (S::kBf16) {
 #pragma unroll
             for (int i = 0; i < kCols; ++i)
@@ -919,7 +925,6 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
 
     // ---------------------------------------------------------------- the walk (one copy of each part: the code is fetched
     // anew by every launch)
-    if (p.test_stall) stage_wait(never_s, 0, &abort_s, 256);
     bool fresh = true, new_seq = cc.tile == 0 && cc.hk == 0 && cc.rb == 0;
     uint32_t phase = 0;
 #pragma unroll 1
@@ -933,6 +938,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             fresh = false;
         }
         if (warp_wait(full_s + kg * kStages + slot, phase, &abort_s)) compute();
+        else stop_s = 1;
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(empty_s + kg * kStages + slot);
         if (++slot == kStages) {

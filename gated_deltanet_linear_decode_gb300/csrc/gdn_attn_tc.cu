@@ -71,7 +71,7 @@ struct TcSmem {
     uint64_t q_ready, s_full[2], p_ready[2], o_done, drained, never;
     PlanSmem plan;
     uint32_t tmem;
-    int flag, stop;
+    int flag, stop;                           // stop: a softmax warp's wait has given up; never taken back
     volatile int abort;
 };
 static_assert(sizeof(TcSmem) <= 3072, "fits");
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
         tc::mbar_init(&sm.o_done, 1);
         tc::mbar_init(&sm.drained, 1);
         tc::mbar_init(&sm.never, 1);
-        sm.abort = (tc::smem_u32(smem) & 1023) != 0;   // the swizzle goes by address bits 7-9
+        sm.abort = sm.stop = (tc::smem_u32(smem) & 1023) != 0;   // the swizzle goes by address bits 7-9
     }
     Cursor cc;
     Share sh;
@@ -312,7 +312,12 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
         const uint32_t my_o = t_o + my_lanes;
         const float c = p.scale * kLog2e;
         float m = -INFINITY, base = 0.f, limit = -INFINITY, l = 0.f;
-        if (p.test_stall) stage_wait(&sm.never, 0, &sm.abort, 256);
+        // A wait of a softmax warp; what it gives up is told before the barrier at the group's end.
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            const bool done = warp_wait(bar, parity, &sm.abort);
+            if (!done) sm.stop = 1;
+            return done;
+        };
         bool fresh = true, first_seg = true, new_seq = cc.tile == 0 && cc.hk == 0 && cc.rb == 0;
         int count = 0;   // tiles of this CTA
         long long seg_first = cc.at;
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                     if (over) atomicOr(p.status + cc.b, kKvBadIndex);
                 }
             }
-            if (warp_wait(&sm.s_full[(count & 1)], (count >> 1) & 1, &sm.abort)) {
+            if (wait(&sm.s_full[(count & 1)], (count >> 1) & 1)) {
                 const uint32_t my_s = t_s + my_lanes + (count & 1) * 128;
                 tc::fence_after_sync();
                 // this row sees the keys of the tile before `sees` that are there
@@ -371,7 +376,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                 }
                 if (__any_sync(0xffffffffu, mx > limit)) {
                     // the tiles before have been added: O stands still
-                    const bool through = fresh || warp_wait(&sm.o_done, (count - 1) & 1, &sm.abort);
+                    const bool through = fresh || wait(&sm.o_done, (count - 1) & 1);
                     tc::fence_after_sync();
                     const float m2 = fmaxf(m, mx);
                     const bool none = m2 == -INFINITY;   // a row that has seen no key
@@ -430,7 +435,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                 tc::tmem_wait_st();
                 // Before the last tile of a group goes off: the one before it has been added, so that the wait for the last
                 // one cannot take the wrong phase for its own.
-                if (!fresh && (cc.tile + 1 == cc.tiles || cc.at + 1 == last)) warp_wait(&sm.o_done, (count - 1) & 1, &sm.abort);
+                if (!fresh && (cc.tile + 1 == cc.tiles || cc.at + 1 == last)) wait(&sm.o_done, (count - 1) & 1);
                 tc::fence_before_sync();
                 tc::mbar_arrive(&sm.p_ready[(count & 1)]);
             }
@@ -440,9 +445,9 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                 const long long g_first = cc.at - cc.tile, g_last = g_first + cc.tiles;   // the group's tiles
                 const bool whole = seg_first == g_first && cc.at + 1 == g_last;
                 const int part = 2 * blockIdx.x + (first_seg ? 0 : 1);
-                warp_wait(&sm.o_done, (count - 1) & 1, &sm.abort);
+                wait(&sm.o_done, (count - 1) & 1);
                 tc::fence_after_sync();
-                if (threadIdx.x == 0) sm.stop = sm.abort;
+                if (p.test_stall && warp == 3 && !stage_wait(&sm.never, 0, &sm.abort, 256)) sm.stop = 1;
                 sm.ml[threadIdx.x] = make_float2(m, l);
                 sync_computing<S>();
                 if (sm.stop) {   // a wait gave up: nothing of this group is written

@@ -59,7 +59,8 @@ typedef struct {
     float eps;          /* RMSNorm eps                                          */
     int32_t act_dtype;  /* gdn_dtype of q, k, v, gate and the cache             */
     int32_t out_dtype;  /* gdn_dtype of the attention's out                     */
-    uint32_t flags;     /* 0, or GDN_FLAG_TEST_STALL (gdn.h; gdn_attn_decode)   */
+    uint32_t flags;     /* 0, or GDN_FLAG_TEST_STALL (gdn.h; in gdn_attn_decode
+                           one warp of a CTA waits while the others go on)      */
 } gdn_attn_dims;
 
 /*
