@@ -451,6 +451,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
         abort_s = 0;
         stop_s = 0;
     }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");   // the barriers are there before asynchronous arrivals on them
     Cursor cc;
     Share sh;
     if (!my_share<S>(p, row_blocks, plan_s, cc, sh)) return;   // (an exit lets the next kernel start, too)

@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
         tc::mbar_init(&sm.never, 1);
         sm.abort = sm.stop = (tc::smem_u32(smem) & 1023) != 0;   // the swizzle goes by address bits 7-9
     }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");   // the barriers are there before asynchronous arrivals on them
     Cursor cc;
     Share sh;
     if (!my_share<S>(p, row_blocks, sm.plan, cc, sh)) return;
