@@ -7,6 +7,12 @@
 // l = l1 e^(m1-m) + l2 e^(m2-m), o likewise, and o / l is the result once.  Scores are kept in base 2
 // (s log2 e).  One pass over the keys; every key and value is read from memory once per block of rows.
 //
+// Strays.  A key that a row does not see has the weight 0 in it, which keeps its value out only if that is finite.  Of the keys
+// that some rows of a block see and others do not -- the last K - 1 of a sequence -- the values are looked at before
+// the products; an infinite or NaN element is zeroed in shared memory, and added to the rows that see its key, from the
+// cache, at the group's end.  (Three tokens, 24 rows, 64 ragged sequences: 107.4 us, 105.5 without; looked at by the computing
+// warps 111, whose registers do not suffice for it.  One token has no such keys and a kernel without all this.)
+//
 // What bounds it: the cache's bytes.  A bf16 key and value of head size d are 4 d bytes for 4 R d operations,
 // so up to about 64 rows (the tensor cores' mma.sync rate against the memory's) the stream is the time, and
 // the whole layout serves it:
@@ -146,6 +152,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+constexpr int kLate = 1 << 30;   // beside a key's head: one of the last K - 1 of its sequence
+
 // Where a walk over the tiles stands: group (b, hk, rb), tile of the group.  `at` numbers the tiles of all groups one
 // after another, each group's followed by cost numbers that no tile has.
 struct Cursor {
@@ -194,8 +202,8 @@ struct Split {
 // row / G for rows under 4096 and G <= 16 (g_inv = 65536 / G rounded up).
 __device__ __forceinline__ int token_of(const AttnParams& p, int row) { return static_cast<int>((static_cast<unsigned>(row) * p.g_inv) >> 16); }
 
-// The result of a row's channels c..c+3, gated, into out.
-template <typename Ta, int D>
+// The result of a row's channels c..c+3, gated, into out; added to what is there if `add`.
+template <typename Ta, int D, bool add = false>
 __device__ __forceinline__ void put(const AttnParams& p, bool out_bf16, int b, int hk, int row, int c, float4 y) {
     const int tok = token_of(p, row), h = hk * p.G + row - tok * p.G;
     const long long t = static_cast<long long>(b) * p.K + tok;
@@ -207,8 +215,75 @@ __device__ __forceinline__ void put(const AttnParams& p, bool out_bf16, int b, i
         y.w *= gate_of(g.w);
     }
     const long long at = (t * p.Hq + h) * D + c;
+    if (add) {
+        const float4 x = out_bf16 ? StateIO<__nv_bfloat16>::ld(static_cast<const __nv_bfloat16*>(p.out) + at)
+                                  : StateIO<float>::ld(static_cast<const float*>(p.out) + at);
+        y = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    }
     if (out_bf16) StateIO<__nv_bfloat16>::st(static_cast<__nv_bfloat16*>(p.out) + at, y);
     else StateIO<float>::st(static_cast<float*>(p.out) + at, y);
+}
+
+// Words of two bf16 or one fp32: bits 15 and 31 (bit 31) of the result are set where an element is infinite or NaN.
+template <typename Ta>
+__device__ __forceinline__ uint32_t stray_bits(uint32_t w) {
+    return sizeof(Ta) == 4 ? (w & 0x7f800000u) + 0x00800000u : (w & 0x7f807f80u) + 0x00800080u;
+}
+template <typename Ta>
+__device__ __forceinline__ bool has_strays(uint4 v) {
+    const uint32_t any = stray_bits<Ta>(v.x) | stray_bits<Ta>(v.y) | stray_bits<Ta>(v.z) | stray_bits<Ta>(v.w);
+    return (any & (sizeof(Ta) == 4 ? 0x80000000u : 0x80008000u)) != 0;
+}
+// Whether there are strays among the values of the keys `late` (bits) of a warp, lane k holding key k's offset.  kChunks: of 16
+// bytes, a value's.  Small, for the registers of the loading warps: in batches of loads 24 rows took 108 us instead of 105.
+template <typename Ta, int kChunks>
+__device__ __forceinline__ bool find_strays(const Ta* v, long long off, uint32_t late) {
+    constexpr int kAtOnce = kChunks < 32 ? 32 / kChunks : 1;   // keys
+    const int lane = threadIdx.x & 31;
+    bool any = false;
+#pragma unroll 1
+    for (int key = (__ffs(late) - 1) / kAtOnce * kAtOnce; key < 32 && late >> key; key += kAtOnce) {
+        const int k = key + lane / kChunks;
+        const long long o = __shfl_sync(0xffffffffu, off, k) + lane % kChunks * (16 / static_cast<int>(sizeof(Ta)));
+        if ((late >> k) & 1) {
+            any |= has_strays<Ta>(*reinterpret_cast<const uint4*>(v + o));
+            if (kChunks > 32) any |= has_strays<Ta>(*reinterpret_cast<const uint4*>(v + o + 32 * (16 / static_cast<int>(sizeof(Ta)))));
+        }
+    }
+    return __any_sync(0xffffffffu, any);
+}
+// Zero what is not finite among 16 bytes in shared memory; true if anything was.
+template <typename Ta>
+__device__ __forceinline__ bool take_strays(uint8_t* at) {
+    uint4* const x = reinterpret_cast<uint4*>(at);
+    if (!has_strays<Ta>(*x)) return false;
+    uint32_t w[4] = {x->x, x->y, x->z, x->w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = stray_bits<Ta>(w[i]);
+        w[i] = sizeof(Ta) == 4 ? (b >> 31 ? 0u : w[i]) : w[i] & ((b >> 31 ? 0u : 0xffff0000u) | ((b >> 15) & 1 ? 0u : 0xffffu));
+    }
+    *x = make_uint4(w[0], w[1], w[2], w[3]);
+    return true;
+}
+
+// The strays of the keys that a row sees, in its channels c..c+3; zeros elsewhere.
+template <typename Ta>
+__device__ __forceinline__ float4 strays_of(const AttnParams& p, const Cursor& cc, int row, int c) {
+    const int end = cc.len - p.K + token_of(p, row);   // the last key that it sees
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int j = max(0, cc.len - p.K + 1); j <= end; ++j) {
+        const int k = j / p.cache.page_size, page = p.block_table[static_cast<size_t>(cc.b) * p.max_pages + k];
+        if (page < 0 || page >= p.cache.num_pages) continue;
+        const float4 v = StateIO<Ta>::ld(static_cast<const Ta*>(p.cache.v) + page * p.cache.page_stride +
+                                         (j - k * p.cache.page_size) * p.cache.token_stride + cc.hk * p.cache.head_stride + c);
+        y.x += isfinite(v.x) ? 0.f : v.x;
+        y.y += isfinite(v.y) ? 0.f : v.y;
+        y.z += isfinite(v.z) ? 0.f : v.z;
+        y.w += isfinite(v.w) ? 0.f : v.w;
+    }
+    return y;
 }
 
 __device__ __forceinline__ float4 times(float4 y, float f) { return make_float4(y.x * f, y.y * f, y.z * f, y.w * f); }
@@ -422,7 +497,8 @@ __device__ __forceinline__ void join_group(const AttnParams& p, bool out_bf16, c
     }
 }
 
-template <class S>
+// kTokens: more than one token a sequence, so that some rows may not see a key that others do.
+template <class S, bool kTokens>
 __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParams p, const int out_bf16) {
     using Ta = typename S::Ta;
     constexpr int D = S::D, NT = S::NT, RG = S::RG, KG = S::KG, KT = S::KT, PW = S::PW, kTile = S::kTile;
@@ -436,7 +512,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
     uint64_t* const never_s = empty_s + KG * kStages;
     volatile uint32_t* const valid_s = reinterpret_cast<uint32_t*>(never_s + 1);   // [KG][kStages][PW]
     __shared__ PlanSmem plan_s;
-    __shared__ int flag_s, stop_s;   // stop: a computing warp has missed a stage; never taken back
+    __shared__ int flag_s, stop_s, strays_s;   // stop: a computing warp has missed a stage, strays: some were found; never taken back
     __shared__ volatile int abort_s;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -449,7 +525,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
     if (threadIdx.x == 0) {
         tc::mbar_init(never_s, 1);
         abort_s = 0;
-        stop_s = 0;
+        stop_s = strays_s = 0;
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");   // the barriers are there before asynchronous arrivals on them
     Cursor cc;
@@ -472,7 +548,8 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
 #pragma unroll 1
         for (int t = 0;; ++t) {
             const int pg = page[0], pg_seq = seq[0];
-            const long long off = pg * p.cache.page_stride + in_page[0] * p.cache.token_stride + head[0] * p.cache.head_stride;
+            const bool pg_late = kTokens && (head[0] & kLate) != 0;
+            const long long off = pg * p.cache.page_stride + in_page[0] * p.cache.token_stride + (kTokens ? head[0] & (kLate - 1) : head[0]) * p.cache.head_stride;
             page[0] = page[1];
             in_page[0] = in_page[1];
             head[0] = head[1];
@@ -483,7 +560,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 if (lane < kKeys && j < cc.len) {
                     const int k = j / ps;
                     in_page[1] = j - k * ps;
-                    head[1] = cc.hk;
+                    head[1] = kTokens && j > cc.len - p.K ? cc.hk | kLate : cc.hk;
                     seq[1] = cc.b;
                     page[1] = p.block_table[static_cast<size_t>(cc.b) * p.max_pages + k];   // looked at when it is used
                 }
@@ -499,6 +576,9 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             if (lane == 0) valid_s[(kg * kStages + slot) * PW + pw] = ok;
             constexpr int kChunks = S::kRowBytes / 16;   // of a row
             const uint32_t st = ring + slot * S::kStageBytes;
+            const uint32_t late = kTokens ? __ballot_sync(0xffffffffu, pg_late) & ok : 0u;
+            bool strays = false;
+            if (kTokens && late) strays = find_strays<Ta, kChunks>(static_cast<const Ta*>(p.cache.v), off, late);
 #pragma unroll
             for (int it = 0; it < kKeys * kChunks / 32; ++it) {
                 const int flat = it * 32 + lane;
@@ -509,6 +589,17 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 const uint32_t dst = st + row * S::kRowBytes + (S::kBf16 ? (ch ^ (row & 7)) : ch) * 16;
                 cp16(dst, static_cast<const Ta*>(p.cache.k) + (n ? o : 0), n);
                 cp16(dst + S::kHalfBytes, static_cast<const Ta*>(p.cache.v) + (n ? o : 0), n);
+            }
+            if (kTokens && strays) {
+                cp_wait_all();
+#pragma unroll 1
+                for (int it = 0; it < kKeys * kChunks / 32; ++it) {
+                    const int key = (it * 32 + lane) / kChunks, ch = (it * 32 + lane) % kChunks, row = pw * kKeys + key;
+                    if ((late >> key) & 1)   // what this lane has copied
+                        take_strays<Ta>(smem + (kg * kStages + slot) * S::kStageBytes + S::kHalfBytes + row * S::kRowBytes + (S::kBf16 ? (ch ^ (row & 7)) : ch) * 16);
+                }
+                strays_s = 1;
+                __syncwarp();   // before lane 0's arrival
             }
             cp_arrive(full_s + kg * kStages + slot);
             if (lane == 0) tc::mbar_arrive(full_s + kg * kStages + slot);
@@ -920,6 +1011,20 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             }
             sync_computing<S>();
         }
+        if (kTokens && strays_s) {   // of this group, or of one before it in this CTA
+#pragma unroll 1
+            for (int i = threadIdx.x; i < rows * (D / 4); i += S::kThreads) {
+                const int row = i / (D / 4), c = i % (D / 4) * 4;
+                const float4 x = strays_of<Ta>(p, cc, cc.rb * S::kRows + row, c);
+                if (x.x == 0.f && x.y == 0.f && x.z == 0.f && x.w == 0.f) continue;
+                if (whole) {
+                    put<Ta, D, true>(p, out_bf16, cc.b, cc.hk, cc.rb * S::kRows + row, c, x);
+                } else {
+                    float4* const at = reinterpret_cast<float4*>(sp.o + (static_cast<size_t>(part) * S::kRows + row) * D + c);
+                    *at = make_float4(at->x + x.x, at->y + x.y, at->z + x.z, at->w + x.w);
+                }
+            }
+        }
         if (whole) return;
         join_group<S>(p, out_bf16, sp, sh, cc, g_first, g_last, rows, join_s, &flag_s);
     };
@@ -961,11 +1066,18 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
     }
 }
 
+template <class S, bool kTokens>
+cudaError_t launch_as(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<S, kTokens>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(attn_decode_kernel<S, kTokens>, dim3(sms), dim3(S::kAll), S::kSmem, stream, p, out_bf16 ? 1 : 0);
+}
+
 template <class S>
 cudaError_t launch(const AttnParams& p, bool out_bf16, int sms, cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_decode_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(attn_decode_kernel<S>, dim3(sms), dim3(S::kAll), S::kSmem, stream, p, out_bf16 ? 1 : 0);
+    if constexpr (S::kRows <= 16)   // more rows have several tokens: a kv head has at most 16 query heads
+        if (p.K == 1) return launch_as<S, false>(p, out_bf16, sms, stream);
+    return launch_as<S, true>(p, out_bf16, sms, stream);
 }
 
 // CTAs of a launch: one per SM (0 if the device cannot be asked).

@@ -71,7 +71,7 @@ struct TcSmem {
     uint64_t q_ready, s_full[2], p_ready[2], o_done, drained, never;
     PlanSmem plan;
     uint32_t tmem;
-    int flag, stop;                           // stop: a softmax warp's wait has given up; never taken back
+    int flag, stop, strays;                   // stop: a softmax warp's wait has given up, strays: some were found; never taken back
     volatile int abort;
 };
 static_assert(sizeof(TcSmem) <= 3072, "fits");
@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
         tc::mbar_init(&sm.o_done, 1);
         tc::mbar_init(&sm.drained, 1);
         tc::mbar_init(&sm.never, 1);
+        sm.strays = 0;
         sm.abort = sm.stop = (tc::smem_u32(smem) & 1023) != 0;   // the swizzle goes by address bits 7-9
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");   // the barriers are there before asynchronous arrivals on them
@@ -322,6 +323,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
         bool fresh = true, first_seg = true, new_seq = cc.tile == 0 && cc.hk == 0 && cc.rb == 0;
         int count = 0;   // tiles of this CTA
         long long seg_first = cc.at;
+        int half0 = 0;   // halves of the tiles of the CTA's groups before this one
 #pragma unroll 1
         while (cc.at < last) {
             const int row0 = cc.rb * NR, rows = min(NR, R - row0);
@@ -423,6 +425,24 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                         tc::tmem_st16(my_s + key0 + i * 32 + q * 16, x);
                     }
                 }
+                if ((cc.tile + 1) * 128 > cc.len - p.K + 1) {
+                    // Strays are taken out here and not by the loading warps, whose loop would grow: 64 rows 179 us against 188.  The
+                    // values have landed when their barrier says so, and the issuing thread waits for all lanes before it uses them.
+                    const int i = static_cast<int>(cc.at - seg_first), n = static_cast<int>(min(static_cast<long long>(cc.tiles - cc.tile + i), last - seg_first));
+                    const int h = half0 + 2 * i + (i + 1 < n ? 2 : 1);   // the keys of the next tile come before these values, but for the last one's
+                    const int k0 = max(0, cc.len - p.K + 1 - cc.tile * 128), k1 = min(128, cc.len - cc.tile * 128);
+                    if (k0 < k1 && wait(sm.full + (h & 15), (h >> 4) & 1)) {
+                        const int u0 = h * S::kCols % kUnits;
+                        bool found = false;
+#pragma unroll 1
+                        for (int x = threadIdx.x; x < (k1 - k0) * (D / 8); x += 128) {
+                            const int ch = x % (D / 8);
+                            found |= take_strays<bf16>(smem + (u0 + ch / 8) % kUnits * kUnit + (k0 + x / (D / 8)) * 128 + ch % 8 * 16);
+                        }
+                        if (found) sm.strays = 1;
+                        tc::fence_proxy_async();
+                    }
+                }
                 if (NR < 128) {   // zeros for the keys that are other lanes'
                     float z[16];
 #pragma unroll
@@ -487,6 +507,10 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                                 const float4 v = *reinterpret_cast<const float4*>(buf + (x + row) * kPitch + ch);
                                 y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
                             }
+                            if (sm.strays) {
+                                const float4 v = strays_of<bf16>(p, cc, row0 + row, h * CH + ch);
+                                y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+                            }
                             if (whole) put<bf16, D>(p, true, cc.b, cc.hk, row0 + row, h * CH + ch, times(y, sm.f[row]));
                             else *reinterpret_cast<float4*>(sp.o + (static_cast<size_t>(part) * NR + row) * D + h * CH + ch) = y;
                         }
@@ -500,6 +524,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
             advance<S>(p, cc, row_blocks);
             fresh = group_done;
             if (group_done) {
+                half0 = 2 * count;
                 new_seq = cc.b != b;
                 seg_first = cc.at;
             }

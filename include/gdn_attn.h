@@ -171,7 +171,9 @@ size_t gdn_attn_decode_workspace_bytes(const gdn_attn_dims* dims, int32_t B, int
  *        max_pages*page_size (taken as that) or a page index lies outside the
  *        cache (its keys are left out)
  * No memory beyond a sequence's length is read, so what lies there (NaN
- * included) does not matter.  Results do not depend on what runs beside the
+ * included) does not matter; nor does a token's key or value to the rows that do
+ * not see it.  An infinite or NaN value element makes that channel of the rows
+ * that see it infinite or NaN.  Results do not depend on what runs beside the
  * call, and are the same from run to run.
  */
 gdn_status gdn_attn_decode(const gdn_attn_dims* dims, const gdn_kv_cache* cache, int32_t B, int32_t K,

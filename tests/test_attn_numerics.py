@@ -5,6 +5,7 @@ import torch
 
 import gated_deltanet_linear_decode_gb300 as gdn
 from tests import attn_ref as R
+from tests import gpu_util as G
 from tests.test_attn_decode import BF, F32, Case
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +32,52 @@ def test_bf16_results_of_long_sums_are_the_nearest_ones(d):
     s = q.double().view(-1, d) @ k.T / np.sqrt(d)
     ref = (torch.softmax(s, -1) @ v).view(B, -1)
     assert float((out != ref.to(BF)).double().mean()) <= 1e-3
+
+
+FORMS = [  # dtype, result, Hq, Hkv, K, d: every kernel form that holds more than one token
+    (BF, BF, 4, 2, 2, 256), (BF, BF, 2, 2, 7, 64), (BF, BF, 10, 2, 3, 128), (BF, BF, 16, 2, 3, 256), (BF, BF, 16, 2, 4, 128),
+    (BF, BF, 16, 2, 8, 256), (BF, BF, 16, 2, 16, 64), (BF, BF, 16, 1, 16, 128), (BF, BF, 8, 2, 16, 128), (BF, BF, 16, 2, 16, 256),
+    (BF, F32, 16, 2, 3, 256), (BF, F32, 16, 2, 4, 64), (BF, F32, 16, 2, 8, 128), (BF, F32, 16, 2, 16, 256),
+    (F32, F32, 2, 2, 2, 64), (F32, F32, 2, 2, 3, 128), (F32, F32, 4, 2, 3, 256), (F32, BF, 8, 2, 4, 64), (F32, F32, 8, 2, 8, 128),
+    (F32, F32, 4, 2, 16, 256), (F32, F32, 16, 2, 16, 64)]
+
+
+@pytest.mark.parametrize("dtype,out_dtype,Hq,Hkv,K,d", FORMS)
+@pytest.mark.parametrize("lens", [[130, 2, 65, 1, 0, 33, 17, 300], [5000, 16], [129] * 170], ids=["short", "split", "many"])
+def test_rows_are_kept_from_later_tokens_that_are_not_finite(dtype, out_dtype, Hq, Hkv, K, d, lens):
+    """Infinities and NaN in the drafted tokens' keys and values reach the rows that see them, in those channels, and no other.  Where
+    nothing infinite is seen the bounds are those of test_attn_decode."""
+    c = Case(lens, K, Hq, Hkv, d, 13, dtype, seed=31)
+    at = lambda t, b, j, h: t[int(c.table[b, j // 13]), j % 13, h]
+    bad = np.zeros((len(lens), K, Hkv, d), dtype=bool)   # by the first drafted token ...
+    for b, n in enumerate(lens):
+        plants = [(n - 1, 0, 3, float("inf")), (n - 1, 0, 8, float("nan")), (n - 1, Hkv - 1, slice(d - 5, d), float("nan"))]
+        if K > 2:
+            plants += [(n - K + 1, 0, d - 1, float("-inf")), (n - 2, 0, 17, float("inf"))]
+        for j, h, ch, x in plants:
+            if j < 0 or j <= n - K:      # (a key that every row sees)
+                continue
+            at(c.v, b, j, h)[ch] = x
+            bad[b, j - n + K:, h, ch] = True   # ... token p sees keys up to n - K + p
+        if n > 2 and b % 2 and K > 1:
+            at(c.k, b, n - 1, 0)[5] = float("nan")
+            bad[b, K - 1, 0] = True
+    v = R.f64(c.v)
+    fin = lambda x: np.nan_to_num(x, nan=0.0, posinf=0.0, neginf=0.0)
+    gate = None if c.gate is None else R.f64(c.gate)
+    ref = R.attn(R.f64(c.q), fin(R.f64(c.k)), fin(v), c.table.numpy(), lens, K, Hq, Hkv, d, gate)
+    got = R.f64(c.run(out_dtype))
+    bad = np.repeat(bad.reshape(len(lens) * K, Hkv, 1, d), Hq // Hkv, 2).reshape(got.shape)
+    assert (np.isfinite(got) == ~bad).all(), (np.argwhere(np.isfinite(got) == bad)[:4], int((np.isfinite(got) == bad).sum()))
+    big = float(np.abs(fin(v)).max())
+    bound = 1e-5 * big if out_dtype == F32 else G.half_ulp_bf16(ref) + 2.0 ** -16 * big
+    assert (np.abs(got - ref) <= bound)[~bad].all()
+
+
+def test_infinite_values_that_a_row_sees():
+    """One infinite value among the drafted tokens', the rows that see it get that infinity, whatever the gate."""
+    c = Case([50], 4, 4, 2, 64, 16, F32, seed=32)
+    c.v[int(c.table[0, 48 // 16]), 48 % 16, 1, 9] = float("-inf")
+    out = R.f64(c.run(F32)).reshape(4, 4, 64)
+    assert np.isfinite(out[:2]).all() and (out[2:, 2:, 9] == -np.inf).all()
+    assert np.isfinite(out[2:, :2]).all() and np.isfinite(np.delete(out[2:, 2:], 9, -1)).all()
