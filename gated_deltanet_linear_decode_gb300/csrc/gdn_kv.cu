@@ -285,12 +285,13 @@ __global__ void __launch_bounds__(kMaxThreads) kv_truncate_kernel(const KvTrunca
     if (threadIdx.x == 0) *p.free_count_out = free_n + pages;
 }
 
-// One cluster of `ctas` CTAs with room for `ints` words.
+// One cluster of `ctas` CTAs with room for `arrays` arrays of B + 1 words.  The kernel's limit is set to what the most sequences
+// need, the same by every call: another thread's call may come between it and the launch.
 template <typename P>
-cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, int threads, size_t ints, cudaStream_t stream) {
-    const size_t smem = ints * 4;
+cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, int threads, size_t arrays, cudaStream_t stream) {
+    const size_t smem = arrays * (static_cast<size_t>(p.B) + 1) * 4;
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(arrays * (kKvMaxSeq + 1) * 4));
         if (e != cudaSuccess) return e;
     }
     return launch_dependent_cluster(kernel, ctas, dim3(ctas), dim3(threads), smem, stream, p);
@@ -429,13 +430,13 @@ cudaError_t append(const KvAppendParams& p, cudaStream_t stream) {
 cudaError_t launch_kv_extend(const KvExtendParams& p, cudaStream_t stream) {
     const int ctas = p.T > kManyRows ? 8 : 1;
     const int threads = p.T <= 256 && p.B <= 256 ? 256 : kMaxThreads;
-    return launch_cluster(kv_extend_kernel, p, ctas, threads, 2 * (static_cast<size_t>(p.B) + 1), stream);
+    return launch_cluster(kv_extend_kernel, p, ctas, threads, 2, stream);
 }
 
 cudaError_t launch_kv_truncate(const KvTruncateParams& p, cudaStream_t stream) {
     const int ctas = p.num_pages > kManyPages ? 8 : 1;
     const int threads = p.B <= 512 ? 256 : kMaxThreads;
-    return launch_cluster(kv_truncate_kernel, p, ctas, threads, static_cast<size_t>(p.B) + 1, stream);
+    return launch_cluster(kv_truncate_kernel, p, ctas, threads, 1, stream);
 }
 
 cudaError_t launch_kv_append(const KvAppendParams& p, int head_dim, int act_dtype, cudaStream_t stream) {

@@ -7,6 +7,7 @@
 #include "gdn_attn_internal.h"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
+#include "gdn_norm.h"
 #include "gdn_vec.cuh"
 
 namespace gdn {
@@ -179,8 +180,8 @@ cudaError_t norm(const NormParams& p, cudaStream_t stream) {
     if (!wide) {
         const int threads = p.H >= 1024 ? 512 : p.H >= 256 ? 128 : 32;
         const int smem = p.H * 4;
-        if (smem > 40 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(norm_residual_any_kernel<Ta, Tr>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (smem > 40 * 1024) {   // the limit is the same for every call: another thread's may come before the launch
+            const cudaError_t e = cudaFuncSetAttribute(norm_residual_any_kernel<Ta, Tr>, cudaFuncAttributeMaxDynamicSharedMemorySize, GDN_NORM_MAX_H * 4);
             if (e != cudaSuccess) return e;
         }
         return launch_dependent(norm_residual_any_kernel<Ta, Tr>, dim3(p.T), dim3(threads), smem, stream, p);
