@@ -70,6 +70,20 @@ gdn_status check_attn_dims(const gdn_attn_dims* d) {
     return GDN_OK;
 }
 
+struct Dim {
+    int64_t n, stride;
+};
+
+// Whether two sets of elements, each {sum of i_d stride_d, 0 <= i_d < n_d} and one `delta` >= 0 elements after the other, meet: delta
+// is then a sum of j_d stride_d with |j_d| < n_d.  The strides fall, each past all that is inside it, so that j_d is
+// the quotient of what is left or the next number.
+bool meet(const Dim* m, int dims, int64_t delta) {
+    if (dims == 0) return delta == 0;
+    if (m->n == 1) return meet(m + 1, dims - 1, delta);
+    const int64_t a = delta < 0 ? -delta : delta, j = a / m->stride;
+    return (j < m->n && meet(m + 1, dims - 1, a - j * m->stride)) || (j + 1 < m->n && meet(m + 1, dims - 1, a - (j + 1) * m->stride));
+}
+
 // The cache's shape, with the strides of dimensions of one set to zero; *bytes = its
 // bytes from the first to the last element, per half.
 gdn_status check_cache(const gdn_attn_dims* d, const gdn_kv_cache* c, gdn::KvCache* out, size_t* bytes) {
@@ -79,25 +93,27 @@ gdn_status check_cache(const gdn_attn_dims* d, const gdn_kv_cache* c, gdn::KvCac
     if (c->k == c->v) return GDN_E_INVALID_ARG;
     const gdn_status s = check_ptrs({c->k, c->v}, {});
     if (s != GDN_OK) return s;
-    struct Dim {
-        int64_t n, stride;
-    } m[3] = {{c->num_pages, c->page_stride}, {c->page_size, c->token_stride}, {d->H_kv, c->head_stride}};
+    Dim m[4] = {{c->num_pages, c->page_stride}, {c->page_size, c->token_stride}, {d->H_kv, c->head_stride}, {d->head_dim, 1}};
     const int64_t vec = 16 / static_cast<int64_t>(elem_size(d->act_dtype));
-    for (Dim& x : m) {
-        if (x.n == 1) x.stride = 0;
-        if (x.stride < 0 || x.stride > kMaxPitch) return GDN_E_INVALID_ARG;
-        if (x.stride % vec != 0) return GDN_E_ALIGNMENT;
+    for (Dim* x = m; x != m + 3; ++x) {
+        if (x->n == 1) x->stride = 0;
+        if (x->stride < 0 || x->stride > kMaxPitch) return GDN_E_INVALID_ARG;
+        if (x->stride % vec != 0) return GDN_E_ALIGNMENT;
     }
     *out = gdn::KvCache{c->k, c->v, c->num_pages, c->page_size, m[0].stride, m[1].stride, m[2].stride};
     // from the smallest stride up, each steps past all that is inside it: no two elements share an address
-    std::sort(m, m + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+    std::sort(m, m + 3, [](const Dim& a, const Dim& b) { return a.stride > b.stride; });
     int64_t span = d->head_dim;
-    for (const Dim& x : m) {
-        if (x.n == 1) continue;
-        if (x.stride < span) return GDN_E_INVALID_ARG;
-        span += (x.n - 1) * x.stride;
+    for (const Dim* x = m + 2; x >= m; --x) {
+        if (x->n == 1) continue;
+        if (x->stride < span) return GDN_E_INVALID_ARG;
+        span += (x->n - 1) * x->stride;
     }
     *bytes = static_cast<size_t>(span) * elem_size(d->act_dtype);
+    // the halves may lie page by page or row by row inside one another, but share no element
+    const uintptr_t k = reinterpret_cast<uintptr_t>(c->k), v = reinterpret_cast<uintptr_t>(c->v);
+    const uintptr_t apart = k < v ? v - k : k - v;
+    if (apart < *bytes && meet(m, 4, static_cast<int64_t>(apart / elem_size(d->act_dtype)))) return GDN_E_INVALID_ARG;
     return GDN_OK;
 }
 
@@ -206,7 +222,7 @@ gdn_status gdn_kv_append(const gdn_attn_dims* dims, const gdn_kv_cache* cache, i
                                               {v, rows_bytes(T, nk, ldv, es)}, {positions, nt}, {slot_map, nt},
                                               {q_norm_w, nw}, {k_norm_w, nw}, {rope_cos, tab}, {rope_sin, tab}};
     const Range qo{q_out, rows_bytes(T, nq, nq, es)}, st{dev_status, 4}, ck{kc.k, kv_bytes}, cv{kc.v, kv_bytes};
-    // the two halves of a cache may lie page by page or row by row inside one another
+    // (the two halves of a cache may lie inside one another: check_cache)
     if (any_overlap({qo, st, ck}, ins) || any_overlap({qo, st, cv}, ins)) return GDN_E_INVALID_ARG;
     gdn::KvAppendParams p{kc, T, dims->H_q, dims->H_kv, dims->rope_dim, n_pos, dims->eps, q, k, v, ldq, ldk, ldv,
                           positions, slot_map, q_norm_w, k_norm_w, rope_cos, rope_sin, q_out, dev_status};

@@ -67,7 +67,8 @@ typedef struct {
  * The cache of one layer: token t of page g, head h, channel i is element
  *   g*page_stride + t*token_stride + h*head_stride + i
  * of k and of v (strides in elements, the same for both; multiples of 16
- * bytes; any order of pages, tokens and heads that does not overlap itself).
+ * bytes; any order of pages, tokens and heads that does not overlap itself; k
+ * and v may lie inside one another, but share no element).
  * num_pages * page_size <= INT32_MAX; a slot is g*page_size + t.
  */
 typedef struct {
