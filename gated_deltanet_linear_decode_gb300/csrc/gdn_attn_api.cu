@@ -16,6 +16,10 @@
 namespace {
 
 constexpr int64_t kMaxPitch = int64_t{1} << 40;   // elements
+constexpr int64_t kMaxSpan = int64_t{1} << 60;    // elements: more than any address space has, and sums of a few stay in 64 bits
+
+// a * b where that is under kMaxSpan, else kMaxSpan (a, b >= 0).
+int64_t times(int64_t a, int64_t b) { return a != 0 && b > kMaxSpan / a ? kMaxSpan : a * b; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -107,7 +111,8 @@ gdn_status check_cache(const gdn_attn_dims* d, const gdn_kv_cache* c, gdn::KvCac
     for (const Dim* x = m + 2; x >= m; --x) {
         if (x->n == 1) continue;
         if (x->stride < span) return GDN_E_INVALID_ARG;
-        span += (x->n - 1) * x->stride;
+        span += times(x->n - 1, x->stride);
+        if (span >= kMaxSpan) return GDN_E_INVALID_ARG;
     }
     *bytes = static_cast<size_t>(span) * elem_size(d->act_dtype);
     // the halves may lie page by page or row by row inside one another, but share no element
@@ -119,7 +124,7 @@ gdn_status check_cache(const gdn_attn_dims* d, const gdn_kv_cache* c, gdn::KvCac
 
 // Bytes from the first to the last element of T rows of n elements at a pitch.
 size_t rows_bytes(int64_t T, int64_t n, int64_t ld, size_t es) {
-    return T > 0 ? static_cast<size_t>((T - 1) * ld + n) * es : 0;
+    return T > 0 ? static_cast<size_t>(times(T - 1, ld) + n) * es : 0;
 }
 
 gdn_status check_pitch(int64_t ld, int64_t n, size_t es) {

@@ -5,7 +5,7 @@ import random
 import pytest
 
 import gated_deltanet_linear_decode_gb300 as gdn
-from tests.test_attn_abi import A, INVALID, OK, adims, append, attn, cache
+from tests.test_attn_abi import A, INVALID, OK, adims, append, attn, cache, norm
 
 
 def status(k, v, pages, ps, strides, **kw):
@@ -49,3 +49,11 @@ def test_against_all_elements():
         assert got == {want}, (n, st, delta)
         seen.add(want)
     assert seen == {OK, INVALID}
+
+
+def test_spans_past_64_bits():
+    """Pitches and strides whose products pass 64 bits: what the rows cover is not taken for what is left of the product."""
+    assert status(0, 1 << 33, 1 << 26, 16, (1 << 38, 512, 256)) == INVALID       # 2^64 elements from page to page
+    T = (1 << 24) + 1                                                            # rows 2^40 elements apart: y covers all that lies after it
+    assert norm(T=T, y=A(0), ldy=1 << 40, gate=None, cols=0, post=None, chan=None, ho=A(90), x=None, pre=None, h=A(90)) == INVALID
+    assert attn(q=A(0) + (1 << 20), kc=cache(k=A(2), v=A(3)), B=T, ldq=1 << 40, out=A(90), ws=A(7)) == INVALID
