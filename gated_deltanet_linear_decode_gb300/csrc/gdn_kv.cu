@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(kMaxThreads) kv_extend_kernel(const KvExtendPa
             // a page of this call is read where it comes from, not where another thread is writing it
             const int page = i < held ? p.block_table[static_cast<size_t>(b) * p.max_pages + i]
                                       : p.free_list[free_n - 1 - page_s[b] - (i - held)];
-            slot = page * p.page_size + (pos - i * p.page_size);
+            if (page >= 0 && page < p.num_pages) slot = page * p.page_size + (pos - i * p.page_size);
+            else if (p.status) atomicOr(p.status + b, kKvBadIndex);
         }
         p.slot_map[t] = slot;
         p.positions[t] = pos;
@@ -268,7 +269,9 @@ __global__ void __launch_bounds__(kMaxThreads) kv_truncate_kernel(const KvTrunca
                     b = find(page_s, p.B, gg);
                     keep = truncate_ask(p, b).keep;
                 }
-                p.free_list[free_n + pages - 1 - gg] = p.block_table[static_cast<size_t>(b) * p.max_pages + keep + gg - page_s[b]];
+                const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + keep + gg - page_s[b]];
+                if ((page < 0 || page >= p.num_pages) && p.status) atomicOr(p.status + b, kKvBadIndex);
+                p.free_list[free_n + pages - 1 - gg] = page;
             }
         }
     }

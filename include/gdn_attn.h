@@ -104,6 +104,8 @@ typedef struct {
  * ask for exceed free_count, when their rows exceed T, or when n_new, seq_len
  * or n_pages is negative or n_pages exceeds max_pages or num_pages.  (What a sequence asks for counts for the ones
  * after it even where it was refused for want of pages or rows.)
+ * A token whose page -- from the block table or the stack -- lies outside
+ * 0..num_pages-1 gets slot -1, and its sequence GDN_KV_BAD_INDEX.
  * B <= GDN_KV_MAX_SEQ (else GDN_E_UNSUPPORTED).  B == 0 only pads the rows.
  */
 gdn_status gdn_kv_extend(int32_t page_size, int32_t num_pages, int32_t B, int32_t max_pages, int32_t T,
@@ -120,7 +122,8 @@ gdn_status gdn_kv_extend(int32_t page_size, int32_t num_pages, int32_t B, int32_
  * that undoes a gdn_kv_extend of the same sequences exactly.  Arguments as in
  * gdn_kv_extend; block_table is only read.  A sequence with new_len outside
  * 0..seq_len, or n_pages outside 0..max_pages, or whose pages would not fit
- * the stack, is refused.
+ * the stack, is refused.  Pages go back as the block table has them; one that
+ * lies outside 0..num_pages-1 gives its sequence GDN_KV_BAD_INDEX.
  */
 gdn_status gdn_kv_truncate(int32_t page_size, int32_t num_pages, int32_t B, int32_t max_pages,
                            const int32_t* new_len, const int32_t* seq_len, const int32_t* n_pages,
