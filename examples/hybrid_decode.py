@@ -8,6 +8,11 @@ page bookkeeping for the new tokens, the DeltaNet layer (norm, projections, recu
 the attention layer (norm, projection, cache append, attention over the paged cache, projection), and after a verify the
 commit of the state and the truncation of the cache.  Lengths, block tables and slots stay on the device, so the plain
 decode step is captured once and replayed as a CUDA graph.
+
+gdn_kv_extend packs the rows of the sequences that it gives tokens, while the other calls have row b*K + p for token p of
+sequence b: the slots and positions are brought to those rows on the device, -1 where a sequence was refused (its table is
+full, or the pages are out).  A refused sequence keeps its cache and, after a verify, its state; its outputs mean nothing,
+`status` names it, and it has to leave the batch before the next step.  The others are not touched by it.
 """
 import argparse
 import os
@@ -51,7 +56,13 @@ class HybridDecoder:
         self.kv = gdn.KvCache(z(pages, page_size, Hkv, D), z(pages, page_size, Hkv, D))
         self.table, self.free = z(B, per_seq, dt=I32), torch.randperm(pages, generator=g, device="cuda").to(I32)
         self.n_free, self.lens, self.held = torch.full((1,), pages, dtype=I32, device="cuda"), z(B, dt=I32), z(B, dt=I32)
-        self.n_new, self.slots, self.pos, self.cu = torch.full((B,), K, dtype=I32, device="cuda"), z(T, dt=I32), z(T, dt=I32), z(B + 1, dt=I32)
+        self.n_new, self.cu = torch.full((B,), K, dtype=I32, device="cuda"), z(B + 1, dt=I32)
+        # slots and positions as gdn_kv_extend packs them, with an entry T for rows that a sequence does not have; then by row b*K + p
+        width = -(-(T + 1) // 4) * 4
+        self.packed, self.by_row, self.at = z(2, width, dt=I32), z(2, width, dt=I32), torch.full((width,), T, dtype=I32, device="cuda")
+        self.packed[0, T] = -1
+        self.slots, self.pos = self.packed[0, :T], self.packed[1, :T]
+        self.token, self.nowhere = torch.arange(K, dtype=I32, device="cuda"), self.at[T]
         self.qkvg, self.q, self.o, self.status = z(T, 2 * nq + 2 * nk), z(T, nq), z(T, nq), z(B, dt=I32)
         self.cuts = (nq, nq + nk, nq + 2 * nk)
         self.ws = z(gdn.gdn_attn_decode_workspace_bytes(self.ad, B, K), dt=torch.uint8)
@@ -65,6 +76,9 @@ class HybridDecoder:
         nd, K = self.nd, self.K
         gdn.gdn_kv_extend(self.ps, self.n_new, self.lens, self.held, self.table, self.free, self.n_free, self.slots, self.pos,
                           self.cu, dev_status=self.status)
+        row = self.cu[:-1, None] + self.token               # where sequence b's token p is in the packed rows, if it is
+        torch.where(row < self.cu[1:, None], row, self.nowhere, out=self.at[:self.T].view(self.B, K))
+        torch.index_select(self.packed, 1, self.at, out=self.by_row)
         self.h.copy_(self.hidden)
         gdn.gdn_norm_residual(nd, self.h, pre_w=self.pre[0], x=self.xn)
         gdn.gdn_in_proj(self.gd, self.xn, *self.W_in, self.x, self.z, self.a, self.b)
@@ -76,17 +90,20 @@ class HybridDecoder:
         gdn.gdn_norm_residual(nd, self.h, self.h, y=self.d, pre_w=self.pre[1], x=self.xn)
         torch.matmul(self.xn, self.W_qkvg.t(), out=self.qkvg)
         a, b, c = self.cuts
-        gdn.gdn_kv_append(self.ad, self.kv, self.qkvg[:, :a], self.qkvg[:, a:b], self.qkvg[:, b:c], self.pos, self.slots, self.q,
-                          q_norm_w=self.q_w, k_norm_w=self.k_w, rope_cos=self.cos, rope_sin=self.sin)
+        gdn.gdn_kv_append(self.ad, self.kv, self.qkvg[:, :a], self.qkvg[:, a:b], self.qkvg[:, b:c], self.by_row[1, :self.T],
+                          self.by_row[0, :self.T], self.q, q_norm_w=self.q_w, k_norm_w=self.k_w, rope_cos=self.cos, rope_sin=self.sin)
         gdn.gdn_attn_decode(self.ad, self.kv, K, self.q, self.table, self.lens, self.o, gate=self.qkvg[:, c:], workspace=self.ws,
                             dev_status=self.status)
         torch.matmul(self.o, self.W_o.t(), out=self.d)
         gdn.gdn_norm_residual(nd, self.h, self.h, y=self.d, pre_w=self.pre[2], x=self.xn)
 
     def commit(self, accept):
-        """After a step of K > 1: keep accept[b] of the drafted tokens, in the state and in the cache."""
+        """After a step of K > 1: keep accept[b] of the drafted tokens, in the state and in the cache; a sequence that the step
+        refused stays as it was."""
+        added = self.cu.diff()
+        accept = torch.minimum(accept, added)               # 0 leaves the state as it is
         gdn.gdn_commit(self.gd, self.K, accept, self.conv_ck, self.S_ck, self.conv, self.S)
-        gdn.gdn_kv_truncate(self.ps, self.lens - (self.K - accept), self.lens, self.held, self.table, self.free, self.n_free,
+        gdn.gdn_kv_truncate(self.ps, self.lens - (added - accept), self.lens, self.held, self.table, self.free, self.n_free,
                             dev_status=self.status)
 
     def capture(self):

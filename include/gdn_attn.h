@@ -97,6 +97,10 @@ typedef struct {
  *                    past the last one get slot -1 and position 0
  *   cu_seqlens [B+1] first row of each sequence
  *   dev_status [B] or NULL
+ * The rows are packed: row b*K + p of gdn_attn_decode is row cu_seqlens[b] + p
+ * here, the same only while every sequence is given exactly K tokens.  Where one
+ * may be refused or idle the caller maps the one to the other (slot -1 for rows
+ * that a sequence does not have; examples/hybrid_decode.py does).
  * Sequences are served in order: sequence b takes its pages from the top of
  * the stack, after those of the sequences before it.  It is refused -- keeps
  * its length and pages, gets no rows -- when its new length needs more than
