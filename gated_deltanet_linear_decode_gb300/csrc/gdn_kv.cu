@@ -386,6 +386,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, sizeof(Ta) == 2 ? 18 : 12) 
         load8(p.rope_sin + tab, x);
 #pragma unroll
         for (int c = 0; c < 8; ++c) B[c] *= d > 0 ? -x[c] : x[c];
+    } else if (half > 0) {
+        // Not rotated: the partner is the channel itself, and halves of the weight leave an infinite one what it is, where A = w and
+        // B = 0 would make it NaN.  (Zeros for the partner instead: heads of 64 35.5 us against 33.9.)
+#pragma unroll
+        for (int c = 0; c < 8; ++c) A[c] = B[c] = 0.5f * A[c];
     }
 #pragma unroll
     for (int s = 0; s < kPass; ++s) {
