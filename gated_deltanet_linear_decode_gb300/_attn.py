@@ -102,7 +102,7 @@ def _rows(t, dtype, T: int, n: int):
     ld, one = t.stride()
     if one != 1 and n > 1:
         raise ValueError("rows must be contiguous")
-    return t.data_ptr(), ld if T > 1 else max(ld, n)
+    return t.data_ptr(), ld if T > 1 else n   # one row's pitch is of no account
 
 
 def _stream(stream):
