@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(512, N <= 2 ? 2 : 1) norm_residual_kernel(Norm
             }
         }
     }
-    if (live && p.gate_cols == 1) g1 = gate_of(ld_act(static_cast<const Ta*>(p.gate) + t * p.ldg));
+    if (live && p.gate_cols == 1) g1 = gate_of<sizeof(Tr) == 4>(ld_act(static_cast<const Ta*>(p.gate) + t * p.ldg));
     float r = 1.f;
     if (p.post_w) {
         float ss = 0.f;
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(512, N <= 2 ? 2 : 1) norm_residual_kernel(Norm
             } else if (p.gate_cols) {
                 g[c].get(w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] *= gate_of(w[e]);
+                for (int e = 0; e < 8; ++e) u[e] *= gate_of<sizeof(Tr) == 4>(w[e]);
             }
             if (p.chan_scale) {
                 load8(p.chan_scale + i * 8, w);
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(512) norm_residual_any_kernel(const NormParams
         if (p.y) {
             float u = ld_act(y + i) * r;
             if (p.post_w) u *= p.post_w[i];
-            if (p.gate_cols) u *= gate_of(ld_act(gate + (p.gate_cols == 1 ? 0 : i)));
+            if (p.gate_cols) u *= gate_of<sizeof(Tr) == 4>(ld_act(gate + (p.gate_cols == 1 ? 0 : i)));
             if (p.chan_scale) u *= p.chan_scale[i];
             v = fmaf(p.alpha, u, v);
         }
