@@ -81,3 +81,39 @@ def test_infinite_values_that_a_row_sees():
     out = R.f64(c.run(F32)).reshape(4, 4, 64)
     assert np.isfinite(out[:2]).all() and (out[2:, 2:, 9] == -np.inf).all()
     assert np.isfinite(out[2:, :2]).all() and np.isfinite(np.delete(out[2:, 2:], 9, -1)).all()
+
+
+def rising(lens, K, Hq, d, dtype, per_tile, seed):
+    """Scores that rise by `per_tile` (base 2) every 128 keys in a third of the rows, half as much in another, fall in the last."""
+    c = Case(lens, K, Hq, 1, d, 16, dtype, seed=seed, gate=False)
+    g = torch.Generator().manual_seed(seed + 1)
+    T, step = len(lens) * K, per_tile / 128 / 1.4427 * d ** 0.5
+    q = torch.randn(T, Hq, d, generator=g)
+    sign = torch.tensor([1.0, 0.5, -1.0])[torch.randint(0, 3, (T, Hq), generator=g)]
+    q[..., 0] = 4 * sign
+    c.q = q.view(T, Hq * d).to(dtype).cuda()
+    for b, n in enumerate(lens):
+        j = torch.arange(n, device="cuda")
+        page = c.table[b].long().cuda()[j // 16]
+        c.k[page, j % 16, 0, 0] = (step / 4 * j).to(dtype)
+    return c
+
+
+@pytest.mark.parametrize("dtype,out_dtype,Hq,K,d", [
+    (BF, BF, 16, 4, 64), (BF, BF, 16, 4, 128), (BF, BF, 16, 4, 256), (BF, BF, 8, 9, 128), (BF, BF, 8, 16, 64), (BF, BF, 8, 16, 128),
+    (BF, BF, 8, 16, 256), (BF, BF, 16, 16, 128), (BF, BF, 8, 1, 128), (BF, F32, 16, 8, 256), (F32, F32, 4, 2, 64)])
+@pytest.mark.parametrize("per_tile", [3, 12, 40])
+@pytest.mark.parametrize("lens", [[9000], [700, 130, 0, 1500, 129], [1000] * 160], ids=["split", "few", "whole"])
+def test_scores_that_rise_along_the_sequence(dtype, out_dtype, Hq, K, d, per_tile, lens):
+    """The running maximum changes in most tiles, in some lanes by far and in others not at all.  An error of 2^-20 of a score moves a
+    weight by as much (see test_attn_decode.test_large_scores); scores reach per_tile * 70 / 1.44."""
+    c = rising(lens, K, Hq, d, dtype, per_tile, seed=40)
+    first = [0, len(lens) // 2, len(lens) - 1] if len(lens) > 10 else range(len(lens))
+    k, v = np.nan_to_num(R.f64(c.k)), np.nan_to_num(R.f64(c.v))
+    got = R.f64(c.run(out_dtype)).reshape(len(lens), K, -1)
+    big, s = float(np.abs(v).max()), per_tile * (max(lens) / 128) / 1.44 + 20
+    for b in first:
+        ref = R.attn(R.f64(c.q).reshape(len(lens), K, -1)[b], k, v, c.table.numpy()[b:b + 1], [lens[b]], K, Hq, 1, d).reshape(K, -1)
+        bound = 2 * s * 2.0 ** -20 * big + (G.half_ulp_bf16(ref) + 2.0 ** -16 * big if out_dtype == BF else 1e-5 * big)
+        err = np.abs(got[b] - ref)
+        assert np.isfinite(got[b]).all() and (err <= bound).all(), float((err - bound).max())
