@@ -99,19 +99,6 @@ struct Shape {
 
 using tc::smem_u32;
 
-// 16 bytes global -> shared; `n` = 16 or 0 (zero fill, nothing read).
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int n) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-}
-// One arrival on `bar` when all cp.async of this thread so far have landed.
-__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
 constexpr int kWaitLimit = 1 << 22;   // polls of a wait before it gives up
 
 // Wait for phase `parity` of `bar`; false when it gives up or another warp has.
@@ -587,11 +574,11 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 const int n = (ok >> key) & 1 ? 16 : 0;
                 const int row = pw * kKeys + key;
                 const uint32_t dst = st + row * S::kRowBytes + (S::kBf16 ? (ch ^ (row & 7)) : ch) * 16;
-                cp16(dst, static_cast<const Ta*>(p.cache.k) + (n ? o : 0), n);
-                cp16(dst + S::kHalfBytes, static_cast<const Ta*>(p.cache.v) + (n ? o : 0), n);
+                tc::cp_async16_zfill(dst, static_cast<const Ta*>(p.cache.k) + (n ? o : 0), n);
+                tc::cp_async16_zfill(dst + S::kHalfBytes, static_cast<const Ta*>(p.cache.v) + (n ? o : 0), n);
             }
             if (kTokens && strays) {
-                cp_wait_all();
+                tc::cp_async_wait_all();
 #pragma unroll 1
                 for (int it = 0; it < kKeys * kChunks / 32; ++it) {
                     const int key = (it * 32 + lane) / kChunks, ch = (it * 32 + lane) % kChunks, row = pw * kKeys + key;
@@ -601,14 +588,14 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
                 strays_s = 1;
                 __syncwarp();   // before lane 0's arrival
             }
-            cp_arrive(full_s + kg * kStages + slot);
+            tc::cp_async_mbar_arrive(full_s + kg * kStages + slot);
             if (lane == 0) tc::mbar_arrive(full_s + kg * kStages + slot);
             if (++slot == kStages) {
                 slot = 0;
                 ++round;
             }
         }
-        cp_wait_all();   // nothing of a call that gives up is in flight when the CTA ends
+        tc::cp_async_wait_all();   // nothing of a call that gives up is in flight when the CTA ends
         return;
     }
 

@@ -175,13 +175,13 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                 }
                 if (c == 0 && i >= 0 && lane == 0) sm.valid[i & 15][pw] = static_cast<uint16_t>(there);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) cp16((e & 1 ? d1 : d0) + unit * kUnit + e * 512, src[e] + c * 64, n[e]);
+                for (int e = 0; e < 4; ++e) tc::cp_async16_zfill((e & 1 ? d1 : d0) + unit * kUnit + e * 512, src[e] + c * 64, n[e]);
                 if (++unit == kUnits) {
                     unit = 0;
                     ++round;
                 }
             }
-            cp_arrive(sm.full + (halves & 15));
+            tc::cp_async_mbar_arrive(sm.full + (halves & 15));
             if (lane == 0) tc::mbar_arrive(sm.full + (halves & 15));
             ++halves;
         };
@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
             if (ok) load(p.cache.v, 0, -1);
             if (ok && !(ends & 3)) load(p.cache.k, 2, i + 2);
         }
-        cp_wait_all();   // nothing is in flight when the CTA ends
+        tc::cp_async_wait_all();   // nothing is in flight when the CTA ends
     } else if (warp == kIssuer) {
         // ------------------------------------------------------------ the issuing thread
         if (lane == 0) {
@@ -308,7 +308,6 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
         // ------------------------------------------------------------ the softmax warps
         const Split sp = split_of<S>(p);
         constexpr int kChunks = NR / 32;           // of 32 keys, a thread's share of a tile
-        constexpr bool kHold = kChunks == 1;       // in registers between maximum and weights; else read twice
         const uint32_t my_lanes = static_cast<uint32_t>(32 * warp) << 16;
         const int r = threadIdx.x % NR, key0 = threadIdx.x / NR * NR;   // this lane's row, its first key of a tile
         const uint32_t my_o = t_o + my_lanes;
@@ -370,12 +369,12 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                         for (int e = 0; e < 32; ++e) s[e] = (w >> e) & 1 ? s[e] : -INFINITY;
                     }
                 };
-                float s[kHold ? kChunks : 1][32], mx = -INFINITY;
+                float w[32], mx = -INFINITY;   // scores for the maximum, read again for the weights
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
-                    scores(i, s[kHold ? i : 0]);
+                    scores(i, w);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, s[kHold ? i : 0][e]);
+                    for (int e = 0; e < 32; ++e) mx = fmaxf(mx, w[e]);
                 }
                 if (__any_sync(0xffffffffu, mx > limit)) {
                     // the tiles before have been added: O stands still
@@ -403,8 +402,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                 // result's own rounding), two keys a column: those of 32 keys take the columns of their scores.
 #pragma unroll
                 for (int i = 0; i < kChunks; ++i) {
-                    float(&w)[32] = s[kHold ? i : 0];
-                    if (!kHold) scores(i, w);
+                    scores(i, w);
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         w[e] = ex2(w[e] - base);
