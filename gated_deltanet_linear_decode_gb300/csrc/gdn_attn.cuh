@@ -101,14 +101,13 @@ using tc::smem_u32;
 
 constexpr int kWaitLimit = 1 << 22;   // polls of a wait before it gives up
 
-// Wait for phase `parity` of `bar`; false when it gives up or another warp has.
+// Wait for phase `parity` of `bar`; false when it gives up or another warp has.  A loop that is not unrolled: there are a score of
+// waits in a kernel, and with 16 polls each written out the tcgen05 kernel had 160 to 190 KB of code, now 100 to 130 (64 rows,
+// heads of 64: 350 us against 262).
 __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int limit = kWaitLimit) {
-    uint32_t done;   // the usual case by itself
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(done) : "r"(smem_u32(bar)), "r"(parity) : "memory");
-    if (done) return true;
-    for (int it = 0; it < limit; it += 16) {
-        if (tc::mbar_wait(bar, parity, 16)) return true;
+#pragma unroll 1
+    for (int it = 0; it < limit; ++it) {
+        if (tc::mbar_wait(bar, parity, 1)) return true;
         if (*abort) return false;
     }
     *abort = 1;
@@ -256,15 +255,15 @@ __device__ __forceinline__ bool take_strays(uint8_t* at) {
 
 // The strays of the keys that a row sees, in its channels c..c+3; zeros elsewhere.
 template <typename Ta>
-__device__ __forceinline__ float4 strays_of(const AttnParams& p, const Cursor& cc, int row, int c) {
-    const int end = cc.len - p.K + token_of(p, row);   // the last key that it sees
+__device__ __forceinline__ float4 strays_of(const AttnParams& p, int b, int hk, int len, int row, int c) {
+    const int end = len - p.K + token_of(p, row);   // the last key that it sees
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int j = max(0, cc.len - p.K + 1); j <= end; ++j) {
-        const int k = j / p.cache.page_size, page = p.block_table[static_cast<size_t>(cc.b) * p.max_pages + k];
+    for (int j = max(0, len - p.K + 1); j <= end; ++j) {
+        const int k = j / p.cache.page_size, page = p.block_table[static_cast<size_t>(b) * p.max_pages + k];
         if (page < 0 || page >= p.cache.num_pages) continue;
         const float4 v = StateIO<Ta>::ld(static_cast<const Ta*>(p.cache.v) + page * p.cache.page_stride +
-                                         (j - k * p.cache.page_size) * p.cache.token_stride + cc.hk * p.cache.head_stride + c);
+                                         (j - k * p.cache.page_size) * p.cache.token_stride + hk * p.cache.head_stride + c);
         y.x += isfinite(v.x) ? 0.f : v.x;
         y.y += isfinite(v.y) ? 0.f : v.y;
         y.z += isfinite(v.z) ? 0.f : v.z;
@@ -566,7 +565,11 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             const uint32_t late = kTokens ? __ballot_sync(0xffffffffu, pg_late) & ok : 0u;
             bool strays = false;
             if (kTokens && late) strays = find_strays<Ta, kChunks>(static_cast<const Ta*>(p.cache.v), off, late);
-#pragma unroll
+            // Copies unrolled in full, but for bf16 heads of 128 with several tokens, where the loading warps' registers do not suffice for
+            // that: 64 ragged sequences, 3 tokens 110 us against 138, 2 tokens 97 against 110; heads of 256 108.8 in fours against 108.1,
+            // of 64 139 against 137, one token 173 either way.
+            constexpr int kUnroll = kTokens && S::kBf16 && D == 128 ? 4 : 16;
+#pragma unroll kUnroll
             for (int it = 0; it < kKeys * kChunks / 32; ++it) {
                 const int flat = it * 32 + lane;
                 const int key = flat / kChunks, ch = flat % kChunks;
@@ -1002,7 +1005,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
 #pragma unroll 1
             for (int i = threadIdx.x; i < rows * (D / 4); i += S::kThreads) {
                 const int row = i / (D / 4), c = i % (D / 4) * 4;
-                const float4 x = strays_of<Ta>(p, cc, cc.rb * S::kRows + row, c);
+                const float4 x = strays_of<Ta>(p, cc.b, cc.hk, cc.len, cc.rb * S::kRows + row, c);
                 if (x.x == 0.f && x.y == 0.f && x.z == 0.f && x.w == 0.f) continue;
                 if (whole) {
                     put<Ta, D, true>(p, out_bf16, cc.b, cc.hk, cc.rb * S::kRows + row, c, x);

@@ -99,6 +99,24 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
         "r"(static_cast<uint32_t>(add)), "n"(kDescHi));
 }
 
+// Add the strays to the rows of a group, in out or in the part at `part`.  A call, for the size of the code around it.
+template <class S>
+__device__ __noinline__ void add_strays(const AttnParams& p, int b, int hk, int row0, int len, int rows, float* part) {
+    constexpr int D = S::D;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < rows * (D / 4); i += S::kThreads) {
+        const int row = i / (D / 4), c = i % (D / 4) * 4;
+        const float4 x = strays_of<bf16>(p, b, hk, len, row0 + row, c);
+        if (x.x == 0.f && x.y == 0.f && x.z == 0.f && x.w == 0.f) continue;
+        if (!part) {
+            put<bf16, D, true>(p, true, b, hk, row0 + row, c, x);
+        } else {
+            float4* const at = reinterpret_cast<float4*>(part + static_cast<size_t>(row) * D + c);
+            *at = make_float4(at->x + x.x, at->y + x.y, at->z + x.z, at->w + x.w);
+        }
+    }
+}
+
 template <class S>
 __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p) {
     constexpr int D = S::D, NR = S::NR, kUnits = S::kUnits;
@@ -505,15 +523,12 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                                 const float4 v = *reinterpret_cast<const float4*>(buf + (x + row) * kPitch + ch);
                                 y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
                             }
-                            if (sm.strays) {
-                                const float4 v = strays_of<bf16>(p, cc, row0 + row, h * CH + ch);
-                                y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
-                            }
                             if (whole) put<bf16, D>(p, true, cc.b, cc.hk, row0 + row, h * CH + ch, times(y, sm.f[row]));
                             else *reinterpret_cast<float4*>(sp.o + (static_cast<size_t>(part) * NR + row) * D + h * CH + ch) = y;
                         }
                         sync_computing<S>();
                     }
+                    if (sm.strays) add_strays<S>(p, cc.b, cc.hk, row0, cc.len, rows, whole ? nullptr : sp.o + static_cast<size_t>(part) * NR * D);
                     if (!whole) join_group<S>(p, true, sp, sh, cc, g_first, g_last, rows, buf, &sm.flag);
                 }
                 first_seg = false;
