@@ -10,17 +10,18 @@
 // Strays.  A key that a row does not see has the weight 0 in it, which keeps its value out only if that is finite.  Of the keys
 // that some rows of a block see and others do not -- the last K - 1 of a sequence -- the values are looked at before
 // the products; an infinite or NaN element is zeroed in shared memory, and added to the rows that see its key, from the
-// cache, at the group's end.  (Three tokens, 24 rows, 64 ragged sequences: 107.4 us, 105.5 without; looked at by the computing
+// cache, at the group's end.  (Three tokens, 24 rows, 64 ragged sequences: 107.7 us, 105.5 without; looked at by the computing
 // warps 111, whose registers do not suffice for it.  One token has no such keys and a kernel without all this.)
 //
-// What bounds it: the cache's bytes.  A bf16 key and value of head size d are 4 d bytes for 4 R d operations,
-// so up to about 64 rows (the tensor cores' mma.sync rate against the memory's) the stream is the time, and
-// the whole layout serves it:
+// What bounds it: the cache's bytes.  A bf16 key and value of head size d are 4 d bytes for 4 R d operations: the stream is the
+// time up to 16 rows (64 ragged sequences of 0.54 GB, heads of 256, floor 80 us: 8 rows 94 us, 16 rows 96); with more the
+// operands' way from shared memory to the products shows (24 rows 108, 32 rows 121).  The layout serves the stream:
 //   * one persistent CTA per SM; the keys of all (sequence, kv head, row block) groups, cut into tiles, are
 //     divided evenly over the CTAs whatever the lengths, from the lengths on the device (no host plan).  A group
 //     counts kGroupCost tiles more than it has, for its begin and end;
 //   * four producer warps issue cp.async (16 bytes a lane, zero fill for keys that are not there) into rings of 16 KB
-//     stages that fill 192 KB of shared memory, most of it in flight; the loads run across group borders.  They have
+//     stages (8 KB for bf16 heads of 64) that fill 192 KB of shared memory (160 or 128 KB beside the queries of many rows), most of
+//     it in flight; the loads run across group borders.  They have
 //     warps of their own because a warp stands still while the memory takes its requests: with the loads in the computing
 //     warps, those spent 175 of 305 us there (64 ragged sequences, 2.2 GB) and the two times added up;
 //   * the other warps are key groups x row groups: KG key groups each walk their own tiles with their own ring, so
@@ -76,7 +77,9 @@ struct Shape {
     static constexpr int kRing = kQBytes > 32768 ? 131072 : kQBytes > 16384 || kRows == 128 ? 163840 : 196608;
     static constexpr int kStages = kRing / kStageBytes / KG;           // of one key group
     static constexpr int kTile = KG * KT;                              // keys of a tile
-    // A group's begin and end, in tiles (64 KB each).  64 ragged sequences, heads of 256, 24 rows: 3 tiles 118 us, 5 tiles 108,
+    // A group's begin and end, in tiles.  A tile is KG stages: 64 KB where it was measured (KG = 4; bf16 heads of 64 32 KB); with the
+    // two and one key groups of many fp32 rows or fp32 results it is a half or a quarter of that, and so is the weight, not measured
+    // apart.  64 ragged sequences, heads of 256, 24 rows: 3 tiles 118 us, 5 tiles 108,
     // 8 tiles 106; heads of 128, 24 rows: 3 tiles 121, 8 tiles 132.  fp32, 16 sequences, 8 rows: heads of 64 1 tile 48.7,
     // 2 tiles 49.9, 5 tiles 56 (9 sequences in pages of 11: 15.8, 15.0, 16.4); of 128 1 tile 68, 2 and 3 tiles 64, 5 tiles 68; of
     // 256 2 tiles 119, 3 tiles 110, 5 tiles 102, 8 tiles 107.
@@ -790,7 +793,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             // apart and 0.11% in fp32 throughout; 64 sequences of up to 16,384 keys).  So a stage is summed by itself and then
             // added with a rounding that goes both ways, where the result is fp32, and where up to 8 rows make it free (heads of
             // 256, 64 ragged sequences, 91.1 us against 91.3).  bf16 results of more rows keep the one running sum, whose drift
-            // is a hundredth of their own rounding: 16 rows would take 94.8 us against 94.6 (heads of 64 118 against 114), 24
+            // is a hundredth of their own rounding: 16 rows took 94.8 us against 94.6 (heads of 64 118 against 114), 24
             // rows 110.8 against 105.6, 32 rows 144 against 124.
             constexpr bool kApart = S::PIECES == 3 || RG * NT == 1;
             constexpr int kMt = SUB == 1 && !kApart ? 4 : 2;   // as kKs above

@@ -1,6 +1,6 @@
 // gdn_attn_api.cu -- the C ABI of include/gdn_attn.h and include/gdn_norm.h:
 // argument validation and dispatch.  Host code only; the work is in
-// gdn_kv.cu, gdn_attn.cu and gdn_norm.cu.
+// gdn_kv.cu, gdn_attn.cuh (gdn_attn_bf16.cu, gdn_attn_f32.cu, gdn_attn_tc.cu) and gdn_norm.cu.
 #include "gdn_attn.h"
 
 #include <cuda_runtime.h>

@@ -2,8 +2,9 @@
 // on the 16-row side and 8 query rows a warp (16 where more would not fit the registers) on the other, so that the
 // few rows of a decode step fill the instruction; see gdn_attn.cuh.
 //
-// Measured, 64 ragged sequences of up to 8192 keys (0.54 GB), 16/2 heads of 256: 8 rows 94 us, 16 rows 96, 24 rows 106, 32 rows
-// 124; of up to 16384 keys, 24/4 heads (2.2 GB): 333 us (6.5 TB/s).  Eight rows a warp and more warps hide the
+// Measured, 64 ragged sequences of up to 8192 keys (0.54 GB), 16/2 heads of 256: 8 rows 94 us, 16 rows 96, 24 rows 108, 32 rows
+// 121; of up to 16384 keys, 24/4 heads (2.2 GB): 333 us (6.5 TB/s).  fp32 results, three parts a weight: 24 rows 125, 64 rows 278, 128
+// rows 576 (floors 81 to 85).  Eight rows a warp and more warps hide the
 // products' latencies better than 16 rows a warp, which read the keys and values from shared memory once for twice the
 // rows: 16 rows took 123 us that way against 103, 24 rows 131 against 117 (before the groups' cost was weighed as it is
 // now); at 32 rows the registers of 16 computing warps no longer suffice.

@@ -5,8 +5,9 @@
 // reduction over the lanes and the weights' way to them whether a query stands in it or not, and a second warp a scheduler
 // hides their latencies.  16 ragged sequences of up to 4096 keys, 8 kv heads, us (floors 21, 43, 86 for heads of 64,
 // 128, 256): up to 4 rows by one warp of 8 rows 63, 72, 115, of 4 rows 41, 53, 96, by two of 2 rows 36, 52; 5 to 8 rows
-// by one warp of 8 64, 73, 124, by two of 4 rows 52, 64, 112, with a group's cost at 3 tiles; as it is now up to 4 rows 35, 52, 94
-// (6.2 TB/s at heads of 256), 5 to 8 rows 50, 64, 102.  9 sequences, 2 tokens, up to 5001 keys, 6/3 heads of 64: 15.0 us (floor 5.2).
+// by one warp of 8 64, 73, 124, by two of 4 rows 52, 64, 112, with a group's cost at 3 tiles; as it is now up to 4 rows 35, 53, 94
+// (6.2 TB/s at heads of 256), 5 to 8 rows 50, 64, 102.  9 to 16 rows 80, 104, 171; 24 rows, heads of 64, 139; 24 rows, 2 kv heads of 256, up to
+// 8192 keys 164 (floor 43).  9 sequences, 2 tokens, up to 5001 keys, 6/3 heads of 64: 15.1 us (floor 5.2).
 #include "gdn_attn.cuh"
 
 namespace gdn {

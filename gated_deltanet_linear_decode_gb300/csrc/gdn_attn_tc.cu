@@ -14,9 +14,10 @@
 // its 128 KB take.  (With the keys or channels on the M side and R on the N side, a product of N = 32 took as long as one
 // of N = 128, and the softmax needed its maximum over lanes.)
 //
-// Measured, 64 ragged sequences of up to 8192 keys (0.54 GB), 16/2 heads of 256: 64 rows 174 us, 128 rows 275 us (252
-// TFLOP/s).  What bounds it: 128 rows the softmax (a thread's 128 keys a tile, 8,300 cycles); 64 rows a group's end,
-// 24,000 cycles twice a CTA, most of it the fetch of code that runs twice.
+// Measured, 64 ragged sequences of up to 8192 keys (0.54 GB, floor 82 us), 16/2 heads of 256: 64 rows 163 us, 128 rows 249 us (277
+// TFLOP/s); 64/8 heads of 64: 248 and 492.  What bounds it: 128 rows the softmax (a thread's 128 keys a tile, 8,300 cycles when they
+// were counted); 64 rows a group's end, much of it the fetch of code that runs about twice a CTA: 100 to 130 KB of it, and where it
+// was 160 to 190 KB all of these took 10 to 40% longer.
 // Roles, one persistent CTA per SM:
 //   warps 0-3   a thread a lane: S from tensor memory, weights e^(s - base) as two bf16 parts back into its place;
 //   warps 4-11  load: cp.async into a ring of 16 KB units, 128 keys x 64 channels each in the 128-byte swizzle
@@ -47,7 +48,7 @@ struct TcShape {
     static constexpr int kLoaders = 8;        // warps that load, 16 keys of a tile each
     static constexpr int kAll = 32 * (4 + kLoaders + 1);
     static constexpr int kTile = 128;         // keys
-    // at d = 256: 64 rows 2 tiles 204 us, 8 tiles 174, 16 tiles 187; 128 rows 8 tiles 288 us, 12 tiles 275
+    // at d = 256, with the larger code (above): 64 rows 2 tiles 204 us, 8 tiles 174, 16 tiles 187; 128 rows 8 tiles 288 us, 12 tiles 275
     static constexpr int kGroupCost = D == 256 ? (NR == 64 ? 8 : 12) : D == 128 ? 6 : 4;
     static constexpr int kCols = D / 64;      // units of a tile's keys, and of its values
     static constexpr int NV = D > 64 ? 128 : 64;   // channels of one product with V: two units side by side, or one
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_tc_kernel(const AttnParams p)
                     }
                 }
                 if ((cc.tile + 1) * 128 > cc.len - p.K + 1) {
-                    // Strays are taken out here and not by the loading warps, whose loop would grow: 64 rows 179 us against 188.  The
+                    // Strays are taken out here and not by the loading warps, whose loop would grow (64 rows 179 us against 188).  The
                     // values have landed when their barrier says so, and the issuing thread waits for all lanes before it uses them.
                     const int i = static_cast<int>(cc.at - seg_first), n = static_cast<int>(min(static_cast<long long>(cc.tiles - cc.tile + i), last - seg_first));
                     const int h = half0 + 2 * i + (i + 1 < n ? 2 : 1);   // the keys of the next tile come before these values, but for the last one's

@@ -309,7 +309,7 @@ cudaError_t launch_cluster(void (*kernel)(P), const P& p, int ctas, int threads,
 // lanes, apart: the partner's channels come by shuffle, as they lie in memory, and norm weight and rotation are
 // one pair of factors a channel, u' = r (u A + partner B), the same for all heads of the job.
 // Small CTAs, so that a finished warp's place is soon another's, and the registers of four head sets without spills.
-// Measured, heads of 256, 64 channels rotated: 8192 tokens of 24/4 heads (271 MB) 49.6 us, 5.5 TB/s; 64 tokens of 16/2 heads
+// Measured, heads of 256, 64 channels rotated: 8192 tokens of 24/4 heads (271 MB) 50.1 us, 5.4 TB/s (fp32 83.8, 6.5 TB/s); 64 tokens of 16/2 heads
 // 2.4 us.  8192 tokens by CTAs of 8 warps, four an SM 54.7 us; 4 warps, eight 52.5, nine 50.1, ten 49.7 (with spills; heads
 // of 64 39 us against 34); 2 warps, sixteen 52.1, eighteen 49.6; 1 warp 66.  By CTAs of 8 warps two and eight head sets a
 // job both 64 us.

@@ -18,7 +18,8 @@ namespace {
 // is held in registers between its passes: with 16-byte accesses (8 channels a thread and chunk) by a CTA, or
 // by 1 to 32 lanes of one where it has at most 256 channels (32768 rows of 256, bf16: 18 us against 34 by a CTA a row).
 // The fp32 weights come from L1 after the first row of an SM.  Measured: 8192 rows of 5120, fp32 stream, gate and scale
-// (587 MB): 96 us, 6.1 TB/s; 64 rows of 2048: 2.8 us, the latency of a launch, its loads and two sums.
+// (587 MB): 98 us, 6.0 TB/s; 64 rows of 2048: 2.7 us, the latency of a launch, its loads and two sums.  Rows off 16 bytes, one element
+// a thread at a time: 8192 of 5119 216 us (bf16 206).
 
 __device__ __forceinline__ float block_sum(float v, float* s) {
     v = warp_sum(v);
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(512, N <= 2 ? 2 : 1) norm_residual_kernel(Norm
         }
     }
     // A row waits for its sums twice, and the rows that fit an SM meanwhile do not keep the memory busy: the row that a later
-    // CTA will take is brought into L2 (8192 x 5120: 106.6 -> 95.7 us; 456 rows ahead 96.5, 1000 rows 106).
+    // CTA will take is brought into L2 (8192 x 5120, with a gate of fewer bits: 106.6 -> 95.7 us; 456 rows ahead 96.5, 1000 rows 106).
     if (!lanes && t + kAhead < p.T) {
 #pragma unroll
         for (int c = 0; c < N; ++c) {
