@@ -444,4 +444,7 @@ def gdn_prefill_chunked_static(dims: GdnDims, w: Weights, cu_seqlens_host, cu_se
 from . import _attn  # noqa: E402  (it needs the helpers above)
 from ._attn import *  # noqa: E402,F401,F403
 
-__all__ += _attn.__all__
+from . import _pages  # noqa: E402
+from ._pages import *  # noqa: E402,F401,F403
+
+__all__ += _attn.__all__ + _pages.__all__

@@ -1,4 +1,4 @@
-"""Bindings of include/gdn_attn.h and include/gdn_norm.h: the paged key-value cache of the
+"""Bindings of include/gdn_attn.h and include/gdn_norm.h (include/gdn_pages.h is in _pages): the paged key-value cache of the
 full-attention layers between the gated DeltaNet ones, the attention of new tokens over it, and the
 norms around a block.  Argument marshalling only, as in the package's __init__."""
 from __future__ import annotations
@@ -12,14 +12,15 @@ from . import GDN_BF16, GDN_FLAG_TEST_STALL, GdnError, _dt, _need, gdn_status_st
 
 __all__ = [
     "GdnAttnDims", "GdnKvCache", "GdnNormDims", "KvCache", "make_attn_dims", "make_norm_dims", "gdn_kv_extend",
-    "gdn_kv_truncate", "gdn_kv_append", "gdn_attn_decode_workspace_bytes", "gdn_attn_decode", "gdn_norm_residual",
+    "gdn_kv_truncate", "gdn_kv_append", "gdn_attn_decode_workspace_bytes", "gdn_attn_decode",
+    "gdn_attn_chunk_workspace_bytes", "gdn_attn_chunk", "gdn_norm_residual",
     "GDN_KV_REFUSED", "GDN_KV_BAD_INDEX", "EXPORTED_SYMBOLS_ATTN",
 ]
 
 GDN_KV_REFUSED, GDN_KV_BAD_INDEX = 32, 64   # dev_status bits
 
 EXPORTED_SYMBOLS_ATTN = ("gdn_kv_extend", "gdn_kv_truncate", "gdn_kv_append", "gdn_attn_decode_workspace_bytes",
-                         "gdn_attn_decode", "gdn_norm_residual")
+                         "gdn_attn_decode", "gdn_attn_chunk_workspace_bytes", "gdn_attn_chunk", "gdn_norm_residual")
 
 _I32 = torch.int32
 _F32 = torch.float32
@@ -58,6 +59,8 @@ def _fn(name: str):
             "gdn_kv_append": (ctypes.c_int, [D, C, I32, P, I64, P, I64, P, I64] + [P] * 6 + [I32, P, P, P]),
             "gdn_attn_decode_workspace_bytes": (SZ, [D, I32, I32]),
             "gdn_attn_decode": (ctypes.c_int, [D, C, I32, I32, I32, P, I64, P, I64, P, P, P, P, SZ, P, P]),
+            "gdn_attn_chunk_workspace_bytes": (SZ, [D, I32, I32]),
+            "gdn_attn_chunk": (ctypes.c_int, [D, C, I32, I32, I32, P, I64, P, I64, P, P, P, P, P, SZ, P, P]),
             "gdn_norm_residual": (ctypes.c_int, [N, I32, P, I64, P, I64, I32, P, P, P, P, P, P, P]),
         }
         for n, (res, args) in sig.items():
@@ -231,6 +234,30 @@ def gdn_attn_decode(dims: GdnAttnDims, cache: KvCache, K: int, q, block_table, s
         dims, c, B, K, P, xq, ldq, xg, ldg, _p(block_table, _I32, (B, P)), _p(seq_len, _I32, (B,)),
         _p(out, _BF16 if dims.out_dtype == GDN_BF16 else _F32, (T, n)), ws, ws_bytes, _opt(dev_status, _I32, (B,)),
         _stream(stream)))
+
+
+def gdn_attn_chunk_workspace_bytes(dims: GdnAttnDims, B: int = 1, T: int = 1) -> int:
+    return int(_fn("gdn_attn_chunk_workspace_bytes")(dims, B, T))
+
+
+def gdn_attn_chunk(dims: GdnAttnDims, cache: KvCache, q, cu_seqlens, block_table, seq_len, out, gate=None,
+                   workspace=None, dev_status=None, stream=None) -> None:
+    """Attention of the last cu_seqlens[b+1] - cu_seqlens[b] tokens of each sequence (packed rows of q, gate and
+    out, any number of them) over the cache; workspace: gdn_attn_chunk_workspace_bytes() bytes, zeroed once before
+    its first use."""
+    B, P = block_table.shape
+    T, n, a = q.shape[0], dims.H_q * dims.head_dim, _act(dims)
+    c = _cache(dims, cache)
+    xq, ldq = _rows(q, a, T, n)
+    xg, ldg = (None, 0) if gate is None else _rows(gate, a, T, n)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        _need(workspace)
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _done("gdn_attn_chunk", _fn("gdn_attn_chunk")(
+        dims, c, B, T, P, xq, ldq, xg, ldg, _p(cu_seqlens, _I32, (B + 1,)), _p(block_table, _I32, (B, P)),
+        _p(seq_len, _I32, (B,)), _p(out, _BF16 if dims.out_dtype == GDN_BF16 else _F32, (T, n)), ws, ws_bytes,
+        _opt(dev_status, _I32, (B,)), _stream(stream)))
 
 
 def gdn_norm_residual(dims: GdnNormDims, h, h_out=None, y=None, gate=None, post_w=None, chan_scale=None, pre_w=None,

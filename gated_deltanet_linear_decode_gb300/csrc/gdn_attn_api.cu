@@ -1,6 +1,6 @@
-// gdn_attn_api.cu -- the C ABI of include/gdn_attn.h and include/gdn_norm.h:
-// argument validation and dispatch.  Host code only; the work is in
-// gdn_kv.cu, gdn_attn.cuh (gdn_attn_bf16.cu, gdn_attn_f32.cu, gdn_attn_tc.cu) and gdn_norm.cu.
+// gdn_attn_api.cu -- the C ABI of include/gdn_attn.h, include/gdn_pages.h and
+// include/gdn_norm.h: argument validation and dispatch.  Host code only; the
+// work is in gdn_kv.cu, gdn_pages.cu, gdn_attn.cuh (gdn_attn_bf16.cu, gdn_attn_f32.cu, gdn_attn_tc.cu), gdn_chunk.cuh and gdn_norm.cu.
 #include "gdn_attn.h"
 
 #include <cuda_runtime.h>
@@ -9,9 +9,11 @@
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+#include <utility>
 
 #include "gdn_attn_internal.h"
 #include "gdn_norm.h"
+#include "gdn_pages.h"
 
 namespace {
 
@@ -20,6 +22,8 @@ constexpr int64_t kMaxSpan = int64_t{1} << 60;    // elements: more than any add
 
 // a * b where that is under kMaxSpan, else kMaxSpan (a, b >= 0).
 int64_t times(int64_t a, int64_t b) { return a != 0 && b > kMaxSpan / a ? kMaxSpan : a * b; }
+
+constexpr int64_t kMaxEntries = int64_t{1} << 30;   // of block tables that share pages, and of what is numbered with them
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -271,6 +275,146 @@ gdn_status gdn_attn_decode(const gdn_attn_dims* dims, const gdn_kv_cache* cache,
                       (dims->flags & GDN_FLAG_TEST_STALL) ? 1 : 0};
     return cuda_status(gdn::launch_attn_decode(p, dims->head_dim, dims->act_dtype, dims->out_dtype,
                                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t gdn_attn_chunk_workspace_bytes(const gdn_attn_dims* dims, int32_t B, int32_t T) {
+    if (check_attn_dims(dims) != GDN_OK || B < 1 || T < 1) return 0;
+    return gdn::chunk_workspace_bytes(dims->head_dim, dims->act_dtype, dims->out_dtype);
+}
+
+gdn_status gdn_attn_chunk(const gdn_attn_dims* dims, const gdn_kv_cache* cache, int32_t B, int32_t T,
+                          int32_t max_pages, const void* q, int64_t ldq, const void* gate, int64_t ldg,
+                          const int32_t* cu_seqlens, const int32_t* block_table, const int32_t* seq_len, void* out,
+                          void* workspace, size_t workspace_bytes, int32_t* dev_status, gdn_stream_t stream) {
+    gdn_status s = check_attn_dims(dims);
+    if (s != GDN_OK) return s;
+    gdn::KvCache kc;
+    size_t kv_bytes = 0;
+    if ((s = check_cache(dims, cache, &kc, &kv_bytes)) != GDN_OK) return s;
+    if (B < 0 || T < 0 || max_pages < 1) return GDN_E_INVALID_ARG;
+    if (static_cast<int64_t>(T) * dims->H_q > INT32_MAX) return GDN_E_INVALID_ARG;   // a row of the output has one index of 31 bits
+    if (B == 0 || T == 0) return GDN_OK;
+    if ((s = check_ptrs({q, cu_seqlens, block_table, seq_len, out}, {gate, workspace, dev_status})) != GDN_OK) return s;
+    const size_t es = elem_size(dims->act_dtype), eo = elem_size(dims->out_dtype);
+    const int64_t n = static_cast<int64_t>(dims->H_q) * dims->head_dim;
+    if (T == 1) ldq = ldg = n;   // one row's pitch is of no account
+    if ((s = check_pitch(ldq, n, es)) != GDN_OK) return s;
+    if (gate && (s = check_pitch(ldg, n, es)) != GDN_OK) return s;
+    const size_t need = gdn_attn_chunk_workspace_bytes(dims, B, T);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_E_WORKSPACE;
+    const size_t nb = static_cast<size_t>(B) * 4;
+    if (any_overlap({{out, rows_bytes(T, n, n, eo)}, {workspace, need}, {dev_status, nb}},
+                    {{kc.k, kv_bytes}, {kc.v, kv_bytes}, {q, rows_bytes(T, n, ldq, es)},
+                     {gate, rows_bytes(T, n, ldg, es)}, {cu_seqlens, nb + 4}, {block_table, nb * max_pages},
+                     {seq_len, nb}}))
+        return GDN_E_INVALID_ARG;
+    gdn::ChunkParams p{kc, B, T, dims->H_q, dims->H_kv, dims->H_q / dims->H_kv, max_pages, dims->scale, q, gate, ldq, ldg,
+                       block_table, seq_len, cu_seqlens, out, workspace, dev_status,
+                       (dims->flags & GDN_FLAG_TEST_STALL) ? 1 : 0};
+    return cuda_status(gdn::launch_attn_chunk(p, dims->head_dim, dims->act_dtype, dims->out_dtype,
+                                              reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_kv_fork(int32_t page_size, int32_t num_pages, int32_t B, int32_t max_pages, int32_t N,
+                       const int32_t* src, const int32_t* dst, const int32_t* len, int32_t* seq_len,
+                       int32_t* n_pages, int32_t* block_table, int32_t* page_refs, const int32_t* free_list,
+                       int32_t* free_count, int32_t* copy_src, int32_t* copy_dst, int32_t* dev_status,
+                       gdn_stream_t stream) {
+    gdn_status s = check_kv_sizes(page_size, num_pages, B, max_pages);
+    if (s != GDN_OK) return s;
+    if (N < 0) return GDN_E_INVALID_ARG;
+    if (N > GDN_KV_MAX_SEQ || static_cast<int64_t>(B) * max_pages > kMaxEntries) return GDN_E_UNSUPPORTED;
+    if (N == 0) return GDN_OK;
+    if ((s = check_ptrs({src, dst, len, page_refs, free_list, free_count, copy_src, copy_dst}, {dev_status})) != GDN_OK)
+        return s;
+    if (B > 0 && (s = check_ptrs({seq_len, n_pages, block_table}, {})) != GDN_OK) return s;
+    const size_t nb = static_cast<size_t>(B) * 4, nn = static_cast<size_t>(N) * 4, np = static_cast<size_t>(num_pages) * 4;
+    if (any_overlap({{seq_len, nb}, {n_pages, nb}, {block_table, nb * max_pages}, {page_refs, np}, {free_count, 4},
+                     {copy_src, nn}, {copy_dst, nn}, {dev_status, nn}},
+                    {{src, nn}, {dst, nn}, {len, nn}, {free_list, np}}))
+        return GDN_E_INVALID_ARG;
+    gdn::KvForkParams p{page_size, num_pages, B, max_pages, N, src, dst, len, seq_len, n_pages, block_table, page_refs,
+                        free_list, free_count, copy_src, copy_dst, dev_status};
+    return cuda_status(gdn::launch_kv_fork(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_kv_release(int32_t page_size, int32_t num_pages, int32_t B, int32_t max_pages,
+                          const int32_t* new_len, int32_t* seq_len, int32_t* n_pages, int32_t* block_table,
+                          int32_t* page_refs, int32_t* free_list, int32_t* free_count, int32_t* copy_src,
+                          int32_t* copy_dst, int32_t* dev_status, gdn_stream_t stream) {
+    gdn_status s = check_kv_sizes(page_size, num_pages, B, max_pages);
+    if (s != GDN_OK) return s;
+    if (static_cast<int64_t>(B) * max_pages > kMaxEntries) return GDN_E_UNSUPPORTED;
+    if (B == 0) return GDN_OK;
+    if ((s = check_ptrs({new_len, seq_len, n_pages, block_table, page_refs, free_list, free_count, copy_src, copy_dst},
+                        {dev_status})) != GDN_OK)
+        return s;
+    const size_t nb = static_cast<size_t>(B) * 4, np = static_cast<size_t>(num_pages) * 4;
+    if (any_overlap({{seq_len, nb}, {n_pages, nb}, {block_table, nb * max_pages}, {page_refs, np}, {free_list, np},
+                     {free_count, 4}, {copy_src, nb}, {copy_dst, nb}, {dev_status, nb}},
+                    {{new_len, nb}}))
+        return GDN_E_INVALID_ARG;
+    gdn::KvReleaseParams p{page_size, num_pages, B, max_pages, new_len, seq_len, n_pages, block_table, page_refs,
+                           free_list, free_count, copy_src, copy_dst, dev_status};
+    return cuda_status(gdn::launch_kv_release(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_kv_compact(int32_t num_pages, int32_t B, int32_t max_pages, const int32_t* n_pages,
+                          const int32_t* block_table, int32_t* block_table_out, int32_t* page_refs,
+                          int32_t* free_list, int32_t* free_count, int32_t* page_map, int32_t n_copy_max,
+                          int32_t* copy_src, int32_t* copy_dst, int32_t* n_copy, int32_t* dev_status,
+                          gdn_stream_t stream) {
+    gdn_status s = check_kv_sizes(1, num_pages, B, max_pages);
+    if (s != GDN_OK) return s;
+    if (n_copy_max < num_pages / 2) return GDN_E_INVALID_ARG;
+    if (num_pages > kMaxEntries || n_copy_max > kMaxEntries || static_cast<int64_t>(B) * max_pages > kMaxEntries)
+        return GDN_E_UNSUPPORTED;
+    if ((s = check_ptrs({page_refs, free_list, free_count, page_map, n_copy}, {dev_status})) != GDN_OK) return s;
+    if (n_copy_max > 0 && (s = check_ptrs({copy_src, copy_dst}, {})) != GDN_OK) return s;
+    if (B > 0 && (s = check_ptrs({n_pages, block_table, block_table_out}, {})) != GDN_OK) return s;
+    const size_t nb = static_cast<size_t>(B) * 4, np = static_cast<size_t>(num_pages) * 4;
+    const size_t nc = static_cast<size_t>(n_copy_max) * 4;
+    if (partly(block_table_out, block_table, nb * max_pages)) return GDN_E_INVALID_ARG;
+    const Range table{block_table_out == block_table ? nullptr : block_table, nb * max_pages};
+    if (any_overlap({{block_table_out, nb * max_pages}, {page_refs, np}, {free_list, np}, {free_count, 4}, {page_map, np},
+                     {copy_src, nc}, {copy_dst, nc}, {n_copy, 4}, {dev_status, nb}},
+                    {{n_pages, nb}, table}))
+        return GDN_E_INVALID_ARG;
+    gdn::KvCompactParams p{num_pages, B, max_pages, n_pages, block_table, block_table_out, page_refs, free_list, free_count,
+                           page_map, n_copy_max, copy_src, copy_dst, n_copy, dev_status};
+    return cuda_status(gdn::launch_kv_compact(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+gdn_status gdn_kv_copy_pages(const gdn_attn_dims* dims, const gdn_kv_cache* cache, int32_t n,
+                             const int32_t* copy_src, const int32_t* copy_dst, int32_t* dev_status,
+                             gdn_stream_t stream) {
+    gdn_status s = check_attn_dims(dims);
+    if (s != GDN_OK) return s;
+    gdn::KvCache kc;
+    size_t kv_bytes = 0;
+    if ((s = check_cache(dims, cache, &kc, &kv_bytes)) != GDN_OK) return s;
+    if (n < 0) return GDN_E_INVALID_ARG;
+    if (n == 0) return GDN_OK;
+    if ((s = check_ptrs({copy_src, copy_dst}, {dev_status})) != GDN_OK) return s;
+    const size_t nn = static_cast<size_t>(n) * 4;
+    const Range a{copy_src, nn}, b{copy_dst, nn}, st{dev_status, 4};
+    // (the two halves of a cache may lie inside one another: check_cache)
+    if (any_overlap({{kc.k, kv_bytes}, st}, {a, b}) || any_overlap({{kc.v, kv_bytes}, st}, {a, b})) return GDN_E_INVALID_ARG;
+    const int64_t vec = 16 / static_cast<int64_t>(elem_size(dims->act_dtype));
+    const int64_t vectors = times(times(kc.page_size, dims->H_kv), dims->head_dim / vec);
+    if (vectors > kMaxEntries) return GDN_E_UNSUPPORTED;
+    // rows of consecutive vectors, the smaller stride inside; dimensions that follow on one another are one
+    Dim in{dims->H_kv, kc.head_stride / vec}, out{kc.page_size, kc.token_stride / vec};
+    if (out.n > 1 && (in.n == 1 || out.stride < in.stride)) std::swap(in, out);
+    int64_t run = dims->head_dim / vec;
+    for (int i = 0; i < 2 && (in.n == 1 || in.stride == run); ++i) {
+        run *= in.n;
+        in = out;
+        out = Dim{1, 0};
+    }
+    gdn::KvCopyParams p{kc, n, copy_src, copy_dst, dev_status, static_cast<int>(vectors), static_cast<int>(run),
+                        static_cast<int>(in.n), 0, kc.page_stride / vec, in.stride, out.stride};
+    return cuda_status(gdn::launch_kv_copy(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 gdn_status gdn_norm_residual(const gdn_norm_dims* dims, int32_t T, const void* y, int64_t ldy, const void* gate,

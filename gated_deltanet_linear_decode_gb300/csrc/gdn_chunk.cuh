@@ -1,0 +1,133 @@
+// gdn_chunk.cuh -- what the kernels of gdn_attn_chunk (include/gdn_attn.h) share: the sequences and a worker's share of the
+// work (gdn_chunk_plan.h), results, and the join of units that several workers hold parts of.
+//
+// Mathematics, as in gdn_attn.cuh: over any set of keys a row has m = max s, l = sum 2^(s-m), o = sum 2^(s-m) v with scores in
+// base 2 (s log2 e); two sets join as m = max(m1, m2), l = l1 2^(m1-m) + l2 2^(m2-m), o likewise, and o / l is the result
+// once.  A row that sees no key has m = -inf, l = 0 and the result 0.
+#pragma once
+
+#include "gdn_attn.cuh"
+#include "gdn_chunk_plan.h"
+
+namespace gdn {
+namespace chunk {
+
+using attn::kLog2e;
+
+constexpr int kMaxWorkers = 512;
+constexpr size_t kCounterBytes = 2 * kMaxWorkers * 4;   // at the start of the workspace: by the worker of a unit's first part, two each
+
+__device__ __forceinline__ bool rows_ok(const ChunkParams& p, int a, int z) { return a >= 0 && a <= z && z <= p.T; }
+
+// Keys that a sequence can have: what its row of the table names, and few enough that a tile past them still has a number of 31 bits.
+__device__ __forceinline__ long long most_keys(const ChunkParams& p) {
+    return least(static_cast<long long>(p.max_pages) * p.cache.page_size, INT32_MAX - 4096);
+}
+
+__device__ __forceinline__ Rows rows_of(const ChunkParams& p, int b) {
+    const int a = p.cu_seqlens[b], z = p.cu_seqlens[b + 1];
+    Rows r{a, 0, static_cast<int>(least(most(p.seq_len[b], 0), most_keys(p)))};
+    if (rows_ok(p, a, z)) r.n = z - a;
+    return r;
+}
+
+// What only the device sees of sequence b's arguments.
+__device__ __forceinline__ void report_rows(const ChunkParams& p, int b) {
+    if (!rows_ok(p, p.cu_seqlens[b], p.cu_seqlens[b + 1]) || p.seq_len[b] > most_keys(p)) atomicOr(p.status + b, kKvBadIndex);
+}
+
+struct PlanSmem {
+    long long sums[32], start;   // by warp
+    int start_b;
+};
+
+// This worker's share and its first part; false if it has none.  All threads of a CTA call it.
+__device__ __forceinline__ bool my_share(const ChunkParams& p, const Line& ln, int worker, int workers, int min_share, PlanSmem& sm, Share& sh, Part& c) {
+    grid_dependency_wait();   // launched as a programmatic dependent: nothing global is touched before the previous kernel is done
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = static_cast<int>(blockDim.x);
+    const int per = (p.B + threads - 1) / threads;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        mine += p.Hkv * ln.head(rows_of(p, b));
+        if (worker == 0 && p.status) report_rows(p, b);
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sm.sums[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+    for (int w = 0; w < threads / 32; ++w) {
+        if (w < warp) before += sm.sums[w];
+        total += sm.sums[w];
+    }
+    before += incl - mine;
+    const int n = total > 0 ? workers_of(total, workers, min_share) : 0;
+    if (worker >= n) return false;
+    sh = Share::of(total, n, worker);
+    if (sh.first >= before && sh.first < before + mine) {   // one thread: its sequences hold the first number
+        long long at = before;
+        int b = b0;
+        for (; b < b1 - 1; ++b) {
+            const long long h = p.Hkv * ln.head(rows_of(p, b));
+            if (sh.first < at + h) break;
+            at += h;
+        }
+        sm.start_b = b;
+        sm.start = at;
+    }
+    __syncthreads();
+    grid_launch_dependents();
+    c.b = sm.start_b;
+    c.r = rows_of(p, c.b);
+    return first_part(ln, sh, p.B, p.Hkv, sm.start, c, [&](int b) { return rows_of(p, b); });
+}
+
+// Rows of a unit, and of row r its token (of the unit) and query head.
+__device__ __forceinline__ int tokens_of(const Line& ln, const Part& c) {
+    return static_cast<int>(least(ln.tokens, c.r.n - static_cast<long long>(c.i) * ln.tokens));
+}
+
+// A row's channels ch..ch+3 of the result, gated.
+template <typename Ta, int D, bool add = false>
+__device__ __forceinline__ void put(const ChunkParams& p, bool out_bf16, long long t, int h, int ch, float4 y) {
+    if (p.gate) {
+        const float4 g = StateIO<Ta>::ld(static_cast<const Ta*>(p.gate) + t * p.ldg + static_cast<long long>(h) * D + ch);
+        y.x *= gate_of(g.x);
+        y.y *= gate_of(g.y);
+        y.z *= gate_of(g.z);
+        y.w *= gate_of(g.w);
+    }
+    const long long at = (t * p.Hq + h) * D + ch;
+    if (add) {
+        const float4 x = out_bf16 ? StateIO<__nv_bfloat16>::ld(static_cast<const __nv_bfloat16*>(p.out) + at)
+                                  : StateIO<float>::ld(static_cast<const float*>(p.out) + at);
+        y = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    }
+    if (out_bf16) StateIO<__nv_bfloat16>::st(static_cast<__nv_bfloat16*>(p.out) + at, y);
+    else StateIO<float>::st(static_cast<float*>(p.out) + at, y);
+}
+
+// Parts of split units: two places a worker, 2 w for one that goes on from the worker before, 2 w + 1 for one that begins here.
+template <int RT, int D>
+struct Parts {
+    int* counters;
+    float* o;      // [2 workers][RT][D]
+    float2* ml;    // [2 workers][RT]
+    __device__ __forceinline__ Parts(void* workspace, int workers)
+        : counters(static_cast<int*>(workspace)),
+          o(reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes)),
+          ml(reinterpret_cast<float2*>(o + static_cast<size_t>(2) * workers * RT * D)) {}
+    __device__ __forceinline__ static size_t place(int worker, const Part& c) { return 2 * static_cast<size_t>(worker) + (c.t0 == 0); }
+};
+template <int RT, int D>
+constexpr size_t parts_bytes(int workers) {
+    return kCounterBytes + static_cast<size_t>(2) * workers * RT * (D * 4 + 8);
+}
+
+}  // namespace chunk
+}  // namespace gdn

@@ -1,0 +1,125 @@
+// gdn_chunk_plan.h -- how gdn_attn_chunk's work is divided.  Host and device code.
+//
+// A unit is up to `tokens` consecutive new tokens of one sequence with one kv head's G query heads: tokens * G rows that share
+// their keys, and see them up to their last token's.  Units are numbered by sequence, kv head, place in the sequence, and lie
+// one after another on a line: a unit takes `cost` numbers for its begin and end, then one for every key that it sees.  The
+// line is divided evenly over the workers; a tile of a unit belongs to the worker in whose share its first key's number lies,
+// and a unit without keys to the one that has its first number.  (Numbers are keys, not tiles, because then what the first u
+// units of a sequence take is a sum in closed form, and a worker finds its first unit by bisection.)
+#pragma once
+
+#ifdef __CUDACC__
+#define GDN_HD __host__ __device__ __forceinline__
+#else
+#define GDN_HD inline
+#endif
+
+namespace gdn {
+namespace chunk {
+
+GDN_HD long long least(long long a, long long b) { return a < b ? a : b; }
+GDN_HD long long most(long long a, long long b) { return a > b ? a : b; }
+// a / b rounded down, with the short division where it will do (a, b >= 0).
+GDN_HD long long quot(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
+}
+
+// The new tokens of one sequence: n rows from row0 on, the last n of its len tokens (len may be less than n).
+struct Rows {
+    int row0, n, len;
+};
+
+struct Line {
+    int tokens, keys, cost;   // tokens of a unit, keys of a tile, numbers for a unit's begin and end
+
+    GDN_HD int units(const Rows& r) const { return static_cast<int>((static_cast<long long>(r.n) + tokens - 1) / tokens); }
+    // keys that unit i sees
+    GDN_HD int seen(const Rows& r, int i) const {
+        const long long s = least((i + 1ll) * tokens, r.n) + r.len - r.n;
+        return s > 0 ? static_cast<int>(s) : 0;
+    }
+    // numbers of units 0..u-1 (u up to units(r))
+    GDN_HD long long before(const Rows& r, int u) const {
+        const int nt = units(r);
+        const long long m = least(u, nt - 1), off = static_cast<long long>(r.len) - r.n;   // units that are full
+        long long sum = static_cast<long long>(u) * cost;
+        const long long i0 = off >= 0 ? 0 : least(m, quot(-off, tokens));   // those before see nothing
+        if (i0 < m) sum += (m - i0) * off + tokens * (m * (m + 1) / 2 - i0 * (i0 + 1) / 2);
+        if (u == nt && nt > 0) sum += most(r.len, 0);
+        return sum;
+    }
+    GDN_HD long long head(const Rows& r) const { return r.n > 0 ? before(r, units(r)) : 0; }
+};
+
+// Worker w's share of `total` numbers among `workers`: [first, last).
+struct Share {
+    long long first, last, total;
+    int workers;
+    GDN_HD static Share of(long long total, int workers, int w) {
+        return Share{quot(total * w, workers), quot(total * (w + 1), workers), total, workers};
+    }
+    // the worker that has number x
+    GDN_HD int owner(long long x) const { return static_cast<int>(quot((x + 1) * workers - 1, total)); }
+};
+// Workers that take part: shares of less than `tile` keys would leave some of them without one.
+GDN_HD int workers_of(long long total, int workers, int min_share) { return static_cast<int>(most(1, least(workers, quot(total, min_share)))); }
+
+// A worker's part of a unit: tiles [t0, t1) of `tiles`.
+struct Part {
+    Rows r;
+    int b, hk, i, tiles, t0, t1;
+    long long at;   // the unit's first number
+
+    GDN_HD bool whole() const { return t0 == 0 && t1 == tiles; }
+};
+
+GDN_HD int tiles_of(int seen, int keys) { return static_cast<int>((static_cast<long long>(seen) + keys - 1) / keys); }
+
+// The tiles of the unit that the share holds; false if there is nothing of it.
+GDN_HD bool clip(const Line& ln, const Share& sh, Part& c) {
+    c.tiles = tiles_of(ln.seen(c.r, c.i), ln.keys);
+    const long long base = c.at + ln.cost;   // the first tile's number
+    c.t0 = sh.first > base ? static_cast<int>(least(c.tiles, quot(sh.first - base + ln.keys - 1, ln.keys))) : 0;
+    c.t1 = sh.last > base ? static_cast<int>(least(c.tiles, quot(sh.last - base + ln.keys - 1, ln.keys))) : 0;
+    return c.tiles > 0 ? c.t0 < c.t1 : c.at >= sh.first && c.at < sh.last;
+}
+
+// On to the next unit with something in the share; false at the share's end.  rows(b): the Rows of sequence b.
+template <class F>
+GDN_HD bool next_part(const Line& ln, const Share& sh, int B, int Hkv, Part& c, F rows) {
+    for (;;) {
+        c.at += ln.cost + ln.seen(c.r, c.i);
+        if (c.at >= sh.last) return false;
+        if (++c.i == ln.units(c.r)) {
+            c.i = 0;
+            if (++c.hk == Hkv) {
+                c.hk = 0;
+                do {
+                    if (++c.b >= B) return false;
+                    c.r = rows(c.b);
+                } while (c.r.n == 0);
+            }
+        }
+        if (clip(ln, sh, c)) return true;
+    }
+}
+
+// The first of them; c.b, c.r are the sequence that has number sh.first, `start` the number where it begins.
+template <class F>
+GDN_HD bool first_part(const Line& ln, const Share& sh, int B, int Hkv, long long start, Part& c, F rows) {
+    const long long head = ln.head(c.r), in = sh.first - start;
+    c.hk = static_cast<int>(quot(in, head));
+    const long long x = in - c.hk * head;
+    int lo = 0, hi = ln.units(c.r);   // the last unit with before(unit) <= x
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (ln.before(c.r, mid) <= x) lo = mid;
+        else hi = mid;
+    }
+    c.i = lo;
+    c.at = sh.first - x + ln.before(c.r, lo);
+    return clip(ln, sh, c) || next_part(ln, sh, B, Hkv, c, rows);
+}
+
+}  // namespace chunk
+}  // namespace gdn

@@ -8,6 +8,13 @@
 
 namespace gdn {
 
+// SMs of the current device; 0 where there is none.
+inline int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return sms;
+}
+
 // cluster > 1: thread-block clusters of that many CTAs.
 template <typename... P, typename... A>
 cudaError_t launch_dependent_cluster(void (*kernel)(P...), int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {

@@ -1,0 +1,499 @@
+// gdn_pages.cu -- pages that sequences share (include/gdn_pages.h): fork, release, compaction, and the copies of pages.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <limits.h>
+
+#include "gdn.h"
+#include "gdn_attn_internal.h"
+#include "gdn_books.cuh"
+#include "gdn_common.cuh"
+#include "gdn_launch.h"
+
+namespace gdn {
+
+namespace {
+
+// The bookkeeping: whole numbers, a few words a sequence and a page entry.  As in gdn_kv.cu one cluster of CTAs, each of which
+// scans all sequences for itself into prefix sums in shared memory; then the page entries -- not the sequences -- are spread
+// over the cluster's threads.  Inputs are outputs: what the scan reads is written behind a cluster barrier.
+constexpr int kBookThreads = 1024;
+constexpr int kManyEntries = 4096;   // pages of a cache above which 8 CTAs take part
+
+__device__ __forceinline__ bool page_ok(int page, int num_pages) { return page >= 0 && page < num_pages; }
+// Words that other CTAs of the cluster change: past L1, which keeps what it has read.
+__device__ __forceinline__ int ld_l2(const int* p) { return __ldcg(p); }
+__device__ __forceinline__ int ld_dsmem_int(const int* local, uint32_t rank) {
+    return __float_as_int(ld_dsmem_f32(reinterpret_cast<const float*>(local), rank));
+}
+__device__ __forceinline__ int cluster_thread() { return static_cast<int>(cluster_ctarank() * blockDim.x + threadIdx.x); }
+__device__ __forceinline__ int cluster_threads() { return static_cast<int>(cluster_ctas() * blockDim.x); }
+
+// ---------------------------------------------------------------- fork
+struct ForkAsk {
+    int dst, full, part;
+    bool ok;   // by itself
+};
+
+__device__ __forceinline__ ForkAsk fork_ask(const KvForkParams& p, int i) {
+    ForkAsk a{-1, 0, 0, false};
+    const int s = p.src[i], d = p.dst[i], n = p.len[i];
+    if (s < 0 || s >= p.B || d < 0 || d >= p.B || s == d || n < 0 || n > p.seq_len[s]) return a;
+    const int held = p.n_pages[s];
+    a.dst = d;
+    a.full = n / p.page_size;
+    a.part = n - a.full * p.page_size > 0;
+    a.ok = held <= p.max_pages && a.full + a.part <= held && p.seq_len[d] == 0 && p.n_pages[d] == 0;
+    return a;
+}
+
+constexpr int kForkRun = 128;   // entries that a warp takes at a time
+
+__global__ void __launch_bounds__(kBookThreads) kv_fork_kernel(const KvForkParams p) {
+    extern __shared__ int smem[];
+    int* const first_s = smem;             // [B] the fork that a sequence is the dst of
+    int* const run_s = first_s + p.B;      // [N + 1] runs of entries before each fork
+    int* const page_s = run_s + p.N + 1;   // [N + 1] pages served before it
+    __shared__ Pair sums[33];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) first_s[b] = INT_MAX;
+    __syncthreads();
+    const int per = (p.N + blockDim.x - 1) / blockDim.x;
+    const int i0 = min(p.N, static_cast<int>(threadIdx.x) * per), i1 = min(p.N, i0 + per);
+    for (int i = i0; i < i1; ++i) {
+        const ForkAsk a = fork_ask(p, i);
+        if (a.ok) atomicMin(first_s + a.dst, i);
+    }
+    __syncthreads();
+    const int free_n = min(max(*p.free_count, 0), p.num_pages);
+    Pair ask{0, 0}, got{0, 0}, total;
+    for (int i = i0; i < i1; ++i) {
+        const ForkAsk a = fork_ask(p, i);
+        if (a.ok && first_s[a.dst] == i) ask.pages += a.part;
+    }
+    // what is served of the asked pages is a prefix of them
+    auto serve = [&](Pair at, auto&& f) {
+        for (int i = i0; i < i1; ++i) {
+            ForkAsk a = fork_ask(p, i);
+            a.ok = a.ok && first_s[a.dst] == i;
+            const int want = a.ok ? a.part : 0;
+            a.ok = a.ok && (want == 0 || at.pages + want <= free_n);
+            at.pages += want;
+            f(i, a);
+        }
+    };
+    const Pair asked = block_prefix(ask, sums, &total);
+    serve(asked, [&](int, const ForkAsk& a) {
+        got.rows += a.ok ? (a.full + kForkRun - 1) / kForkRun : 0;
+        got.pages += a.ok ? a.part : 0;
+    });
+    Pair at = block_prefix(got, sums, &total);
+    const bool first_cta = cluster_ctarank() == 0;
+    serve(asked, [&](int i, const ForkAsk& a) {
+        run_s[i] = static_cast<int>(at.rows);
+        page_s[i] = static_cast<int>(at.pages);
+        at.rows += a.ok ? (a.full + kForkRun - 1) / kForkRun : 0;
+        at.pages += a.ok ? a.part : 0;
+        if (!a.ok) {
+            // (only this fork can be the first of its dst, so nobody else looks at the word)
+            if (a.dst >= 0 && first_s[a.dst] == i) first_s[a.dst] = INT_MAX;
+            if (first_cta && p.status) atomicOr(p.status + i, kKvRefused);
+        }
+    });
+    if (threadIdx.x == 0) {
+        run_s[p.N] = static_cast<int>(total.rows);
+        page_s[p.N] = static_cast<int>(total.pages);
+    }
+    __syncthreads();
+    auto served = [&](int i) {
+        const int d = p.dst[i];
+        return d >= 0 && d < p.B && first_s[d] == i;
+    };
+    const int runs = run_s[p.N], pages = page_s[p.N], lane = threadIdx.x & 31;
+    for (int c = cluster_thread() >> 5; c < runs; c += cluster_threads() >> 5) {
+        const int i = find(run_s, p.N, c), full = p.len[i] / p.page_size, col0 = (c - run_s[i]) * kForkRun;
+        const int* const from = p.block_table + static_cast<size_t>(p.src[i]) * p.max_pages;
+        int* const to = p.block_table + static_cast<size_t>(p.dst[i]) * p.max_pages;
+        int page[kForkRun / 32];
+#pragma unroll
+        for (int k = 0; k < kForkRun / 32; ++k) {
+            const int col = col0 + k * 32 + lane;
+            page[k] = col < full ? from[col] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kForkRun / 32; ++k) {
+            const int col = col0 + k * 32 + lane;
+            if (col >= full) continue;
+            to[col] = page[k];
+            if (page_ok(page[k], p.num_pages)) atomicAdd(p.page_refs + page[k], 1);
+            else if (p.status) atomicOr(p.status + i, kKvBadIndex);
+        }
+    }
+    for (int i = cluster_thread(); i < p.N; i += cluster_threads()) {
+        int a = -1, b = -1;
+        if (served(i) && page_s[i + 1] > page_s[i]) {
+            const int full = p.len[i] / p.page_size;
+            a = p.block_table[static_cast<size_t>(p.src[i]) * p.max_pages + full];
+            b = p.free_list[free_n - 1 - page_s[i]];
+            p.block_table[static_cast<size_t>(p.dst[i]) * p.max_pages + full] = b;
+            if (!page_ok(a, p.num_pages) || !page_ok(b, p.num_pages)) {
+                a = b = -1;
+                if (p.status) atomicOr(p.status + i, kKvBadIndex);
+            }
+        }
+        p.copy_src[i] = a;
+        p.copy_dst[i] = b;
+    }
+    cluster_sync_all();
+    if (!first_cta) return;
+    for (int i = threadIdx.x; i < p.N; i += blockDim.x) {
+        if (!served(i)) continue;
+        const int n = p.len[i], d = p.dst[i];
+        p.seq_len[d] = n;
+        p.n_pages[d] = n / p.page_size + (page_s[i + 1] - page_s[i]);
+    }
+    if (threadIdx.x == 0) *p.free_count = free_n - pages;
+}
+
+// ---------------------------------------------------------------- release
+// A sequence gives up its entries from..held-1 (the first of them the kept one that a copy replaces, if `copy`).
+struct ReleaseAsk {
+    int from, held, stay;
+    bool ok, copy;
+};
+
+__device__ __forceinline__ ReleaseAsk release_ask(const KvReleaseParams& p, int b) {
+    ReleaseAsk r{0, p.n_pages[b], 0, false, false};
+    const int n = p.new_len[b];
+    r.stay = r.from = r.held;
+    r.ok = n >= 0 && n <= p.seq_len[b] && r.held >= 0 && r.held <= p.max_pages;
+    if (!r.ok) return r;
+    const int need = n / p.page_size + (n % p.page_size > 0);
+    r.stay = r.from = min(need, r.held);
+    if (n % p.page_size > 0 && need <= r.held) {
+        const int page = p.block_table[static_cast<size_t>(b) * p.max_pages + need - 1];
+        r.copy = page_ok(page, p.num_pages) && p.page_refs[page] > 0;
+        r.from -= r.copy;
+    }
+    return r;
+}
+
+// Which of a page's holders gives it back?  Phase by phase, a cluster barrier between them: every entry given up takes one from
+// its page's count; where that is below zero, the entries put in their numbers (INT_MIN + number, the least stays); the
+// entry that finds its own there is the one.  So the count itself is all the scratch, and the result the same in any order.
+__global__ void __launch_bounds__(kBookThreads) kv_release_kernel(const KvReleaseParams p) {
+    extern __shared__ int smem[];
+    int* const drop_s = smem;               // [B + 1] entries given up before each sequence
+    int* const copy_s = drop_s + p.B + 1;   // [B + 1] copies before it
+    int* const from_s = copy_s + p.B + 1;   // [B] its first entry given up; -1 - that where it is refused
+    __shared__ Pair sums[33];
+    __shared__ int mine_s;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int per = (p.B + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+    const int free_n = min(max(*p.free_count, 0), p.num_pages);
+    Pair ask{0, 0}, got{0, 0}, total;
+    for (int b = b0; b < b1; ++b) ask.pages += release_ask(p, b).copy;
+    Pair asked = block_prefix(ask, sums, &total);
+    const bool first_cta = cluster_ctarank() == 0;
+    auto serve = [&](Pair at, auto&& f) {
+        for (int b = b0; b < b1; ++b) {
+            const ReleaseAsk r = release_ask(p, b);
+            const bool ok = r.ok && (!r.copy || at.pages + 1 <= free_n);
+            at.pages += r.copy;
+            f(b, r, ok);
+        }
+    };
+    serve(asked, [&](int, const ReleaseAsk& r, bool ok) {
+        got.rows += ok ? r.held - r.from : 0;
+        got.pages += ok && r.copy;
+    });
+    Pair at = block_prefix(got, sums, &total);
+    serve(asked, [&](int b, const ReleaseAsk& r, bool ok) {
+        drop_s[b] = static_cast<int>(at.rows);
+        copy_s[b] = static_cast<int>(at.pages);
+        from_s[b] = ok ? r.from : -1 - r.from;
+        at.rows += ok ? r.held - r.from : 0;
+        at.pages += ok && r.copy;
+        if (!ok && first_cta && p.status) atomicOr(p.status + b, kKvRefused);
+    });
+    if (threadIdx.x == 0) {
+        drop_s[p.B] = static_cast<int>(total.rows);
+        copy_s[p.B] = static_cast<int>(total.pages);
+    }
+    cluster_sync_all();   // all have read the counts
+    const int drops = drop_s[p.B], copies = copy_s[p.B], all = cluster_threads();
+    // this thread's entries: consecutive ones, for their order
+    const int each = (drops + all - 1) / all;
+    const int g0 = min(static_cast<long long>(drops), static_cast<long long>(cluster_thread()) * each), g1 = min(drops, g0 + each);
+    auto entries = [&](auto&& f) {   // f(sequence, entry of the table, number); the table is left until the last time
+        if (g0 >= g1) return;
+        int b = find(drop_s, p.B, g0);
+        for (int g = g0; g < g1; ++g) {
+            while (g >= drop_s[b + 1]) ++b;
+            f(b, p.block_table + static_cast<size_t>(b) * p.max_pages + from_s[b] + g - drop_s[b], g);
+        }
+    };
+    entries([&](int b, const int* e, int) {
+        const int page = *e;
+        if (page_ok(page, p.num_pages)) atomicSub(p.page_refs + page, 1);
+        else if (p.status) atomicOr(p.status + b, kKvBadIndex);
+    });
+    for (int b = cluster_thread(); b < p.B; b += all) {
+        int src = -1, dst = -1;
+        if (copy_s[b + 1] > copy_s[b]) {
+            src = p.block_table[static_cast<size_t>(b) * p.max_pages + from_s[b]];
+            dst = p.free_list[free_n - 1 - copy_s[b]];
+        }
+        p.copy_src[b] = src;
+        p.copy_dst[b] = dst;
+    }
+    cluster_sync_all();
+    entries([&](int, const int* e, int g) {
+        const int page = *e;
+        if (page_ok(page, p.num_pages) && ld_l2(p.page_refs + page) < 0) atomicMin(p.page_refs + page, INT_MIN + g);
+    });
+    cluster_sync_all();
+    Pair back{0, 0};
+    entries([&](int, const int* e, int g) {
+        const int page = *e;
+        back.pages += page_ok(page, p.num_pages) && ld_l2(p.page_refs + page) == INT_MIN + g;
+    });
+    const Pair before = block_prefix(back, sums, &total);
+    if (threadIdx.x == 0) mine_s = static_cast<int>(total.pages);
+    cluster_sync_all();
+    int rank = static_cast<int>(before.pages), pushed = 0;
+    for (uint32_t c = 0; c < cluster_ctas(); ++c) {
+        const int n = ld_dsmem_int(&mine_s, c);
+        if (c < cluster_ctarank()) rank += n;
+        pushed += n;
+    }
+    const int base = free_n - copies;   // the stack without the pages for copies
+    entries([&](int b, int* e, int g) {
+        const int page = *e;
+        if (page_ok(page, p.num_pages) && ld_l2(p.page_refs + page) == INT_MIN + g) {
+            const long long place = static_cast<long long>(base) + pushed - 1 - rank++;
+            p.page_refs[page] = 0;
+            if (place < p.num_pages) p.free_list[place] = page;
+            else if (p.status) atomicOr(p.status + b, kKvBadIndex);
+        }
+        if (g == drop_s[b] && copy_s[b + 1] > copy_s[b]) {
+            const int fresh = ld_l2(p.copy_dst + b);
+            *e = fresh;
+            if (!page_ok(fresh, p.num_pages)) {
+                p.copy_src[b] = p.copy_dst[b] = -1;
+                if (p.status) atomicOr(p.status + b, kKvBadIndex);
+            }
+        }
+    });
+    if (first_cta)
+        for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+            if (from_s[b] < 0) continue;
+            p.seq_len[b] = p.new_len[b];
+            p.n_pages[b] = from_s[b] + (copy_s[b + 1] - copy_s[b]);
+        }
+    if (first_cta && threadIdx.x == 0) *p.free_count = min(base + pushed, p.num_pages);
+    cluster_sync_all();   // no CTA ends while others read its shared memory
+}
+
+// ---------------------------------------------------------------- compaction
+// The number of a page among those in use by ballots: a warp walks a run of pages, 32 at a time, and prefix sums over the
+// warps' totals give each its start.  With `used` known, the r-th page from the top of those at `used` and above goes to the
+// r-th place from the bottom that is not in use: each finds its own r, and writes itself into the pair of that number.
+__global__ void __launch_bounds__(kBookThreads) kv_compact_kernel(const KvCompactParams p) {
+    extern __shared__ int smem[];
+    int* const held_s = smem;   // [B + 1] entries before each sequence
+    __shared__ Pair sums[33];
+    __shared__ int used_s, holes_s;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int me = cluster_thread(), all = cluster_threads(), lane = threadIdx.x & 31;
+    const bool first_cta = cluster_ctarank() == 0;
+    for (int g = me; g < p.num_pages; g += all) p.page_refs[g] = 0;
+    const int per = (p.B + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
+    auto held = [&](int b) {
+        const int n = p.n_pages[b];
+        return n >= 0 && n <= p.max_pages ? n : 0;
+    };
+    Pair ask{0, 0}, total;
+    for (int b = b0; b < b1; ++b) {
+        ask.pages += held(b);
+        if (first_cta && p.status && (p.n_pages[b] < 0 || p.n_pages[b] > p.max_pages)) atomicOr(p.status + b, kKvBadIndex);
+    }
+    Pair at = block_prefix(ask, sums, &total);
+    for (int b = b0; b < b1; ++b) {
+        held_s[b] = static_cast<int>(at.pages);
+        at.pages += held(b);
+    }
+    if (threadIdx.x == 0) held_s[p.B] = static_cast<int>(total.pages);
+    if (threadIdx.x == 0) holes_s = 0;
+    cluster_sync_all();
+    const int entries = held_s[p.B];
+    // a warp takes 128 consecutive entries at a time: one bisection serves those of one sequence
+    auto each_entry = [&](auto&& f) {
+        for (long long c = static_cast<long long>(me >> 5) * 128; c < entries; c += static_cast<long long>(all >> 5) * 128) {
+            const int bc = find(held_s, p.B, static_cast<int>(c)), end = held_s[bc + 1];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const long long g = c + i * 32 + lane;
+                if (g >= entries) continue;
+                const int b = g < end ? bc : find(held_s, p.B, static_cast<int>(g));
+                f(b, static_cast<size_t>(b) * p.max_pages + static_cast<size_t>(g - held_s[b]));
+            }
+        }
+    };
+    each_entry([&](int b, size_t e) {
+        const int page = p.block_table[e];
+        if (page_ok(page, p.num_pages)) atomicAdd(p.page_refs + page, 1);
+        else if (p.status) atomicOr(p.status + b, kKvBadIndex);
+    });
+    cluster_sync_all();
+    // this warp's run of pages
+    const int warps = all >> 5, run = (p.num_pages / 32 + (p.num_pages % 32 > 0) + warps - 1) / warps;   // of 32 pages
+    const long long p0 = static_cast<long long>(me >> 5) * run * 32, p1 = min(static_cast<long long>(p.num_pages), p0 + static_cast<long long>(run) * 32);
+    int in_use = 0;
+    for (long long g = p0; g < p1; g += 32) {
+        const bool u = g + lane < p1 && ld_l2(p.page_refs + g + lane) > 0;
+        in_use += __popc(__ballot_sync(0xffffffffu, u));
+    }
+    Pair before = block_prefix(Pair{lane == 0 ? in_use : 0, 0}, sums, &total);
+    if (threadIdx.x == 0) used_s = static_cast<int>(total.rows);
+    cluster_sync_all();
+    int below = static_cast<int>(__shfl_sync(0xffffffffu, before.rows, 0)), used = 0;
+    for (uint32_t c = 0; c < cluster_ctas(); ++c) {
+        const int n = ld_dsmem_int(&used_s, c);
+        if (c < cluster_ctarank()) below += n;
+        used += n;
+    }
+    int holes = 0;
+    for (long long g = p0; g < p1; g += 32) {
+        const int page = static_cast<int>(g) + lane;
+        const bool in = g + lane < p1;
+        const int count = in ? ld_l2(p.page_refs + page) : 0;
+        const uint32_t set = __ballot_sync(0xffffffffu, count > 0);
+        if (in) {
+            const int n = below + __popc(set & ((1u << lane) - 1u));   // in use below this page
+            if (count > 0 && page < used) {
+                p.page_map[page] = page;
+                p.page_refs[page] = count - 1;
+            } else if (count > 0) {
+                p.copy_src[used - 1 - n] = page;
+            } else {
+                p.page_map[page] = -1;
+                if (page < used) {
+                    p.copy_dst[page - n] = page;
+                    ++holes;
+                }
+            }
+        }
+        below += __popc(set);
+    }
+    for (int o = 16; o > 0; o >>= 1) holes += __shfl_xor_sync(0xffffffffu, holes, o);
+    if (lane == 0 && holes > 0) atomicAdd(&holes_s, holes);
+    cluster_sync_all();
+    int moves = 0;
+    for (uint32_t c = 0; c < cluster_ctas(); ++c) moves += ld_dsmem_int(&holes_s, c);
+    for (int r = me; r < p.n_copy_max; r += all) {
+        if (r < moves) {
+            const int src = ld_l2(p.copy_src + r), dst = ld_l2(p.copy_dst + r);
+            p.page_map[src] = dst;
+            p.page_refs[dst] = ld_l2(p.page_refs + src) - 1;
+            p.page_refs[src] = 0;
+        } else {
+            p.copy_src[r] = p.copy_dst[r] = -1;
+        }
+    }
+    for (int i = me; i < p.num_pages - used; i += all) p.free_list[i] = p.num_pages - 1 - i;
+    if (me == 0) {
+        *p.free_count = p.num_pages - used;
+        *p.n_copy = moves;
+    }
+    cluster_sync_all();
+    each_entry([&](int, size_t e) {
+        const int page = p.block_table[e];
+        p.table_out[e] = page_ok(page, p.num_pages) ? ld_l2(p.page_map + page) : page;
+    });
+}
+
+// One cluster of `ctas` CTAs with `words` words of shared memory, most of them `most` (the kernel's limit, the same by every
+// call: another thread's call may come between it and the launch).
+template <typename P>
+cudaError_t launch_books(void (*kernel)(P), const P& p, bool many, size_t words, size_t most, cudaStream_t stream) {
+    const size_t smem = words * 4;
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most * 4));
+        if (e != cudaSuccess) return e;
+    }
+    const int ctas = many ? 8 : 1;
+    return launch_dependent_cluster(kernel, ctas, dim3(ctas), dim3(kBookThreads), smem, stream, p);
+}
+
+// ---------------------------------------------------------------- copies
+// Elementwise, every byte read and written once: bound by the memory.  A CTA takes 256 x 8 accesses of 16 bytes of one
+// page's keys or values at a time, all loads before the first store.  A page is `outer` runs of `inner` runs of `run`
+// consecutive vectors (one run where it lies in one piece).
+constexpr int kCopyThreads = 256, kCopyBatch = 8;
+
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const KvCopyParams p) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const long long items = static_cast<long long>(p.n) * 2 * p.chunks;
+    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+        const int chunk = static_cast<int>(it % p.chunks);
+        const long long pair = it / p.chunks;
+        const int i = static_cast<int>(pair >> 1);
+        const int src = p.copy_src[i], dst = p.copy_dst[i];
+        if (src < 0 || dst < 0) continue;
+        if (src >= p.cache.num_pages || dst >= p.cache.num_pages) {
+            if (p.status && threadIdx.x == 0) atomicOr(p.status, kKvBadIndex);
+            continue;
+        }
+        uint4* const half = static_cast<uint4*>(pair & 1 ? p.cache.v : p.cache.k);
+        const uint4* const from = half + src * p.page_stride;
+        uint4* const to = half + dst * p.page_stride;
+        uint4 v[kCopyBatch];
+        long long at[kCopyBatch];
+#pragma unroll
+        for (int k = 0; k < kCopyBatch; ++k) {
+            const unsigned x = (static_cast<unsigned>(chunk) * kCopyBatch + k) * kCopyThreads + threadIdx.x;
+            at[k] = -1;
+            if (x < static_cast<unsigned>(p.vectors)) {
+                const unsigned row = x / p.run, o = row / p.inner;
+                at[k] = o * p.outer_stride + (row - o * p.inner) * p.inner_stride + (x - row * p.run);
+                v[k] = from[at[k]];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kCopyBatch; ++k)
+            if (at[k] >= 0) to[at[k]] = v[k];
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_fork(const KvForkParams& p, cudaStream_t stream) {
+    return launch_books(kv_fork_kernel, p, p.num_pages > kManyEntries, static_cast<size_t>(p.B) + 2 * (static_cast<size_t>(p.N) + 1),
+                        3 * (kKvMaxSeq + 1), stream);
+}
+
+cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {
+    return launch_books(kv_release_kernel, p, p.num_pages > kManyEntries, 3 * (static_cast<size_t>(p.B) + 1), 3 * (kKvMaxSeq + 1), stream);
+}
+
+cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t stream) {
+    return launch_books(kv_compact_kernel, p, p.num_pages > kManyEntries, static_cast<size_t>(p.B) + 1, kKvMaxSeq + 1, stream);
+}
+
+cudaError_t launch_kv_copy(KvCopyParams p, cudaStream_t stream) {
+    constexpr int kPiece = kCopyThreads * kCopyBatch;
+    p.chunks = p.vectors / kPiece + (p.vectors % kPiece > 0);
+    const int sms = sm_count();
+    if (sms == 0) return cudaErrorInvalidDevice;
+    const long long items = static_cast<long long>(p.n) * 2 * p.chunks;
+    const int ctas = static_cast<int>(items < sms * 8ll ? items : sms * 8ll);
+    return launch_dependent(kv_copy_kernel, dim3(ctas), dim3(kCopyThreads), 0, stream, p);
+}
+
+}  // namespace gdn

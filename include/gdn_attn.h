@@ -1,9 +1,10 @@
 /*
  * gdn_attn.h -- the full-attention side of a hybrid layer stack in libgdn.so:
  * a paged key-value cache (its page bookkeeping and the append of new tokens)
- * and the attention of new tokens over it, for a caller that decodes the
- * gated DeltaNet layers of include/gdn.h and also has the full-attention
- * layers between them.
+ * and the attention of new tokens over it -- a few a sequence of a decode step,
+ * or the chunks of prompts -- for a caller that runs the gated DeltaNet layers
+ * of include/gdn.h and also has the full-attention layers between them.
+ * Pages that sequences share are in include/gdn_pages.h.
  *
  * Source of the layer: xwen CLAUDE.md page, "Architecture cheat sheet (Qwen
  * 3.6, ggml-org GGUF)": full attention at every fourth layer, with RMSNorm of
@@ -32,9 +33,9 @@
  *   GDN_KV_REFUSED   the page bookkeeping left the sequence as it was
  *   GDN_KV_BAD_INDEX a length, page, slot or position outside its range; the
  *                    keys or tokens concerned were left out
- *   16 (bit 4)       a bounded wait inside gdn_attn_decode gave up: outputs of
- *                    the sequence were not (fully) written, and the workspace
- *                    has to be zeroed before its next use
+ *   16 (bit 4)       a bounded wait inside gdn_attn_decode or gdn_attn_chunk
+ *                    gave up: outputs of the sequence were not (fully) written,
+ *                    and the workspace has to be zeroed before its next use
  */
 #ifndef GDN_ATTN_H
 #define GDN_ATTN_H
@@ -188,6 +189,44 @@ gdn_status gdn_attn_decode(const gdn_attn_dims* dims, const gdn_kv_cache* cache,
                            int32_t max_pages, const void* q, int64_t ldq, const void* gate, int64_t ldg,
                            const int32_t* block_table, const int32_t* seq_len, void* out, void* workspace,
                            size_t workspace_bytes, int32_t* dev_status, gdn_stream_t stream);
+
+/*
+ * gdn_attn_chunk_workspace_bytes -- device scratch that gdn_attn_chunk needs
+ * (0 for arguments that it refuses).  It depends on dims alone: a workspace
+ * serves calls of any B >= 1 and T >= 1.
+ */
+size_t gdn_attn_chunk_workspace_bytes(const gdn_attn_dims* dims, int32_t B, int32_t T);
+
+/*
+ * gdn_attn_chunk -- steps 4-5 for the last tokens of each of B sequences, any
+ * number of them: the prompts of a batch, pieces of long ones, single tokens
+ * of others in the same call.  The tokens are already in the cache.  Sequence
+ * b has rows cu_seqlens[b] .. cu_seqlens[b+1]-1 (packed, as gdn_kv_extend
+ * leaves them), n_b of them, which are its last n_b tokens: its row p sees keys
+ * 0 .. seq_len[b] - n_b + p; none when that is negative.
+ *   q    [T][H_q*head_dim], row pitch ldq elements (a multiple of 16 bytes)
+ *   gate as q, row pitch ldg, or NULL for no gate
+ *   cu_seqlens [B+1], block_table [B][max_pages], seq_len [B]   on the device
+ *   out  [T][H_q*head_dim]; rows of no sequence are left as they are
+ *   workspace of at least gdn_attn_chunk_workspace_bytes() bytes, zeroed by the
+ *        caller once, before its first use, and as in gdn_attn_decode ready for
+ *        the next call after every call; calls that may run at the same time
+ *        need one each (also one that is not a gdn_attn_decode call's)
+ *   dev_status [B] or NULL: GDN_KV_BAD_INDEX as in gdn_attn_decode, and for a
+ *        sequence with cu_seqlens[b] > cu_seqlens[b+1] or either outside 0..T,
+ *        which has no rows then (rows that two sequences claim hold the result
+ *        of either)
+ * What gdn_attn_decode promises holds here too: memory beyond a sequence's
+ * length is not read, a token's key or value does not matter to the rows that
+ * do not see it, whatever it is, and results are the same from run to run.
+ * A bf16 result's softmax weights are rounded to bf16 before the product with
+ * the values (2^-8 of a weight at most, beside the result's own rounding);
+ * an fp32 result's are not.
+ */
+gdn_status gdn_attn_chunk(const gdn_attn_dims* dims, const gdn_kv_cache* cache, int32_t B, int32_t T,
+                          int32_t max_pages, const void* q, int64_t ldq, const void* gate, int64_t ldg,
+                          const int32_t* cu_seqlens, const int32_t* block_table, const int32_t* seq_len, void* out,
+                          void* workspace, size_t workspace_bytes, int32_t* dev_status, gdn_stream_t stream);
 
 #ifdef __cplusplus
 }
