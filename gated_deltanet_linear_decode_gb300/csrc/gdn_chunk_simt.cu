@@ -301,7 +301,8 @@ cudaError_t by_head(const ChunkParams& p, int head_dim, bool out_bf16, int sms, 
 
 }  // namespace chunk
 
-size_t chunk_workspace_bytes(int head_dim, int, int) {
+size_t chunk_workspace_bytes(int head_dim, int act_dtype, int out_dtype) {
+    if (act_dtype == GDN_BF16 && out_dtype == GDN_BF16) return chunk::tc_workspace_bytes(head_dim);
     if (head_dim == 64) return chunk::parts_bytes<chunk::kRt, 64>(chunk::kMaxWorkers);
     if (head_dim == 128) return chunk::parts_bytes<chunk::kRt, 128>(chunk::kMaxWorkers);
     return chunk::parts_bytes<chunk::kRt, 256>(chunk::kMaxWorkers);
@@ -311,6 +312,7 @@ cudaError_t launch_attn_chunk(const ChunkParams& p, int head_dim, int act_dtype,
     const int sms = sm_count();
     if (sms == 0) return cudaErrorInvalidDevice;
     const bool out_bf16 = out_dtype == GDN_BF16;
+    if (act_dtype == GDN_BF16 && out_bf16) return chunk::launch_tc(p, head_dim, sms, stream);
     if (act_dtype == GDN_BF16) return chunk::by_head<__nv_bfloat16>(p, head_dim, out_bf16, sms, stream);
     return chunk::by_head<float>(p, head_dim, out_bf16, sms, stream);
 }
