@@ -129,7 +129,8 @@ constexpr size_t parts_bytes(int workers) {
     return kCounterBytes + static_cast<size_t>(2) * workers * RT * (D * 4 + 8);
 }
 
-cudaError_t launch_tc(const ChunkParams& p, int head_dim, int sms, cudaStream_t stream);   // bf16 cache and result
+// bf16 cache and result; *done = false where the driver makes no tensor map of the strides.
+cudaError_t launch_tc(const ChunkParams& p, int head_dim, int sms, bool* done, cudaStream_t stream);
 size_t tc_workspace_bytes(int head_dim);
 
 }  // namespace chunk

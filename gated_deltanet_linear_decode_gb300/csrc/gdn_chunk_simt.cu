@@ -312,7 +312,11 @@ cudaError_t launch_attn_chunk(const ChunkParams& p, int head_dim, int act_dtype,
     const int sms = sm_count();
     if (sms == 0) return cudaErrorInvalidDevice;
     const bool out_bf16 = out_dtype == GDN_BF16;
-    if (act_dtype == GDN_BF16 && out_bf16) return chunk::launch_tc(p, head_dim, sms, stream);
+    if (act_dtype == GDN_BF16 && out_bf16) {
+        bool done;
+        const cudaError_t e = chunk::launch_tc(p, head_dim, sms, &done, stream);
+        if (e != cudaSuccess || done) return e;
+    }
     if (act_dtype == GDN_BF16) return chunk::by_head<__nv_bfloat16>(p, head_dim, out_bf16, sms, stream);
     return chunk::by_head<float>(p, head_dim, out_bf16, sms, stream);
 }
