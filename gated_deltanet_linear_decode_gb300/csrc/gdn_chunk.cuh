@@ -36,6 +36,12 @@ __device__ __forceinline__ void report_rows(const ChunkParams& p, int b) {
     if (!rows_ok(p, p.cu_seqlens[b], p.cu_seqlens[b + 1]) || p.seq_len[b] > most_keys(p)) atomicOr(p.status + b, kKvBadIndex);
 }
 
+// On to the worker's next part (gdn_chunk_plan.h).  A call: it comes once a part in several places of a kernel, and inlined its
+// divisions made a kernel of 200 KB, whose warps waited for instructions a third of their time.
+static __device__ __noinline__ bool to_next_part(const ChunkParams& p, const Line& ln, const Share& sh, Part& c) {
+    return next_part(ln, sh, p.B, p.Hkv, c, [&](int b) { return rows_of(p, b); });
+}
+
 struct PlanSmem {
     long long sums[32], start;   // by warp
     int start_b;
@@ -84,7 +90,7 @@ __device__ __forceinline__ bool my_share(const ChunkParams& p, const Line& ln, i
     grid_launch_dependents();
     c.b = sm.start_b;
     c.r = rows_of(p, c.b);
-    return first_part(ln, sh, p.B, p.Hkv, sm.start, c, [&](int b) { return rows_of(p, b); });
+    return first_part(ln, sh, sm.start, c) || to_next_part(p, ln, sh, c);
 }
 
 // Rows of a unit, and of row r its token (of the unit) and query head.

@@ -104,9 +104,9 @@ GDN_HD bool next_part(const Line& ln, const Share& sh, int B, int Hkv, Part& c, 
     }
 }
 
-// The first of them; c.b, c.r are the sequence that has number sh.first, `start` the number where it begins.
-template <class F>
-GDN_HD bool first_part(const Line& ln, const Share& sh, int B, int Hkv, long long start, Part& c, F rows) {
+// The unit that has number sh.first; false if none of its tiles is the share's (then next_part's is the first).  c.b, c.r are the
+// sequence that has the number, `start` the number where it begins.
+GDN_HD bool first_part(const Line& ln, const Share& sh, long long start, Part& c) {
     const long long head = ln.head(c.r), in = sh.first - start;
     c.hk = static_cast<int>(quot(in, head));
     const long long x = in - c.hk * head;
@@ -118,7 +118,7 @@ GDN_HD bool first_part(const Line& ln, const Share& sh, int B, int Hkv, long lon
     }
     c.i = lo;
     c.at = sh.first - x + ln.before(c.r, lo);
-    return clip(ln, sh, c) || next_part(ln, sh, B, Hkv, c, rows);
+    return clip(ln, sh, c);
 }
 
 }  // namespace chunk

@@ -39,7 +39,7 @@ __device__ __forceinline__ void unpack16(const uint4& w, float (&v)[4], const fl
 }
 
 template <class S>
-__global__ void __launch_bounds__(kThreads, S::kCtas) chunk_simt_kernel(const ChunkParams p, const bool out_bf16) {
+__global__ void __launch_bounds__(kThreads, S::kCtas) chunk_simt_kernel(const __grid_constant__ ChunkParams p, const bool out_bf16) {
     using Ta = typename S::Ta;
     constexpr int D = S::D, kE = 16 / S::kEs;   // elements of 16 bytes
     extern __shared__ __align__(16) uint8_t smem[];
@@ -58,7 +58,6 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) chunk_simt_kernel(const Ch
     const Parts<kRt, D> parts(p.workspace, static_cast<int>(gridDim.x));
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const float scale = p.scale * kLog2e;
-    auto rows = [&](int b) { return rows_of(p, b); };
     // this thread's key of a tile, a quarter of its channels
     const int my_key = threadIdx.x >> 2, quarter = threadIdx.x & 3;
     auto load_rows = [&](const void* half, long long off, bool there, uint8_t* to) {
@@ -278,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) chunk_simt_kernel(const Ch
             }
         }
         __syncthreads();
-    } while (next_part(ln, sh, p.B, p.Hkv, c, rows));
+    } while (to_next_part(p, ln, sh, c));
 }
 
 template <typename Ta, int D>

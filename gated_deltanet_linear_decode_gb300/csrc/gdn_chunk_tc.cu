@@ -5,17 +5,17 @@
 // of the values half of the channels, and the tensor cores read both.  So a key and a value come from L2 once for 256 rows
 // (at d = 256 a tile's products take 2,048 cycles and its copies 32 bytes a cycle of every SM; with 128 rows a CTA it were 64).
 //
-// Roles of a CTA's 10 warps:
+// Roles of a CTA's 11 warps:
 //   0-7   softmax: a thread has one row (tensor-memory lane) and 64 of a tile's 128 keys; the two threads of a row meet in shared
 //         memory for the maximum.  The result is rescaled only when a row's maximum has risen by more than 2^kSlack.
-//   8     loads by TMA, from a tensor map of [page][token][head][channel] that serves any strides: boxes of 64 channels of as
-//         many tokens as always lie in one page (16, or the largest power of two that divides the page), each lane its own
-//         boxes' page.  Keys past the end and pages outside the cache are coordinates outside the map, which read as zeros
+//   8     copies queries and keys by TMA, from a tensor map that serves any strides; each lane looks up its keys' pages, one
+//         issues the copies.  Keys past the end and pages outside the cache are coordinates outside the map, which read as zeros
+//   10    copies values
 //   9     one thread of the first CTA: issues the products
 //
-// The products of one tile's S are issued before those of the O of the tile before (NS tiles before, where S has two places),
-// so that the softmax of a tile runs beside products.  Every order between products that touch the same tensor memory goes
-// through a barrier.
+// S has two places, so that the softmax of a tile runs beside the products of others.  At d = 256 the tensor memory is full with
+// them and O: the weights then take the place of their scores, and the S after next waits for the product with them.  Every
+// order between products that touch the same tensor memory goes through a barrier.
 //
 // A weight is rounded to bf16 (2^-9 of it at most): with a second part for what the rounding leaves, as gdn_attn_decode has
 // it, which is bound by memory, the product with the values would take twice the time, half again as much for the whole.
@@ -32,16 +32,15 @@ namespace {
 using bf16 = __nv_bfloat16;
 using attn::kWaitLimit;
 using attn::stage_wait;
-using attn::warp_wait;
 using tc::smem_u32;
 constexpr int kDrainLimit = 1 << 14;   // polls for what is in flight at the end
 constexpr float kSlack = 8.0f;   // how far a score may pass its row's base
-constexpr int kRows = 256, kKeys = 128, kThreads = 320, kSoft = 256;
+constexpr int kRows = 256, kKeys = 128, kThreads = 352, kSoft = 256, NS = 2;   // places of S
 
 template <int D_>
 struct Tc {
     static constexpr int D = D_;
-    static constexpr int NS = D == 256 ? 1 : 2;               // places of S; P has two
+    static constexpr bool kOver = D == 256;                   // P lies where its S was, for want of tensor memory
     static constexpr int kVCh = D == 256 ? 128 : 64;          // channels of a CTA's values (heads of 64: all of them, in both)
     static constexpr int kStageK = kKeys * D, kStageV = kKeys * 2 * kVCh;   // bytes: 64 keys, 128 keys' values
     static constexpr int RK = D == 256 ? 2 : D == 128 ? 5 : 6;
@@ -49,9 +48,10 @@ struct Tc {
     static constexpr int kQ = 128 * D * 2;
     static constexpr int kSmem = kQ + RK * kStageK + RV * kStageV + 3072;
     // tensor memory
-    static constexpr int kO = 0, kS = D == 256 ? 256 : 128, kP = 384;
+    static constexpr int kO = 0, kS = kOver ? 256 : 128, kP = kOver ? kS : 384;
+    static constexpr int kPStep = kOver ? 128 : 64, kPHalf = kOver ? 64 : 32;   // columns from one P to the other, from one half of the keys to the other
     static constexpr int kCost = 256;
-    static_assert(kSmem <= 232448 && kS + NS * 128 <= kP, "shape");
+    static_assert(kSmem <= 232448, "shape");
 };
 
 struct Smem {
@@ -79,12 +79,12 @@ __device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_cta(smem_u32(bar), rank)) : "memory");
 }
 
-// A box of the map at (channel, head, token, page) into this CTA's shared memory, its bytes counted by the first CTA's barrier
-// (at cluster address `bar`).
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int ch, int head, int token, int page, uint32_t bar) {
+// A box of the map at (token, block of 64 channels, head, page) into this CTA's shared memory, its bytes counted by the first CTA's
+// barrier (at cluster address `bar`).
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int token, int block, int head, int page, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(ch), "r"(head), "r"(token), "r"(page), "r"(bar)
+        "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(block), "r"(head), "r"(page), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map, int ch, int head, int token, uint32_t bar) {
@@ -92,6 +92,21 @@ __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map,
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(ch), "r"(head), "r"(token), "r"(bar)
         : "memory");
+}
+
+// A wait of a whole warp, at which one lane looks.  (A wait of 32 lanes at one barrier is 32 waits for the unit that serves them: with
+// eight warps of them at it, one more thread's wait for what had long been there took 235 cycles.)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    int done = 0;
+    if ((threadIdx.x & 31) == 0) done = stage_wait(bar, parity, abort);
+    return __shfl_sync(0xffffffffu, done, 0) != 0;
+}
+
+// One lane of a converged warp (the compiler knows that it is one).
+__device__ __forceinline__ bool elected() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Arrive at `bar` in both CTAs when every product issued so far is done.
@@ -105,11 +120,11 @@ __device__ __forceinline__ void commit_both(uint64_t* bar) {
 // and, for values, how far the next 64 channels are.
 constexpr uint32_t kDesc128 = (1024u >> 4) | (1u << 14) | (2u << 29);
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %6};\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc),
-        "r"(static_cast<uint32_t>(add)), "n"(kDesc128));
+        "r"(static_cast<uint32_t>(add)), "n"(kDesc128), "r"(b_hi));
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool add) {
     asm volatile(
@@ -158,24 +173,34 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-// A walk over the tiles of a worker's parts.
+// How keys and values lie in a stage.  A box is `tokens` tokens of one page and `blocks` blocks of 64 channels; its block of `tokens`
+// rows of 128 bytes is followed by the next block, and a box by the next.  As the tensor cores want it: for keys (whose 8-row
+// groups have one distance) boxes of 8 tokens and all blocks, or one block of all 64 keys; for values (whose 16 keys of a product
+// lie in one box) any number of tokens from 16 up and both blocks.  Pages that 8 or 16 do not divide give boxes of one block and
+// fewer tokens, which make up blocks of 64 keys or 128 values.
+struct Boxes {
+    int tokens, blocks;   // of a box
+    int rows;             // of a block in shared memory, a power of two
+};
+
+// A walk over the tiles of a worker's parts.  The part lies in memory (to_next_part is a call), what every tile asks for does not.
 struct Walk {
-    Part c;
-    int t;
+    Part& c;
+    int t, t0, t1;
     bool more;
-    template <class F>
-    __device__ __forceinline__ void settle(const ChunkParams& p, const Line& ln, const Share& sh, F rows) {   // past parts without tiles
-        while (more && c.t0 >= c.t1) more = next_part(ln, sh, p.B, p.Hkv, c, rows);
-        t = c.t0;
+    __device__ __forceinline__ Walk(Part& first, const ChunkParams& p, const Line& ln, const Share& sh) : c(first), more(true) { settle(p, ln, sh); }
+    __device__ __forceinline__ void settle(const ChunkParams& p, const Line& ln, const Share& sh) {   // past parts without tiles
+        while (more && c.t0 >= c.t1) more = to_next_part(p, ln, sh, c);
+        t = t0 = c.t0;
+        t1 = c.t1;
     }
-    template <class F>
-    __device__ __forceinline__ void next(const ChunkParams& p, const Line& ln, const Share& sh, F rows) {
-        if (++t < c.t1) return;
-        more = next_part(ln, sh, p.B, p.Hkv, c, rows);
-        settle(p, ln, sh, rows);
+    __device__ __forceinline__ void next(const ChunkParams& p, const Line& ln, const Share& sh) {
+        if (++t < t1) return;
+        more = to_next_part(p, ln, sh, c);
+        settle(p, ln, sh);
     }
-    __device__ __forceinline__ bool first() const { return t == c.t0; }
-    __device__ __forceinline__ bool last() const { return t + 1 == c.t1; }
+    __device__ __forceinline__ bool first() const { return t == t0; }
+    __device__ __forceinline__ bool last() const { return t + 1 == t1; }
 };
 
 // The strays of a unit's late keys (gdn_attn.cuh; those that its first row does not see) are added to the rows that see them,
@@ -214,8 +239,9 @@ __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 5, %0;" 
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                    const __grid_constant__ CUtensorMap q_map, const int box) {
-    constexpr int D = S::D, NS = S::NS, RK = S::RK, RV = S::RV;
+                    const __grid_constant__ CUtensorMap q_map, const Boxes kb, const Boxes vb) {
+    constexpr int D = S::D, RK = S::RK, RV = S::RV;
+    constexpr int kKBlocks = D / 64, kVBlocks = S::kVCh / 64;   // blocks of 64 channels in a CTA's stages
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const q_s = smem;
     uint8_t* const k_s = q_s + S::kQ;
@@ -250,9 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cta_tokens = 128 / p.G, cta_rows = cta_tokens * p.G;   // of a unit, in each CTA
     const Line ln{2 * cta_tokens, kKeys, S::kCost};
     Share sh;
-    Walk w;
-    if (!my_share(p, ln, worker, workers, kKeys, sm.plan, sh, w.c)) return;   // both CTAs of a pair, or neither
-    auto rows = [&](int b) { return rows_of(p, b); };
+    Part c;
+    if (!my_share(p, ln, worker, workers, kKeys, sm.plan, sh, c)) return;   // both CTAs of a pair, or neither
     // rows past cta_rows, which no copy writes
     for (int i = threadIdx.x; i < (128 - cta_rows) * (D / 8); i += kThreads)
         *reinterpret_cast<uint4*>(q_s + i / ((128 - cta_rows) * 8) * 16384 + cta_rows * 128 + i % ((128 - cta_rows) * 8) * 16) = make_uint4(0, 0, 0, 0);
@@ -267,43 +292,43 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     const uint32_t t_o = sm.tmem + S::kO, t_s = sm.tmem + S::kS, t_p = sm.tmem + S::kP;
 
-    if (warp == 8) {
-        // ------------------------------------------------------------ copies
-        w.more = true;
-        w.settle(p, ln, sh, rows);
-        const int ps = p.cache.page_size, groups = kKeys / box, k_groups = groups / 2, k_first = static_cast<int>(rank) * k_groups;
-        // Lane l has the tile's groups of `box` keys l + 32 k.  Of tile i: [0] tile g (values), .. [NS] tile g + NS (keys), [NS + 1]
-        // the one being looked up.
-        constexpr int A = NS + 2, kPer = 4;
-        int page[A][kPer], in[A][kPer], head[A], seq[A], q_tok[A];   // in -1: no key; seq -1: no tile; q_tok -1: not a part's first
-#pragma unroll
-        for (int i = 0; i < A; ++i) {
-            seq[i] = q_tok[i] = -1;
-            head[i] = 0;
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) page[i][k] = in[i][k] = -1;
-        }
+    if (warp == 8 || warp == 10) {
+        // ------------------------------------------------------------ copies: warp 8 queries and keys, warp 10 values
+        Walk w(c, p, ln, sh);
+        const bool keys = warp == 8;
+        const Boxes bx = keys ? kb : vb;
+        const int ps = p.cache.page_size, groups = kKeys / bx.tokens;
+        // Lane l has the tile's groups of bx.tokens keys l + 32 k, [0] of the tile to be copied, [1] of the one being looked up.
+        constexpr int kPer = 4;
+        int page[2][kPer] = {}, in[2][kPer] = {}, head[2] = {}, seq[2] = {}, q_tok[2] = {};   // in -1: no key; seq -1: no tile; q_tok -1: not a part's first
         bool ok = true;
-        const uint32_t ring_k = smem_u32(k_s), ring_v = smem_u32(v_s);
-        int parts_begun = 0, n_k = 0, n_v = 0;
+        int parts_begun = 0, part_seq = 0, part_head = 0;
+        int end = 0;               // keys from `end` on are nobody's
+        const int* table = nullptr;   // the sequence's pages
         auto look_up = [&](int a) {
             seq[a] = -1;
             if (!w.more) return;
-            seq[a] = w.c.b;
-            head[a] = w.c.hk;
-            q_tok[a] = w.first() ? w.c.r.row0 + w.c.i * ln.tokens + static_cast<int>(rank) * cta_tokens : -1;
-            const int end = ln.seen(w.c.r, w.c.i);   // keys from `end` on are nobody's
+            q_tok[a] = -1;
+            if (w.first()) {
+                part_seq = c.b;
+                part_head = c.hk;
+                q_tok[a] = c.r.row0 + c.i * ln.tokens + static_cast<int>(rank) * cta_tokens;
+                end = ln.seen(c.r, c.i);
+                table = p.block_table + static_cast<size_t>(c.b) * p.max_pages;
+            }
+            seq[a] = part_seq;
+            head[a] = part_head;
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
-                const int i = lane + 32 * k, j = w.t * kKeys + i * box;
+                const int i = lane + 32 * k, j = w.t * kKeys + i * bx.tokens;
                 in[a][k] = page[a][k] = -1;
                 if (i < groups && j < end) {
                     const int x = j / ps;
                     in[a][k] = j - x * ps;
-                    page[a][k] = p.block_table[static_cast<size_t>(w.c.b) * p.max_pages + x];   // looked at when it is used
+                    page[a][k] = table[x];   // looked at when it is used
                 }
             }
-            w.next(p, ln, sh, rows);
+            w.next(p, ln, sh);
         };
         // The bytes of both CTAs are expected by the first one, and the second one arrives.
         auto announce = [&](uint64_t* bar, uint32_t bytes) {
@@ -314,151 +339,141 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             return in_cta(smem_u32(bar), 0);
         };
-        auto load_queries = [&](int a) {
-            if (parts_begun > 0) ok = ok && warp_wait(&sm.q_empty, (parts_begun - 1) & 1, &sm.abort);
-            if (!ok) return;
-            ++parts_begun;
-            const uint32_t bar = announce(&sm.q_full, 2 * cta_rows * D * 2);
-            if (lane < D / 64) tma_load_q(smem_u32(q_s) + lane * 16384, &q_map, lane * 64, head[a] * p.G, q_tok[a], bar);
-        };
-        auto load_keys = [&](int a) {
-            const int st = n_k % RK;
-            if (n_k >= RK) ok = ok && warp_wait(sm.k_empty + st, (n_k / RK - 1) & 1, &sm.abort);
-            if (!ok) return;
-            if (lane < 4) sm.valid[n_k & 15][lane] = 0xffffffffu;
-            bool bad = false;
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) bad |= in[a][k] >= 0 && (page[a][k] < 0 || page[a][k] >= p.cache.num_pages);
-            if (__any_sync(0xffffffffu, bad)) {
-                if (bad && p.status) atomicOr(p.status + seq[a], kKvBadIndex);
-                __syncwarp();
-#pragma unroll
-                for (int k = 0; k < kPer; ++k)
-                    if (in[a][k] >= 0 && (page[a][k] < 0 || page[a][k] >= p.cache.num_pages)) {
-                        const int key = (lane + 32 * k) * box;
-                        atomicAnd(&sm.valid[n_k & 15][key >> 5], ~(((1u << box) - 1u) << (key & 31)));
-                    }
-            }
-            __syncwarp();
-            const uint32_t bar = announce(sm.k_full + st, 2 * S::kStageK);
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int i = lane + 32 * k - k_first;
-                if (i >= 0 && i < k_groups)
-#pragma unroll
-                    for (int c = 0; c < D / 64; ++c)
-                        tma_load(ring_k + st * S::kStageK + c * 8192 + i * box * 128, &k_map, c * 64, head[a], max(in[a][k], 0), page[a][k], bar);
-            }
-            ++n_k;
-        };
-        auto load_values = [&](int a) {
-            const int st = n_v % RV;
-            if (n_v >= RV) ok = ok && warp_wait(sm.v_empty + st, (n_v / RV - 1) & 1, &sm.abort);
-            if (!ok) return;
-            const uint32_t bar = announce(sm.v_full + st, 2 * S::kStageV);
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int i = lane + 32 * k;
-                if (i < groups)
-#pragma unroll
-                    for (int c = 0; c < S::kVCh / 64; ++c)
-                        tma_load(ring_v + st * S::kStageV + c * 16384 + i * box * 128, &v_map, (D > 64 ? static_cast<int>(rank) * S::kVCh : 0) + c * 64,
-                                 head[a], max(in[a][k], 0), page[a][k], bar);
-            }
-            ++n_v;
-        };
-        auto next_keys = [&](int a) {
-            if (q_tok[a] >= 0) load_queries(a);
-            load_keys(a);
-        };
-#pragma unroll
-        for (int i = 0; i <= NS; ++i) look_up(i);
-#pragma unroll
-        for (int i = 0; i < NS; ++i)
-            if (seq[i] >= 0) next_keys(i);
+        // copies of the tile at [0]: groups [g0, g0 + n), all blocks from `block` on
+        const int shift = __ffs(bx.rows / bx.tokens) - 1;   // groups of a block in shared memory
+        auto copy = [&](uint32_t stage, const CUtensorMap* map, int g0, int n, int block, int blocks, uint32_t bar) {
 #pragma unroll 1
-        while (ok && seq[0] >= 0) {
-            look_up(NS + 1);
-            const bool more = seq[NS] >= 0, after = q_tok[NS] >= 0;   // a next part's queries wait for the last S before them
-            if (more && !after) load_keys(NS);
-            load_values(0);
-            if (more && after) next_keys(NS);
-#pragma unroll
-            for (int i = 0; i <= NS; ++i) {
-                head[i] = head[i + 1];
-                seq[i] = seq[i + 1];
-                q_tok[i] = q_tok[i + 1];
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) {
-                    page[i][k] = page[i + 1][k];
-                    in[i][k] = in[i + 1][k];
-                }
+            for (int r = 0; r < n; ++r) {
+                const int i = g0 + r, k = i >> 5;
+                const int pg = __shfl_sync(0xffffffffu, k == 0 ? page[0][0] : k == 1 ? page[0][1] : k == 2 ? page[0][2] : page[0][3], i & 31);
+                const int tk = __shfl_sync(0xffffffffu, k == 0 ? in[0][0] : k == 1 ? in[0][1] : k == 2 ? in[0][2] : in[0][3], i & 31);
+                const int box = r >> shift;
+                uint32_t dst = stage + (box * blocks * bx.rows + (r - (box << shift)) * bx.tokens) * 128;
+#pragma unroll 1
+                for (int c = 0; c < blocks; c += bx.blocks, dst += bx.rows * 128)
+                    if (elected()) tma_load(dst, map, max(tk, 0), block + c, head[0], pg, bar);
             }
+        };
+        int n = -1;   // tiles copied
+#pragma unroll 1
+        for (;; ++n) {
+            head[0] = head[1];
+            seq[0] = seq[1];
+            q_tok[0] = q_tok[1];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                page[0][k] = page[1][k];
+                in[0][k] = in[1][k];
+            }
+            if (n >= 0 && seq[0] < 0) break;
+            look_up(1);
+            if (n < 0) continue;
+            if (keys) {
+                if (q_tok[0] >= 0) {
+                    if (parts_begun > 0) ok = ok && warp_wait(&sm.q_empty, (parts_begun - 1) & 1, &sm.abort);
+                    if (!ok) break;
+                    ++parts_begun;
+                    const uint32_t bar = announce(&sm.q_full, 2 * cta_rows * D * 2);
+                    if (elected()) {
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) tma_load_q(smem_u32(q_s) + c * 16384, &q_map, c * 64, head[0] * p.G, q_tok[0], bar);
+                    }
+                }
+                if (n >= RK) ok = ok && warp_wait(sm.k_empty + n % RK, (n / RK - 1) & 1, &sm.abort);
+                if (!ok) break;
+                if (lane < 4) sm.valid[n & 15][lane] = 0xffffffffu;
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) bad |= in[0][k] >= 0 && (page[0][k] < 0 || page[0][k] >= p.cache.num_pages);
+                if (__any_sync(0xffffffffu, bad)) {
+                    if (bad && p.status) atomicOr(p.status + seq[0], kKvBadIndex);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < kPer; ++k)
+                        if (in[0][k] >= 0 && (page[0][k] < 0 || page[0][k] >= p.cache.num_pages))
+                            for (int key = (lane + 32 * k) * bx.tokens; key < (lane + 32 * k + 1) * bx.tokens; ++key)
+                                atomicAnd(&sm.valid[n & 15][key >> 5], ~(1u << (key & 31)));
+                }
+                __syncwarp();
+            } else {
+                if (n >= RV) ok = ok && warp_wait(sm.v_empty + n % RV, (n / RV - 1) & 1, &sm.abort);
+                if (!ok) break;
+            }
+            const uint32_t bar = announce(keys ? sm.k_full + n % RK : sm.v_full + n % RV, keys ? 2 * S::kStageK : 2 * S::kStageV);
+            copy(keys ? smem_u32(k_s) + n % RK * S::kStageK : smem_u32(v_s) + n % RV * S::kStageV, keys ? &k_map : &v_map,
+                 keys ? static_cast<int>(rank) * groups / 2 : 0, keys ? groups / 2 : groups, !keys && D > 64 ? static_cast<int>(rank) * kVBlocks : 0,
+                 keys ? kKBlocks : kVBlocks, bar);
         }
         // nothing is in flight when the pair ends: the last copies of every stage have landed (limits of their own, for after a give-up)
         if (rank == 0) {
-            for (int n = max(0, n_k - RK); n < n_k; ++n) tc::mbar_wait(sm.k_full + n % RK, (n / RK) & 1, kDrainLimit);
-            for (int n = max(0, n_v - RV); n < n_v; ++n) tc::mbar_wait(sm.v_full + n % RV, (n / RV) & 1, kDrainLimit);
+            const int r = keys ? RK : RV;
+            for (int i = max(0, n - r); i < n; ++i) tc::mbar_wait((keys ? sm.k_full : sm.v_full) + i % r, (i / r) & 1, kDrainLimit);
             if (parts_begun > 0) tc::mbar_wait(&sm.q_full, (parts_begun - 1) & 1, kDrainLimit);
         }
     } else if (warp == 9) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             // -------------------------------------------------------- products
-            w.more = true;
-            w.settle(p, ln, sh, rows);
+            Walk w(c, p, ln, sh);
             bool ok = true;
             int nq = 0, units = 0;   // S issued, parts begun
             uint32_t firsts = 0;     // by tile mod 32: the first of a part
             constexpr uint32_t id_s = tc::idesc_bf16(256, 128);
             constexpr uint32_t id_o = tc::idesc_f16(256, 2 * S::kVCh, 0, 1, 0) | (1u << 7) | (1u << 10);
             const uint32_t q_lo = (smem_u32(q_s) >> 4) + (1u << 16), k_lo = (smem_u32(k_s) >> 4) + (1u << 16);
-            const uint32_t v_lo = (smem_u32(v_s) >> 4) + ((16384u >> 4) << 16);
-            auto keys_landed = [&]() {
-                if (w.first()) ok = ok && stage_wait(&sm.q_full, units++ & 1, &sm.abort);
-                ok = ok && stage_wait(sm.k_full + nq % RK, (nq / RK) & 1, &sm.abort);
-            };
+            // K: from one 8-row group to the next, from one block of 64 channels to the next; V: blocks lie vb.rows rows apart
+            const uint32_t k_hi = (kDesc128 & ~0x3FFFu) | (kb.rows == 8 ? kKBlocks * 1024 >> 4 : 1024 >> 4), k_block = kb.rows * 128 >> 4;
+            const int v_shift = __ffs(vb.rows) - 1;
+            const uint32_t v_lo = (smem_u32(v_s) >> 4) + (static_cast<uint32_t>(vb.rows * 128 >> 4) << 16);
             auto issue_s = [&]() {   // of tile number nq, whose operands have landed
                 const uint32_t d = t_s + nq % NS * 128, b = k_lo + nq % RK * (S::kStageK >> 4);
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(d, q_lo + c * (16384 >> 4) + 2 * kk, b + c * (8192 >> 4) + 2 * kk, id_s, (c | kk) != 0);
+                        mma_ss(d, q_lo + c * (16384 >> 4) + 2 * kk, b + c * k_block + 2 * kk, k_hi, id_s, (c | kk) != 0);
                 commit_both(sm.s_full + nq % NS);
                 commit_both(sm.k_empty + nq % RK);
                 if (w.last()) commit_both(&sm.q_empty);
-                firsts = (firsts & ~(1u << (nq & 31))) | (static_cast<uint32_t>(w.first()) << (nq & 31));
-                ++nq;
-                w.next(p, ln, sh, rows);
             };
-            for (int i = 0; i < NS && w.more && ok; ++i) {
-                keys_landed();
-                tc::fence_after_sync();
-                if (ok) issue_s();
-            }
-#pragma unroll 1
-            for (int g = 0; g < nq && ok; ++g) {
-                const bool after = !w.more || w.first();   // a next part's queries may be late: not before this tile's O
-                if (!after) keys_landed();
-                ok = ok && stage_wait(sm.v_full + g % RV, (g / RV) & 1, &sm.abort);
-                ok = ok && stage_wait(sm.p_ready + (g & 1), (g >> 1) & 1, &sm.abort);
-                if (!ok) break;
-                tc::fence_after_sync();
-                if (!after) issue_s();   // into the place that the softmax has read
-                const uint32_t a = t_p + (g & 1) * 64, b = v_lo + g % RV * (S::kStageV >> 4);
+            auto issue_o = [&](int g) {
+                const uint32_t a = t_p + (g & 1) * S::kPStep, b = v_lo + g % RV * (S::kStageV >> 4);
                 const bool add = !((firsts >> (g & 31)) & 1);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) mma_ts(t_o, a + ks * 8, b + ks * (2048 >> 4), id_o, add || ks != 0);
+                for (int ks = 0; ks < 8; ++ks) {
+                    const int box = ks * 16 >> v_shift;
+                    mma_ts(t_o, a + ks / 4 * S::kPHalf + ks % 4 * 8, b + ((box * (kVBlocks - 1) * vb.rows + ks * 16) * 128 >> 4), id_o, add || ks != 0);
+                }
                 commit_both(sm.pv_done + (g & 1));
                 commit_both(sm.v_empty + g % RV);
-                if (after && w.more) {
-                    keys_landed();
+            };
+            // Turn g: the product with tile g's weights, then S of tile g + NS, into the place that the softmax has read -- and the product has,
+            // where P lies there.
+#pragma unroll 1
+            for (int g = -NS; ok && (g < nq || w.more); ++g) {
+                if (g >= 0) {
+                    ok = ok && stage_wait(sm.v_full + g % RV, (g / RV) & 1, &sm.abort);
+                    ok = ok && stage_wait(sm.p_ready + (g & 1), (g >> 1) & 1, &sm.abort);
+                    if (!ok) break;
                     tc::fence_after_sync();
-                    if (ok) issue_s();
+                    if (elected()) issue_o(g);
+                    __syncwarp();
+                }
+                if (w.more) {
+                    if (w.first()) ok = ok && stage_wait(&sm.q_full, units++ & 1, &sm.abort);
+                    ok = ok && stage_wait(sm.k_full + nq % RK, (nq / RK) & 1, &sm.abort);
+                    if (S::kOver && g >= 0) ok = ok && stage_wait(sm.pv_done + (g & 1), (g >> 1) & 1, &sm.abort);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (elected()) issue_s();
+                    __syncwarp();
+                    firsts = (firsts & ~(1u << (nq & 31))) | (static_cast<uint32_t>(w.first()) << (nq & 31));
+                    ++nq;
+                    w.next(p, ln, sh);
                 }
             }
             // everything issued is through before the pair ends
-            asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&sm.drained)) : "memory");
+            if (elected())
+                asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&sm.drained)) : "memory");
             tc::mbar_wait(&sm.drained, 0, kDrainLimit);
         }
         __syncwarp();
@@ -477,14 +492,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int g = 0;           // tile number
         uint32_t told = 0;   // phases of v_told
-        Part& c = w.c;
         do {
+            const int t0 = c.t0, t1 = c.t1;
             const int tok0 = c.i * ln.tokens, n_tok = tokens_of(ln, c), off = c.r.len - c.r.n;
             const int here = min(max(n_tok - cta_tok, 0), cta_tokens) * p.G;   // rows of this CTA
             const int end = ln.seen(c.r, c.i);
             float m = -INFINITY, base = 0.f, limit = -INFINITY, l = 0.f;
 #pragma unroll 1
-            for (int t = c.t0; t < c.t1; ++t, ++g) {
+            for (int t = t0; t < t1; ++t, ++g) {
                 if (!wait(sm.s_full + g % NS, (g / NS) & 1)) continue;
                 tc::fence_after_sync();
                 float s[2][32];
@@ -527,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sync_row_halves(quarter);
                 mx = fmaxf(mx, sm.mx[g & 1][half ^ 1][row]);
                 if (__any_sync(0xffffffffu, mx > limit)) {   // the same for both halves
-                    const bool fresh = t == c.t0;
+                    const bool fresh = t == t0;
                     // the tile before has been added: O stands still
                     const bool through = fresh || wait(sm.pv_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
                     tc::fence_after_sync();
@@ -549,8 +564,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (g >= 2) wait(sm.pv_done + (g & 1), ((g >> 1) - 1) & 1);   // the weights that were in this place have been read
-                tc::fence_after_sync();
+                if (!S::kOver && g >= 2) {   // the weights that were in this place have been read
+                    wait(sm.pv_done + (g & 1), ((g >> 1) - 1) & 1);
+                    tc::fence_after_sync();
+                }
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -562,14 +579,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum[e & 1] = add2(sum[e & 1], y);
                         w2[e] = StateIO<bf16>::pack(y.x, y.y);
                     }
-                    tmem_st16u(t_p + my_lanes + (g & 1) * 64 + half * 32 + i * 16, w2);
+                    tmem_st16u(t_p + my_lanes + (g & 1) * S::kPStep + half * S::kPHalf + i * 16, w2);
                 }
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 if (late) {
                     // Strays among the values that some rows do not see are taken out of this CTA's channels, and what the boxes brought from
                     // behind the last key that anyone sees.
-                    const int k0 = max(0, off + tok0 + 1 - t * kKeys), kend = end - t * kKeys, k1 = min(kKeys, (kend + box - 1) / box * box);
+                    const int k0 = max(0, off + tok0 + 1 - t * kKeys), kend = end - t * kKeys, k1 = min(kKeys, (kend + vb.tokens - 1) / vb.tokens * vb.tokens);
                     bool landed = k0 < k1;
                     if (landed) {   // the first CTA's barrier tells of both; it tells the second one
                         if (rank == 0) {
@@ -586,7 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int x = threadIdx.x; x < (k1 - k0) * (S::kVCh / 8); x += kSoft) {
                             const int key = k0 + x / (S::kVCh / 8), ch = x % (S::kVCh / 8);
-                            uint8_t* const at = st + ch / 8 * 16384 + key * 128 + ((ch ^ key) & 7) * 16;
+                            const int box = key >> (__ffs(vb.rows) - 1);
+                            uint8_t* const at = st + (box * (kVBlocks - 1) * vb.rows + ch / 8 * vb.rows + key) * 128 + ((ch ^ key) & 7) * 16;
                             if (key < kend) found |= attn::take_strays<bf16>(at);
                             else *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
                         }
@@ -695,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_before_sync();
             }
             sync_softmax();   // the sums and sm.last have been read
-        } while (next_part(ln, sh, p.B, p.Hkv, c, rows));
+        } while (to_next_part(p, ln, sh, c));
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -704,33 +722,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem), "r"(512));
 }
 
-// Boxes of 64 channels of one head of `box` tokens of a page, from any strides; false if the driver refuses them.
-bool cache_map(CUtensorMap* m, const ChunkParams& p, const void* half, int D, int box) {
+// Boxes of one head of a page, from any strides: (64 channels, token, block of 64 channels, head, page); false if the driver
+// refuses them.
+bool cache_map(CUtensorMap* m, const ChunkParams& p, const void* half, int D, const Boxes& b) {
     const KvCache& c = p.cache;
     auto bytes = [&](long long stride) { return stride ? static_cast<uint64_t>(stride) * 2 : static_cast<uint64_t>(D) * 2; };
-    const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.Hkv), static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(c.num_pages)};
-    const uint64_t strides[3] = {bytes(c.head_stride), bytes(c.token_stride), bytes(c.page_stride)};
-    const uint32_t boxes[4] = {64, 1, static_cast<uint32_t>(box), 1};
-    return make_tensor_map_bf16(m, half, 4, dims, strides, boxes);
+    const uint64_t dims[5] = {64, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(D / 64), static_cast<uint64_t>(p.Hkv),
+                              static_cast<uint64_t>(c.num_pages)};
+    const uint64_t strides[4] = {bytes(c.token_stride), 128, bytes(c.head_stride), bytes(c.page_stride)};
+    const uint32_t boxes[5] = {64, static_cast<uint32_t>(b.tokens), static_cast<uint32_t>(b.blocks), 1, 1};
+    return make_tensor_map_bf16(m, half, 5, dims, strides, boxes);
 }
 
 template <int D>
 cudaError_t launch(const ChunkParams& p, int sms, bool* done, cudaStream_t stream) {
     using S = Tc<D>;
     *done = false;
-    int box = 16;   // tokens that always lie in one page
-    while (p.cache.page_size % box != 0) box /= 2;
+    int two = 128;   // tokens that always lie in one page
+    while (p.cache.page_size % two != 0) two /= 2;
+    const int k_blocks = D / 64, v_blocks = S::kVCh / 64;
+    const Boxes kb = two >= 64 ? Boxes{64, 1, 64} : two >= 8 ? Boxes{8, k_blocks, 8} : Boxes{two, 1, 64};
+    const Boxes vb = two >= 16 ? Boxes{two, v_blocks, two} : Boxes{two, 1, 128};
     CUtensorMap k, v, q;
     const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.Hq), static_cast<uint64_t>(p.T)};
     const uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(p.ldq) * 2};
     const uint32_t boxes[3] = {64, static_cast<uint32_t>(p.G), static_cast<uint32_t>(128 / p.G)};
-    if (!cache_map(&k, p, p.cache.k, D, box) || !cache_map(&v, p, p.cache.v, D, box) || !make_tensor_map_bf16(&q, p.q, 3, dims, strides, boxes))
+    if (!cache_map(&k, p, p.cache.k, D, kb) || !cache_map(&v, p, p.cache.v, D, vb) || !make_tensor_map_bf16(&q, p.q, 3, dims, strides, boxes))
         return cudaSuccess;
     *done = true;
     const cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     const int pairs = min(sms / 2, kMaxWorkers / 2);
-    return launch_dependent_cluster(chunk_tc_kernel<S>, 2, dim3(2 * pairs), dim3(kThreads), S::kSmem, stream, p, k, v, q, box);
+    return launch_dependent_cluster(chunk_tc_kernel<S>, 2, dim3(2 * pairs), dim3(kThreads), S::kSmem, stream, p, k, v, q, kb, vb);
 }
 
 }  // namespace

@@ -50,7 +50,7 @@ int main() {
             Part c{};
             c.b = b;
             c.r = rs[b];
-            for (bool ok = first_part(ln, sh, B, Hkv, start[b], c, rows); ok; ok = next_part(ln, sh, B, Hkv, c, rows)) {
+            for (bool ok = first_part(ln, sh, start[b], c) || next_part(ln, sh, B, Hkv, c, rows); ok; ok = next_part(ln, sh, B, Hkv, c, rows)) {
                 got[std::make_tuple(c.b, c.hk, c.i)].push_back({w, c});
                 if (!c.whole()) ++(c.t0 == 0 ? begins : goes_on);
             }
