@@ -79,12 +79,12 @@ __device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_cta(smem_u32(bar), rank)) : "memory");
 }
 
-// A box of the map at (token, block of 64 channels, head, page) into this CTA's shared memory, its bytes counted by the first CTA's
-// barrier (at cluster address `bar`).
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int token, int block, int head, int page, uint32_t bar) {
+// A box of the map at (0, c1, .. c4) into this CTA's shared memory, its bytes counted by the first CTA's barrier (at cluster address
+// `bar`).
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int c1, int c2, int c3, int c4, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(token), "r"(block), "r"(head), "r"(page), "r"(bar)
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
         : "memory");
 }
 __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map, int ch, int head, int token, uint32_t bar) {
@@ -126,11 +126,11 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo,
         "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(idesc),
         "r"(static_cast<uint32_t>(add)), "n"(kDesc128), "r"(b_hi));
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
         "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d), "r"(a), "r"(b_lo), "r"(idesc),
-        "r"(static_cast<uint32_t>(add)), "n"(kDesc128));
+        "r"(static_cast<uint32_t>(add)), "r"(b_hi));
 }
 
 // 32 consecutive columns of this thread's lane, to be waited for; 32 words to such columns.
@@ -173,14 +173,20 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-// How keys and values lie in a stage.  A box is `tokens` tokens of one page and `blocks` blocks of 64 channels; its block of `tokens`
-// rows of 128 bytes is followed by the next block, and a box by the next.  As the tensor cores want it: for keys (whose 8-row
-// groups have one distance) boxes of 8 tokens and all blocks, or one block of all 64 keys; for values (whose 16 keys of a product
-// lie in one box) any number of tokens from 16 up and both blocks.  Pages that 8 or 16 do not divide give boxes of one block and
-// fewer tokens, which make up blocks of 64 keys or 128 values.
+// The boxes that are copied.  A stage holds groups of 8 tokens, of each its blocks of 64 channels, of each 8 rows of 128 bytes: with
+// that, keys and values have one distance from a group to the next and one from a block to the next, as the tensor cores want it.
+// Where pages are a multiple of 8 tokens and follow one another, or the heads of one do, the map is (64 channels, 8 tokens, block,
+// group of 8, page and head) and a box is all the blocks of as many tokens as always lie in one page.  (A copy takes its thread
+// 150 cycles: pages of 16 by boxes of 8 keys, or 16 tokens' one block, were bound by that.)  Otherwise it is (64 channels, token,
+// block, head, page) and a box one block of 1 to 8 tokens.
 struct Boxes {
-    int tokens, blocks;   // of a box
-    int rows;             // of a block in shared memory, a power of two
+    int tokens;        // of a box
+    int whole;         // the first kind of map
+    int group, head;   // what a page adds to the coordinates of group and head there
+};
+struct Division {   // by the page size, of 31 bits: x -> x * mul >> 32 >> shift, or x where mul is 0
+    uint32_t mul, shift;
+    __device__ __forceinline__ int of(int x) const { return mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), mul) >> shift) : x; }
 };
 
 // A walk over the tiles of a worker's parts.  The part lies in memory (to_next_part is a call), what every tile asks for does not.
@@ -239,7 +245,7 @@ __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 5, %0;" 
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                    const __grid_constant__ CUtensorMap q_map, const Boxes kb, const Boxes vb) {
+                    const __grid_constant__ CUtensorMap q_map, const Boxes kb, const Boxes vb, const Division by_page) {
     constexpr int D = S::D, RK = S::RK, RV = S::RV;
     constexpr int kKBlocks = D / 64, kVBlocks = S::kVCh / 64;   // blocks of 64 channels in a CTA's stages
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -320,10 +326,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             head[a] = part_head;
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
+                if (k > 0 && groups <= 32 * k) break;
                 const int i = lane + 32 * k, j = w.t * kKeys + i * bx.tokens;
                 in[a][k] = page[a][k] = -1;
                 if (i < groups && j < end) {
-                    const int x = j / ps;
+                    const int x = by_page.of(j);
                     in[a][k] = j - x * ps;
                     page[a][k] = table[x];   // looked at when it is used
                 }
@@ -339,19 +346,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             return in_cta(smem_u32(bar), 0);
         };
-        // copies of the tile at [0]: groups [g0, g0 + n), all blocks from `block` on
-        const int shift = __ffs(bx.rows / bx.tokens) - 1;   // groups of a block in shared memory
+        // copies of the tile at [0]: boxes [g0, g0 + n), all blocks from `block` on, by the lanes that have them
         auto copy = [&](uint32_t stage, const CUtensorMap* map, int g0, int n, int block, int blocks, uint32_t bar) {
 #pragma unroll 1
-            for (int r = 0; r < n; ++r) {
-                const int i = g0 + r, k = i >> 5;
-                const int pg = __shfl_sync(0xffffffffu, k == 0 ? page[0][0] : k == 1 ? page[0][1] : k == 2 ? page[0][2] : page[0][3], i & 31);
-                const int tk = __shfl_sync(0xffffffffu, k == 0 ? in[0][0] : k == 1 ? in[0][1] : k == 2 ? in[0][2] : in[0][3], i & 31);
-                const int box = r >> shift;
-                uint32_t dst = stage + (box * blocks * bx.rows + (r - (box << shift)) * bx.tokens) * 128;
+            for (int k = g0 >> 5; k <= (g0 + n - 1) >> 5; ++k) {
+                const int pg = k == 0 ? page[0][0] : k == 1 ? page[0][1] : k == 2 ? page[0][2] : page[0][3];
+                const int tk = max(k == 0 ? in[0][0] : k == 1 ? in[0][1] : k == 2 ? in[0][2] : in[0][3], 0);
+                const int r = lane + 32 * k - g0, row = r * bx.tokens;
+                uint32_t dst = stage + (row >> 3) * blocks * 1024 + (row & 7) * 128;
+                if (r >= 0 && r < n) {
+                    if (bx.whole) {
+                        const bool there = pg >= 0 && pg < p.cache.num_pages;   // (the coordinates of another would be some other's)
+                        tma_load(dst, map, 0, block, there ? pg * bx.group + (tk >> 3) : 0, there ? pg * bx.head + head[0] : -1, bar);
+                    } else {
 #pragma unroll 1
-                for (int c = 0; c < blocks; c += bx.blocks, dst += bx.rows * 128)
-                    if (elected()) tma_load(dst, map, max(tk, 0), block + c, head[0], pg, bar);
+                        for (int c = 0; c < blocks; ++c, dst += 1024) tma_load(dst, map, tk, block + c, head[0], pg, bar);
+                    }
+                }
+                __syncwarp();
             }
         };
         int n = -1;   // tiles copied
@@ -420,17 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t id_s = tc::idesc_bf16(256, 128);
             constexpr uint32_t id_o = tc::idesc_f16(256, 2 * S::kVCh, 0, 1, 0) | (1u << 7) | (1u << 10);
             const uint32_t q_lo = (smem_u32(q_s) >> 4) + (1u << 16), k_lo = (smem_u32(k_s) >> 4) + (1u << 16);
-            // K: from one 8-row group to the next, from one block of 64 channels to the next; V: blocks lie vb.rows rows apart
-            const uint32_t k_hi = (kDesc128 & ~0x3FFFu) | (kb.rows == 8 ? kKBlocks * 1024 >> 4 : 1024 >> 4), k_block = kb.rows * 128 >> 4;
-            const int v_shift = __ffs(vb.rows) - 1;
-            const uint32_t v_lo = (smem_u32(v_s) >> 4) + (static_cast<uint32_t>(vb.rows * 128 >> 4) << 16);
+            // from one group of 8 to the next; from one block of 64 channels to the next, 1024 bytes
+            constexpr uint32_t k_hi = (kDesc128 & ~0x3FFFu) | (kKBlocks * 1024 >> 4), v_hi = (kDesc128 & ~0x3FFFu) | (kVBlocks * 1024 >> 4);
+            const uint32_t v_lo = (smem_u32(v_s) >> 4) + ((1024u >> 4) << 16);
             auto issue_s = [&]() {   // of tile number nq, whose operands have landed
                 const uint32_t d = t_s + nq % NS * 128, b = k_lo + nq % RK * (S::kStageK >> 4);
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(d, q_lo + c * (16384 >> 4) + 2 * kk, b + c * k_block + 2 * kk, k_hi, id_s, (c | kk) != 0);
+                        mma_ss(d, q_lo + c * (16384 >> 4) + 2 * kk, b + c * (1024 >> 4) + 2 * kk, k_hi, id_s, (c | kk) != 0);
                 commit_both(sm.s_full + nq % NS);
                 commit_both(sm.k_empty + nq % RK);
                 if (w.last()) commit_both(&sm.q_empty);
@@ -439,10 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t a = t_p + (g & 1) * S::kPStep, b = v_lo + g % RV * (S::kStageV >> 4);
                 const bool add = !((firsts >> (g & 31)) & 1);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const int box = ks * 16 >> v_shift;
-                    mma_ts(t_o, a + ks / 4 * S::kPHalf + ks % 4 * 8, b + ((box * (kVBlocks - 1) * vb.rows + ks * 16) * 128 >> 4), id_o, add || ks != 0);
-                }
+                for (int ks = 0; ks < 8; ++ks) mma_ts(t_o, a + ks / 4 * S::kPHalf + ks % 4 * 8, b + ks * (kVBlocks * 2048 >> 4), v_hi, id_o, add || ks != 0);
                 commit_both(sm.pv_done + (g & 1));
                 commit_both(sm.v_empty + g % RV);
             };
@@ -603,8 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int x = threadIdx.x; x < (k1 - k0) * (S::kVCh / 8); x += kSoft) {
                             const int key = k0 + x / (S::kVCh / 8), ch = x % (S::kVCh / 8);
-                            const int box = key >> (__ffs(vb.rows) - 1);
-                            uint8_t* const at = st + (box * (kVBlocks - 1) * vb.rows + ch / 8 * vb.rows + key) * 128 + ((ch ^ key) & 7) * 16;
+                            uint8_t* const at = st + (key >> 3) * (kVBlocks * 1024) + ch / 8 * 1024 + (key & 7) * 128 + ((ch ^ key) & 7) * 16;
                             if (key < kend) found |= attn::take_strays<bf16>(at);
                             else *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
                         }
@@ -722,15 +729,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem), "r"(512));
 }
 
-// Boxes of one head of a page, from any strides: (64 channels, token, block of 64 channels, head, page); false if the driver
-// refuses them.
-bool cache_map(CUtensorMap* m, const ChunkParams& p, const void* half, int D, const Boxes& b) {
+// The map of a half of the cache, and the boxes of up to `most` tokens and `blocks` blocks; false if the driver refuses it.
+bool cache_map(CUtensorMap* m, Boxes* b, const ChunkParams& p, const void* half, int D, int most, int blocks) {
     const KvCache& c = p.cache;
     auto bytes = [&](long long stride) { return stride ? static_cast<uint64_t>(stride) * 2 : static_cast<uint64_t>(D) * 2; };
-    const uint64_t dims[5] = {64, static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(D / 64), static_cast<uint64_t>(p.Hkv),
-                              static_cast<uint64_t>(c.num_pages)};
+    const uint64_t ps = c.page_size, pages = c.num_pages, heads = p.Hkv, parts = D / 64;
+    int two = 128;   // tokens that always lie in one page
+    while (c.page_size % two != 0) two /= 2;
+    const bool pages_follow = pages == 1 || c.page_stride == c.page_size * c.token_stride;
+    const bool heads_follow = pages == 1 || heads == 1 || c.page_stride == p.Hkv * c.head_stride;
+    *b = Boxes{two < most ? two : most, two >= 8 && (pages_follow || (heads_follow && pages * heads <= INT32_MAX)), 0, 0};
+    if (b->whole) {
+        b->group = pages_follow ? c.page_size / 8 : 0;
+        b->head = pages_follow ? 0 : p.Hkv;
+        const uint64_t dims[5] = {64, 8, parts, pages_follow ? pages * ps / 8 : ps / 8, pages_follow ? heads : pages * heads};
+        const uint64_t strides[4] = {bytes(c.token_stride), 128, bytes(c.token_stride) * 8, pages_follow || heads > 1 ? bytes(c.head_stride) : bytes(c.page_stride)};
+        const uint32_t boxes[5] = {64, 8, static_cast<uint32_t>(blocks), static_cast<uint32_t>(b->tokens / 8), 1};
+        return make_tensor_map_bf16(m, half, 5, dims, strides, boxes);
+    }
+    b->tokens = two < 8 ? two : 8;
+    const uint64_t dims[5] = {64, ps, parts, heads, pages};
     const uint64_t strides[4] = {bytes(c.token_stride), 128, bytes(c.head_stride), bytes(c.page_stride)};
-    const uint32_t boxes[5] = {64, static_cast<uint32_t>(b.tokens), static_cast<uint32_t>(b.blocks), 1, 1};
+    const uint32_t boxes[5] = {64, static_cast<uint32_t>(b->tokens), 1, 1, 1};
     return make_tensor_map_bf16(m, half, 5, dims, strides, boxes);
 }
 
@@ -738,22 +758,22 @@ template <int D>
 cudaError_t launch(const ChunkParams& p, int sms, bool* done, cudaStream_t stream) {
     using S = Tc<D>;
     *done = false;
-    int two = 128;   // tokens that always lie in one page
-    while (p.cache.page_size % two != 0) two /= 2;
-    const int k_blocks = D / 64, v_blocks = S::kVCh / 64;
-    const Boxes kb = two >= 64 ? Boxes{64, 1, 64} : two >= 8 ? Boxes{8, k_blocks, 8} : Boxes{two, 1, 64};
-    const Boxes vb = two >= 16 ? Boxes{two, v_blocks, two} : Boxes{two, 1, 128};
+    Boxes kb, vb;
+    Division by_page{0, 0};
+    int bits = 0;   // of page_size, rounded up
+    while ((1ll << bits) < p.cache.page_size) ++bits;
+    if (bits > 0) by_page = Division{static_cast<uint32_t>(((1ull << (31 + bits)) + p.cache.page_size - 1) / p.cache.page_size), static_cast<uint32_t>(bits - 1)};
     CUtensorMap k, v, q;
     const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.Hq), static_cast<uint64_t>(p.T)};
     const uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(p.ldq) * 2};
     const uint32_t boxes[3] = {64, static_cast<uint32_t>(p.G), static_cast<uint32_t>(128 / p.G)};
-    if (!cache_map(&k, p, p.cache.k, D, kb) || !cache_map(&v, p, p.cache.v, D, vb) || !make_tensor_map_bf16(&q, p.q, 3, dims, strides, boxes))
+    if (!cache_map(&k, &kb, p, p.cache.k, D, 64, D / 64) || !cache_map(&v, &vb, p, p.cache.v, D, 128, S::kVCh / 64) || !make_tensor_map_bf16(&q, p.q, 3, dims, strides, boxes))
         return cudaSuccess;
     *done = true;
     const cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     const int pairs = min(sms / 2, kMaxWorkers / 2);
-    return launch_dependent_cluster(chunk_tc_kernel<S>, 2, dim3(2 * pairs), dim3(kThreads), S::kSmem, stream, p, k, v, q, kb, vb);
+    return launch_dependent_cluster(chunk_tc_kernel<S>, 2, dim3(2 * pairs), dim3(kThreads), S::kSmem, stream, p, k, v, q, kb, vb, by_page);
 }
 
 }  // namespace
