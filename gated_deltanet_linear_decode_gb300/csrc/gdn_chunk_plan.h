@@ -8,6 +8,8 @@
 // units of a sequence take is a sum in closed form, and a worker finds its first unit by bisection.)
 #pragma once
 
+#include <stdint.h>
+
 #ifdef __CUDACC__
 #define GDN_HD __host__ __device__ __forceinline__
 #else
@@ -21,7 +23,7 @@ GDN_HD long long least(long long a, long long b) { return a < b ? a : b; }
 GDN_HD long long most(long long a, long long b) { return a > b ? a : b; }
 // a / b rounded down, with the short division where it will do (a, b >= 0).
 GDN_HD long long quot(long long a, long long b) {
-    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<unsigned>(a) / static_cast<unsigned>(b)) : a / b;
+    return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
 }
 
 // The new tokens of one sequence: n rows from row0 on, the last n of its len tokens (len may be less than n).
@@ -30,9 +32,10 @@ struct Rows {
 };
 
 struct Line {
-    int tokens, keys, cost;   // tokens of a unit, keys of a tile, numbers for a unit's begin and end
+    int tokens, key_bits, cost;   // tokens of a unit, log2 of a tile's keys, numbers for a unit's begin and end
 
-    GDN_HD int units(const Rows& r) const { return static_cast<int>((static_cast<long long>(r.n) + tokens - 1) / tokens); }
+    GDN_HD int keys() const { return 1 << key_bits; }
+    GDN_HD int units(const Rows& r) const { return static_cast<int>((static_cast<uint32_t>(r.n) + static_cast<uint32_t>(tokens) - 1) / static_cast<uint32_t>(tokens)); }
     // keys that unit i sees
     GDN_HD int seen(const Rows& r, int i) const {
         const long long s = least((i + 1ll) * tokens, r.n) + r.len - r.n;
@@ -67,20 +70,21 @@ GDN_HD int workers_of(long long total, int workers, int min_share) { return stat
 // A worker's part of a unit: tiles [t0, t1) of `tiles`.
 struct Part {
     Rows r;
-    int b, hk, i, tiles, t0, t1;
+    int units;      // of the sequence and a kv head
+    int b, hk, i, seen, tiles, t0, t1;
     long long at;   // the unit's first number
 
     GDN_HD bool whole() const { return t0 == 0 && t1 == tiles; }
 };
 
-GDN_HD int tiles_of(int seen, int keys) { return static_cast<int>((static_cast<long long>(seen) + keys - 1) / keys); }
-
 // The tiles of the unit that the share holds; false if there is nothing of it.
 GDN_HD bool clip(const Line& ln, const Share& sh, Part& c) {
-    c.tiles = tiles_of(ln.seen(c.r, c.i), ln.keys);
+    const int up = ln.keys() - 1;
+    c.seen = ln.seen(c.r, c.i);
+    c.tiles = static_cast<int>((static_cast<uint32_t>(c.seen) + up) >> ln.key_bits);
     const long long base = c.at + ln.cost;   // the first tile's number
-    c.t0 = sh.first > base ? static_cast<int>(least(c.tiles, quot(sh.first - base + ln.keys - 1, ln.keys))) : 0;
-    c.t1 = sh.last > base ? static_cast<int>(least(c.tiles, quot(sh.last - base + ln.keys - 1, ln.keys))) : 0;
+    c.t0 = sh.first > base ? static_cast<int>(least(c.tiles, (sh.first - base + up) >> ln.key_bits)) : 0;
+    c.t1 = sh.last > base ? static_cast<int>(least(c.tiles, (sh.last - base + up) >> ln.key_bits)) : 0;
     return c.tiles > 0 ? c.t0 < c.t1 : c.at >= sh.first && c.at < sh.last;
 }
 
@@ -88,9 +92,9 @@ GDN_HD bool clip(const Line& ln, const Share& sh, Part& c) {
 template <class F>
 GDN_HD bool next_part(const Line& ln, const Share& sh, int B, int Hkv, Part& c, F rows) {
     for (;;) {
-        c.at += ln.cost + ln.seen(c.r, c.i);
+        c.at += ln.cost + c.seen;
         if (c.at >= sh.last) return false;
-        if (++c.i == ln.units(c.r)) {
+        if (++c.i == c.units) {
             c.i = 0;
             if (++c.hk == Hkv) {
                 c.hk = 0;
@@ -98,6 +102,7 @@ GDN_HD bool next_part(const Line& ln, const Share& sh, int B, int Hkv, Part& c, 
                     if (++c.b >= B) return false;
                     c.r = rows(c.b);
                 } while (c.r.n == 0);
+                c.units = ln.units(c.r);
             }
         }
         if (clip(ln, sh, c)) return true;
@@ -110,7 +115,8 @@ GDN_HD bool first_part(const Line& ln, const Share& sh, long long start, Part& c
     const long long head = ln.head(c.r), in = sh.first - start;
     c.hk = static_cast<int>(quot(in, head));
     const long long x = in - c.hk * head;
-    int lo = 0, hi = ln.units(c.r);   // the last unit with before(unit) <= x
+    c.units = ln.units(c.r);
+    int lo = 0, hi = c.units;   // the last unit with before(unit) <= x
     while (hi - lo > 1) {
         const int mid = lo + (hi - lo) / 2;
         if (ln.before(c.r, mid) <= x) lo = mid;

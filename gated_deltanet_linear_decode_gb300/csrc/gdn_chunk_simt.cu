@@ -50,7 +50,8 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) chunk_simt_kernel(const __
     __shared__ PlanSmem plan_s;
     __shared__ uint8_t there_s[2][kKt];
     __shared__ int last_s;
-    const Line ln{kRt / p.G, kKt, S::kCost};
+    const Line ln{kRt / p.G, 6, S::kCost};
+    static_assert(kKt == 1 << 6, "keys of a tile");
     Share sh;
     Part c;
     const int worker = static_cast<int>(blockIdx.x);
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) chunk_simt_kernel(const __
 
     do {
         const int tok0 = c.i * ln.tokens, n_rows = tokens_of(ln, c) * p.G, off = c.r.len - c.r.n;
-        const int end = ln.seen(c.r, c.i);   // keys from here on are nobody's
+        const int end = c.seen;   // keys from here on are nobody's
         long long key_off = 0;
         bool there = false;
         auto look_up = [&](int t) {

@@ -34,6 +34,7 @@ using attn::kWaitLimit;
 using attn::stage_wait;
 using tc::smem_u32;
 constexpr int kDrainLimit = 1 << 14;   // polls for what is in flight at the end
+constexpr int kMinShare = 512;        // keys of a worker, at least
 constexpr float kSlack = 8.0f;   // how far a score may pass its row's base
 constexpr int kRows = 256, kKeys = 128, kThreads = 352, kSoft = 256, NS = 2;   // places of S
 
@@ -50,7 +51,7 @@ struct Tc {
     // tensor memory
     static constexpr int kO = 0, kS = kOver ? 256 : 128, kP = kOver ? kS : 384;
     static constexpr int kPStep = kOver ? 128 : 64, kPHalf = kOver ? 64 : 32;   // columns from one P to the other, from one half of the keys to the other
-    static constexpr int kCost = 256;
+    static constexpr int kCost = D == 256 ? 1024 : 768;       // of a unit: its begin and end take as long as so many keys
     static_assert(kSmem <= 232448, "shape");
 };
 
@@ -189,6 +190,28 @@ struct Division {   // by the page size, of 31 bits: x -> x * mul >> 32 >> shift
     __device__ __forceinline__ int of(int x) const { return mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), mul) >> shift) : x; }
 };
 
+// 16 bf16 of a row: one access of 32 bytes where rows begin on such, else two of 16.  (A part's end is bound by these: each
+// of a warp's lanes has another row, and an access of a lane takes its turn whatever its size.)
+__device__ __forceinline__ void load16(const void* at, bool whole, uint32_t (&v)[8]) {
+    if (whole) {
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]) : "l"(at));
+    } else {
+        const uint4 a = static_cast<const uint4*>(at)[0], b = static_cast<const uint4*>(at)[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+}
+__device__ __forceinline__ void store16(void* at, bool whole, const uint32_t (&v)[8]) {
+    if (whole) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                     "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+    } else {
+        static_cast<uint4*>(at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+        static_cast<uint4*>(at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
+__device__ __forceinline__ bool on32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31) == 0; }
+
 // A walk over the tiles of a worker's parts.  The part lies in memory (to_next_part is a call), what every tile asks for does not.
 struct Walk {
     Part& c;
@@ -239,6 +262,42 @@ __device__ __noinline__ void add_strays(const ChunkParams& p, const Part& c, int
     }
 }
 
+// The join of n parts of a few rows, by items of a row's 4 channels: eight parts' loads together.  A call, for the size of the
+// code around it.
+template <int D>
+__device__ __noinline__ void join_few(const ChunkParams& p, const Part& c, const Parts<kRows, D>& parts, int w0, int n, int tok0, int cta_tok, int rows, int row0) {
+    constexpr int kAt = 8;
+    auto row_of = [&](int k) { return (k == 0 ? 2 * static_cast<size_t>(w0) + 1 : 2 * static_cast<size_t>(w0 + k)) * kRows + row0; };
+#pragma unroll 1
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kSoft) {
+        const int r = i / (D / 4), ch = i % (D / 4) * 4, in = r / p.G;
+        float mm = -INFINITY, ll = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) mm = fmaxf(mm, __ldcg(&parts.ml[row_of(k) + r].x));
+        mm = mm == -INFINITY ? 0.f : mm;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int k0 = 0; k0 < n; k0 += kAt) {   // past the last part it again, without weight
+            float2 z[kAt];
+            float4 x[kAt];
+#pragma unroll
+            for (int v = 0; v < kAt; ++v) {
+                const size_t at = row_of(min(k0 + v, n - 1)) + r;
+                z[v] = __ldcg(parts.ml + at);
+                x[v] = __ldcg(reinterpret_cast<const float4*>(parts.o + at * D + ch));
+            }
+#pragma unroll
+            for (int v = 0; v < kAt; ++v) {
+                if (k0 + v >= n) break;
+                const float f = ex2(z[v].x - mm);
+                ll = fmaf(f, z[v].y, ll);
+                y = make_float4(fmaf(f, x[v].x, y.x), fmaf(f, x[v].y, y.y), fmaf(f, x[v].z, y.z), fmaf(f, x[v].w, y.w));
+            }
+        }
+        put<bf16, D>(p, true, static_cast<long long>(c.r.row0) + tok0 + cta_tok + in, c.hk * p.G + r - in * p.G, ch, attn::times(y, ll == 0.f ? 0.f : 1.0f / ll));
+    }
+}
+
 __device__ __forceinline__ void sync_row_halves(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); }
 __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 5, %0;" ::"n"(kSoft) : "memory"); }
 
@@ -280,10 +339,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");   // the barriers are there before asynchronous arrivals on them
     const int cta_tokens = 128 / p.G, cta_rows = cta_tokens * p.G;   // of a unit, in each CTA
-    const Line ln{2 * cta_tokens, kKeys, S::kCost};
+    const Line ln{2 * cta_tokens, 7, S::kCost};
+    static_assert(kKeys == 1 << 7, "keys of a tile");
     Share sh;
     Part c;
-    if (!my_share(p, ln, worker, workers, kKeys, sm.plan, sh, c)) return;   // both CTAs of a pair, or neither
+    if (!my_share(p, ln, worker, workers, kMinShare, sm.plan, sh, c)) return;   // both CTAs of a pair, or neither
     // rows past cta_rows, which no copy writes
     for (int i = threadIdx.x; i < (128 - cta_rows) * (D / 8); i += kThreads)
         *reinterpret_cast<uint4*>(q_s + i / ((128 - cta_rows) * 8) * 16384 + cta_rows * 128 + i % ((128 - cta_rows) * 8) * 16) = make_uint4(0, 0, 0, 0);
@@ -319,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 part_seq = c.b;
                 part_head = c.hk;
                 q_tok[a] = c.r.row0 + c.i * ln.tokens + static_cast<int>(rank) * cta_tokens;
-                end = ln.seen(c.r, c.i);
+                end = c.seen;
                 table = p.block_table + static_cast<size_t>(c.b) * p.max_pages;
             }
             seq[a] = part_seq;
@@ -504,8 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int t0 = c.t0, t1 = c.t1;
             const int tok0 = c.i * ln.tokens, n_tok = tokens_of(ln, c), off = c.r.len - c.r.n;
             const int here = min(max(n_tok - cta_tok, 0), cta_tokens) * p.G;   // rows of this CTA
-            const int end = ln.seen(c.r, c.i);
-            float m = -INFINITY, base = 0.f, limit = -INFINITY, l = 0.f;
+            const int end = c.seen;
+            float m = -INFINITY, base = 0.f, limit = -INFINITY, l = 0.f;   // m: base, or -inf for a row that has seen no key
 #pragma unroll 1
             for (int t = t0; t < t1; ++t, ++g) {
                 if (!wait(sm.s_full + g % NS, (g / NS) & 1)) continue;
@@ -549,17 +609,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sm.mx[g & 1][half][row] = mx;
                 sync_row_halves(quarter);
                 mx = fmaxf(mx, sm.mx[g & 1][half ^ 1][row]);
-                if (__any_sync(0xffffffffu, mx > limit)) {   // the same for both halves
+                // (a row's base moves by its own scores alone: its result does not depend on the rows beside it)
+                const bool up = mx > limit;
+                if (__any_sync(0xffffffffu, up)) {   // the same for both halves
                     const bool fresh = t == t0;
                     // the tile before has been added: O stands still
                     const bool through = fresh || wait(sm.pv_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
                     tc::fence_after_sync();
-                    const float m2 = fmaxf(m, mx);
-                    const bool none = m2 == -INFINITY;   // a row that has seen no key
-                    const float f = none ? 0.f : ex2(m - m2);
-                    m = m2;
-                    base = none ? 0.f : m2;
-                    limit = none ? -INFINITY : m2 + kSlack;
+                    const float f = up ? ex2(m - mx) : 1.0f;
+                    if (up) {
+                        m = base = mx;
+                        limit = mx + kSlack;
+                    }
                     l *= f;
                     if (!fresh && through) {
 #pragma unroll 1
@@ -629,15 +690,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) arrive_at(sm.p_ready + (g & 1), 0);
             }
             // -------------------------------------------------------- the part's end
-            const bool any = c.t0 < c.t1, whole = c.whole();
-            const size_t place = Parts<kRows, D>::place(worker, c);
+            const bool any = t0 < t1, whole = c.whole();
             const long long tr = static_cast<long long>(c.r.row0) + tok0 + tok;
             const int h = c.hk * p.G + row - in * p.G, ch0 = half * (D / 2);
-            const bool gated = whole && p.gate && row < here;
-            const uint4* const gate = static_cast<const uint4*>(p.gate) + (tr * p.ldg + static_cast<long long>(h) * D + ch0) / 8;
-            uint4 gate_next[4];   // of 32 channels; asked for while the last products run
-#pragma unroll
-            for (int q = 0; q < 4; ++q) gate_next[q] = gated ? gate[q] : make_uint4(0, 0, 0, 0);
+            const bool gated = p.gate && row < here;
+            const bf16* const gate = static_cast<const bf16*>(p.gate) + (tr * p.ldg + static_cast<long long>(h) * D + ch0);
+            if (gated)   // the gate's lines, while the last products run
+                for (int i = 0; i < D / 2; i += 64) prefetch_l2(gate + i);
+            Part next = c;   // and the way to the next part
+            const bool more = to_next_part(p, ln, sh, next);
             if (any) wait(sm.pv_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
             tc::fence_after_sync();
             if (p.test_stall && warp == 3 && !stage_wait(&sm.never, 0, &sm.abort, 256)) sm.stop = 1;
@@ -646,49 +707,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (sm.stop) {   // a wait gave up: nothing of this part is written
                 if (threadIdx.x == 0 && p.status) atomicOr(p.status + c.b, 16);
             } else {
+                const float sum = sm.mx[0][0][row] + sm.mx[0][1][row];
                 const Parts<kRows, D> parts(p.workspace, workers);
-                const float sum = sm.mx[0][0][row] + sm.mx[0][1][row], f = whole ? (sum == 0.f ? 0.f : 1.0f / sum) : 1.0f;
+                const size_t place = Parts<kRows, D>::place(worker, c);
                 float* const part = parts.o + (place * kRows + rank * 128) * D;
+                bool result = whole;   // this CTA has the rows' result, here or with the other parts
+                int n = 1, w0 = 0;
+                if (!whole) {
+                    const bool ws32 = on32(p.workspace);
 #pragma unroll 1
-                for (int i = 0; i < D / 2; i += 32) {
-                    float v[32];
-                    if (any) tc::tmem_ld32(my_o + i, v);
-                    uint4 gate_now[4];
+                    for (int i = 0; i < D / 2; i += 32) {
+                        float v[32];
+                        tc::tmem_ld32(my_o + i, v);
+                        if (row < here) {
+                            float* const to = part + static_cast<size_t>(row) * D + ch0 + i;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        gate_now[q] = gate_next[q];
-                        if (gated && i + 32 < D / 2) gate_next[q] = gate[i / 8 + 4 + q];
-                    }
-                    if (row < here) {
+                            for (int e = 0; e < 32; e += 8) {
+                                uint32_t y[8];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            float y[8];
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) y[x] = any ? v[e + x] * f : 0.f;
-                            if (whole) {
-                                if (p.gate) {
-                                    const uint32_t x[4] = {gate_now[e / 8].x, gate_now[e / 8].y, gate_now[e / 8].z, gate_now[e / 8].w};
-#pragma unroll
-                                    for (int q = 0; q < 4; ++q) {
-                                        y[2 * q] *= gate_of<false>(__uint_as_float(x[q] << 16));
-                                        y[2 * q + 1] *= gate_of<false>(__uint_as_float(x[q] & 0xffff0000u));
-                                    }
-                                }
-                                store8(static_cast<bf16*>(p.out) + (tr * p.Hq + h) * D + ch0 + i + e, y);
-                            } else {
-                                store8(part + static_cast<size_t>(row) * D + ch0 + i + e, y);
+                                for (int q = 0; q < 8; ++q) y[q] = __float_as_uint(v[e + q]);
+                                store16(to + e, ws32, y);
                             }
                         }
                     }
-                }
-                if (!whole && half == 0 && row < here) parts.ml[place * kRows + rank * 128 + row] = make_float2(m, sum);
-                if (sm.strays) {
-                    sync_softmax();
-                    add_strays<D>(p, c, tok0, cta_tok, here, whole ? nullptr : part);
-                }
-                if (!whole) {   // the worker that arrives last joins this CTA's rows of all parts, in their order
+                    if (half == 0 && row < here) parts.ml[place * kRows + rank * 128 + row] = make_float2(m, sum);
+                    if (sm.strays) {
+                        sync_softmax();
+                        add_strays<D>(p, c, tok0, cta_tok, here, part);
+                    }
+                    // the worker that arrives last joins this CTA's rows of all parts
                     const long long first = c.at + ln.cost;
-                    const int w0 = sh.owner(first), n = sh.owner(first + static_cast<long long>(kKeys) * (c.tiles - 1)) - w0 + 1;
+                    w0 = sh.owner(first);
+                    n = sh.owner(first + static_cast<long long>(kKeys) * (c.tiles - 1)) - w0 + 1;
                     sync_softmax();
                     if (threadIdx.x == 0) {
                         unsigned old;
@@ -696,31 +746,90 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sm.last = old == static_cast<unsigned>(n - 1);
                     }
                     sync_softmax();
-                    if (sm.last) {
-                        auto at = [&](int k) { return (k == 0 ? 2 * static_cast<size_t>(w0) + 1 : 2 * static_cast<size_t>(w0 + k)) * kRows + rank * 128; };
-#pragma unroll 1
-                        for (int i = threadIdx.x; i < here * (D / 4); i += kSoft) {
-                            const int r = i / (D / 4), ch = i % (D / 4) * 4, tk = r / p.G;
-                            float mm = -INFINITY, ll = 0.f;
-                            for (int k = 0; k < n; ++k) mm = fmaxf(mm, __ldcg(parts.ml + at(k) + r).x);
-                            const float b0 = mm == -INFINITY ? 0.f : mm;
-                            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                            for (int k = 0; k < n; ++k) {
-                                const float2 z = __ldcg(parts.ml + at(k) + r);
-                                const float fk = ex2(z.x - b0);
-                                const float4 v = __ldcg(reinterpret_cast<const float4*>(parts.o + (at(k) + r) * D + ch));
-                                ll = fmaf(fk, z.y, ll);
-                                y = make_float4(fmaf(fk, v.x, y.x), fmaf(fk, v.y, y.y), fmaf(fk, v.z, y.z), fmaf(fk, v.w, y.w));
-                            }
-                            put<bf16, D>(p, true, static_cast<long long>(c.r.row0) + tok0 + cta_tok + tk, c.hk * p.G + r - tk * p.G, ch,
-                                         attn::times(y, ll == 0.f ? 0.f : 1.0f / ll));
+                    result = sm.last;
+                }
+                auto row_of = [&](int k) { return (k == 0 ? 2 * static_cast<size_t>(w0) + 1 : 2 * static_cast<size_t>(w0 + k)) * kRows + rank * 128; };
+                if (result && !whole && here * (D / 4) <= 4 * kSoft) {
+                    join_few<D>(p, c, parts, w0, n, tok0, cta_tok, here, static_cast<int>(rank) * 128);
+                } else if (result) {
+                    // of several parts in their order, whoever was last: statistics first
+                    float mm = m, ll = sum;
+                    if (!whole && row < here) {
+                        mm = -INFINITY;
+                        ll = 0.f;
+#pragma unroll 4
+                        for (int k = 0; k < n; ++k) mm = fmaxf(mm, __ldcg(&parts.ml[row_of(k) + row].x));
+                        mm = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 4
+                        for (int k = 0; k < n; ++k) {
+                            const float2 z = __ldcg(parts.ml + row_of(k) + row);
+                            ll = fmaf(ex2(z.x - mm), z.y, ll);
                         }
+                    }
+                    const float f = ll == 0.f ? 0.f : 1.0f / ll;
+                    const bool gate32 = on32(p.gate) && p.ldg % 16 == 0, out32 = on32(p.out);
+                    bf16* const to = static_cast<bf16*>(p.out) + (tr * p.Hq + h) * D + ch0;
+#pragma unroll 1
+                    for (int i = 0; i < D / 2; i += 32) {
+                        uint32_t gt[2][8];
+                        if (gated) {
+                            load16(gate + i, gate32, gt[0]);
+                            load16(gate + i + 16, gate32, gt[1]);
+                        }
+                        float v[32];
+                        if (whole) {
+                            if (any) tc::tmem_ld32(my_o + i, v);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                            if (row < here)
+#pragma unroll 1
+                                for (int k = 0; k < n; ++k) {
+                                    const float4* const x = reinterpret_cast<const float4*>(parts.o + (row_of(k) + row) * D + ch0 + i);
+                                    const float fk = ex2(__ldcg(&parts.ml[row_of(k) + row].x) - mm);
+                                    float4 y[8];
+#pragma unroll
+                                    for (int q = 0; q < 8; ++q) y[q] = __ldcg(x + q);
+#pragma unroll
+                                    for (int q = 0; q < 8; ++q) {
+                                        v[4 * q] = fmaf(fk, y[q].x, v[4 * q]);
+                                        v[4 * q + 1] = fmaf(fk, y[q].y, v[4 * q + 1]);
+                                        v[4 * q + 2] = fmaf(fk, y[q].z, v[4 * q + 2]);
+                                        v[4 * q + 3] = fmaf(fk, y[q].w, v[4 * q + 3]);
+                                    }
+                                }
+                        }
+                        if (row < here) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = any ? v[e] * f : 0.f;
+                            if (gated) {
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    const uint32_t x = gt[e / 16][e % 16 / 2];
+                                    v[e] *= gate_of<false>(__uint_as_float(x << 16));
+                                    v[e + 1] *= gate_of<false>(__uint_as_float(x & 0xffff0000u));
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; e += 16) {
+                                uint32_t y[8];
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) y[q] = StateIO<bf16>::pack(v[e + 2 * q], v[e + 2 * q + 1]);
+                                store16(to + i + e, out32, y);
+                            }
+                        }
+                    }
+                    if (whole && sm.strays) {
+                        sync_softmax();
+                        add_strays<D>(p, c, tok0, cta_tok, here, nullptr);
                     }
                 }
                 tc::fence_before_sync();
             }
             sync_softmax();   // the sums and sm.last have been read
-        } while (to_next_part(p, ln, sh, c));
+            if (!more) break;
+            c = next;
+        } while (true);
     }
     tc::fence_before_sync();
     __syncthreads();

@@ -19,7 +19,7 @@ int main() {
     std::srand(1);
     for (int it = 0; it < 6000; ++it) {
         const int G = 1 + std::rand() % 16, RT = std::rand() % 2 ? 256 : 64, costs[4] = {1, 64, 200, 700};
-        const Line ln{RT / G, std::rand() % 2 ? 128 : 64, costs[std::rand() % 4]};
+        const Line ln{RT / G, std::rand() % 2 ? 7 : 6, costs[std::rand() % 4]};
         const int B = 1 + std::rand() % 6, Hkv = 1 + std::rand() % 3;
         std::vector<Rows> rs;
         std::vector<long long> start;
@@ -40,7 +40,7 @@ int main() {
             row += n;
         }
         if (total == 0) continue;
-        const int W = workers_of(total, 1 + std::rand() % 500, (std::rand() % 2 ? 1 : 2) * ln.keys);
+        const int W = workers_of(total, 1 + std::rand() % 500, (std::rand() % 2 ? 1 : 2) * ln.keys());
         std::map<std::tuple<int, int, int>, std::vector<std::pair<int, Part>>> got;
         auto rows = [&](int b) { return rs[b]; };
         for (int w = 0; w < W; ++w) {
@@ -72,7 +72,7 @@ int main() {
                     if (c.tiles == 0) continue;
                     const Share sh = Share::of(total, W, 0);
                     const long long base = c.at + ln.cost;
-                    const int w0 = sh.owner(base), w1 = sh.owner(base + static_cast<long long>(ln.keys) * (c.tiles - 1));
+                    const int w0 = sh.owner(base), w1 = sh.owner(base + static_cast<long long>(ln.keys()) * (c.tiles - 1));
                     NEED(w0 == v.front().first && w1 == v.back().first && w1 - w0 + 1 == static_cast<int>(v.size()));
                 }
         NEED(units == got.size());
