@@ -31,7 +31,6 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 using attn::kWaitLimit;
-using attn::stage_wait;
 using tc::smem_u32;
 constexpr int kDrainLimit = 1 << 14;   // polls for what is in flight at the end
 constexpr int kMinShare = 512;        // keys of a worker, at least
@@ -62,7 +61,7 @@ struct Smem {
     uint64_t q_full, q_empty, s_full[2], p_ready[2], pv_done[2], v_told[2], drained, never;
     PlanSmem plan;
     uint32_t tmem;
-    int last, stop, strays;           // stop: a softmax warp's wait has given up; strays: some were found; never taken back
+    int last, stop, strays;           // stop: a softmax warp has seen abort; strays: some were found; never taken back
     volatile int abort;
 };
 static_assert(sizeof(Smem) <= 3072, "fits");
@@ -95,12 +94,24 @@ __device__ __forceinline__ void tma_load_q(uint32_t dst, const CUtensorMap* map,
         : "memory");
 }
 
-// A wait of a whole warp, at which one lane looks.  (A wait of 32 lanes at one barrier is 32 waits for the unit that serves them: with
-// eight warps of them at it, one more thread's wait for what had long been there took 235 cycles.)
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    int done = 0;
-    if ((threadIdx.x & 31) == 0) done = stage_wait(bar, parity, abort);
-    return __shfl_sync(0xffffffffu, done, 0) != 0;
+// Wait for phase `parity` of `bar`.  A wait that gives up, or finds that another of the CTA has, returns as well: who goes on to
+// use what it waited for looks at `abort` first.  (Made like this a wait for what is there takes 73 cycles; with an answer
+// that the caller branches on 184, by one lane and a shuffle 290.)
+__device__ __forceinline__ bool is_there(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+__device__ __noinline__ void long_wait(uint32_t bar, uint32_t parity, volatile int* abort, int limit) {
+#pragma unroll 1
+    for (int it = 0; it < limit; ++it) {
+        if (is_there(bar, parity) || *abort) return;
+    }
+    *abort = 1;
+}
+__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (!is_there(smem_u32(bar), parity)) long_wait(smem_u32(bar), parity, abort, kWaitLimit);
 }
 
 // One lane of a converged warp (the compiler knows that it is one).
@@ -367,7 +378,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Lane l has the tile's groups of bx.tokens keys l + 32 k, [0] of the tile to be copied, [1] of the one being looked up.
         constexpr int kPer = 4;
         int page[2][kPer] = {}, in[2][kPer] = {}, head[2] = {}, seq[2] = {}, q_tok[2] = {};   // in -1: no key; seq -1: no tile; q_tok -1: not a part's first
-        bool ok = true;
         int parts_begun = 0, part_seq = 0, part_head = 0;
         int end = 0;               // keys from `end` on are nobody's
         const int* table = nullptr;   // the sequence's pages
@@ -442,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n < 0) continue;
             if (keys) {
                 if (q_tok[0] >= 0) {
-                    if (parts_begun > 0) ok = ok && warp_wait(&sm.q_empty, (parts_begun - 1) & 1, &sm.abort);
-                    if (!ok) break;
+                    if (parts_begun > 0) wait_for(&sm.q_empty, (parts_begun - 1) & 1, &sm.abort);
+                    if (sm.abort) break;
                     ++parts_begun;
                     const uint32_t bar = announce(&sm.q_full, 2 * cta_rows * D * 2);
                     if (elected()) {
@@ -451,8 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int c = 0; c < D / 64; ++c) tma_load_q(smem_u32(q_s) + c * 16384, &q_map, c * 64, head[0] * p.G, q_tok[0], bar);
                     }
                 }
-                if (n >= RK) ok = ok && warp_wait(sm.k_empty + n % RK, (n / RK - 1) & 1, &sm.abort);
-                if (!ok) break;
+                if (n >= RK) wait_for(sm.k_empty + n % RK, (n / RK - 1) & 1, &sm.abort);
+                if (sm.abort) break;
                 if (lane < 4) sm.valid[n & 15][lane] = 0xffffffffu;
                 bool bad = false;
 #pragma unroll
@@ -468,8 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             } else {
-                if (n >= RV) ok = ok && warp_wait(sm.v_empty + n % RV, (n / RV - 1) & 1, &sm.abort);
-                if (!ok) break;
+                if (n >= RV) wait_for(sm.v_empty + n % RV, (n / RV - 1) & 1, &sm.abort);
+                if (sm.abort) break;
             }
             const uint32_t bar = announce(keys ? sm.k_full + n % RK : sm.v_full + n % RV, keys ? 2 * S::kStageK : 2 * S::kStageV);
             copy(keys ? smem_u32(k_s) + n % RK * S::kStageK : smem_u32(v_s) + n % RV * S::kStageV, keys ? &k_map : &v_map,
@@ -486,7 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rank == 0) {
             // -------------------------------------------------------- products
             Walk w(c, p, ln, sh);
-            bool ok = true;
             int nq = 0, units = 0;   // S issued, parts begun
             uint32_t firsts = 0;     // by tile mod 32: the first of a part
             constexpr uint32_t id_s = tc::idesc_bf16(256, 128);
@@ -517,20 +526,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             // Turn g: the product with tile g's weights, then S of tile g + NS, into the place that the softmax has read -- and the product has,
             // where P lies there.
 #pragma unroll 1
-            for (int g = -NS; ok && (g < nq || w.more); ++g) {
+            for (int g = -NS; g < nq || w.more; ++g) {
                 if (g >= 0) {
-                    ok = ok && stage_wait(sm.v_full + g % RV, (g / RV) & 1, &sm.abort);
-                    ok = ok && stage_wait(sm.p_ready + (g & 1), (g >> 1) & 1, &sm.abort);
-                    if (!ok) break;
+                    wait_for(sm.v_full + g % RV, (g / RV) & 1, &sm.abort);
+                    wait_for(sm.p_ready + (g & 1), (g >> 1) & 1, &sm.abort);
+                    if (sm.abort) break;
                     tc::fence_after_sync();
                     if (elected()) issue_o(g);
                     __syncwarp();
                 }
                 if (w.more) {
-                    if (w.first()) ok = ok && stage_wait(&sm.q_full, units++ & 1, &sm.abort);
-                    ok = ok && stage_wait(sm.k_full + nq % RK, (nq / RK) & 1, &sm.abort);
-                    if (S::kOver && g >= 0) ok = ok && stage_wait(sm.pv_done + (g & 1), (g >> 1) & 1, &sm.abort);
-                    if (!ok) break;
+                    if (w.first()) wait_for(&sm.q_full, units++ & 1, &sm.abort);
+                    wait_for(sm.k_full + nq % RK, (nq / RK) & 1, &sm.abort);
+                    if (S::kOver && g >= 0) wait_for(sm.pv_done + (g & 1), (g >> 1) & 1, &sm.abort);
+                    if (sm.abort) break;
                     tc::fence_after_sync();
                     if (elected()) issue_s();
                     __syncwarp();
@@ -553,11 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float scale = p.scale * kLog2e, size = scale == 0.f ? 1.f : fabsf(scale);
         const int in = row / p.G;   // token of this CTA's
         const int cta_tok = static_cast<int>(rank) * cta_tokens, tok = cta_tok + in;   // of the unit's
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            const bool done = warp_wait(bar, parity, &sm.abort);
-            if (!done) sm.stop = 1;
-            return done;
-        };
+        auto wait = [&](uint64_t* bar, uint32_t parity) { wait_for(bar, parity, &sm.abort); };
         int g = 0;           // tile number
         uint32_t told = 0;   // phases of v_told
         do {
@@ -568,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = -INFINITY, base = 0.f, limit = -INFINITY, l = 0.f;   // m: base, or -inf for a row that has seen no key
 #pragma unroll 1
             for (int t = t0; t < t1; ++t, ++g) {
-                if (!wait(sm.s_full + g % NS, (g / NS) & 1)) continue;
+                wait(sm.s_full + g % NS, (g / NS) & 1);
                 tc::fence_after_sync();
                 float s[2][32];
                 const uint32_t my_s = t_s + my_lanes + g % NS * 128 + half * 64;
@@ -614,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, up)) {   // the same for both halves
                     const bool fresh = t == t0;
                     // the tile before has been added: O stands still
-                    const bool through = fresh || wait(sm.pv_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+                    if (!fresh) wait(sm.pv_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
                     tc::fence_after_sync();
                     const float f = up ? ex2(m - mx) : 1.0f;
                     if (up) {
@@ -622,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         limit = mx + kSlack;
                     }
                     l *= f;
-                    if (!fresh && through) {
+                    if (!fresh) {
 #pragma unroll 1
                         for (int i = 0; i < D / 2; i += 32) {
                             float v[32];
@@ -659,10 +664,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bool landed = k0 < k1;
                     if (landed) {   // the first CTA's barrier tells of both; it tells the second one
                         if (rank == 0) {
-                            landed = wait(sm.v_full + g % RV, (g / RV) & 1);
+                            wait(sm.v_full + g % RV, (g / RV) & 1);
+                            landed = !sm.abort;
                             if (landed && threadIdx.x == 0) arrive_at(sm.v_told + (g & 1), 1);
                         } else {
-                            landed = wait(sm.v_told + (g & 1), (told >> (g & 1)) & 1);
+                            wait(sm.v_told + (g & 1), (told >> (g & 1)) & 1);
+                            landed = !sm.abort;
                         }
                         told ^= 1u << (g & 1);
                     }
@@ -701,7 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool more = to_next_part(p, ln, sh, next);
             if (any) wait(sm.pv_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
             tc::fence_after_sync();
-            if (p.test_stall && warp == 3 && !stage_wait(&sm.never, 0, &sm.abort, 256)) sm.stop = 1;
+            if (p.test_stall && warp == 3) long_wait(smem_u32(&sm.never), 0, &sm.abort, 256);
+            if (sm.abort) sm.stop = 1;   // told before the barrier, behind which all look
             sm.mx[0][half][row] = l;   // (all have read the last tile's maximum: its weights were waited for)
             sync_softmax();
             if (sm.stop) {   // a wait gave up: nothing of this part is written
