@@ -6,16 +6,16 @@
 // (at d = 256 a tile's products take 2,048 cycles and its copies 32 bytes a cycle of every SM; with 128 rows a CTA it were 64).
 //
 // Roles of a CTA's 11 warps:
-//   0-7   softmax: a thread has one row (tensor-memory lane) and 64 of a tile's 128 keys; the two threads of a row meet in shared
-//         memory for the maximum.  The result is rescaled only when a row's maximum has risen by more than 2^kSlack.
+//   0-7   softmax, two groups that take turns: a thread has one row (tensor-memory lane) of every other tile.  A tile's maximum needs
+//         the base that the other group had for the tile before; the weights' powers of one run beside the maxima of the next.
+//         The result is rescaled only when a row's maximum has risen by more than 2^kSlack.
 //   8     copies queries and keys by TMA, from a tensor map that serves any strides; each lane looks up its keys' pages, one
 //         issues the copies.  Keys past the end and pages outside the cache are coordinates outside the map, which read as zeros
 //   10    copies values
 //   9     one thread of the first CTA: issues the products
 //
-// S has two places, so that the softmax of a tile runs beside the products of others.  At d = 256 the tensor memory is full with
-// them and O: the weights then take the place of their scores, and the S after next waits for the product with them.  Every
-// order between products that touch the same tensor memory goes through a barrier.
+// S has two or three places, as the tensor memory allows, so that the softmax of tiles runs beside the products of others.  The
+// weights take the place of scores that have been read; the S that comes into their place waits for the product with them.
 //
 // A weight is rounded to bf16 (2^-9 of it at most): with a second part for what the rounding leaves, as gdn_attn_decode has
 // it, which is bound by memory, the product with the values would take twice the time, half again as much for the whole.
@@ -35,12 +35,12 @@ using tc::smem_u32;
 constexpr int kDrainLimit = 1 << 14;   // polls for what is in flight at the end
 constexpr int kMinShare = 512;        // keys of a worker, at least
 constexpr float kSlack = 8.0f;   // how far a score may pass its row's base
-constexpr int kRows = 256, kKeys = 128, kThreads = 352, kSoft = 256, NS = 2;   // places of S
+constexpr int kRows = 256, kKeys = 128, kThreads = 352, kSoft = 256;
 
 template <int D_>
 struct Tc {
     static constexpr int D = D_;
-    static constexpr bool kOver = D == 256;                   // P lies where its S was, for want of tensor memory
+    static constexpr int NS = D == 256 ? 2 : 3;               // places of S, and of the weights that take a part of it
     static constexpr int kVCh = D == 256 ? 128 : 64;          // channels of a CTA's values (heads of 64: all of them, in both)
     static constexpr int kStageK = kKeys * D, kStageV = kKeys * 2 * kVCh;   // bytes: 64 keys, 128 keys' values
     static constexpr int RK = D == 256 ? 2 : D == 128 ? 5 : 6;
@@ -48,17 +48,18 @@ struct Tc {
     static constexpr int kQ = 128 * D * 2;
     static constexpr int kSmem = kQ + RK * kStageK + RV * kStageV + 3072;
     // tensor memory
-    static constexpr int kO = 0, kS = kOver ? 256 : 128, kP = kOver ? kS : 384;
-    static constexpr int kPStep = kOver ? 128 : 64, kPHalf = kOver ? 64 : 32;   // columns from one P to the other, from one half of the keys to the other
+    static constexpr int kO = 0, kS = D == 256 ? 256 : 128;
     static constexpr int kCost = D == 256 ? 1024 : 768;       // of a unit: its begin and end take as long as so many keys
-    static_assert(kSmem <= 232448, "shape");
+    static_assert(kSmem <= 232448 && kS + NS * 128 <= 512, "shape");
 };
 
 struct Smem {
-    float mx[2][2][128];              // by tile mod 2, half of the keys, row; at a part's end the sums, in [0]
+    float base[2][128];               // of a row's weights, by tile mod 2
+    float sum[2][128];                // at a part's end the groups' shares, relative to their base
     uint32_t valid[16][4];            // keys of a tile that are there, by tile mod 16
     uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
-    uint64_t q_full, q_empty, s_full[2], p_ready[2], pv_done[2], v_told[2], drained, never;
+    uint64_t q_full, q_empty, s_full[3], p_ready[3], pv_done[3], drained, never;   // by place of S
+    uint64_t v_told[6];               // by tile mod 6: one of them is always the same group's, and not passed twice before it has looked
     PlanSmem plan;
     uint32_t tmem;
     int last, stop, strays;           // stop: a softmax warp has seen abort; strays: some were found; never taken back
@@ -309,14 +310,16 @@ __device__ __noinline__ void join_few(const ChunkParams& p, const Part& c, const
     }
 }
 
-__device__ __forceinline__ void sync_row_halves(int quarter) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); }
-__device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 5, %0;" ::"n"(kSoft) : "memory"); }
+// A group's warp lets the other group's warp of the same rows have its base (barriers 1 to 8).
+__device__ __forceinline__ void give_base(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(1 + id) : "memory"); }
+__device__ __forceinline__ void take_base(int id) { asm volatile("bar.sync %0, 64;" ::"r"(1 + id) : "memory"); }
+__device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 9, %0;" ::"n"(kSoft) : "memory"); }
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                     const __grid_constant__ CUtensorMap q_map, const Boxes kb, const Boxes vb, const Division by_page) {
-    constexpr int D = S::D, RK = S::RK, RV = S::RV;
+    constexpr int D = S::D, NS = S::NS, RK = S::RK, RV = S::RV;
     constexpr int kKBlocks = D / 64, kVBlocks = S::kVCh / 64;   // blocks of 64 channels in a CTA's stages
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const q_s = smem;
@@ -337,12 +340,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         tc::mbar_init(&sm.q_full, 2);
         tc::mbar_init(&sm.q_empty, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NS; ++i) {
             tc::mbar_init(sm.s_full + i, 1);
-            tc::mbar_init(sm.p_ready + i, 16);   // the softmax warps of both CTAs
+            tc::mbar_init(sm.p_ready + i, 8);   // a tile's softmax warps of both CTAs
             tc::mbar_init(sm.pv_done + i, 1);
-            tc::mbar_init(sm.v_told + i, 1);
         }
+        for (int i = 0; i < 6; ++i) tc::mbar_init(sm.v_told + i, 1);
         tc::mbar_init(&sm.drained, 1);
         tc::mbar_init(&sm.never, 1);
         sm.strays = 0;
@@ -367,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     cluster_sync_all();   // the other CTA's barriers are there too
     tc::fence_after_sync();
-    const uint32_t t_o = sm.tmem + S::kO, t_s = sm.tmem + S::kS, t_p = sm.tmem + S::kP;
+    const uint32_t t_o = sm.tmem + S::kO, t_s = sm.tmem + S::kS;
 
     if (warp == 8 || warp == 10) {
         // ------------------------------------------------------------ copies: warp 8 queries and keys, warp 10 values
@@ -516,20 +519,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (w.last()) commit_both(&sm.q_empty);
             };
             auto issue_o = [&](int g) {
-                const uint32_t a = t_p + (g & 1) * S::kPStep, b = v_lo + g % RV * (S::kStageV >> 4);
+                const uint32_t a = t_s + g % NS * 128, b = v_lo + g % RV * (S::kStageV >> 4);
                 const bool add = !((firsts >> (g & 31)) & 1);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) mma_ts(t_o, a + ks / 4 * S::kPHalf + ks % 4 * 8, b + ks * (kVBlocks * 2048 >> 4), v_hi, id_o, add || ks != 0);
-                commit_both(sm.pv_done + (g & 1));
+                for (int ks = 0; ks < 8; ++ks) mma_ts(t_o, a + ks * 8, b + ks * (kVBlocks * 2048 >> 4), v_hi, id_o, add || ks != 0);
+                commit_both(sm.pv_done + g % NS);
                 commit_both(sm.v_empty + g % RV);
             };
-            // Turn g: the product with tile g's weights, then S of tile g + NS, into the place that the softmax has read -- and the product has,
-            // where P lies there.
+            // Turn g: the product with tile g's weights, then S of tile g + NS into the place that these had.
 #pragma unroll 1
             for (int g = -NS; g < nq || w.more; ++g) {
                 if (g >= 0) {
                     wait_for(sm.v_full + g % RV, (g / RV) & 1, &sm.abort);
-                    wait_for(sm.p_ready + (g & 1), (g >> 1) & 1, &sm.abort);
+                    wait_for(sm.p_ready + g % NS, (g / NS) & 1, &sm.abort);
                     if (sm.abort) break;
                     tc::fence_after_sync();
                     if (elected()) issue_o(g);
@@ -538,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (w.more) {
                     if (w.first()) wait_for(&sm.q_full, units++ & 1, &sm.abort);
                     wait_for(sm.k_full + nq % RK, (nq / RK) & 1, &sm.abort);
-                    if (S::kOver && g >= 0) wait_for(sm.pv_done + (g & 1), (g >> 1) & 1, &sm.abort);
+                    if (g >= 0) wait_for(sm.pv_done + g % NS, (g / NS) & 1, &sm.abort);
                     if (sm.abort) break;
                     tc::fence_after_sync();
                     if (elected()) issue_s();
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ softmax
         const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
         const uint32_t my_lanes = static_cast<uint32_t>(32 * quarter) << 16;
-        const uint32_t my_o = t_o + my_lanes + half * (D / 2);
+        const uint32_t my_o = t_o + my_lanes + half * (D / 2);   // at a part's end a thread has half of its row's channels
         const float scale = p.scale * kLog2e, size = scale == 0.f ? 1.f : fabsf(scale);
         const int in = row / p.G;   // token of this CTA's
         const int cta_tok = static_cast<int>(rank) * cta_tokens, tok = cta_tok + in;   // of the unit's
@@ -570,91 +572,105 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tok0 = c.i * ln.tokens, n_tok = tokens_of(ln, c), off = c.r.len - c.r.n;
             const int here = min(max(n_tok - cta_tok, 0), cta_tokens) * p.G;   // rows of this CTA
             const int end = c.seen;
-            float m = -INFINITY, base = 0.f, limit = -INFINITY, l = 0.f;   // m: base, or -inf for a row that has seen no key
+            float m = -INFINITY, l = 0.f;   // of a row: the base of its weights, -inf before it has seen a key; this thread's share of their sum
 #pragma unroll 1
             for (int t = t0; t < t1; ++t, ++g) {
+                if ((g & 1) != half) continue;   // the other group's
                 wait(sm.s_full + g % NS, (g / NS) & 1);
                 tc::fence_after_sync();
-                float s[2][32];
-                const uint32_t my_s = t_s + my_lanes + g % NS * 128 + half * 64;
-                tmem_ask32(my_s, s[0]);
-                tmem_ask32(my_s + 32, s[1]);
-                const uint32_t there[2] = {sm.valid[g & 15][2 * half], sm.valid[g & 15][2 * half + 1]};
+                const uint32_t my_s = t_s + my_lanes + g % NS * 128;
                 // late: some rows do not see some of the tile's keys
                 const bool late = (t + 1) * kKeys > off + tok0 + 1;
-                tmem_wait_for(s[0]);
-                tmem_wait_for(s[1]);
-                if (!(scale > 0.f)) {
-                    const float sign = scale < 0.f ? -1.f : 0.f;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[i][e] *= sign;
-                }
-                if (late || (there[0] & there[1]) != 0xffffffffu) {
-                    const int sees = min(off + tok0 + tok + 1, end) - t * kKeys - half * 64;
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int n = sees - i * 32;
-                        const uint32_t x = n <= 0 ? 0u : n >= 32 ? there[i] : there[i] & ((1u << n) - 1u);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) s[i][e] = (x >> e) & 1 ? s[i][e] : -INFINITY;
-                    }
-                }
-                float mx;
-                {
-                    float a = fmaxf(s[0][0], s[0][1]), b = fmaxf(s[1][0], s[1][1]);
-#pragma unroll
-                    for (int e = 2; e < 32; e += 2) {
-                        a = max3(a, s[0][e], s[0][e + 1]);
-                        b = max3(b, s[1][e], s[1][e + 1]);
-                    }
-                    mx = fmaxf(a, b) * size;
-                }
-                sm.mx[g & 1][half][row] = mx;
-                sync_row_halves(quarter);
-                mx = fmaxf(mx, sm.mx[g & 1][half ^ 1][row]);
-                // (a row's base moves by its own scores alone: its result does not depend on the rows beside it)
-                const bool up = mx > limit;
-                if (__any_sync(0xffffffffu, up)) {   // the same for both halves
-                    const bool fresh = t == t0;
-                    // the tile before has been added: O stands still
-                    if (!fresh) wait(sm.pv_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
-                    tc::fence_after_sync();
-                    const float f = up ? ex2(m - mx) : 1.0f;
-                    if (up) {
-                        m = base = mx;
-                        limit = mx + kSlack;
-                    }
-                    l *= f;
-                    if (!fresh) {
+                const uint4 there = *reinterpret_cast<const uint4*>(sm.valid[g & 15]);
+                if (late || (there.x & there.y & there.z & there.w) != 0xffffffffu || !(scale > 0.f)) {
+                    // scores of keys that a row does not see, and the scale's sign, are seen to in place
+                    const int sees = min(off + tok0 + tok + 1, end) - t * kKeys;
+                    const float sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
 #pragma unroll 1
-                        for (int i = 0; i < D / 2; i += 32) {
-                            float v[32];
-                            tc::tmem_ld32(my_o + i, v);
+                    for (int i = 0; i < 4; ++i) {
+                        float s[32];
+                        tc::tmem_ld32(my_s + i * 32, s);
+                        const uint32_t w = sm.valid[g & 15][i];
+                        const int n = sees - i * 32;
+                        const uint32_t x = n <= 0 ? 0u : n >= 32 ? w : w & ((1u << n) - 1u);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] *= f;
-                            tc::tmem_st32(my_o + i, v);
-                        }
+                        for (int e = 0; e < 32; ++e) s[e] = (x >> e) & 1 ? s[e] * sign : -INFINITY;
+                        tc::tmem_st32(my_s + i * 32, s);
+                    }
+                    tc::tmem_wait_st();
+                }
+                float s0[32], s1[32];   // scores for the maximum, read again for the weights
+                tmem_ask32(my_s, s0);
+                tmem_ask32(my_s + 32, s1);
+                float ma = -INFINITY, mb = -INFINITY;
+                auto larger = [&](const float (&s)[32]) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        ma = max3(ma, s[e], s[e + 1]);
+                        mb = max3(mb, s[e + 2], s[e + 3]);
+                    }
+                };
+                tmem_wait_for(s0);
+                tmem_wait_for(s1);
+                larger(s0);
+                tmem_ask32(my_s + 64, s0);
+                larger(s1);
+                tmem_ask32(my_s + 96, s1);
+                tmem_wait_for(s0);
+                tmem_wait_for(s1);
+                larger(s0);
+                larger(s1);
+                tmem_ask32(my_s, s0);
+                const float mx = fmaxf(ma, mb) * size;
+                // the base that the other group had for the tile before, and this tile's for it
+                if (g > 0) take_base(quarter + 4 * (half ^ 1));
+                const float before = t == t0 ? -INFINITY : sm.base[half ^ 1][row];
+                // (a row's base moves by its own scores alone: its result does not depend on the rows beside it)
+                const bool up = mx > before + kSlack;   // (above -inf, at a row's first keys)
+                const float now = up ? mx : before;
+                sm.base[half][row] = now;
+                give_base(quarter + 4 * half);
+                if (t > t0 && __any_sync(0xffffffffu, up)) {
+                    wait(sm.pv_done + (g - 1) % NS, ((g - 1) / NS) & 1);   // the tile before has been added: O stands still
+                    tc::fence_after_sync();
+                    const float f = up ? ex2(before - now) : 1.0f;
+#pragma unroll 1
+                    for (int i = 0; i < D; i += 32) {
+                        float v[32];
+                        tc::tmem_ld32(t_o + my_lanes + i, v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] *= f;
+                        tc::tmem_st32(t_o + my_lanes + i, v);
                     }
                 }
-                if (!S::kOver && g >= 2) {   // the weights that were in this place have been read
-                    wait(sm.pv_done + (g & 1), ((g >> 1) - 1) & 1);
-                    tc::fence_after_sync();
+                if (now != m) {
+                    l *= ex2(m - now);   // (m -inf: there is none yet)
+                    m = now;
                 }
+                const float base = m == -INFINITY ? 0.f : m;
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                auto weights = [&](int i, const float (&s)[32]) {   // two keys a column, in the place of scores that have been read
                     uint32_t w2[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const float2 x = fma2(make_float2(s[i][2 * e], s[i][2 * e + 1]), make_float2(size, size), make_float2(-base, -base));
+                        const float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(size, size), make_float2(-base, -base));
                         const float2 y = make_float2(ex2(x.x), ex2(x.y));
                         sum[e & 1] = add2(sum[e & 1], y);
                         w2[e] = StateIO<bf16>::pack(y.x, y.y);
                     }
-                    tmem_st16u(t_p + my_lanes + (g & 1) * S::kPStep + half * S::kPHalf + i * 16, w2);
-                }
+                    tmem_st16u(my_s + i * 16, w2);
+                };
+                tmem_wait_for(s0);
+                tmem_ask32(my_s + 32, s1);
+                tmem_wait_for(s1);
+                weights(0, s0);
+                tmem_ask32(my_s + 64, s0);
+                tmem_wait_for(s0);
+                weights(1, s1);
+                tmem_ask32(my_s + 96, s1);
+                tmem_wait_for(s1);
+                weights(2, s0);
+                weights(3, s1);
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 if (late) {
@@ -666,18 +682,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (rank == 0) {
                             wait(sm.v_full + g % RV, (g / RV) & 1);
                             landed = !sm.abort;
-                            if (landed && threadIdx.x == 0) arrive_at(sm.v_told + (g & 1), 1);
+                            if (landed && (threadIdx.x & 127) == 0) arrive_at(sm.v_told + g % 6, 1);
                         } else {
-                            wait(sm.v_told + (g & 1), (told >> (g & 1)) & 1);
+                            wait(sm.v_told + g % 6, (told >> (g % 6)) & 1);
                             landed = !sm.abort;
                         }
-                        told ^= 1u << (g & 1);
+                        told ^= 1u << (g % 6);
                     }
                     if (landed) {
                         uint8_t* const st = v_s + g % RV * S::kStageV;
                         bool found = false;
 #pragma unroll 1
-                        for (int x = threadIdx.x; x < (k1 - k0) * (S::kVCh / 8); x += kSoft) {
+                        for (int x = threadIdx.x & 127; x < (k1 - k0) * (S::kVCh / 8); x += 128) {
                             const int key = k0 + x / (S::kVCh / 8), ch = x % (S::kVCh / 8);
                             uint8_t* const at = st + (key >> 3) * (kVBlocks * 1024) + ch / 8 * 1024 + (key & 7) * 128 + ((ch ^ key) & 7) * 16;
                             if (key < kend) found |= attn::take_strays<bf16>(at);
@@ -694,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) arrive_at(sm.p_ready + (g & 1), 0);
+                if (lane == 0) arrive_at(sm.p_ready + g % NS, 0);
             }
             // -------------------------------------------------------- the part's end
             const bool any = t0 < t1, whole = c.whole();
@@ -706,16 +722,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < D / 2; i += 64) prefetch_l2(gate + i);
             Part next = c;   // and the way to the next part
             const bool more = to_next_part(p, ln, sh, next);
-            if (any) wait(sm.pv_done + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+            if (any) wait(sm.pv_done + (g - 1) % NS, ((g - 1) / NS) & 1);
             tc::fence_after_sync();
             if (p.test_stall && warp == 3) long_wait(smem_u32(&sm.never), 0, &sm.abort, 256);
             if (sm.abort) sm.stop = 1;   // told before the barrier, behind which all look
-            sm.mx[0][half][row] = l;   // (all have read the last tile's maximum: its weights were waited for)
+            // the sum relative to the last tile's base, which the group of that tile has
+            sm.sum[half][row] = l;
+            sm.base[half][row] = m;
             sync_softmax();
             if (sm.stop) {   // a wait gave up: nothing of this part is written
                 if (threadIdx.x == 0 && p.status) atomicOr(p.status + c.b, 16);
             } else {
-                const float sum = sm.mx[0][0][row] + sm.mx[0][1][row];
+                m = sm.base[any ? (g - 1) & 1 : 0][row];
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) sum += sm.base[i][row] == -INFINITY ? 0.f : sm.sum[i][row] * ex2(sm.base[i][row] - m);
                 const Parts<kRows, D> parts(p.workspace, workers);
                 const size_t place = Parts<kRows, D>::place(worker, c);
                 float* const part = parts.o + (place * kRows + rank * 128) * D;
@@ -838,6 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!more) break;
             c = next;
         } while (true);
+        if (g > 0 && (g & 1) == half) take_base(quarter + 4 * (half ^ 1));   // the last one given
     }
     tc::fence_before_sync();
     __syncthreads();

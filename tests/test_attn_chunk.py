@@ -163,6 +163,14 @@ def test_long_and_split(dt, odt, new, lens):
     check(R.Batch(new, lens, 4, 1, 256, 64, dt, seed=8), odt)
 
 
+@pytest.mark.parametrize("dt,odt", [(BF, BF), (BF, F32)])
+@pytest.mark.parametrize("d,G,Hkv,new,lens", [(128, 8, 16, [600, 350], [700, 3000]), (64, 8, 16, [900], [1100]), (256, 6, 8, [500, 260], [500, 1500]),
+                                              (128, 3, 24, [700, 90, 1], [700, 2500, 4000])])
+def test_many_parts_and_tiles_a_worker(dt, odt, d, G, Hkv, new, lens):
+    """Workers with several units one after another, of one tile to dozens of tiles."""
+    check(R.Batch(new, lens, G * Hkv, Hkv, d, 16, dt, seed=21), odt)
+
+
 @pytest.mark.parametrize("dt,odt", KINDS)
 @pytest.mark.parametrize("rise", [0.02, -0.02])
 def test_scores_that_rise_along_the_sequence(dt, odt, rise):
