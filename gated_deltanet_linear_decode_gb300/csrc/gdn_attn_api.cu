@@ -334,7 +334,7 @@ gdn_status gdn_kv_fork(int32_t page_size, int32_t num_pages, int32_t B, int32_t 
                     {{src, nn}, {dst, nn}, {len, nn}, {free_list, np}}))
         return GDN_E_INVALID_ARG;
     gdn::KvForkParams p{page_size, num_pages, B, max_pages, N, src, dst, len, seq_len, n_pages, block_table, page_refs,
-                        free_list, free_count, copy_src, copy_dst, dev_status};
+                        free_list, free_count, copy_src, copy_dst, dev_status, 0};
     return cuda_status(gdn::launch_kv_fork(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -355,7 +355,7 @@ gdn_status gdn_kv_release(int32_t page_size, int32_t num_pages, int32_t B, int32
                     {{new_len, nb}}))
         return GDN_E_INVALID_ARG;
     gdn::KvReleaseParams p{page_size, num_pages, B, max_pages, new_len, seq_len, n_pages, block_table, page_refs,
-                           free_list, free_count, copy_src, copy_dst, dev_status};
+                           free_list, free_count, copy_src, copy_dst, dev_status, 0};
     return cuda_status(gdn::launch_kv_release(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

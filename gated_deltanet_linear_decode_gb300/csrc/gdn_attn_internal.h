@@ -117,6 +117,7 @@ struct KvForkParams {
     int* copy_src;
     int* copy_dst;
     int* status;          // optional [N]
+    int room;             // filled in at the launch, as in KvReleaseParams
 };
 
 struct KvReleaseParams {
@@ -131,6 +132,7 @@ struct KvReleaseParams {
     int* copy_src;
     int* copy_dst;
     int* status;          // optional [B]
+    int room;             // filled in at the launch: words for the pages' counts in shared memory, or 0
 };
 
 struct KvCompactParams {
@@ -182,8 +184,8 @@ size_t attn_workspace_bytes(int B, int K, int Hq, int Hkv, int head_dim, int act
 cudaError_t launch_attn_decode(const AttnParams& p, int head_dim, int act_dtype, int out_dtype, cudaStream_t stream);
 size_t chunk_workspace_bytes(int head_dim, int act_dtype, int out_dtype);
 cudaError_t launch_attn_chunk(const ChunkParams& p, int head_dim, int act_dtype, int out_dtype, cudaStream_t stream);
-cudaError_t launch_kv_fork(const KvForkParams& p, cudaStream_t stream);
-cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream);
+cudaError_t launch_kv_fork(KvForkParams p, cudaStream_t stream);         // these two fill in room
+cudaError_t launch_kv_release(KvReleaseParams p, cudaStream_t stream);
 cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t stream);
 cudaError_t launch_kv_copy(KvCopyParams p, cudaStream_t stream);   // fills in chunks
 cudaError_t launch_norm_residual(const NormParams& p, int act_dtype, int res_dtype, cudaStream_t stream);

@@ -17,7 +17,13 @@ namespace {
 // scans all sequences for itself into prefix sums in shared memory; then the page entries -- not the sequences -- are spread
 // over the cluster's threads.  Inputs are outputs: what the scan reads is written behind a cluster barrier.
 constexpr int kBookThreads = 1024;
-constexpr int kManyEntries = 4096;   // pages of a cache above which 8 CTAs take part
+constexpr int kManyEntries = 4096;   // entries of the tables (or pages) above which 8 CTAs take part
+// Pages whose counts are summed in shared memory before they go to page_refs, one addition a page and CTA.  Additions to a few
+// lines of memory take their turn, some 20 ns each whoever makes them: 63 forks of 1024 pages of a cache of 1100 took 48 us
+// by 8 and by 64 CTAs and their release 160, with counts in shared memory 12 and 21.  In larger caches the pages lie in more
+// lines.
+constexpr int kCountPages = 24 * 1024;
+constexpr size_t kMostWords = 56 * 1024;   // of dynamic shared memory
 
 __device__ __forceinline__ bool page_ok(int page, int num_pages) { return page >= 0 && page < num_pages; }
 // Words that other CTAs of the cluster change: past L1, which keeps what it has read.
@@ -48,58 +54,59 @@ __device__ __forceinline__ ForkAsk fork_ask(const KvForkParams& p, int i) {
 
 constexpr int kForkRun = 128;   // entries that a warp takes at a time
 
-__global__ void __launch_bounds__(kBookThreads) kv_fork_kernel(const KvForkParams p) {
+__global__ void __launch_bounds__(kBookThreads, 1) kv_fork_kernel(const KvForkParams p) {
     extern __shared__ int smem[];
     int* const first_s = smem;             // [B] the fork that a sequence is the dst of
     int* const run_s = first_s + p.B;      // [N + 1] runs of entries before each fork
     int* const page_s = run_s + p.N + 1;   // [N + 1] pages served before it
+    int* const count_s = page_s + p.N + 1;   // [num_pages] if there are few
     __shared__ Pair sums[33];
     grid_dependency_wait();
     grid_launch_dependents();
+    const bool counted = p.room > 0;
     for (int b = threadIdx.x; b < p.B; b += blockDim.x) first_s[b] = INT_MAX;
+    if (counted)
+        for (int g = threadIdx.x; g < p.num_pages; g += blockDim.x) count_s[g] = 0;
     __syncthreads();
     const int per = (p.N + blockDim.x - 1) / blockDim.x;
     const int i0 = min(p.N, static_cast<int>(threadIdx.x) * per), i1 = min(p.N, i0 + per);
-    for (int i = i0; i < i1; ++i) {
+    for (int i = i0; i < i1; ++i) {   // each thread's own forks, so far: runs (-1: refused by itself), pages
         const ForkAsk a = fork_ask(p, i);
+        run_s[i] = a.ok ? (a.full + kForkRun - 1) / kForkRun : -1;
+        page_s[i] = a.part;
         if (a.ok) atomicMin(first_s + a.dst, i);
     }
     __syncthreads();
     const int free_n = min(max(*p.free_count, 0), p.num_pages);
+    const bool first_cta = cluster_ctarank() == 0;
     Pair ask{0, 0}, got{0, 0}, total;
     for (int i = i0; i < i1; ++i) {
-        const ForkAsk a = fork_ask(p, i);
-        if (a.ok && first_s[a.dst] == i) ask.pages += a.part;
+        if (run_s[i] >= 0 && first_s[p.dst[i]] != i) run_s[i] = -1;   // another has its dst
+        ask.pages += run_s[i] >= 0 ? page_s[i] : 0;
     }
     // what is served of the asked pages is a prefix of them
-    auto serve = [&](Pair at, auto&& f) {
-        for (int i = i0; i < i1; ++i) {
-            ForkAsk a = fork_ask(p, i);
-            a.ok = a.ok && first_s[a.dst] == i;
-            const int want = a.ok ? a.part : 0;
-            a.ok = a.ok && (want == 0 || at.pages + want <= free_n);
-            at.pages += want;
-            f(i, a);
+    long long used = block_prefix(ask, sums, &total).pages;
+    for (int i = i0; i < i1; ++i) {
+        used += run_s[i] >= 0 ? page_s[i] : 0;
+        if (run_s[i] >= 0 && page_s[i] > 0 && used > free_n) {
+            run_s[i] = -1;
+            first_s[p.dst[i]] = INT_MAX;   // (only the first of a dst writes its word, and every other has been refused)
         }
-    };
-    const Pair asked = block_prefix(ask, sums, &total);
-    serve(asked, [&](int, const ForkAsk& a) {
-        got.rows += a.ok ? (a.full + kForkRun - 1) / kForkRun : 0;
-        got.pages += a.ok ? a.part : 0;
-    });
-    Pair at = block_prefix(got, sums, &total);
-    const bool first_cta = cluster_ctarank() == 0;
-    serve(asked, [&](int i, const ForkAsk& a) {
-        run_s[i] = static_cast<int>(at.rows);
-        page_s[i] = static_cast<int>(at.pages);
-        at.rows += a.ok ? (a.full + kForkRun - 1) / kForkRun : 0;
-        at.pages += a.ok ? a.part : 0;
-        if (!a.ok) {
-            // (only this fork can be the first of its dst, so nobody else looks at the word)
-            if (a.dst >= 0 && first_s[a.dst] == i) first_s[a.dst] = INT_MAX;
+        if (run_s[i] < 0) {
+            run_s[i] = page_s[i] = 0;
             if (first_cta && p.status) atomicOr(p.status + i, kKvRefused);
         }
-    });
+        got.rows += run_s[i];
+        got.pages += page_s[i];
+    }
+    Pair at = block_prefix(got, sums, &total);
+    for (int i = i0; i < i1; ++i) {
+        const int n = run_s[i], k = page_s[i];
+        run_s[i] = static_cast<int>(at.rows);
+        page_s[i] = static_cast<int>(at.pages);
+        at.rows += n;
+        at.pages += k;
+    }
     if (threadIdx.x == 0) {
         run_s[p.N] = static_cast<int>(total.rows);
         page_s[p.N] = static_cast<int>(total.pages);
@@ -109,9 +116,12 @@ __global__ void __launch_bounds__(kBookThreads) kv_fork_kernel(const KvForkParam
         const int d = p.dst[i];
         return d >= 0 && d < p.B && first_s[d] == i;
     };
-    const int runs = run_s[p.N], pages = page_s[p.N], lane = threadIdx.x & 31;
-    for (int c = cluster_thread() >> 5; c < runs; c += cluster_threads() >> 5) {
-        const int i = find(run_s, p.N, c), full = p.len[i] / p.page_size, col0 = (c - run_s[i]) * kForkRun;
+    const int runs = run_s[p.N], lane = threadIdx.x & 31, ctas = static_cast<int>(cluster_ctas());
+    // a CTA has consecutive runs: of forks of one sequence, as they often are, the same pages
+    const int each = (runs + ctas - 1) / ctas, c0 = static_cast<int>(cluster_ctarank()) * each, c1 = min(runs, c0 + each);
+    for (int c = c0 + static_cast<int>(threadIdx.x >> 5); c < c1; c += static_cast<int>(blockDim.x >> 5)) {
+        const int i = find(run_s, p.N, c);
+        const int full = p.len[i] / p.page_size, col0 = (c - run_s[i]) * kForkRun;
         const int* const from = p.block_table + static_cast<size_t>(p.src[i]) * p.max_pages;
         int* const to = p.block_table + static_cast<size_t>(p.dst[i]) * p.max_pages;
         int page[kForkRun / 32];
@@ -125,9 +135,14 @@ __global__ void __launch_bounds__(kBookThreads) kv_fork_kernel(const KvForkParam
             const int col = col0 + k * 32 + lane;
             if (col >= full) continue;
             to[col] = page[k];
-            if (page_ok(page[k], p.num_pages)) atomicAdd(p.page_refs + page[k], 1);
+            if (page_ok(page[k], p.num_pages)) atomicAdd((counted ? count_s : p.page_refs) + page[k], 1);
             else if (p.status) atomicOr(p.status + i, kKvBadIndex);
         }
+    }
+    if (counted) {
+        __syncthreads();
+        for (int g = threadIdx.x; g < p.num_pages; g += blockDim.x)
+            if (count_s[g] > 0) atomicAdd(p.page_refs + g, count_s[g]);
     }
     for (int i = cluster_thread(); i < p.N; i += cluster_threads()) {
         int a = -1, b = -1;
@@ -144,7 +159,7 @@ __global__ void __launch_bounds__(kBookThreads) kv_fork_kernel(const KvForkParam
         p.copy_src[i] = a;
         p.copy_dst[i] = b;
     }
-    cluster_sync_all();
+    cluster_sync_all();   // all have read the lengths
     if (!first_cta) return;
     for (int i = threadIdx.x; i < p.N; i += blockDim.x) {
         if (!served(i)) continue;
@@ -152,7 +167,7 @@ __global__ void __launch_bounds__(kBookThreads) kv_fork_kernel(const KvForkParam
         p.seq_len[d] = n;
         p.n_pages[d] = n / p.page_size + (page_s[i + 1] - page_s[i]);
     }
-    if (threadIdx.x == 0) *p.free_count = free_n - pages;
+    if (threadIdx.x == 0) *p.free_count = free_n - page_s[p.N];
 }
 
 // ---------------------------------------------------------------- release
@@ -181,11 +196,14 @@ __device__ __forceinline__ ReleaseAsk release_ask(const KvReleaseParams& p, int 
 // Which of a page's holders gives it back?  Phase by phase, a cluster barrier between them: every entry given up takes one from
 // its page's count; where that is below zero, the entries put in their numbers (INT_MIN + number, the least stays); the
 // entry that finds its own there is the one.  So the count itself is all the scratch, and the result the same in any order.
-__global__ void __launch_bounds__(kBookThreads) kv_release_kernel(const KvReleaseParams p) {
+constexpr int kHold = 6;              // blocks of a warp in registers
+constexpr int kNone = INT_MIN;        // (pages below zero are taken as -1)
+__global__ void __launch_bounds__(kBookThreads, 1) kv_release_kernel(const KvReleaseParams p) {
     extern __shared__ int smem[];
-    int* const drop_s = smem;               // [B + 1] entries given up before each sequence
+    int* const drop_s = smem;               // [B + 1] blocks of up to 128 entries given up before each sequence
     int* const copy_s = drop_s + p.B + 1;   // [B + 1] copies before it
     int* const from_s = copy_s + p.B + 1;   // [B] its first entry given up; -1 - that where it is refused
+    int* const count_s = from_s + p.B + 1;  // [num_pages] if there are few
     __shared__ Pair sums[33];
     __shared__ int mine_s;
     grid_dependency_wait();
@@ -194,52 +212,105 @@ __global__ void __launch_bounds__(kBookThreads) kv_release_kernel(const KvReleas
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
     const int free_n = min(max(*p.free_count, 0), p.num_pages);
     Pair ask{0, 0}, got{0, 0}, total;
-    for (int b = b0; b < b1; ++b) ask.pages += release_ask(p, b).copy;
-    Pair asked = block_prefix(ask, sums, &total);
+    for (int b = b0; b < b1; ++b) {   // each thread's own sequences, so far
+        const ReleaseAsk r = release_ask(p, b);
+        drop_s[b] = (r.held - r.from + 127) / 128;
+        copy_s[b] = r.copy;
+        from_s[b] = r.ok ? r.from : -1 - r.from;
+        ask.pages += r.copy;
+    }
+    const Pair asked = block_prefix(ask, sums, &total);
     const bool first_cta = cluster_ctarank() == 0;
-    auto serve = [&](Pair at, auto&& f) {
-        for (int b = b0; b < b1; ++b) {
-            const ReleaseAsk r = release_ask(p, b);
-            const bool ok = r.ok && (!r.copy || at.pages + 1 <= free_n);
-            at.pages += r.copy;
-            f(b, r, ok);
+    long long used = asked.pages;
+    for (int b = b0; b < b1; ++b) {
+        used += copy_s[b];
+        if (from_s[b] >= 0 && copy_s[b] && used > free_n) from_s[b] = -1 - from_s[b];   // the pages are out
+        if (from_s[b] < 0) {
+            drop_s[b] = copy_s[b] = 0;
+            if (first_cta && p.status) atomicOr(p.status + b, kKvRefused);
         }
-    };
-    serve(asked, [&](int, const ReleaseAsk& r, bool ok) {
-        got.rows += ok ? r.held - r.from : 0;
-        got.pages += ok && r.copy;
-    });
+        got.rows += drop_s[b];
+        got.pages += copy_s[b];
+    }
     Pair at = block_prefix(got, sums, &total);
-    serve(asked, [&](int b, const ReleaseAsk& r, bool ok) {
+    for (int b = b0; b < b1; ++b) {
+        const int n = drop_s[b], k = copy_s[b];
         drop_s[b] = static_cast<int>(at.rows);
         copy_s[b] = static_cast<int>(at.pages);
-        from_s[b] = ok ? r.from : -1 - r.from;
-        at.rows += ok ? r.held - r.from : 0;
-        at.pages += ok && r.copy;
-        if (!ok && first_cta && p.status) atomicOr(p.status + b, kKvRefused);
-    });
+        at.rows += n;
+        at.pages += k;
+    }
     if (threadIdx.x == 0) {
         drop_s[p.B] = static_cast<int>(total.rows);
         copy_s[p.B] = static_cast<int>(total.pages);
     }
     cluster_sync_all();   // all have read the counts
-    const int drops = drop_s[p.B], copies = copy_s[p.B], all = cluster_threads();
-    // this thread's entries: consecutive ones, for their order
-    const int each = (drops + all - 1) / all;
-    const int g0 = min(static_cast<long long>(drops), static_cast<long long>(cluster_thread()) * each), g1 = min(drops, g0 + each);
-    auto entries = [&](auto&& f) {   // f(sequence, entry of the table, number); the table is left until the last time
-        if (g0 >= g1) return;
-        int b = find(drop_s, p.B, g0);
-        for (int g = g0; g < g1; ++g) {
-            while (g >= drop_s[b + 1]) ++b;
-            f(b, p.block_table + static_cast<size_t>(b) * p.max_pages + from_s[b] + g - drop_s[b], g);
+    const int blocks = drop_s[p.B], copies = copy_s[p.B], all = cluster_threads(), lane = threadIdx.x & 31;
+    // this warp's blocks: consecutive ones, of which the first kHold lie in registers, their loads issued together
+    const int each = static_cast<int>((static_cast<long long>(blocks) * 32 + all - 1) / all);
+    const long long k0 = static_cast<long long>(cluster_thread() >> 5) * each;
+    const int k1 = static_cast<int>(min(static_cast<long long>(blocks), k0 + each));
+    const bool counted = p.room > 0;
+    auto sequence_of = [&](int k, int b) {   // from b, one that is not behind it, on
+        if (k >= drop_s[b + 1] && k >= drop_s[++b + 1]) b = find(drop_s, p.B, k);
+        return b;
+    };
+    int held[kHold][4];
+    {
+        int b = 0, n[kHold];
+        const int* e[kHold];
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            n[i] = 0;
+            e[i] = nullptr;
+            if (k0 + i < k1) {
+                const int k = static_cast<int>(k0) + i;
+                b = i == 0 ? find(drop_s, p.B, k) : sequence_of(k, b);
+                const int col0 = (k - drop_s[b]) * 128 + lane;
+                n[i] = p.n_pages[b] - from_s[b] - col0;
+                e[i] = p.block_table + static_cast<size_t>(b) * p.max_pages + from_s[b] + col0;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kHold; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) held[i][j] = 32 * j < n[i] ? max(e[i][32 * j], -1) : kNone;
+    }
+    // f(number, page) of the entries in order: the page, or kNone where there is none.  By whole warps; what is kNone in a register
+    // stays so, and f may make it so.
+    auto entries = [&](auto&& f) {
+#pragma unroll
+        for (int i = 0; i < kHold; ++i) {
+            if (k0 + i >= k1) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f((static_cast<int>(k0) + i) * 128 + 32 * j + lane, held[i][j]);
+        }
+        int b = k0 + kHold < k1 ? find(drop_s, p.B, static_cast<int>(k0) + kHold) : 0;
+        for (long long k = k0 + kHold; k < k1; ++k) {
+            b = sequence_of(static_cast<int>(k), b);
+            const int col0 = (static_cast<int>(k) - drop_s[b]) * 128 + lane, n = p.n_pages[b] - from_s[b] - col0;
+            const int* const e = p.block_table + static_cast<size_t>(b) * p.max_pages + from_s[b] + col0;
+            int page[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) page[j] = 32 * j < n ? max(e[32 * j], -1) : kNone;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f(static_cast<int>(k) * 128 + 32 * j + lane, page[j]);
         }
     };
-    entries([&](int b, const int* e, int) {
-        const int page = *e;
-        if (page_ok(page, p.num_pages)) atomicSub(p.page_refs + page, 1);
-        else if (p.status) atomicOr(p.status + b, kKvBadIndex);
+    auto in_cache = [&](int page) { return page_ok(page, p.num_pages); };
+    if (counted) {
+        for (int g = threadIdx.x; g < p.num_pages; g += blockDim.x) count_s[g] = 0;
+        __syncthreads();
+    }
+    entries([&](int at, int& page) {
+        if (in_cache(page)) atomicAdd((counted ? count_s : p.page_refs) + page, counted ? 1 : -1);
+        else if (page != kNone && p.status) atomicOr(p.status + find(drop_s, p.B, at >> 7), kKvBadIndex);
     });
+    if (counted) {
+        __syncthreads();
+        for (int g = threadIdx.x; g < p.num_pages; g += blockDim.x)
+            if (count_s[g] > 0) atomicSub(p.page_refs + g, count_s[g]);
+    }
     for (int b = cluster_thread(); b < p.B; b += all) {
         int src = -1, dst = -1;
         if (copy_s[b + 1] > copy_s[b]) {
@@ -250,43 +321,54 @@ __global__ void __launch_bounds__(kBookThreads) kv_release_kernel(const KvReleas
         p.copy_dst[b] = dst;
     }
     cluster_sync_all();
-    entries([&](int, const int* e, int g) {
-        const int page = *e;
-        if (page_ok(page, p.num_pages) && ld_l2(p.page_refs + page) < 0) atomicMin(p.page_refs + page, INT_MIN + g);
+    if (counted) {   // the counts as they are now
+        for (int g = threadIdx.x; g < p.num_pages; g += blockDim.x) count_s[g] = ld_l2(p.page_refs + g);
+        cluster_sync_all();
+    }
+    auto none_holds = [&](int page) { return in_cache(page) && (counted ? count_s[page] : ld_l2(p.page_refs + page)) < 0; };
+    entries([&](int at, int& page) {
+        if (none_holds(page)) atomicMin(p.page_refs + page, INT_MIN + at);
+        else page = kNone;
     });
     cluster_sync_all();
-    Pair back{0, 0};
-    entries([&](int, const int* e, int g) {
-        const int page = *e;
-        back.pages += page_ok(page, p.num_pages) && ld_l2(p.page_refs + page) == INT_MIN + g;
+    auto ours = [&](int page, int at) { return none_holds(page) && ld_l2(p.page_refs + page) == INT_MIN + at; };
+    int back = 0;
+    entries([&](int at, int& page) {
+        const bool mine = ours(page, at);
+        if (!mine) page = kNone;
+        back += __popc(__ballot_sync(0xffffffffu, mine));
     });
-    const Pair before = block_prefix(back, sums, &total);
+    const Pair before = block_prefix(Pair{0, lane == 0 ? back : 0}, sums, &total);
     if (threadIdx.x == 0) mine_s = static_cast<int>(total.pages);
     cluster_sync_all();
-    int rank = static_cast<int>(before.pages), pushed = 0;
+    int rank = static_cast<int>(__shfl_sync(0xffffffffu, before.pages, 0)), pushed = 0;
     for (uint32_t c = 0; c < cluster_ctas(); ++c) {
         const int n = ld_dsmem_int(&mine_s, c);
         if (c < cluster_ctarank()) rank += n;
         pushed += n;
     }
     const int base = free_n - copies;   // the stack without the pages for copies
-    entries([&](int b, int* e, int g) {
-        const int page = *e;
-        if (page_ok(page, p.num_pages) && ld_l2(p.page_refs + page) == INT_MIN + g) {
-            const long long place = static_cast<long long>(base) + pushed - 1 - rank++;
+    entries([&](int at, int& page) {
+        const bool mine = ours(page, at);
+        const uint32_t set = __ballot_sync(0xffffffffu, mine);
+        if (mine) {
+            const long long place = static_cast<long long>(base) + pushed - 1 - (rank + __popc(set & ((1u << lane) - 1u)));
             p.page_refs[page] = 0;
             if (place < p.num_pages) p.free_list[place] = page;
-            else if (p.status) atomicOr(p.status + b, kKvBadIndex);
+            else if (p.status) atomicOr(p.status + find(drop_s, p.B, at >> 7), kKvBadIndex);
         }
-        if (g == drop_s[b] && copy_s[b + 1] > copy_s[b]) {
-            const int fresh = ld_l2(p.copy_dst + b);
-            *e = fresh;
-            if (!page_ok(fresh, p.num_pages)) {
-                p.copy_src[b] = p.copy_dst[b] = -1;
-                if (p.status) atomicOr(p.status + b, kKvBadIndex);
-            }
-        }
+        rank += __popc(set);
     });
+    cluster_sync_all();   // the tables have been read
+    for (int b = cluster_thread(); b < p.B; b += all) {
+        if (copy_s[b + 1] == copy_s[b]) continue;
+        const int fresh = ld_l2(p.copy_dst + b);
+        p.block_table[static_cast<size_t>(b) * p.max_pages + from_s[b]] = fresh;
+        if (!page_ok(fresh, p.num_pages)) {
+            p.copy_src[b] = p.copy_dst[b] = -1;
+            if (p.status) atomicOr(p.status + b, kKvBadIndex);
+        }
+    }
     if (first_cta)
         for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
             if (from_s[b] < 0) continue;
@@ -301,7 +383,7 @@ __global__ void __launch_bounds__(kBookThreads) kv_release_kernel(const KvReleas
 // The number of a page among those in use by ballots: a warp walks a run of pages, 32 at a time, and prefix sums over the
 // warps' totals give each its start.  With `used` known, the r-th page from the top of those at `used` and above goes to the
 // r-th place from the bottom that is not in use: each finds its own r, and writes itself into the pair of that number.
-__global__ void __launch_bounds__(kBookThreads) kv_compact_kernel(const KvCompactParams p) {
+__global__ void __launch_bounds__(kBookThreads, 1) kv_compact_kernel(const KvCompactParams p) {
     extern __shared__ int smem[];
     int* const held_s = smem;   // [B + 1] entries before each sequence
     __shared__ Pair sums[33];
@@ -417,16 +499,15 @@ __global__ void __launch_bounds__(kBookThreads) kv_compact_kernel(const KvCompac
     });
 }
 
-// One cluster of `ctas` CTAs with `words` words of shared memory, most of them `most` (the kernel's limit, the same by every
-// call: another thread's call may come between it and the launch).
+// One cluster of `ctas` CTAs with `words` words of shared memory, most of them `most` (the kernel's limit, the same by every call:
+// another thread's call may come between it and the launch).
 template <typename P>
-cudaError_t launch_books(void (*kernel)(P), const P& p, bool many, size_t words, size_t most, cudaStream_t stream) {
+cudaError_t launch_books(void (*kernel)(P), const P& p, int ctas, size_t words, size_t most, cudaStream_t stream) {
     const size_t smem = words * 4;
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most * 4));
         if (e != cudaSuccess) return e;
     }
-    const int ctas = many ? 8 : 1;
     return launch_dependent_cluster(kernel, ctas, dim3(ctas), dim3(kBookThreads), smem, stream, p);
 }
 
@@ -473,17 +554,24 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_kernel(const KvCopyParam
 
 }  // namespace
 
-cudaError_t launch_kv_fork(const KvForkParams& p, cudaStream_t stream) {
-    return launch_books(kv_fork_kernel, p, p.num_pages > kManyEntries, static_cast<size_t>(p.B) + 2 * (static_cast<size_t>(p.N) + 1),
-                        3 * (kKvMaxSeq + 1), stream);
+// Words for the counts of a cache's pages beside `books` others; 0 where there are too many.
+int count_room(int num_pages, size_t books) { return num_pages <= kCountPages && books + num_pages <= kMostWords ? num_pages : 0; }
+
+cudaError_t launch_kv_fork(KvForkParams p, cudaStream_t stream) {
+    const size_t books = static_cast<size_t>(p.B) + 2 * (static_cast<size_t>(p.N) + 1);
+    p.room = count_room(p.num_pages, books);
+    return launch_books(kv_fork_kernel, p, static_cast<size_t>(p.N) * p.max_pages > kManyEntries ? 8 : 1, books + p.room, kMostWords, stream);
 }
 
-cudaError_t launch_kv_release(const KvReleaseParams& p, cudaStream_t stream) {
-    return launch_books(kv_release_kernel, p, p.num_pages > kManyEntries, 3 * (static_cast<size_t>(p.B) + 1), 3 * (kKvMaxSeq + 1), stream);
+cudaError_t launch_kv_release(KvReleaseParams p, cudaStream_t stream) {
+    const size_t books = 3 * (static_cast<size_t>(p.B) + 1);
+    p.room = count_room(p.num_pages, books);
+    return launch_books(kv_release_kernel, p, static_cast<size_t>(p.B) * p.max_pages > kManyEntries ? 8 : 1, books + p.room, kMostWords, stream);
 }
 
 cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t stream) {
-    return launch_books(kv_compact_kernel, p, p.num_pages > kManyEntries, static_cast<size_t>(p.B) + 1, kKvMaxSeq + 1, stream);
+    const bool many = p.num_pages > kManyEntries || static_cast<size_t>(p.B) * p.max_pages > kManyEntries;
+    return launch_books(kv_compact_kernel, p, many ? 8 : 1, static_cast<size_t>(p.B) + 1, kKvMaxSeq + 1, stream);
 }
 
 cudaError_t launch_kv_copy(KvCopyParams p, cudaStream_t stream) {
