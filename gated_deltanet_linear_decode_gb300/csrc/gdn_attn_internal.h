@@ -101,6 +101,7 @@ struct ChunkParams {
     void* workspace;
     int* status;          // optional [B]
     int test_stall;       // GDN_FLAG_TEST_STALL
+    int heads;            // filled in at the launch: Hkv, times what a head's units are divided in by channels
 };
 
 struct KvForkParams {

@@ -39,7 +39,7 @@ __device__ __forceinline__ void report_rows(const ChunkParams& p, int b) {
 // On to the worker's next part (gdn_chunk_plan.h).  A call: it comes once a part in several places of a kernel, and inlined its
 // divisions made a kernel of 200 KB, whose warps waited for instructions a third of their time.
 static __device__ __noinline__ bool to_next_part(const ChunkParams& p, const Line& ln, const Share& sh, Part& c) {
-    return next_part(ln, sh, p.B, p.Hkv, c, [&](int b) { return rows_of(p, b); });
+    return next_part(ln, sh, p.B, p.heads, c, [&](int b) { return rows_of(p, b); });
 }
 
 struct PlanSmem {
@@ -55,7 +55,7 @@ __device__ __forceinline__ bool my_share(const ChunkParams& p, const Line& ln, i
     const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
-        mine += p.Hkv * ln.head(rows_of(p, b));
+        mine += p.heads * ln.head(rows_of(p, b));
         if (worker == 0 && p.status) report_rows(p, b);
     }
     long long incl = mine;
@@ -79,7 +79,7 @@ __device__ __forceinline__ bool my_share(const ChunkParams& p, const Line& ln, i
         long long at = before;
         int b = b0;
         for (; b < b1 - 1; ++b) {
-            const long long h = p.Hkv * ln.head(rows_of(p, b));
+            const long long h = p.heads * ln.head(rows_of(p, b));
             if (sh.first < at + h) break;
             at += h;
         }
@@ -135,9 +135,9 @@ constexpr size_t parts_bytes(int workers) {
     return kCounterBytes + static_cast<size_t>(2) * workers * RT * (D * 4 + 8);
 }
 
-// bf16 cache and result; *done = false where the driver makes no tensor map of the strides.
-cudaError_t launch_tc(const ChunkParams& p, int head_dim, int sms, bool* done, cudaStream_t stream);
-size_t tc_workspace_bytes(int head_dim);
+// bf16 cache; *done = false where there is no tensor map of the strides.
+cudaError_t launch_tc(const ChunkParams& p, int head_dim, bool out_bf16, int sms, bool* done, cudaStream_t stream);
+size_t tc_workspace_bytes(int head_dim, bool out_bf16);
 
 }  // namespace chunk
 }  // namespace gdn

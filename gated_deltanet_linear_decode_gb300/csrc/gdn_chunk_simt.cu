@@ -282,8 +282,10 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) chunk_simt_kernel(const __
 }
 
 template <typename Ta, int D>
-cudaError_t launch(const ChunkParams& p, bool out_bf16, int sms, cudaStream_t stream) {
+cudaError_t launch(const ChunkParams& from, bool out_bf16, int sms, cudaStream_t stream) {
     using S = Simt<Ta, D>;
+    ChunkParams p = from;
+    p.heads = p.Hkv;
     const cudaError_t e = cudaFuncSetAttribute(chunk_simt_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     const int ctas = min(sms * S::kCtas, kMaxWorkers);
@@ -302,19 +304,21 @@ cudaError_t by_head(const ChunkParams& p, int head_dim, bool out_bf16, int sms, 
 }  // namespace chunk
 
 size_t chunk_workspace_bytes(int head_dim, int act_dtype, int out_dtype) {
-    if (act_dtype == GDN_BF16 && out_dtype == GDN_BF16) return chunk::tc_workspace_bytes(head_dim);
-    if (head_dim == 64) return chunk::parts_bytes<chunk::kRt, 64>(chunk::kMaxWorkers);
-    if (head_dim == 128) return chunk::parts_bytes<chunk::kRt, 128>(chunk::kMaxWorkers);
-    return chunk::parts_bytes<chunk::kRt, 256>(chunk::kMaxWorkers);
+    const size_t n = head_dim == 64    ? chunk::parts_bytes<chunk::kRt, 64>(chunk::kMaxWorkers)
+                     : head_dim == 128 ? chunk::parts_bytes<chunk::kRt, 128>(chunk::kMaxWorkers)
+                                       : chunk::parts_bytes<chunk::kRt, 256>(chunk::kMaxWorkers);
+    if (act_dtype != GDN_BF16) return n;
+    const size_t n_tc = chunk::tc_workspace_bytes(head_dim, out_dtype == GDN_BF16);
+    return n > n_tc ? n : n_tc;
 }
 
 cudaError_t launch_attn_chunk(const ChunkParams& p, int head_dim, int act_dtype, int out_dtype, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms == 0) return cudaErrorInvalidDevice;
     const bool out_bf16 = out_dtype == GDN_BF16;
-    if (act_dtype == GDN_BF16 && out_bf16) {
+    if (act_dtype == GDN_BF16) {
         bool done;
-        const cudaError_t e = chunk::launch_tc(p, head_dim, sms, &done, stream);
+        const cudaError_t e = chunk::launch_tc(p, head_dim, out_bf16, sms, &done, stream);
         if (e != cudaSuccess || done) return e;
     }
     if (act_dtype == GDN_BF16) return chunk::by_head<__nv_bfloat16>(p, head_dim, out_bf16, sms, stream);

@@ -1,4 +1,4 @@
-// gdn_chunk_tc.cu -- gdn_attn_chunk over a bf16 cache with a bf16 result: products on the 5th-generation tensor cores.
+// gdn_chunk_tc.cu -- gdn_attn_chunk over a bf16 cache: products on the 5th-generation tensor cores.
 //
 // A worker is a pair of CTAs (a cluster, two SMs) that work on one unit of up to 256 rows: S = Q . K^T and O += P . V with M = 256,
 // 128 rows in each CTA's tensor memory.  The pair shares every tile of 128 keys: of the keys each CTA has 64 in its shared memory,
@@ -17,8 +17,15 @@
 // S has two or three places, as the tensor memory allows, so that the softmax of tiles runs beside the products of others.  The
 // weights take the place of scores that have been read; the S that comes into their place waits for the product with them.
 //
-// A weight is rounded to bf16 (2^-9 of it at most): with a second part for what the rounding leaves, as gdn_attn_decode has
-// it, which is bound by memory, the product with the values would take twice the time, half again as much for the whole.
+// For a bf16 result a weight is rounded to bf16 (2^-9 of it at most): with a second part for what the rounding leaves, as
+// gdn_attn_decode has it, which is bound by memory, the product with the values would take twice the time, half again as much
+// for the whole.
+//
+// For an fp32 result a weight is three bf16 parts, which together have all its bits.  They take 192 columns a place of S, and a sum
+// over many tiles in tensor memory would be cut at every product (2^-24 or so of it, always towards zero: 1e-4 after 32,768 keys).
+// So a unit has 64 channels of the values -- a head of 256 is four units, which compute the same weights -- and a tile's O is
+// its own; a thread adds it to its row's 64 sums in registers, each group those of its tiles, relative to a base of its own.
+// (Heads of 64, 64 tokens each of 16 sequences of up to 4,096: 40 us; in fp32 on the CUDA cores 186.)
 #include <cuda.h>
 
 #include "gdn_chunk.cuh"
@@ -37,20 +44,24 @@ constexpr int kMinShare = 512;        // keys of a worker, at least
 constexpr float kSlack = 8.0f;   // how far a score may pass its row's base
 constexpr int kRows = 256, kKeys = 128, kThreads = 352, kSoft = 256;
 
-template <int D_>
+template <int D_, bool kF32_>
 struct Tc {
     static constexpr int D = D_;
-    static constexpr int NS = D == 256 ? 2 : 3;               // places of S, and of the weights that take a part of it
-    static constexpr int kVCh = D == 256 ? 128 : 64;          // channels of a CTA's values (heads of 64: all of them, in both)
+    static constexpr bool kF32 = kF32_;                       // the result
+    static constexpr int DV = kF32 ? 64 : D, kSlices = D / DV;   // channels of the values that a unit has
+    static constexpr int NS = kF32 || D == 256 ? 2 : 3;       // places of S, and of the weights that take a part of it
+    static constexpr int kVCh = kF32 ? 32 : D == 256 ? 128 : 64;   // channels of a CTA's values (bf16 results of heads of 64: all of them, in both)
+    static constexpr int kBlock = kF32 ? 32 : 64;             // channels of a row of a box of values
     static constexpr int kStageK = kKeys * D, kStageV = kKeys * 2 * kVCh;   // bytes: 64 keys, 128 keys' values
-    static constexpr int RK = D == 256 ? 2 : D == 128 ? 5 : 6;
-    static constexpr int RV = D == 256 ? 3 : D == 128 ? 5 : 6;
+    static constexpr int RK = kF32 ? (D == 256 ? 4 : 6) : D == 256 ? 2 : D == 128 ? 5 : 6;
+    static constexpr int RV = kF32 ? (D == 256 ? 3 : 6) : D == 256 ? 3 : D == 128 ? 5 : 6;
     static constexpr int kQ = 128 * D * 2;
     static constexpr int kSmem = kQ + RK * kStageK + RV * kStageV + 3072;
-    // tensor memory
-    static constexpr int kO = 0, kS = D == 256 ? 256 : 128;
-    static constexpr int kCost = D == 256 ? 1024 : 768;       // of a unit: its begin and end take as long as so many keys
-    static_assert(kSmem <= 232448 && kS + NS * 128 <= 512, "shape");
+    // tensor memory: O (of fp32 results two, by tile mod 2), the places; in a place of fp32 results S is behind 64 columns
+    static constexpr int kO = 0, kS = kF32 ? 128 : D == 256 ? 256 : 128;
+    static constexpr int kPlace = kF32 ? 192 : 128, kScores = kF32 ? 64 : 0;
+    static constexpr int kCost = D == 256 ? 896 : 640;        // of a unit: its begin and end take as long as so many keys
+    static_assert(kSmem <= 232448 && kS + NS * kPlace <= 512, "shape");
 };
 
 struct Smem {
@@ -132,6 +143,8 @@ __device__ __forceinline__ void commit_both(uint64_t* bar) {
 // Upper word of the shared-memory descriptors: 128-byte swizzle, 8-row groups 1024 bytes apart.  The lower word is the address / 16
 // and, for values, how far the next 64 channels are.
 constexpr uint32_t kDesc128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+// 64-byte swizzle, for values of 32 channels.
+constexpr uint32_t kDesc64 = (512u >> 4) | (1u << 14) | (4u << 29);
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add) {
     asm volatile(
@@ -172,6 +185,11 @@ __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t (&v)[1
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
@@ -244,13 +262,19 @@ struct Walk {
     __device__ __forceinline__ bool last() const { return t + 1 == t1; }
 };
 
+// A part in the workspace: of each CTA by 8 channels its 128 rows' -- what a warp's lanes, of a row each, write and read is
+// consecutive.  (By rows a part of 128 KB took 4.3 us to write, and six of them 28 to join.)
+__device__ __forceinline__ uint32_t part_at(int row, int ch) { return static_cast<uint32_t>((ch >> 3) * 128 + row) * 8 + (ch & 7); }
+
 // The strays of a unit's late keys (gdn_attn.cuh; those that its first row does not see) are added to the rows that see them,
 // in out or in the part at `part`: this CTA's rows, whose first token is the unit's token cta_tok.  A call, for the size of the code around it.
-template <int D>
+template <class S>
 __device__ __noinline__ void add_strays(const ChunkParams& p, const Part& c, int tok0, int cta_tok, int rows, float* part) {
+    constexpr int DV = S::DV;
+    const int hk = c.hk / S::kSlices, ch0 = c.hk % S::kSlices * DV;
 #pragma unroll 1
-    for (int i = threadIdx.x; i < rows * (D / 4); i += kSoft) {
-        const int row = i / (D / 4), ch = i % (D / 4) * 4, in = row / p.G, tok = cta_tok + in, h = c.hk * p.G + row - in * p.G;
+    for (int i = threadIdx.x; i < rows * (DV / 4); i += kSoft) {
+        const int row = i / (DV / 4), ch = i % (DV / 4) * 4, in = row / p.G, tok = cta_tok + in, h = hk * p.G + row - in * p.G;
         const int off = c.r.len - c.r.n;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
@@ -258,7 +282,7 @@ __device__ __noinline__ void add_strays(const ChunkParams& p, const Part& c, int
             const int k = j / p.cache.page_size, page = p.block_table[static_cast<size_t>(c.b) * p.max_pages + k];
             if (page < 0 || page >= p.cache.num_pages) continue;
             const float4 v = StateIO<bf16>::ld(static_cast<const bf16*>(p.cache.v) + page * p.cache.page_stride +
-                                               (j - k * p.cache.page_size) * p.cache.token_stride + c.hk * p.cache.head_stride + ch);
+                                               (j - k * p.cache.page_size) * p.cache.token_stride + hk * p.cache.head_stride + ch0 + ch);
             y.x += isfinite(v.x) ? 0.f : v.x;
             y.y += isfinite(v.y) ? 0.f : v.y;
             y.z += isfinite(v.z) ? 0.f : v.z;
@@ -266,9 +290,9 @@ __device__ __noinline__ void add_strays(const ChunkParams& p, const Part& c, int
         }
         if (y.x == 0.f && y.y == 0.f && y.z == 0.f && y.w == 0.f) continue;
         if (!part) {
-            put<bf16, D, true>(p, true, static_cast<long long>(c.r.row0) + tok0 + tok, h, ch, y);
+            put<bf16, S::D, true>(p, !S::kF32, static_cast<long long>(c.r.row0) + tok0 + tok, h, ch0 + ch, y);
         } else {
-            float4* const at = reinterpret_cast<float4*>(part + static_cast<size_t>(row) * D + ch);
+            float4* const at = reinterpret_cast<float4*>(part + part_at(row, ch));
             *at = make_float4(at->x + y.x, at->y + y.y, at->z + y.z, at->w + y.w);
         }
     }
@@ -276,13 +300,13 @@ __device__ __noinline__ void add_strays(const ChunkParams& p, const Part& c, int
 
 // The join of n parts of a few rows, by items of a row's 4 channels: eight parts' loads together.  A call, for the size of the
 // code around it.
-template <int D>
-__device__ __noinline__ void join_few(const ChunkParams& p, const Part& c, const Parts<kRows, D>& parts, int w0, int n, int tok0, int cta_tok, int rows, int row0) {
-    constexpr int kAt = 8;
+template <class S>
+__device__ __noinline__ void join_few(const ChunkParams& p, const Part& c, const Parts<kRows, S::DV>& parts, int w0, int n, int tok0, int cta_tok, int rows, int row0) {
+    constexpr int kAt = 8, D = S::DV;
     auto row_of = [&](int k) { return (k == 0 ? 2 * static_cast<size_t>(w0) + 1 : 2 * static_cast<size_t>(w0 + k)) * kRows + row0; };
 #pragma unroll 1
     for (int i = threadIdx.x; i < rows * (D / 4); i += kSoft) {
-        const int r = i / (D / 4), ch = i % (D / 4) * 4, in = r / p.G;
+        const int r = i / 2 % rows, ch = i / 2 / rows * 8 + i % 2 * 4, in = r / p.G;
         float mm = -INFINITY, ll = 0.f;
 #pragma unroll 8
         for (int k = 0; k < n; ++k) mm = fmaxf(mm, __ldcg(&parts.ml[row_of(k) + r].x));
@@ -294,9 +318,9 @@ __device__ __noinline__ void join_few(const ChunkParams& p, const Part& c, const
             float4 x[kAt];
 #pragma unroll
             for (int v = 0; v < kAt; ++v) {
-                const size_t at = row_of(min(k0 + v, n - 1)) + r;
-                z[v] = __ldcg(parts.ml + at);
-                x[v] = __ldcg(reinterpret_cast<const float4*>(parts.o + at * D + ch));
+                const size_t at = row_of(min(k0 + v, n - 1));
+                z[v] = __ldcg(parts.ml + at + r);
+                x[v] = __ldcg(reinterpret_cast<const float4*>(parts.o + at * D + part_at(r, ch)));
             }
 #pragma unroll
             for (int v = 0; v < kAt; ++v) {
@@ -306,7 +330,8 @@ __device__ __noinline__ void join_few(const ChunkParams& p, const Part& c, const
                 y = make_float4(fmaf(f, x[v].x, y.x), fmaf(f, x[v].y, y.y), fmaf(f, x[v].z, y.z), fmaf(f, x[v].w, y.w));
             }
         }
-        put<bf16, D>(p, true, static_cast<long long>(c.r.row0) + tok0 + cta_tok + in, c.hk * p.G + r - in * p.G, ch, attn::times(y, ll == 0.f ? 0.f : 1.0f / ll));
+        put<bf16, S::D>(p, !S::kF32, static_cast<long long>(c.r.row0) + tok0 + cta_tok + in, c.hk / S::kSlices * p.G + r - in * p.G, c.hk % S::kSlices * D + ch,
+                        attn::times(y, ll == 0.f ? 0.f : 1.0f / ll));
     }
 }
 
@@ -319,8 +344,8 @@ template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                     const __grid_constant__ CUtensorMap q_map, const Boxes kb, const Boxes vb, const Division by_page) {
-    constexpr int D = S::D, NS = S::NS, RK = S::RK, RV = S::RV;
-    constexpr int kKBlocks = D / 64, kVBlocks = S::kVCh / 64;   // blocks of 64 channels in a CTA's stages
+    constexpr int D = S::D, DV = S::DV, NS = S::NS, RK = S::RK, RV = S::RV;
+    constexpr int kKBlocks = D / 64, kVBlocks = S::kVCh / S::kBlock;   // blocks of channels in a CTA's stages
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t* const q_s = smem;
     uint8_t* const k_s = q_s + S::kQ;
@@ -380,8 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ps = p.cache.page_size, groups = kKeys / bx.tokens;
         // Lane l has the tile's groups of bx.tokens keys l + 32 k, [0] of the tile to be copied, [1] of the one being looked up.
         constexpr int kPer = 4;
-        int page[2][kPer] = {}, in[2][kPer] = {}, head[2] = {}, seq[2] = {}, q_tok[2] = {};   // in -1: no key; seq -1: no tile; q_tok -1: not a part's first
-        int parts_begun = 0, part_seq = 0, part_head = 0;
+        int page[2][kPer] = {}, in[2][kPer] = {}, head[2] = {}, slice[2] = {}, seq[2] = {}, q_tok[2] = {};   // in -1: no key; seq -1: no tile; q_tok -1: not a part's first
+        int parts_begun = 0, part_seq = 0, part_head = 0, part_slice = 0;
         int end = 0;               // keys from `end` on are nobody's
         const int* table = nullptr;   // the sequence's pages
         auto look_up = [&](int a) {
@@ -390,13 +415,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             q_tok[a] = -1;
             if (w.first()) {
                 part_seq = c.b;
-                part_head = c.hk;
+                part_head = c.hk / S::kSlices;
+                part_slice = c.hk % S::kSlices;
                 q_tok[a] = c.r.row0 + c.i * ln.tokens + static_cast<int>(rank) * cta_tokens;
                 end = c.seen;
                 table = p.block_table + static_cast<size_t>(c.b) * p.max_pages;
             }
             seq[a] = part_seq;
             head[a] = part_head;
+            slice[a] = part_slice;
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 if (k > 0 && groups <= 32 * k) break;
@@ -420,20 +447,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             return in_cta(smem_u32(bar), 0);
         };
         // copies of the tile at [0]: boxes [g0, g0 + n), all blocks from `block` on, by the lanes that have them
+        const int row_bytes = keys ? 128 : 2 * S::kBlock;
         auto copy = [&](uint32_t stage, const CUtensorMap* map, int g0, int n, int block, int blocks, uint32_t bar) {
 #pragma unroll 1
             for (int k = g0 >> 5; k <= (g0 + n - 1) >> 5; ++k) {
                 const int pg = k == 0 ? page[0][0] : k == 1 ? page[0][1] : k == 2 ? page[0][2] : page[0][3];
                 const int tk = max(k == 0 ? in[0][0] : k == 1 ? in[0][1] : k == 2 ? in[0][2] : in[0][3], 0);
                 const int r = lane + 32 * k - g0, row = r * bx.tokens;
-                uint32_t dst = stage + (row >> 3) * blocks * 1024 + (row & 7) * 128;
+                uint32_t dst = stage + (row >> 3) * blocks * 8 * row_bytes + (row & 7) * row_bytes;
                 if (r >= 0 && r < n) {
                     if (bx.whole) {
                         const bool there = pg >= 0 && pg < p.cache.num_pages;   // (the coordinates of another would be some other's)
                         tma_load(dst, map, 0, block, there ? pg * bx.group + (tk >> 3) : 0, there ? pg * bx.head + head[0] : -1, bar);
                     } else {
 #pragma unroll 1
-                        for (int c = 0; c < blocks; ++c, dst += 1024) tma_load(dst, map, tk, block + c, head[0], pg, bar);
+                        for (int c = 0; c < blocks; ++c, dst += 8 * row_bytes) tma_load(dst, map, tk, block + c, head[0], pg, bar);
                     }
                 }
                 __syncwarp();
@@ -443,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (;; ++n) {
             head[0] = head[1];
+            slice[0] = slice[1];
             seq[0] = seq[1];
             q_tok[0] = q_tok[1];
 #pragma unroll
@@ -486,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const uint32_t bar = announce(keys ? sm.k_full + n % RK : sm.v_full + n % RV, keys ? 2 * S::kStageK : 2 * S::kStageV);
             copy(keys ? smem_u32(k_s) + n % RK * S::kStageK : smem_u32(v_s) + n % RV * S::kStageV, keys ? &k_map : &v_map,
-                 keys ? static_cast<int>(rank) * groups / 2 : 0, keys ? groups / 2 : groups, !keys && D > 64 ? static_cast<int>(rank) * kVBlocks : 0,
+                 keys ? static_cast<int>(rank) * groups / 2 : 0, keys ? groups / 2 : groups, keys ? 0 : S::kF32 ? 2 * slice[0] + static_cast<int>(rank) : D > 64 ? static_cast<int>(rank) * kVBlocks : 0,
                  keys ? kKBlocks : kVBlocks, bar);
         }
         // nothing is in flight when the pair ends: the last copies of every stage have landed (limits of their own, for after a give-up)
@@ -505,10 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint32_t id_o = tc::idesc_f16(256, 2 * S::kVCh, 0, 1, 0) | (1u << 7) | (1u << 10);
             const uint32_t q_lo = (smem_u32(q_s) >> 4) + (1u << 16), k_lo = (smem_u32(k_s) >> 4) + (1u << 16);
             // from one group of 8 to the next; from one block of 64 channels to the next, 1024 bytes
-            constexpr uint32_t k_hi = (kDesc128 & ~0x3FFFu) | (kKBlocks * 1024 >> 4), v_hi = (kDesc128 & ~0x3FFFu) | (kVBlocks * 1024 >> 4);
+            constexpr uint32_t k_hi = (kDesc128 & ~0x3FFFu) | (kKBlocks * 1024 >> 4), v_hi = S::kF32 ? kDesc64 : (kDesc128 & ~0x3FFFu) | (kVBlocks * 1024 >> 4);
             const uint32_t v_lo = (smem_u32(v_s) >> 4) + ((1024u >> 4) << 16);
             auto issue_s = [&]() {   // of tile number nq, whose operands have landed
-                const uint32_t d = t_s + nq % NS * 128, b = k_lo + nq % RK * (S::kStageK >> 4);
+                const uint32_t d = t_s + nq % NS * S::kPlace + S::kScores, b = k_lo + nq % RK * (S::kStageK >> 4);
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
 #pragma unroll
@@ -519,10 +548,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (w.last()) commit_both(&sm.q_empty);
             };
             auto issue_o = [&](int g) {
-                const uint32_t a = t_s + g % NS * 128, b = v_lo + g % RV * (S::kStageV >> 4);
-                const bool add = !((firsts >> (g & 31)) & 1);
+                const uint32_t a = t_s + g % NS * S::kPlace, b = v_lo + g % RV * (S::kStageV >> 4);
+                if constexpr (S::kF32) {   // a tile's own O, of the weights' smallest parts first
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) mma_ts(t_o, a + ks * 8, b + ks * (kVBlocks * 2048 >> 4), v_hi, id_o, add || ks != 0);
+                    for (int part = 2; part >= 0; --part)
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_ts(t_o + (g & 1) * 64, a + (part == 0 ? ks * 8 : 48 + part * 16 + ks / 2 * 32 + ks % 2 * 8), b + ks * (1024 >> 4), v_hi, id_o, part != 2 || ks != 0);
+                } else {
+                    const bool add = !((firsts >> (g & 31)) & 1);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) mma_ts(t_o, a + ks * 8, b + ks * (kVBlocks * 2048 >> 4), v_hi, id_o, add || ks != 0);
+                }
                 commit_both(sm.pv_done + g % NS);
                 commit_both(sm.v_empty + g % RV);
             };
@@ -560,25 +597,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ softmax
         const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
         const uint32_t my_lanes = static_cast<uint32_t>(32 * quarter) << 16;
-        const uint32_t my_o = t_o + my_lanes + half * (D / 2);   // at a part's end a thread has half of its row's channels
+        const uint32_t my_o = t_o + my_lanes + half * (DV / 2);   // at a part's end a thread has half of its row's channels
         const float scale = p.scale * kLog2e, size = scale == 0.f ? 1.f : fabsf(scale);
         const int in = row / p.G;   // token of this CTA's
         const int cta_tok = static_cast<int>(rank) * cta_tokens, tok = cta_tok + in;   // of the unit's
         auto wait = [&](uint64_t* bar, uint32_t parity) { wait_for(bar, parity, &sm.abort); };
         int g = 0;           // tile number
         uint32_t told = 0;   // phases of v_told
+        // acc = acc * f + tile's O, of which `at` has 64 columns
+        auto add_o = [&](float (&acc)[S::kF32 ? 64 : 1], uint32_t at, int tile, float f) {
+            wait(sm.pv_done + tile % NS, (tile / NS) & 1);
+            tc::fence_after_sync();
+            if constexpr (S::kF32) {
+#pragma unroll
+                for (int i = 0; i < 64; i += 32) {
+                    float v[32];
+                    tc::tmem_ld32(at + i, v);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float2 x = fma2(make_float2(acc[i + e], acc[i + e + 1]), make_float2(f, f), make_float2(v[e], v[e + 1]));
+                        acc[i + e] = x.x;
+                        acc[i + e + 1] = x.y;
+                    }
+                }
+            }
+        };
         do {
             const int t0 = c.t0, t1 = c.t1;
             const int tok0 = c.i * ln.tokens, n_tok = tokens_of(ln, c), off = c.r.len - c.r.n;
             const int here = min(max(n_tok - cta_tok, 0), cta_tokens) * p.G;   // rows of this CTA
             const int end = c.seen;
+            float acc[S::kF32 ? 64 : 1] = {};   // fp32 results: the row's sums over this group's tiles but for the newest,
+            float to_next = 1.0f;                    // relative to the base of the newest but one; times this to that of the newest
             float m = -INFINITY, l = 0.f;   // of a row: the base of its weights, -inf before it has seen a key; this thread's share of their sum
 #pragma unroll 1
             for (int t = t0; t < t1; ++t, ++g) {
                 if ((g & 1) != half) continue;   // the other group's
                 wait(sm.s_full + g % NS, (g / NS) & 1);
                 tc::fence_after_sync();
-                const uint32_t my_s = t_s + my_lanes + g % NS * 128;
+                const uint32_t my_s = t_s + my_lanes + g % NS * S::kPlace + S::kScores;
                 // late: some rows do not see some of the tile's keys
                 const bool late = (t + 1) * kKeys > off + tok0 + 1;
                 const uint4 there = *reinterpret_cast<const uint4*>(sm.valid[g & 15]);
@@ -620,57 +677,102 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_for(s1);
                 larger(s0);
                 larger(s1);
-                tmem_ask32(my_s, s0);
                 const float mx = fmaxf(ma, mb) * size;
-                // the base that the other group had for the tile before, and this tile's for it
-                if (g > 0) take_base(quarter + 4 * (half ^ 1));
-                const float before = t == t0 ? -INFINITY : sm.base[half ^ 1][row];
-                // (a row's base moves by its own scores alone: its result does not depend on the rows beside it)
-                const bool up = mx > before + kSlack;   // (above -inf, at a row's first keys)
-                const float now = up ? mx : before;
-                sm.base[half][row] = now;
-                give_base(quarter + 4 * half);
-                if (t > t0 && __any_sync(0xffffffffu, up)) {
-                    wait(sm.pv_done + (g - 1) % NS, ((g - 1) / NS) & 1);   // the tile before has been added: O stands still
-                    tc::fence_after_sync();
-                    const float f = up ? ex2(before - now) : 1.0f;
-#pragma unroll 1
-                    for (int i = 0; i < D; i += 32) {
-                        float v[32];
-                        tc::tmem_ld32(t_o + my_lanes + i, v);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] *= f;
-                        tc::tmem_st32(t_o + my_lanes + i, v);
-                    }
-                }
-                if (now != m) {
-                    l *= ex2(m - now);   // (m -inf: there is none yet)
-                    m = now;
-                }
-                const float base = m == -INFINITY ? 0.f : m;
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                auto weights = [&](int i, const float (&s)[32]) {   // two keys a column, in the place of scores that have been read
-                    uint32_t w2[16];
+                if constexpr (S::kF32) {
+                    // The groups' bases and sums are apart until the part's end.  The tile before of this group has its O by now, or soon.
+                    const float now = fmaxf(m, mx);
+                    if (t >= t0 + 2) add_o(acc, t_o + my_lanes + half * 64, g - 2, to_next);
+                    to_next = now == m ? 1.0f : ex2(m - now);
+                    l *= to_next;
+                    m = now;
+                    const float base = m == -INFINITY ? 0.f : m;
+                    // 32 weights: bf16 parts, each of what the ones before leave -- all bits of a weight.  The first parts go before the
+                    // scores, the other two into the place of the scores that they are from
+                    auto weights = [&](int i, const float (&s)[32]) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(size, size), make_float2(-base, -base));
-                        const float2 y = make_float2(ex2(x.x), ex2(x.y));
-                        sum[e & 1] = add2(sum[e & 1], y);
-                        w2[e] = StateIO<bf16>::pack(y.x, y.y);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t w[3][8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const int at = 16 * h + 2 * e;
+                                const float2 x = fma2(make_float2(s[at], s[at + 1]), make_float2(size, size), make_float2(-base, -base));
+                                float2 y = make_float2(ex2(x.x), ex2(x.y));
+                                sum[e & 1] = add2(sum[e & 1], y);
+#pragma unroll
+                                for (int part = 0; part < 3; ++part) {
+                                    const uint32_t z = w[part][e] = StateIO<bf16>::pack(y.x, y.y);
+                                    if (part < 2) y = fma2(make_float2(__uint_as_float(z << 16), __uint_as_float(z & 0xffff0000u)), make_float2(-1.f, -1.f), y);
+                                }
+                            }
+                            tmem_st8u(my_s - 64 + i * 16 + 8 * h, w[0]);
+                            tmem_st8u(my_s + i * 32 + 8 * h, w[1]);
+                            tmem_st8u(my_s + i * 32 + 16 + 8 * h, w[2]);
+                        }
+                    };
+                    tmem_ask32(my_s, s0);
+                    tmem_wait_for(s0);
+                    tmem_ask32(my_s + 32, s1);
+                    weights(0, s0);
+                    tmem_wait_for(s1);
+                    tmem_ask32(my_s + 64, s0);
+                    weights(1, s1);
+                    tmem_wait_for(s0);
+                    tmem_ask32(my_s + 96, s1);
+                    weights(2, s0);
+                    tmem_wait_for(s1);
+                    weights(3, s1);
+                } else {
+                    tmem_ask32(my_s, s0);
+                    // the base that the other group had for the tile before, and this tile's for it
+                    if (g > 0) take_base(quarter + 4 * (half ^ 1));
+                    const float before = t == t0 ? -INFINITY : sm.base[half ^ 1][row];
+                    // (a row's base moves by its own scores alone: its result does not depend on the rows beside it)
+                    const bool up = mx > before + kSlack;   // (above -inf, at a row's first keys)
+                    const float now = up ? mx : before;
+                    sm.base[half][row] = now;
+                    give_base(quarter + 4 * half);
+                    if (t > t0 && __any_sync(0xffffffffu, up)) {
+                        wait(sm.pv_done + (g - 1) % NS, ((g - 1) / NS) & 1);   // the tile before has been added: O stands still
+                        tc::fence_after_sync();
+                        const float f = up ? ex2(before - now) : 1.0f;
+#pragma unroll 1
+                        for (int i = 0; i < D; i += 32) {
+                            float v[32];
+                            tc::tmem_ld32(t_o + my_lanes + i, v);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] *= f;
+                            tc::tmem_st32(t_o + my_lanes + i, v);
+                        }
                     }
-                    tmem_st16u(my_s + i * 16, w2);
-                };
-                tmem_wait_for(s0);
-                tmem_ask32(my_s + 32, s1);
-                tmem_wait_for(s1);
-                weights(0, s0);
-                tmem_ask32(my_s + 64, s0);
-                tmem_wait_for(s0);
-                weights(1, s1);
-                tmem_ask32(my_s + 96, s1);
-                tmem_wait_for(s1);
-                weights(2, s0);
-                weights(3, s1);
+                    if (now != m) {
+                        l *= ex2(m - now);   // (m -inf: there is none yet)
+                        m = now;
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+                    auto weights = [&](int i, const float (&s)[32]) {   // two keys a column, in the place of scores that have been read
+                        uint32_t w2[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 x = fma2(make_float2(s[2 * e], s[2 * e + 1]), make_float2(size, size), make_float2(-base, -base));
+                            const float2 y = make_float2(ex2(x.x), ex2(x.y));
+                            sum[e & 1] = add2(sum[e & 1], y);
+                            w2[e] = StateIO<bf16>::pack(y.x, y.y);
+                        }
+                        tmem_st16u(my_s + i * 16, w2);
+                    };
+                    tmem_wait_for(s0);
+                    tmem_ask32(my_s + 32, s1);
+                    tmem_wait_for(s1);
+                    weights(0, s0);
+                    tmem_ask32(my_s + 64, s0);
+                    tmem_wait_for(s0);
+                    weights(1, s1);
+                    tmem_ask32(my_s + 96, s1);
+                    tmem_wait_for(s1);
+                    weights(2, s0);
+                    weights(3, s1);
+                }
                 sum[0] = add2(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 if (late) {
@@ -695,7 +797,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int x = threadIdx.x & 127; x < (k1 - k0) * (S::kVCh / 8); x += 128) {
                             const int key = k0 + x / (S::kVCh / 8), ch = x % (S::kVCh / 8);
-                            uint8_t* const at = st + (key >> 3) * (kVBlocks * 1024) + ch / 8 * 1024 + (key & 7) * 128 + ((ch ^ key) & 7) * 16;
+                            uint8_t* const at = S::kF32 ? st + key * 64 + (ch ^ ((key >> 1) & 3)) * 16
+                                                        : st + (key >> 3) * (kVBlocks * 1024) + ch / 8 * 1024 + (key & 7) * 128 + ((ch ^ key) & 7) * 16;
                             if (key < kend) found |= attn::take_strays<bf16>(at);
                             else *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
                         }
@@ -715,15 +818,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- the part's end
             const bool any = t0 < t1, whole = c.whole();
             const long long tr = static_cast<long long>(c.r.row0) + tok0 + tok;
-            const int h = c.hk * p.G + row - in * p.G, ch0 = half * (D / 2);
+            const int h = c.hk / S::kSlices * p.G + row - in * p.G, ch0 = half * (DV / 2), col0 = c.hk % S::kSlices * DV + ch0;   // of the part, of the head
             const bool gated = p.gate && row < here;
-            const bf16* const gate = static_cast<const bf16*>(p.gate) + (tr * p.ldg + static_cast<long long>(h) * D + ch0);
+            const bf16* const gate = static_cast<const bf16*>(p.gate) + (tr * p.ldg + static_cast<long long>(h) * D + col0);
             if (gated)   // the gate's lines, while the last products run
-                for (int i = 0; i < D / 2; i += 64) prefetch_l2(gate + i);
+                for (int i = 0; i < DV / 2; i += 64) prefetch_l2(gate + i);
+            if constexpr (S::kF32) {   // the groups' sums to where their last O was
+                const int mine = (g - 1 - half) & 1 ? g - 2 : g - 1;
+                if (mine >= g - (t1 - t0)) add_o(acc, t_o + my_lanes + half * 64, mine, to_next);
+#pragma unroll
+                for (int i = 0; i < 64; i += 32) tc::tmem_st32(t_o + my_lanes + half * 64 + i, reinterpret_cast<float(&)[32]>(acc[i]));
+                tc::tmem_wait_st();
+                tc::fence_before_sync();
+            }
             Part next = c;   // and the way to the next part
             const bool more = to_next_part(p, ln, sh, next);
-            if (any) wait(sm.pv_done + (g - 1) % NS, ((g - 1) / NS) & 1);
-            tc::fence_after_sync();
+            if constexpr (!S::kF32) {
+                if (any) wait(sm.pv_done + (g - 1) % NS, ((g - 1) / NS) & 1);
+                tc::fence_after_sync();
+            }
             if (p.test_stall && warp == 3) long_wait(smem_u32(&sm.never), 0, &sm.abort, 256);
             if (sm.abort) sm.stop = 1;   // told before the barrier, behind which all look
             // the sum relative to the last tile's base, which the group of that tile has
@@ -733,36 +846,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (sm.stop) {   // a wait gave up: nothing of this part is written
                 if (threadIdx.x == 0 && p.status) atomicOr(p.status + c.b, 16);
             } else {
-                m = sm.base[any ? (g - 1) & 1 : 0][row];
-                float sum = 0.f;
+                m = S::kF32 ? fmaxf(sm.base[0][row], sm.base[1][row]) : sm.base[any ? (g - 1) & 1 : 0][row];
+                float sum = 0.f, fg[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) sum += sm.base[i][row] == -INFINITY ? 0.f : sm.sum[i][row] * ex2(sm.base[i][row] - m);
-                const Parts<kRows, D> parts(p.workspace, workers);
-                const size_t place = Parts<kRows, D>::place(worker, c);
-                float* const part = parts.o + (place * kRows + rank * 128) * D;
+                for (int i = 0; i < 2; ++i) {
+                    fg[i] = sm.base[i][row] == -INFINITY ? 0.f : ex2(sm.base[i][row] - m);
+                    sum += fg[i] == 0.f ? 0.f : sm.sum[i][row] * fg[i];
+                }
+                if constexpr (S::kF32) tc::fence_after_sync();
+                auto load_o = [&](int i, float (&v)[32]) {   // columns i.. of this thread's half, relative to m
+                    tc::tmem_ld32(my_o + i, v);
+                    if constexpr (S::kF32) {
+                        float w[32];
+                        tc::tmem_ld32(my_o + 64 + i, w);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = fmaf(v[e], fg[0], w[e] * fg[1]);
+                    }
+                };
+                const Parts<kRows, DV> parts(p.workspace, workers);
+                const size_t place = Parts<kRows, DV>::place(worker, c);
+                float* const part = parts.o + (place * kRows + rank * 128) * DV;
                 bool result = whole;   // this CTA has the rows' result, here or with the other parts
                 int n = 1, w0 = 0;
+                const bool ws32 = on32(p.workspace);
                 if (!whole) {
-                    const bool ws32 = on32(p.workspace);
 #pragma unroll 1
-                    for (int i = 0; i < D / 2; i += 32) {
+                    for (int i = 0; i < DV / 2; i += 32) {
                         float v[32];
-                        tc::tmem_ld32(my_o + i, v);
+                        load_o(i, v);
                         if (row < here) {
-                            float* const to = part + static_cast<size_t>(row) * D + ch0 + i;
+                            float* const to = part + part_at(row, ch0 + i);
 #pragma unroll
                             for (int e = 0; e < 32; e += 8) {
                                 uint32_t y[8];
 #pragma unroll
                                 for (int q = 0; q < 8; ++q) y[q] = __float_as_uint(v[e + q]);
-                                store16(to + e, ws32, y);
+                                store16(to + e * 128, ws32, y);
                             }
                         }
                     }
                     if (half == 0 && row < here) parts.ml[place * kRows + rank * 128 + row] = make_float2(m, sum);
                     if (sm.strays) {
                         sync_softmax();
-                        add_strays<D>(p, c, tok0, cta_tok, here, part);
+                        add_strays<S>(p, c, tok0, cta_tok, here, part);
                     }
                     // the worker that arrives last joins this CTA's rows of all parts
                     const long long first = c.at + ln.cost;
@@ -778,8 +904,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     result = sm.last;
                 }
                 auto row_of = [&](int k) { return (k == 0 ? 2 * static_cast<size_t>(w0) + 1 : 2 * static_cast<size_t>(w0 + k)) * kRows + rank * 128; };
-                if (result && !whole && here * (D / 4) <= 4 * kSoft) {
-                    join_few<D>(p, c, parts, w0, n, tok0, cta_tok, here, static_cast<int>(rank) * 128);
+                if (result && !whole && here * (DV / 4) <= 4 * kSoft) {
+                    join_few<S>(p, c, parts, w0, n, tok0, cta_tok, here, static_cast<int>(rank) * 128);
                 } else if (result) {
                     // of several parts in their order, whoever was last: statistics first
                     float mm = m, ll = sum;
@@ -797,9 +923,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const float f = ll == 0.f ? 0.f : 1.0f / ll;
                     const bool gate32 = on32(p.gate) && p.ldg % 16 == 0, out32 = on32(p.out);
-                    bf16* const to = static_cast<bf16*>(p.out) + (tr * p.Hq + h) * D + ch0;
+                    const long long to = (tr * p.Hq + h) * D + col0;
 #pragma unroll 1
-                    for (int i = 0; i < D / 2; i += 32) {
+                    for (int i = 0; i < DV / 2; i += 32) {
                         uint32_t gt[2][8];
                         if (gated) {
                             load16(gate + i, gate32, gt[0]);
@@ -807,24 +933,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         float v[32];
                         if (whole) {
-                            if (any) tc::tmem_ld32(my_o + i, v);
+                            if (any) load_o(i, v);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = 0.f;
                             if (row < here)
 #pragma unroll 1
-                                for (int k = 0; k < n; ++k) {
-                                    const float4* const x = reinterpret_cast<const float4*>(parts.o + (row_of(k) + row) * D + ch0 + i);
-                                    const float fk = ex2(__ldcg(&parts.ml[row_of(k) + row].x) - mm);
-                                    float4 y[8];
+                                for (int k = 0; k < n; k += 2) {   // two parts' loads together; past the last part it again, without weight
+                                    uint32_t y[2][4][8];
+                                    float fk[2];
 #pragma unroll
-                                    for (int q = 0; q < 8; ++q) y[q] = __ldcg(x + q);
+                                    for (int x = 0; x < 2; ++x) {
+                                        const size_t first = row_of(min(k + x, n - 1));
+                                        fk[x] = k + x < n ? __ldcg(&parts.ml[first + row].x) : -INFINITY;
 #pragma unroll
-                                    for (int q = 0; q < 8; ++q) {
-                                        v[4 * q] = fmaf(fk, y[q].x, v[4 * q]);
-                                        v[4 * q + 1] = fmaf(fk, y[q].y, v[4 * q + 1]);
-                                        v[4 * q + 2] = fmaf(fk, y[q].z, v[4 * q + 2]);
-                                        v[4 * q + 3] = fmaf(fk, y[q].w, v[4 * q + 3]);
+                                        for (int q = 0; q < 4; ++q) load16(parts.o + first * DV + part_at(row, ch0 + i + 8 * q), ws32, y[x][q]);
+                                    }
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x) {
+                                        if (k + x == n) break;   // (nothing without weight is added: it may be infinite)
+                                        const float fx = ex2(fk[x] - mm);
+#pragma unroll
+                                        for (int q = 0; q < 32; ++q) v[q] = fmaf(fx, __uint_as_float(y[x][q / 8][q % 8]), v[q]);
                                     }
                                 }
                         }
@@ -835,22 +965,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
                                     const uint32_t x = gt[e / 16][e % 16 / 2];
-                                    v[e] *= gate_of<false>(__uint_as_float(x << 16));
-                                    v[e + 1] *= gate_of<false>(__uint_as_float(x & 0xffff0000u));
+                                    v[e] *= gate_of<S::kF32>(__uint_as_float(x << 16));
+                                    v[e + 1] *= gate_of<S::kF32>(__uint_as_float(x & 0xffff0000u));
                                 }
                             }
 #pragma unroll
-                            for (int e = 0; e < 32; e += 16) {
+                            for (int e = 0; e < 32; e += S::kF32 ? 8 : 16) {
                                 uint32_t y[8];
 #pragma unroll
-                                for (int q = 0; q < 8; ++q) y[q] = StateIO<bf16>::pack(v[e + 2 * q], v[e + 2 * q + 1]);
-                                store16(to + i + e, out32, y);
+                                for (int q = 0; q < 8; ++q) y[q] = S::kF32 ? __float_as_uint(v[e + q]) : StateIO<bf16>::pack(v[e + 2 * q & 31], v[e + 2 * q + 1 & 31]);
+                                if constexpr (S::kF32) store16(static_cast<float*>(p.out) + to + i + e, out32, y);
+                                else store16(static_cast<bf16*>(p.out) + to + i + e, out32, y);
                             }
                         }
                     }
                     if (whole && sm.strays) {
                         sync_softmax();
-                        add_strays<D>(p, c, tok0, cta_tok, here, nullptr);
+                        add_strays<S>(p, c, tok0, cta_tok, here, nullptr);
                     }
                 }
                 tc::fence_before_sync();
@@ -859,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!more) break;
             c = next;
         } while (true);
-        if (g > 0 && (g & 1) == half) take_base(quarter + 4 * (half ^ 1));   // the last one given
+        if (!S::kF32 && g > 0 && (g & 1) == half) take_base(quarter + 4 * (half ^ 1));   // the last one given
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -868,11 +999,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem), "r"(512));
 }
 
-// The map of a half of the cache, and the boxes of up to `most` tokens and `blocks` blocks; false if the driver refuses it.
-bool cache_map(CUtensorMap* m, Boxes* b, const ChunkParams& p, const void* half, int D, int most, int blocks) {
+// The map of a half of the cache, and the boxes of up to `most` tokens and `blocks` blocks of `block` channels; false if the driver refuses it.
+bool cache_map(CUtensorMap* m, Boxes* b, const ChunkParams& p, const void* half, int D, int most, int blocks, uint32_t block) {
     const KvCache& c = p.cache;
     auto bytes = [&](long long stride) { return stride ? static_cast<uint64_t>(stride) * 2 : static_cast<uint64_t>(D) * 2; };
-    const uint64_t ps = c.page_size, pages = c.num_pages, heads = p.Hkv, parts = D / 64;
+    const uint64_t ps = c.page_size, pages = c.num_pages, heads = p.Hkv, parts = D / block;
     int two = 128;   // tokens that always lie in one page
     while (c.page_size % two != 0) two /= 2;
     const bool pages_follow = pages == 1 || c.page_stride == c.page_size * c.token_stride;
@@ -881,21 +1012,24 @@ bool cache_map(CUtensorMap* m, Boxes* b, const ChunkParams& p, const void* half,
     if (b->whole) {
         b->group = pages_follow ? c.page_size / 8 : 0;
         b->head = pages_follow ? 0 : p.Hkv;
-        const uint64_t dims[5] = {64, 8, parts, pages_follow ? pages * ps / 8 : ps / 8, pages_follow ? heads : pages * heads};
-        const uint64_t strides[4] = {bytes(c.token_stride), 128, bytes(c.token_stride) * 8, pages_follow || heads > 1 ? bytes(c.head_stride) : bytes(c.page_stride)};
-        const uint32_t boxes[5] = {64, 8, static_cast<uint32_t>(blocks), static_cast<uint32_t>(b->tokens / 8), 1};
+        const uint64_t dims[5] = {block, 8, parts, pages_follow ? pages * ps / 8 : ps / 8, pages_follow ? heads : pages * heads};
+        const uint64_t strides[4] = {bytes(c.token_stride), 2 * block, bytes(c.token_stride) * 8, pages_follow || heads > 1 ? bytes(c.head_stride) : bytes(c.page_stride)};
+        const uint32_t boxes[5] = {block, 8, static_cast<uint32_t>(blocks), static_cast<uint32_t>(b->tokens / 8), 1};
         return make_tensor_map_bf16(m, half, 5, dims, strides, boxes);
     }
     b->tokens = two < 8 ? two : 8;
-    const uint64_t dims[5] = {64, ps, parts, heads, pages};
-    const uint64_t strides[4] = {bytes(c.token_stride), 128, bytes(c.head_stride), bytes(c.page_stride)};
-    const uint32_t boxes[5] = {64, static_cast<uint32_t>(b->tokens), 1, 1, 1};
+    if (b->tokens * block * 2 < 128) return false;   // where a box goes is a multiple of 128 bytes
+    const uint64_t dims[5] = {block, ps, parts, heads, pages};
+    const uint64_t strides[4] = {bytes(c.token_stride), 2 * block, bytes(c.head_stride), bytes(c.page_stride)};
+    const uint32_t boxes[5] = {block, static_cast<uint32_t>(b->tokens), 1, 1, 1};
     return make_tensor_map_bf16(m, half, 5, dims, strides, boxes);
 }
 
-template <int D>
-cudaError_t launch(const ChunkParams& p, int sms, bool* done, cudaStream_t stream) {
-    using S = Tc<D>;
+template <class S>
+cudaError_t launch(const ChunkParams& from, int sms, bool* done, cudaStream_t stream) {
+    constexpr int D = S::D;
+    ChunkParams p = from;
+    p.heads = p.Hkv * S::kSlices;
     *done = false;
     Boxes kb, vb;
     Division by_page{0, 0};
@@ -906,7 +1040,7 @@ cudaError_t launch(const ChunkParams& p, int sms, bool* done, cudaStream_t strea
     const uint64_t dims[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.Hq), static_cast<uint64_t>(p.T)};
     const uint64_t strides[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(p.ldq) * 2};
     const uint32_t boxes[3] = {64, static_cast<uint32_t>(p.G), static_cast<uint32_t>(128 / p.G)};
-    if (!cache_map(&k, &kb, p, p.cache.k, D, 64, D / 64) || !cache_map(&v, &vb, p, p.cache.v, D, 128, S::kVCh / 64) || !make_tensor_map_bf16(&q, p.q, 3, dims, strides, boxes))
+    if (!cache_map(&k, &kb, p, p.cache.k, D, 64, D / 64, 64) || !cache_map(&v, &vb, p, p.cache.v, D, 128, S::kVCh / S::kBlock, S::kBlock) || !make_tensor_map_bf16(&q, p.q, 3, dims, strides, boxes))
         return cudaSuccess;
     *done = true;
     const cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
@@ -917,16 +1051,16 @@ cudaError_t launch(const ChunkParams& p, int sms, bool* done, cudaStream_t strea
 
 }  // namespace
 
-size_t tc_workspace_bytes(int head_dim) {
-    if (head_dim == 64) return parts_bytes<kRows, 64>(kMaxWorkers / 2);
+size_t tc_workspace_bytes(int head_dim, bool out_bf16) {
+    if (head_dim == 64 || !out_bf16) return parts_bytes<kRows, 64>(kMaxWorkers / 2);
     if (head_dim == 128) return parts_bytes<kRows, 128>(kMaxWorkers / 2);
     return parts_bytes<kRows, 256>(kMaxWorkers / 2);
 }
 
-cudaError_t launch_tc(const ChunkParams& p, int head_dim, int sms, bool* done, cudaStream_t stream) {
-    if (head_dim == 64) return launch<64>(p, sms, done, stream);
-    if (head_dim == 128) return launch<128>(p, sms, done, stream);
-    return launch<256>(p, sms, done, stream);
+cudaError_t launch_tc(const ChunkParams& p, int head_dim, bool out_bf16, int sms, bool* done, cudaStream_t stream) {
+    if (head_dim == 64) return out_bf16 ? launch<Tc<64, false>>(p, sms, done, stream) : launch<Tc<64, true>>(p, sms, done, stream);
+    if (head_dim == 128) return out_bf16 ? launch<Tc<128, false>>(p, sms, done, stream) : launch<Tc<128, true>>(p, sms, done, stream);
+    return out_bf16 ? launch<Tc<256, false>>(p, sms, done, stream) : launch<Tc<256, true>>(p, sms, done, stream);
 }
 
 }  // namespace chunk

@@ -150,7 +150,7 @@ cudaError_t launch_state_reset(const ResetParams& p, cudaStream_t stream);
 // false if the driver refuses it (gdn_tma.cu).
 bool make_tensor_map_bf16_sw128(CUtensorMap* m, const void* base, int inner, int outer, int box_outer);
 // The same of `rank` <= 5 dimensions (innermost first, its elements consecutive; strides of the others in bytes) and any box of
-// up to 64 elements of the innermost.
+// up to 64 elements of the innermost; with 32 of them the swizzle is that of 64 bytes.
 bool make_tensor_map_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
 
 // One GEMM of a projection call: out [T][rows] = in [T][K] . W [rows][K]^T (bf16).
