@@ -15,7 +15,9 @@ namespace chunk {
 using attn::kLog2e;
 
 constexpr int kMaxWorkers = 512;
-constexpr size_t kCounterBytes = 2 * kMaxWorkers * 4;   // at the start of the workspace: by the worker of a unit's first part, two each
+// At the start of the workspace: by the worker of a unit's first part, two for each pair of CTAs; behind kMaxWorkers of them by the
+// worker of the first of some parts of a unit, two each for whether it is the unit's first one.
+constexpr size_t kCounterBytes = 4 * kMaxWorkers * 4;
 
 __device__ __forceinline__ bool rows_ok(const ChunkParams& p, int a, int z) { return a >= 0 && a <= z && z <= p.T; }
 

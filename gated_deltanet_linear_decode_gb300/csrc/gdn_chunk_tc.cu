@@ -41,6 +41,7 @@ using attn::kWaitLimit;
 using tc::smem_u32;
 constexpr int kDrainLimit = 1 << 14;   // polls for what is in flight at the end
 constexpr int kMinShare = 512;        // keys of a worker, at least
+constexpr int kJoin = 8;              // parts that are joined at a time, of units with many of them
 constexpr float kSlack = 8.0f;   // how far a score may pass its row's base
 constexpr int kRows = 256, kKeys = 128, kThreads = 352, kSoft = 256;
 
@@ -266,6 +267,9 @@ struct Walk {
 // consecutive.  (By rows a part of 128 KB took 4.3 us to write, and six of them 28 to join.)
 __device__ __forceinline__ uint32_t part_at(int row, int ch) { return static_cast<uint32_t>((ch >> 3) * 128 + row) * 8 + (ch & 7); }
 
+// All softmax warps.
+__device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 9, %0;" ::"n"(kSoft) : "memory"); }
+
 // The strays of a unit's late keys (gdn_attn.cuh; those that its first row does not see) are added to the rows that see them,
 // in out or in the part at `part`: this CTA's rows, whose first token is the unit's token cta_tok.  A call, for the size of the code around it.
 template <class S>
@@ -338,7 +342,6 @@ __device__ __noinline__ void join_few(const ChunkParams& p, const Part& c, const
 // A group's warp lets the other group's warp of the same rows have its base (barriers 1 to 8).
 __device__ __forceinline__ void give_base(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(1 + id) : "memory"); }
 __device__ __forceinline__ void take_base(int id) { asm volatile("bar.sync %0, 64;" ::"r"(1 + id) : "memory"); }
-__device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 9, %0;" ::"n"(kSoft) : "memory"); }
 
 template <class S>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -866,10 +869,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const Parts<kRows, DV> parts(p.workspace, workers);
                 const size_t place = Parts<kRows, DV>::place(worker, c);
                 float* const part = parts.o + (place * kRows + rank * 128) * DV;
-                bool result = whole;   // this CTA has the rows' result, here or with the other parts
-                int n = 1, w0 = 0;
-                const bool ws32 = on32(p.workspace);
+                bool result = whole;   // this CTA finishes the rows
                 if (!whole) {
+                    const bool ws32 = on32(p.workspace);
 #pragma unroll 1
                     for (int i = 0; i < DV / 2; i += 32) {
                         float v[32];
@@ -890,38 +892,100 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sync_softmax();
                         add_strays<S>(p, c, tok0, cta_tok, here, part);
                     }
-                    // the worker that arrives last joins this CTA's rows of all parts
+                    // the worker that arrives last joins this CTA's rows of all parts; of many parts with many rows the last of each kJoin
+                    // joins those first, for one CTA reads no more than some 70 bytes a ns
                     const long long first = c.at + ln.cost;
-                    w0 = sh.owner(first);
-                    n = sh.owner(first + static_cast<long long>(kKeys) * (c.tiles - 1)) - w0 + 1;
-                    sync_softmax();
-                    if (threadIdx.x == 0) {
-                        unsigned old;
-                        asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(parts.counters + 2 * w0 + rank), "r"(n - 1) : "memory");
-                        sm.last = old == static_cast<unsigned>(n - 1);
-                    }
-                    sync_softmax();
-                    result = sm.last;
-                }
-                auto row_of = [&](int k) { return (k == 0 ? 2 * static_cast<size_t>(w0) + 1 : 2 * static_cast<size_t>(w0 + k)) * kRows + rank * 128; };
-                if (result && !whole && here * (DV / 4) <= 4 * kSoft) {
-                    join_few<S>(p, c, parts, w0, n, tok0, cta_tok, here, static_cast<int>(rank) * 128);
-                } else if (result) {
-                    // of several parts in their order, whoever was last: statistics first
-                    float mm = m, ll = sum;
-                    if (!whole && row < here) {
-                        mm = -INFINITY;
-                        ll = 0.f;
-#pragma unroll 4
-                        for (int k = 0; k < n; ++k) mm = fmaxf(mm, __ldcg(&parts.ml[row_of(k) + row].x));
-                        mm = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-                        for (int k = 0; k < n; ++k) {
-                            const float2 z = __ldcg(parts.ml + row_of(k) + row);
-                            ll = fmaf(ex2(z.x - mm), z.y, ll);
+                    const int w0 = sh.owner(first), n = sh.owner(first + static_cast<long long>(kKeys) * (c.tiles - 1)) - w0 + 1;
+                    const bool few = here * (DV / 4) <= 4 * kSoft;
+                    const int row0 = static_cast<int>(rank) * 128;
+                    const bool twice = n > kJoin && !few;
+#pragma unroll 1
+                    for (bool first_time = twice;; first_time = false) {
+                        // parts `from`, `from` + step, .. of the unit, `these` of them, to the first one's place or at last to tensor memory
+                        const int from = first_time ? (worker - w0) / kJoin * kJoin : 0, step = twice && !first_time ? kJoin : 1;
+                        const int these = first_time ? min(kJoin, n - from) : (n + step - 1) / step;
+                        sync_softmax();
+                        if (threadIdx.x == 0) {
+                            unsigned old;
+                            int* const counter = parts.counters + (first_time ? kMaxWorkers + 4 * (w0 + from) + 2 * (from == 0) : 2 * w0) + rank;
+                            asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(these - 1) : "memory");
+                            sm.last = old == static_cast<unsigned>(these - 1);
                         }
+                        sync_softmax();
+                        if (!sm.last) break;
+                        if (few) {
+                            join_few<S>(p, c, parts, w0, n, tok0, cta_tok, here, row0);
+                            break;
+                        }
+                        auto row_of = [&](int k) {
+                            const int at = from + k * step;
+                            return static_cast<uint32_t>((at == 0 ? 2 * w0 + 1 : 2 * (w0 + at)) * kRows + row0);
+                        };
+                        // in their order, whoever was last: statistics first
+                        m = -INFINITY;
+                        sum = 0.f;
+                        if (row < here)
+#pragma unroll 2
+                            for (int k = 0; k < these; ++k) m = fmaxf(m, __ldcg(&parts.ml[row_of(k) + row].x));
+                        const float base = m == -INFINITY ? 0.f : m;
+                        if (row < here)
+#pragma unroll 2
+                            for (int k = 0; k < these; ++k) {
+                                const float2 z = __ldcg(parts.ml + row_of(k) + row);
+                                sum = fmaf(ex2(z.x - base), z.y, sum);
+                            }
+#pragma unroll 1
+                        for (int i = 0; i < DV / 2; i += 32) {
+                            float v[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                            if (row < here)
+#pragma unroll 1
+                                for (int k = 0; k < these; k += 2) {   // two parts' loads together; past the last part it again
+                                    uint32_t y[2][4][8];
+                                    float mk[2];
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x) {
+                                        const uint32_t at = row_of(min(k + x, these - 1));
+                                        mk[x] = __ldcg(&parts.ml[at + row].x);
+#pragma unroll
+                                        for (int q = 0; q < 4; ++q) load16(parts.o + at * DV + part_at(row, ch0 + i + 8 * q), ws32, y[x][q]);
+                                    }
+#pragma unroll
+                                    for (int x = 0; x < 2; ++x) {
+                                        if (k + x == these) break;   // (not added with a weight of zero: it may be infinite)
+                                        const float fk = ex2(mk[x] - base);
+#pragma unroll
+                                        for (int q = 0; q < 32; ++q) v[q] = fmaf(fk, __uint_as_float(y[x][q / 8][q % 8]), v[q]);
+                                    }
+                                }
+                            if (first_time) {
+                                if (row < here) {
+                                    float* const to = parts.o + row_of(0) * DV + part_at(row, ch0 + i);
+#pragma unroll
+                                    for (int e = 0; e < 32; e += 8) {
+                                        uint32_t y[8];
+#pragma unroll
+                                        for (int q = 0; q < 8; ++q) y[q] = __float_as_uint(v[e + q]);
+                                        store16(to + e * 128, ws32, y);
+                                    }
+                                }
+                            } else {
+                                __syncwarp();
+                                tc::tmem_st32(my_o + i, v);
+                            }
+                        }
+                        if (!first_time) {
+                            tc::tmem_wait_st();
+                            result = true;
+                            break;
+                        }
+                        sync_softmax();   // all have read the statistics
+                        if (half == 0 && row < here) parts.ml[row_of(0) + row] = make_float2(m, sum);
                     }
-                    const float f = ll == 0.f ? 0.f : 1.0f / ll;
+                }
+                if (result) {   // in tensor memory
+                    const float f = sum == 0.f ? 0.f : 1.0f / sum;
                     const bool gate32 = on32(p.gate) && p.ldg % 16 == 0, out32 = on32(p.out);
                     const long long to = (tr * p.Hq + h) * D + col0;
 #pragma unroll 1
@@ -932,32 +996,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             load16(gate + i + 16, gate32, gt[1]);
                         }
                         float v[32];
-                        if (whole) {
-                            if (any) load_o(i, v);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = 0.f;
-                            if (row < here)
-#pragma unroll 1
-                                for (int k = 0; k < n; k += 2) {   // two parts' loads together; past the last part it again, without weight
-                                    uint32_t y[2][4][8];
-                                    float fk[2];
-#pragma unroll
-                                    for (int x = 0; x < 2; ++x) {
-                                        const size_t first = row_of(min(k + x, n - 1));
-                                        fk[x] = k + x < n ? __ldcg(&parts.ml[first + row].x) : -INFINITY;
-#pragma unroll
-                                        for (int q = 0; q < 4; ++q) load16(parts.o + first * DV + part_at(row, ch0 + i + 8 * q), ws32, y[x][q]);
-                                    }
-#pragma unroll
-                                    for (int x = 0; x < 2; ++x) {
-                                        if (k + x == n) break;   // (nothing without weight is added: it may be infinite)
-                                        const float fx = ex2(fk[x] - mm);
-#pragma unroll
-                                        for (int q = 0; q < 32; ++q) v[q] = fmaf(fx, __uint_as_float(y[x][q / 8][q % 8]), v[q]);
-                                    }
-                                }
-                        }
+                        if (!whole) tc::tmem_ld32(my_o + i, v);
+                        else if (any) load_o(i, v);
                         if (row < here) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = any ? v[e] * f : 0.f;
