@@ -17,7 +17,7 @@
 // S has two or three places, as the tensor memory allows, so that the softmax of tiles runs beside the products of others.  The
 // weights take the place of scores that have been read; the S that comes into their place waits for the product with them.
 //
-// For a bf16 result a weight is rounded to bf16 (2^-9 of it at most): with a second part for what the rounding leaves, as
+// For a bf16 result a weight is rounded to bf16 (2^-8 of it at most): with a second part for what the rounding leaves, as
 // gdn_attn_decode has it, which is bound by memory, the product with the values would take twice the time, half again as much
 // for the whole.
 //
@@ -40,6 +40,7 @@ using bf16 = __nv_bfloat16;
 using attn::kWaitLimit;
 using tc::smem_u32;
 constexpr int kDrainLimit = 1 << 14;   // polls for what is in flight at the end
+constexpr int kDrainCycles = 1 << 17;  // and a time for it after a give-up
 constexpr int kMinShare = 512;        // keys of a worker, at least
 constexpr int kJoin = 8;              // parts that are joined at a time, of units with many of them
 constexpr float kSlack = 8.0f;   // how far a score may pass its row's base
@@ -521,11 +522,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                  keys ? static_cast<int>(rank) * groups / 2 : 0, keys ? groups / 2 : groups, keys ? 0 : S::kF32 ? 2 * slice[0] + static_cast<int>(rank) : D > 64 ? static_cast<int>(rank) * kVBlocks : 0,
                  keys ? kKBlocks : kVBlocks, bar);
         }
-        // nothing is in flight when the pair ends: the last copies of every stage have landed (limits of their own, for after a give-up)
+        // Nothing is in flight when the pair ends: the last copies of every stage have landed.  After a give-up the two CTAs may have
+        // stopped at different tiles, and no barrier tells of those that only one has copied: they get more time than any copy takes.
         if (rank == 0) {
             const int r = keys ? RK : RV;
             for (int i = max(0, n - r); i < n; ++i) tc::mbar_wait((keys ? sm.k_full : sm.v_full) + i % r, (i / r) & 1, kDrainLimit);
             if (parts_begun > 0) tc::mbar_wait(&sm.q_full, (parts_begun - 1) & 1, kDrainLimit);
+        }
+        if (sm.abort) {
+            const long long from = clock64();
+            while (clock64() - from < kDrainCycles) {
+            }
         }
     } else if (warp == 9) {
         if (rank == 0) {

@@ -60,8 +60,10 @@ typedef struct {
     float eps;          /* RMSNorm eps                                          */
     int32_t act_dtype;  /* gdn_dtype of q, k, v, gate and the cache             */
     int32_t out_dtype;  /* gdn_dtype of the attention's out                     */
-    uint32_t flags;     /* 0, or GDN_FLAG_TEST_STALL (gdn.h; in gdn_attn_decode
-                           one warp of a CTA waits while the others go on)      */
+    uint32_t flags;     /* 0, or GDN_FLAG_TEST_STALL (gdn.h; in gdn_attn_decode,
+                           and in gdn_attn_chunk over a bf16 cache whose pages
+                           hold an even number of tokens, one warp of a CTA
+                           waits while the others go on)                        */
 } gdn_attn_dims;
 
 /*
@@ -216,12 +218,15 @@ size_t gdn_attn_chunk_workspace_bytes(const gdn_attn_dims* dims, int32_t B, int3
  *        sequence with cu_seqlens[b] > cu_seqlens[b+1] or either outside 0..T,
  *        which has no rows then (rows that two sequences claim hold the result
  *        of either)
- * What gdn_attn_decode promises holds here too: memory beyond a sequence's
- * length is not read, a token's key or value does not matter to the rows that
- * do not see it, whatever it is, and results are the same from run to run.
+ * What gdn_attn_decode promises holds here too: what lies beyond a sequence's
+ * length does not matter (of its last page it may be read, other pages are not),
+ * nor does a token's key or value to the rows that do not see it, whatever it
+ * is; and results do not depend on what runs beside the call, and are the same
+ * from run to run.
  * A bf16 result's softmax weights are rounded to bf16 before the product with
  * the values (2^-8 of a weight at most, beside the result's own rounding);
- * an fp32 result's are not.
+ * an fp32 result's are not.  A bf16 cache is read through the tensor cores, an
+ * fp32 one is worked on by the CUDA cores.
  */
 gdn_status gdn_attn_chunk(const gdn_attn_dims* dims, const gdn_kv_cache* cache, int32_t B, int32_t T,
                           int32_t max_pages, const void* q, int64_t ldq, const void* gate, int64_t ldg,

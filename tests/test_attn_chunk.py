@@ -330,3 +330,47 @@ def test_a_prompt_as_it_would_be_run():
     gdn.gdn_kv_copy_pages(dims, kv, ms, md)
     step([5, 20, 1, 2])
     assert st.tolist() == [0] * 4 and fst.tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("dt,odt", [(BF, BF), (BF, F32), (F32, F32)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_units_of_dozens_of_parts(dt, odt, d):
+    """Many rows over a long sequence: more parts of a unit than are joined at a time."""
+    check(R.Batch([70], [20000], 4, 1, d, 16, dt, gate=True, seed=d), odt)
+    check(R.Batch([3, 33], [4000, 9000], 8, 1, d, 64, dt, seed=d + 1), odt)
+
+
+@pytest.mark.parametrize("dt,odt", [(BF, BF), (BF, F32)])
+@pytest.mark.parametrize("order,pad", [((0, 1, 2, 3), 3), ((0, 2, 1, 3), 5), ((1, 0, 2, 3), 0), ((2, 0, 1, 3), 0), ((1, 2, 0, 3), 0), ((2, 1, 0, 3), 1)])
+@pytest.mark.parametrize("d,ps", [(64, 16), (128, 24), (256, 6), (256, 8)])
+def test_orders_of_the_cache(dt, odt, order, pad, d, ps):
+    """Pages, tokens and heads in any order in memory, with room between."""
+    b = R.Batch([90, 5], [200, 301], 6, 3, d, ps, dt, seed=31)
+    want = run(b, odt)
+
+    def laid(t):
+        shape = [t.shape[i] for i in order]
+        shape[1] += pad
+        back = torch.empty(shape, dtype=dt, device="cuda").fill_(math.nan)
+        view = back.permute([order.index(i) for i in range(4)])
+        for i in range(3):
+            view = view.narrow(i, 0, t.shape[i])
+        view.copy_(t)
+        return view
+
+    b.k, b.v = laid(b.k), laid(b.v)
+    assert torch.equal(run(b, odt), want)
+
+
+@pytest.mark.parametrize("odt", [BF, F32])
+@pytest.mark.parametrize("new,lens", [([40, 300], [500, 700]), ([3], [9000]), ([64], [9000])])
+def test_a_wait_that_gives_up(odt, new, lens):
+    """GDN_FLAG_TEST_STALL: the kernel ends, says so, and writes no result; with a workspace of zeros the next call is as ever."""
+    b = R.Batch(new, lens, 8, 1, 128, 16, seed=41)
+    want, st = run(b, odt), torch.zeros(len(new), dtype=torch.int32, device="cuda")
+    ws = torch.zeros_like(workspace(gdn.make_attn_dims(8, 1, 128, BF, odt)))
+    out = run(b, odt, status=st, ws=ws, test_stall=True)
+    assert st.tolist() == [16] * len(new) and torch.all(out == 7.0)
+    ws.zero_()
+    st.zero_()
+    assert torch.equal(run(b, odt, status=st, ws=ws), want) and not st.any()
