@@ -19,7 +19,7 @@ struct Simt {
     static constexpr int kV = kKt * D * kEs, kPp = kKt + 4;
     static constexpr int kSmem = 2 * kRt * kPitch + kV + kRt * kPp * 4;
     static constexpr int kCtas = kSmem * 2 <= 224 * 1024 ? 2 : 1;   // an SM
-    static constexpr int kCost = 128;
+    static constexpr int kCost = 64;
 };
 
 // n = 8 (bf16) or 4 elements of 16 bytes.
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, S::kCtas) chunk_simt_kernel(const __
                 for (int r = 0; r < 4; ++r)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) a[r][k] = make_float2(0.f, 0.f);
-#pragma unroll 2
+#pragma unroll 4
                 for (int x = 0; x < D / kE; ++x) {
                     float q[4][kE], kk[kE];
 #pragma unroll
