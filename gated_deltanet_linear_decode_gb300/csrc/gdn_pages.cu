@@ -383,6 +383,8 @@ __global__ void __launch_bounds__(kBookThreads, 1) kv_release_kernel(const KvRel
 // The number of a page among those in use by ballots: a warp walks a run of pages, 32 at a time, and prefix sums over the
 // warps' totals give each its start.  With `used` known, the r-th page from the top of those at `used` and above goes to the
 // r-th place from the bottom that is not in use: each finds its own r, and writes itself into the pair of that number.
+// Bound by the latency of its phases (five cluster barriers): 64 sequences of up to 1,024 pages in a cache half of it free take 25 us,
+// of which the memory would need 0.2; 8 of up to 32 pages 8 us, one CTA.
 __global__ void __launch_bounds__(kBookThreads, 1) kv_compact_kernel(const KvCompactParams p) {
     extern __shared__ int smem[];
     int* const held_s = smem;   // [B + 1] entries before each sequence
@@ -512,7 +514,8 @@ cudaError_t launch_books(void (*kernel)(P), const P& p, int ctas, size_t words, 
 }
 
 // ---------------------------------------------------------------- copies
-// Elementwise, every byte read and written once: bound by the memory.  A CTA takes 256 x 8 accesses of 16 bytes of one
+// Elementwise, every byte read and written once: bound by the memory (16,000 pages of 16 tokens of 4 heads of 256, 2.1 GB, 333 us,
+// 6.3 TB/s, 93% of what one large copy reaches).  A CTA takes 256 x 8 accesses of 16 bytes of one
 // page's keys or values at a time, all loads before the first store.  A page is `outer` runs of `inner` runs of `run`
 // consecutive vectors (one run where it lies in one piece).
 constexpr int kCopyThreads = 256, kCopyBatch = 8;
