@@ -45,6 +45,7 @@ constexpr int kMinShare = 512;        // keys of a worker, at least
 constexpr int kJoin = 8;              // parts that are joined at a time, of units with many of them
 constexpr float kSlack = 8.0f;   // how far a score may pass its row's base
 constexpr int kRows = 256, kKeys = 128, kThreads = 352, kSoft = 256;
+constexpr int kRest = 3 * 1024;   // bytes of shared memory beside queries, keys and values
 
 template <int D_, bool kF32_>
 struct Tc {
@@ -58,7 +59,7 @@ struct Tc {
     static constexpr int RK = kF32 ? (D == 256 ? 4 : 6) : D == 256 ? 2 : D == 128 ? 5 : 6;
     static constexpr int RV = kF32 ? (D == 256 ? 3 : 6) : D == 256 ? 3 : D == 128 ? 5 : 6;
     static constexpr int kQ = 128 * D * 2;
-    static constexpr int kSmem = kQ + RK * kStageK + RV * kStageV + 3072;
+    static constexpr int kSmem = kQ + RK * kStageK + RV * kStageV + kRest;
     // tensor memory: O (of fp32 results two, by tile mod 2), the places; in a place of fp32 results S is behind 64 columns
     static constexpr int kO = 0, kS = kF32 ? 128 : D == 256 ? 256 : 128;
     static constexpr int kPlace = kF32 ? 192 : 128, kScores = kF32 ? 64 : 0;
@@ -78,7 +79,7 @@ struct Smem {
     int last, stop, strays;           // stop: a softmax warp has seen abort; strays: some were found; never taken back
     volatile int abort;
 };
-static_assert(sizeof(Smem) <= 3072, "fits");
+static_assert(sizeof(Smem) <= kRest, "fits");
 
 // ---------------------------------------------------------------- the pair
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
@@ -1046,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(sm.tmem), "r"(512));
 }
 
-// The map of a half of the cache, and the boxes of up to `most` tokens and `blocks` blocks of `block` channels; false if the driver refuses it.
+// The map of a half of the cache, and the boxes of up to `most` tokens and `blocks` blocks of `block` channels; false if there can be none.
 bool cache_map(CUtensorMap* m, Boxes* b, const ChunkParams& p, const void* half, int D, int most, int blocks, uint32_t block) {
     const KvCache& c = p.cache;
     auto bytes = [&](long long stride) { return stride ? static_cast<uint64_t>(stride) * 2 : static_cast<uint64_t>(D) * 2; };
