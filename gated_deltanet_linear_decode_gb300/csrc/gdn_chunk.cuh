@@ -124,17 +124,17 @@ __device__ __forceinline__ void put(const ChunkParams& p, bool out_bf16, long lo
 template <int RT, int D>
 struct Parts {
     int* counters;
-    float* o;      // [2 workers][RT][D]
+    float* o;      // [2 workers][RT][D], on 32 bytes
     float2* ml;    // [2 workers][RT]
     __device__ __forceinline__ Parts(void* workspace, int workers)
         : counters(static_cast<int*>(workspace)),
-          o(reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kCounterBytes)),
+          o(reinterpret_cast<float*>((reinterpret_cast<uintptr_t>(workspace) + kCounterBytes + 31) & ~static_cast<uintptr_t>(31))),
           ml(reinterpret_cast<float2*>(o + static_cast<size_t>(2) * workers * RT * D)) {}
     __device__ __forceinline__ static size_t place(int worker, const Part& c) { return 2 * static_cast<size_t>(worker) + (c.t0 == 0); }
 };
 template <int RT, int D>
 constexpr size_t parts_bytes(int workers) {
-    return kCounterBytes + static_cast<size_t>(2) * workers * RT * (D * 4 + 8);
+    return kCounterBytes + 32 + static_cast<size_t>(2) * workers * RT * (D * 4 + 8);
 }
 
 // bf16 cache; *done = false where there is no tensor map of the strides.

@@ -5,13 +5,15 @@
 // of the values half of the channels, and the tensor cores read both.  So a key and a value come from L2 once for 256 rows
 // (at d = 256 a tile's products take 2,048 cycles and its copies 32 bytes a cycle of every SM; with 128 rows a CTA it were 64).
 //
-// Roles of a CTA's 11 warps:
+// Roles of a CTA's 12 warps:
 //   0-7   softmax, two groups that take turns: a thread has one row (tensor-memory lane) of every other tile.  A tile's maximum needs
 //         the base that the other group had for the tile before; the weights' powers of one run beside the maxima of the next.
 //         The result is rescaled only when a row's maximum has risen by more than 2^kSlack.
-//   8     copies queries and keys by TMA, from a tensor map that serves any strides; each lane looks up its keys' pages, one
-//         issues the copies.  Keys past the end and pages outside the cache are coordinates outside the map, which read as zeros
+//   8     copies keys by TMA, from a tensor map that serves any strides; each lane looks up its keys' pages and copies them.  Keys
+//         past the end and pages outside the cache are coordinates outside the map, which read as zeros
 //   10    copies values
+//   11    copies queries (with the keys' copies a part's first keys had to wait for the last part's queries to be done with, and
+//         came 2 us late)
 //   9     one thread of the first CTA: issues the products
 //
 // S has two or three places, as the tensor memory allows, so that the softmax of tiles runs beside the products of others.  The
@@ -44,7 +46,7 @@ constexpr int kDrainCycles = 1 << 17;  // and a time for it after a give-up
 constexpr int kMinShare = 512;        // keys of a worker, at least
 constexpr int kJoin = 8;              // parts that are joined at a time, of units with many of them
 constexpr float kSlack = 8.0f;   // how far a score may pass its row's base
-constexpr int kRows = 256, kKeys = 128, kThreads = 352, kSoft = 256;
+constexpr int kRows = 256, kKeys = 128, kThreads = 384, kSoft = 256;
 constexpr int kRest = 3 * 1024;   // bytes of shared memory beside queries, keys and values
 
 template <int D_, bool kF32_>
@@ -63,7 +65,8 @@ struct Tc {
     // tensor memory: O (of fp32 results two, by tile mod 2), the places; in a place of fp32 results S is behind 64 columns
     static constexpr int kO = 0, kS = kF32 ? 128 : D == 256 ? 256 : 128;
     static constexpr int kPlace = kF32 ? 192 : 128, kScores = kF32 ? 64 : 0;
-    static constexpr int kCost = D == 256 ? 896 : 640;        // of a unit: its begin and end take as long as so many keys
+    static constexpr int kCost = D == 256 ? 768 : 512;        // of a unit: its begin and end take as long as so many keys
+    static constexpr bool kGates = DV <= 128;                 // a row's gates are loaded before its sums are there (ragged prompts 1,221 -> 1,158 us)
     static_assert(kSmem <= 232448 && kS + NS * kPlace <= 512, "shape");
 };
 
@@ -74,7 +77,14 @@ struct Smem {
     uint64_t k_full[8], k_empty[8], v_full[8], v_empty[8];
     uint64_t q_full, q_empty, s_full[3], p_ready[3], pv_done[3], drained, never;   // by place of S
     uint64_t v_told[6];               // by tile mod 6: one of them is always the same group's, and not passed twice before it has looked
-    PlanSmem plan;
+    union {
+        PlanSmem plan;                // until the roles begin
+        struct {
+            int tiles[16];            // of a part that has some, by its number mod 16; 0: there is none
+            Part next;                // at a part's end what comes then, if there is more
+            int more;
+        } way;
+    };
     uint32_t tmem;
     int last, stop, strays;           // stop: a softmax warp has seen abort; strays: some were found; never taken back
     volatile int abort;
@@ -402,33 +412,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_after_sync();
     const uint32_t t_o = sm.tmem + S::kO, t_s = sm.tmem + S::kS;
 
+    // The bytes of both CTAs are expected by the first one, and the second one arrives.
+    auto announce = [&](uint64_t* bar, uint32_t bytes) {
+        if (lane == 0) {
+            if (rank == 0) tc::mbar_expect_tx(bar, bytes);
+            else arrive_at(bar, 0);
+        }
+        __syncwarp();
+        return in_cta(smem_u32(bar), 0);
+    };
+    auto rest = [&]() {   // after a give-up: more time than any copy takes
+        if (!sm.abort) return;
+        const long long from = clock64();
+        while (clock64() - from < kDrainCycles) {
+        }
+    };
     if (warp == 8 || warp == 10) {
-        // ------------------------------------------------------------ copies: warp 8 queries and keys, warp 10 values
+        // ------------------------------------------------------------ copies: warp 8 keys, warp 10 values
         Walk w(c, p, ln, sh);
         const bool keys = warp == 8;
         const Boxes bx = keys ? kb : vb;
         const int ps = p.cache.page_size, groups = kKeys / bx.tokens;
         // Lane l has the tile's groups of bx.tokens keys l + 32 k, [0] of the tile to be copied, [1] of the one being looked up.
         constexpr int kPer = 4;
-        int page[2][kPer] = {}, in[2][kPer] = {}, head[2] = {}, slice[2] = {}, seq[2] = {}, q_tok[2] = {};   // in -1: no key; seq -1: no tile; q_tok -1: not a part's first
-        int parts_begun = 0, part_seq = 0, part_head = 0, part_slice = 0;
+        int page[2][kPer] = {}, in[2][kPer] = {}, head[2] = {}, slice[2] = {}, seq[2] = {}, tiles[2] = {};   // in -1: no key; seq -1: no tile
+        int parts = 0, part_seq = 0, part_head = 0, part_slice = 0;
         int end = 0;               // keys from `end` on are nobody's
         const int* table = nullptr;   // the sequence's pages
         auto look_up = [&](int a) {
             seq[a] = -1;
             if (!w.more) return;
-            q_tok[a] = -1;
             if (w.first()) {
                 part_seq = c.b;
                 part_head = c.hk / S::kSlices;
                 part_slice = c.hk % S::kSlices;
-                q_tok[a] = c.r.row0 + c.i * ln.tokens + static_cast<int>(rank) * cta_tokens;
                 end = c.seen;
                 table = p.block_table + static_cast<size_t>(c.b) * p.max_pages;
             }
             seq[a] = part_seq;
             head[a] = part_head;
             slice[a] = part_slice;
+            tiles[a] = w.first() ? w.t1 - w.t0 : 0;
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 if (k > 0 && groups <= 32 * k) break;
@@ -441,15 +465,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             w.next(p, ln, sh);
-        };
-        // The bytes of both CTAs are expected by the first one, and the second one arrives.
-        auto announce = [&](uint64_t* bar, uint32_t bytes) {
-            if (lane == 0) {
-                if (rank == 0) tc::mbar_expect_tx(bar, bytes);
-                else arrive_at(bar, 0);
-            }
-            __syncwarp();
-            return in_cta(smem_u32(bar), 0);
         };
         // copies of the tile at [0]: boxes [g0, g0 + n), all blocks from `block` on, by the lanes that have them
         const int row_bytes = keys ? 128 : 2 * S::kBlock;
@@ -478,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             head[0] = head[1];
             slice[0] = slice[1];
             seq[0] = seq[1];
-            q_tok[0] = q_tok[1];
+            tiles[0] = tiles[1];
 #pragma unroll
             for (int k = 0; k < kPer; ++k) {
                 page[0][k] = page[1][k];
@@ -488,18 +503,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             look_up(1);
             if (n < 0) continue;
             if (keys) {
-                if (q_tok[0] >= 0) {
-                    if (parts_begun > 0) wait_for(&sm.q_empty, (parts_begun - 1) & 1, &sm.abort);
-                    if (sm.abort) break;
-                    ++parts_begun;
-                    const uint32_t bar = announce(&sm.q_full, 2 * cta_rows * D * 2);
-                    if (elected()) {
-#pragma unroll
-                        for (int c = 0; c < D / 64; ++c) tma_load_q(smem_u32(q_s) + c * 16384, &q_map, c * 64, head[0] * p.G, q_tok[0], bar);
-                    }
-                }
                 if (n >= RK) wait_for(sm.k_empty + n % RK, (n / RK - 1) & 1, &sm.abort);
                 if (sm.abort) break;
+                if (tiles[0] > 0) {   // a part's first
+                    if (lane == 0) sm.way.tiles[parts & 15] = tiles[0];
+                    ++parts;
+                }
                 if (lane < 4) sm.valid[n & 15][lane] = 0xffffffffu;
                 bool bad = false;
 #pragma unroll
@@ -523,23 +532,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                  keys ? static_cast<int>(rank) * groups / 2 : 0, keys ? groups / 2 : groups, keys ? 0 : S::kF32 ? 2 * slice[0] + static_cast<int>(rank) : D > 64 ? static_cast<int>(rank) * kVBlocks : 0,
                  keys ? kKBlocks : kVBlocks, bar);
         }
+        int landed = max(0, n - (keys ? RK : RV));   // tiles before this one have been used
+        if (keys && !sm.abort) {   // the products' warp learns that there are no more
+            if (n >= RK) wait_for(sm.k_empty + n % RK, (n / RK - 1) & 1, &sm.abort);
+            if (lane == 0) sm.way.tiles[parts & 15] = 0;
+            announce(sm.k_full + n % RK, 0);
+            landed = max(0, n + 1 - RK);
+        }
         // Nothing is in flight when the pair ends: the last copies of every stage have landed.  After a give-up the two CTAs may have
-        // stopped at different tiles, and no barrier tells of those that only one has copied: they get more time than any copy takes.
+        // stopped at different tiles, and no barrier tells of those that only one has copied.
         if (rank == 0) {
             const int r = keys ? RK : RV;
-            for (int i = max(0, n - r); i < n; ++i) tc::mbar_wait((keys ? sm.k_full : sm.v_full) + i % r, (i / r) & 1, kDrainLimit);
-            if (parts_begun > 0) tc::mbar_wait(&sm.q_full, (parts_begun - 1) & 1, kDrainLimit);
+            for (int i = landed; i < n; ++i) tc::mbar_wait((keys ? sm.k_full : sm.v_full) + i % r, (i / r) & 1, kDrainLimit);
         }
-        if (sm.abort) {
-            const long long from = clock64();
-            while (clock64() - from < kDrainCycles) {
+        rest();
+    } else if (warp == 11) {
+        // ------------------------------------------------------------ queries
+        int n = 0, before = 0;   // parts with tiles, tiles of the last one
+        for (bool more = true; more; more = to_next_part(p, ln, sh, c)) {
+            if (c.t0 >= c.t1) continue;
+            if (n > 0) {   // for all of the last part: with a limit more for every 32,768 tiles, which take some 40 ms
+                for (int i = 0; i < before >> 15; ++i)
+                    for (int it = 0; it < kWaitLimit && !is_there(smem_u32(&sm.q_empty), (n - 1) & 1) && !sm.abort; ++it) {
+                    }
+                wait_for(&sm.q_empty, (n - 1) & 1, &sm.abort);
             }
+            if (sm.abort) break;
+            before = c.t1 - c.t0;
+            const uint32_t bar = announce(&sm.q_full, 2 * cta_rows * D * 2);
+            if (elected()) {
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x)
+                    tma_load_q(smem_u32(q_s) + x * 16384, &q_map, x * 64, c.hk / S::kSlices * p.G, c.r.row0 + c.i * ln.tokens + static_cast<int>(rank) * cta_tokens, bar);
+            }
+            __syncwarp();
+            ++n;
         }
+        if (rank == 0 && n > 0) tc::mbar_wait(&sm.q_full, (n - 1) & 1, kDrainLimit);
+        rest();
     } else if (warp == 9) {
         if (rank == 0) {
             // -------------------------------------------------------- products
-            Walk w(c, p, ln, sh);
-            int nq = 0, units = 0;   // S issued, parts begun
+            // (How many tiles a part has the keys' copier tells: the way to the next part, in code that is not at hand then, takes 2 us.)
+            int nq = 0, units = 0, left = 0;   // S issued, parts begun, tiles of the newest one to come
+            bool end = false;
             uint32_t firsts = 0;     // by tile mod 32: the first of a part
             constexpr uint32_t id_s = tc::idesc_bf16(256, 128);
             constexpr uint32_t id_o = tc::idesc_f16(256, 2 * S::kVCh, 0, 1, 0) | (1u << 7) | (1u << 10);
@@ -556,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mma_ss(d, q_lo + c * (16384 >> 4) + 2 * kk, b + c * (1024 >> 4) + 2 * kk, k_hi, id_s, (c | kk) != 0);
                 commit_both(sm.s_full + nq % NS);
                 commit_both(sm.k_empty + nq % RK);
-                if (w.last()) commit_both(&sm.q_empty);
+                if (left == 1) commit_both(&sm.q_empty);
             };
             auto issue_o = [&](int g) {
                 const uint32_t a = t_s + g % NS * S::kPlace, b = v_lo + g % RV * (S::kStageV >> 4);
@@ -576,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // Turn g: the product with tile g's weights, then S of tile g + NS into the place that these had.
 #pragma unroll 1
-            for (int g = -NS; g < nq || w.more; ++g) {
+            for (int g = -NS; g < nq; ++g) {
                 if (g >= 0) {
                     wait_for(sm.v_full + g % RV, (g / RV) & 1, &sm.abort);
                     wait_for(sm.p_ready + g % NS, (g / NS) & 1, &sm.abort);
@@ -585,17 +621,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elected()) issue_o(g);
                     __syncwarp();
                 }
-                if (w.more) {
-                    if (w.first()) wait_for(&sm.q_full, units++ & 1, &sm.abort);
+                if (!end) {
                     wait_for(sm.k_full + nq % RK, (nq / RK) & 1, &sm.abort);
-                    if (g >= 0) wait_for(sm.pv_done + g % NS, (g / NS) & 1, &sm.abort);
                     if (sm.abort) break;
-                    tc::fence_after_sync();
-                    if (elected()) issue_s();
-                    __syncwarp();
-                    firsts = (firsts & ~(1u << (nq & 31))) | (static_cast<uint32_t>(w.first()) << (nq & 31));
-                    ++nq;
-                    w.next(p, ln, sh);
+                    const bool first = left == 0;
+                    if (first) {
+                        left = sm.way.tiles[units & 15];
+                        end = left == 0;
+                    }
+                    if (!end) {
+                        if (first) wait_for(&sm.q_full, units++ & 1, &sm.abort);
+                        if (g >= 0) wait_for(sm.pv_done + g % NS, (g / NS) & 1, &sm.abort);
+                        if (sm.abort) break;
+                        tc::fence_after_sync();
+                        if (elected()) issue_s();
+                        __syncwarp();
+                        firsts = (firsts & ~(1u << (nq & 31))) | (static_cast<uint32_t>(first) << (nq & 31));
+                        ++nq;
+                        --left;
+                    }
                 }
             }
             // everything issued is through before the pair ends
@@ -654,12 +698,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // scores of keys that a row does not see, and the scale's sign, are seen to in place
                     const int sees = min(off + tok0 + tok + 1, end) - t * kKeys;
                     const float sign = scale > 0.f ? 1.f : scale < 0.f ? -1.f : 0.f;
+                    // (the warp's first row sees the least; where that costs registers that the sums of fp32 results need, it is not asked)
+                    const int all_see = !S::kF32 && scale > 0.f ? __shfl_sync(0xffffffffu, sees, 0) : 0;
 #pragma unroll 1
                     for (int i = 0; i < 4; ++i) {
-                        float s[32];
-                        tc::tmem_ld32(my_s + i * 32, s);
                         const uint32_t w = sm.valid[g & 15][i];
                         const int n = sees - i * 32;
+                        if (all_see - i * 32 >= 32 && w == 0xffffffffu) continue;
+                        float s[32];
+                        tc::tmem_ld32(my_s + i * 32, s);
                         const uint32_t x = n <= 0 ? 0u : n >= 32 ? w : w & ((1u << n) - 1u);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) s[e] = (x >> e) & 1 ? s[e] * sign : -INFINITY;
@@ -830,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool any = t0 < t1, whole = c.whole();
             const long long tr = static_cast<long long>(c.r.row0) + tok0 + tok;
             const int h = c.hk / S::kSlices * p.G + row - in * p.G, ch0 = half * (DV / 2), col0 = c.hk % S::kSlices * DV + ch0;   // of the part, of the head
-            const bool gated = p.gate && row < here;
+            const bool gated = p.gate && row < here, gate32 = on32(p.gate) && p.ldg % 16 == 0;
             const bf16* const gate = static_cast<const bf16*>(p.gate) + (tr * p.ldg + static_cast<long long>(h) * D + col0);
             if (gated)   // the gate's lines, while the last products run
                 for (int i = 0; i < DV / 2; i += 64) prefetch_l2(gate + i);
@@ -842,8 +889,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tmem_wait_st();
                 tc::fence_before_sync();
             }
-            Part next = c;   // and the way to the next part
-            const bool more = to_next_part(p, ln, sh, next);
+            if ((g & 1) == half && quarter == 0) {   // the way to the next part, by a warp of the group that did not have the last tile
+                Part next = c;
+                const bool more = to_next_part(p, ln, sh, next);
+                if ((threadIdx.x & 127) == 0) {
+                    sm.way.next = next;
+                    sm.way.more = more;
+                }
+            }
+            uint32_t gt[DV / 64][2][8];   // the gates of this thread's channels; all of them now where there are few
+            auto gates = [&](int i) {
+                load16(gate + 32 * i, gate32, gt[i][0]);
+                load16(gate + 32 * i + 16, gate32, gt[i][1]);
+            };
+            if (S::kGates && whole && gated) {
+#pragma unroll
+                for (int i = 0; i < DV / 64; ++i) gates(i);
+            }
             if constexpr (!S::kF32) {
                 if (any) wait(sm.pv_done + (g - 1) % NS, ((g - 1) / NS) & 1);
                 tc::fence_after_sync();
@@ -879,7 +941,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float* const part = parts.o + (place * kRows + rank * 128) * DV;
                 bool result = whole;   // this CTA finishes the rows
                 if (!whole) {
-                    const bool ws32 = on32(p.workspace);
 #pragma unroll 1
                     for (int i = 0; i < DV / 2; i += 32) {
                         float v[32];
@@ -891,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 uint32_t y[8];
 #pragma unroll
                                 for (int q = 0; q < 8; ++q) y[q] = __float_as_uint(v[e + q]);
-                                store16(to + e * 128, ws32, y);
+                                store16(to + e * 128, true, y);
                             }
                         }
                     }
@@ -957,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         const uint32_t at = row_of(min(k + x, these - 1));
                                         mk[x] = __ldcg(&parts.ml[at + row].x);
 #pragma unroll
-                                        for (int q = 0; q < 4; ++q) load16(parts.o + at * DV + part_at(row, ch0 + i + 8 * q), ws32, y[x][q]);
+                                        for (int q = 0; q < 4; ++q) load16(parts.o + at * DV + part_at(row, ch0 + i + 8 * q), true, y[x][q]);
                                     }
 #pragma unroll
                                     for (int x = 0; x < 2; ++x) {
@@ -975,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         uint32_t y[8];
 #pragma unroll
                                         for (int q = 0; q < 8; ++q) y[q] = __float_as_uint(v[e + q]);
-                                        store16(to + e * 128, ws32, y);
+                                        store16(to + e * 128, true, y);
                                     }
                                 }
                             } else {
@@ -994,15 +1055,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (result) {   // in tensor memory
                     const float f = sum == 0.f ? 0.f : 1.0f / sum;
-                    const bool gate32 = on32(p.gate) && p.ldg % 16 == 0, out32 = on32(p.out);
+                    const bool out32 = on32(p.out);
                     const long long to = (tr * p.Hq + h) * D + col0;
-#pragma unroll 1
-                    for (int i = 0; i < DV / 2; i += 32) {
-                        uint32_t gt[2][8];
-                        if (gated) {
-                            load16(gate + i, gate32, gt[0]);
-                            load16(gate + i + 16, gate32, gt[1]);
-                        }
+                    auto finish = [&](int i, const uint32_t (&gt)[2][8]) {   // channels i.. of this thread's
                         float v[32];
                         if (!whole) tc::tmem_ld32(my_o + i, v);
                         else if (any) load_o(i, v);
@@ -1026,6 +1081,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 else store16(static_cast<bf16*>(p.out) + to + i + e, out32, y);
                             }
                         }
+                    };
+                    if constexpr (S::kGates) {
+                        if (!whole && gated) {
+#pragma unroll
+                            for (int i = 0; i < DV / 64; ++i) gates(i);
+                        }
+#pragma unroll
+                        for (int i = 0; i < DV / 64; ++i) finish(32 * i, gt[i]);
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < DV / 2; i += 32) {
+                            if (gated) {
+                                load16(gate + i, gate32, gt[0][0]);
+                                load16(gate + i + 16, gate32, gt[0][1]);
+                            }
+                            finish(i, gt[0]);
+                        }
                     }
                     if (whole && sm.strays) {
                         sync_softmax();
@@ -1034,9 +1106,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc::fence_before_sync();
             }
-            sync_softmax();   // the sums and sm.last have been read
+            const bool more = sm.way.more;
+            if (more) c = sm.way.next;
+            sync_softmax();   // the sums, sm.last and sm.way.next have been read
             if (!more) break;
-            c = next;
         } while (true);
         if (!S::kF32 && g > 0 && (g & 1) == half) take_base(quarter + 4 * (half ^ 1));   // the last one given
     }
