@@ -27,7 +27,7 @@
 // over many tiles in tensor memory would be cut at every product (2^-24 or so of it, always towards zero: 1e-4 after 32,768 keys).
 // So a unit has 64 channels of the values -- a head of 256 is four units, which compute the same weights -- and a tile's O is
 // its own; a thread adds it to its row's 64 sums in registers, each group those of its tiles, relative to a base of its own.
-// (Heads of 64, 64 tokens each of 16 sequences of up to 4,096: 40 us; in fp32 on the CUDA cores 186.)
+// (Heads of 64, 64 tokens each of 16 sequences of up to 4,096: 41 us; in fp32 on the CUDA cores 186.)
 #include <cuda.h>
 
 #include "gdn_chunk.cuh"
