@@ -17,7 +17,10 @@ namespace {
 // scans all sequences for itself into prefix sums in shared memory; then the page entries -- not the sequences -- are spread
 // over the cluster's threads.  Inputs are outputs: what the scan reads is written behind a cluster barrier.
 constexpr int kBookThreads = 1024;
-constexpr int kManyEntries = 4096;   // entries of the tables (or pages) above which 8 CTAs take part
+// CTAs by the entries of the tables (or pages) that there may be.  16 forks of 256 pages and their release (4,600 entries) by 1, 8, 16
+// CTAs 15.2, 17.3, 18.6 us, 8 of 1,024 (9,400) 18.1, 18.2, 19.1, compaction of 16 sequences of up to 1,024 (16,600) 32, 18, 20, 63
+// forks of 1,024 pages (66,000) 25 by 8 and 24 by 16, 400 forks on prefixes of up to 2,048 (890,000) 587, 86, 52.
+int ctas_for(size_t entries) { return entries > 32768 ? 16 : entries > 8192 ? 8 : 1; }
 // Pages whose counts are summed in shared memory before they go to page_refs, one addition a page and CTA.  Additions to a few
 // lines of memory take their turn, some 20 ns each whoever makes them: 63 forks of 1024 pages of a cache of 1100 took 48 us
 // by 8 and by 64 CTAs and their release 160, with counts in shared memory 12 and 21.  In larger caches the pages lie in more
@@ -383,7 +386,7 @@ __global__ void __launch_bounds__(kBookThreads, 1) kv_release_kernel(const KvRel
 // The number of a page among those in use by ballots: a warp walks a run of pages, 32 at a time, and prefix sums over the
 // warps' totals give each its start.  With `used` known, the r-th page from the top of those at `used` and above goes to the
 // r-th place from the bottom that is not in use: each finds its own r, and writes itself into the pair of that number.
-// Bound by the latency of its phases (five cluster barriers): 64 sequences of up to 1,024 pages in a cache half of it free take 25 us,
+// Bound by the latency of its phases (five cluster barriers): 64 sequences of up to 1,024 pages in a cache half of it free take 22 us,
 // of which the memory would need 0.2; 8 of up to 32 pages 8 us, one CTA.
 __global__ void __launch_bounds__(kBookThreads, 1) kv_compact_kernel(const KvCompactParams p) {
     extern __shared__ int smem[];
@@ -501,13 +504,17 @@ __global__ void __launch_bounds__(kBookThreads, 1) kv_compact_kernel(const KvCom
     });
 }
 
-// One cluster of `ctas` CTAs with `words` words of shared memory, most of them `most` (the kernel's limit, the same by every call:
+// One cluster of `ctas` CTAs (more than 8 have to be allowed) with `words` words of shared memory, most of them `most` (the kernel's limit, the same by every call:
 // another thread's call may come between it and the launch).
 template <typename P>
 cudaError_t launch_books(void (*kernel)(P), const P& p, int ctas, size_t words, size_t most, cudaStream_t stream) {
     const size_t smem = words * 4;
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most * 4));
+        if (e != cudaSuccess) return e;
+    }
+    if (ctas > 8) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     return launch_dependent_cluster(kernel, ctas, dim3(ctas), dim3(kBookThreads), smem, stream, p);
@@ -563,18 +570,18 @@ int count_room(int num_pages, size_t books) { return num_pages <= kCountPages &&
 cudaError_t launch_kv_fork(KvForkParams p, cudaStream_t stream) {
     const size_t books = static_cast<size_t>(p.B) + 2 * (static_cast<size_t>(p.N) + 1);
     p.room = count_room(p.num_pages, books);
-    return launch_books(kv_fork_kernel, p, static_cast<size_t>(p.N) * p.max_pages > kManyEntries ? 8 : 1, books + p.room, kMostWords, stream);
+    return launch_books(kv_fork_kernel, p, ctas_for(static_cast<size_t>(p.N) * p.max_pages), books + p.room, kMostWords, stream);
 }
 
 cudaError_t launch_kv_release(KvReleaseParams p, cudaStream_t stream) {
     const size_t books = 3 * (static_cast<size_t>(p.B) + 1);
     p.room = count_room(p.num_pages, books);
-    return launch_books(kv_release_kernel, p, static_cast<size_t>(p.B) * p.max_pages > kManyEntries ? 8 : 1, books + p.room, kMostWords, stream);
+    return launch_books(kv_release_kernel, p, ctas_for(static_cast<size_t>(p.B) * p.max_pages), books + p.room, kMostWords, stream);
 }
 
 cudaError_t launch_kv_compact(const KvCompactParams& p, cudaStream_t stream) {
-    const bool many = p.num_pages > kManyEntries || static_cast<size_t>(p.B) * p.max_pages > kManyEntries;
-    return launch_books(kv_compact_kernel, p, many ? 8 : 1, static_cast<size_t>(p.B) + 1, kKvMaxSeq + 1, stream);
+    const size_t entries = static_cast<size_t>(p.B) * p.max_pages, pages = static_cast<size_t>(p.num_pages);
+    return launch_books(kv_compact_kernel, p, ctas_for(entries > pages ? entries : pages), static_cast<size_t>(p.B) + 1, kKvMaxSeq + 1, stream);
 }
 
 cudaError_t launch_kv_copy(KvCopyParams p, cudaStream_t stream) {

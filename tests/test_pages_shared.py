@@ -105,6 +105,12 @@ def test_forks_releases_and_compactions(B, ps, max_len):
     assert sorted(s.free.tolist()) == list(range(s.m.N))
 
 
+@pytest.mark.parametrize("B,ps,max_len", [(400, 1, 300), (64, 16, 20000), (8000, 16, 60)])
+def test_large_tables(B, ps, max_len):
+    """As above with tables of 48,000 to 120,000 entries: clusters of 16 CTAs, and more blocks of entries a warp than it holds."""
+    test_forks_releases_and_compactions(B, ps, max_len)
+
+
 def test_fork_then_release_restores_the_stack():
     rng = random.Random(5)
     s = Books(rng, 40, 8, [200, 77, 64] + [0] * 37, 60)
