@@ -16,6 +16,11 @@
 //         came 2 us late)
 //   9     one thread of the first CTA: issues the products
 //
+// Bound by the products where units are long: 8,192 tokens, 24/4 heads of 256, 539 us, 1.53 PFLOP/s, 80% of what a large matrix product
+// reaches; a tile of 128 keys takes some 2,400 cycles.  Elsewhere by a part's begin and end: 8 ragged prompts of up to 4,096
+// tokens, 64/8 heads of 128, 1,151 us, 1.03 PFLOP/s; tiles take 0.82 us each, the rest of a part 5 us.  And where calls are small by
+// a chain of latencies: 37 tokens behind 740, 16/2 heads of 256, 26 us.
+//
 // S has two or three places, as the tensor memory allows, so that the softmax of tiles runs beside the products of others.  The
 // weights take the place of scores that have been read; the S that comes into their place waits for the product with them.
 //
