@@ -374,3 +374,42 @@ def test_a_wait_that_gives_up(odt, new, lens):
     ws.zero_()
     st.zero_()
     assert torch.equal(run(b, odt, status=st, ws=ws), want) and not st.any()
+
+
+@pytest.mark.parametrize("dt,odt", KINDS)
+@pytest.mark.parametrize("d", [64, 256])
+def test_buffers_on_16_bytes_only(dt, odt, d):
+    """A workspace, a result, queries and gates that begin 16 bytes past a multiple of 32; nothing is written outside."""
+    b = R.Batch([70, 3], [9000, 200], 4, 1, d, 16, dt, gate=True, seed=51)
+    want = run(b, odt)
+    dims = gdn.make_attn_dims(4, 1, d, dt, odt)
+    need = gdn.gdn_attn_chunk_workspace_bytes(dims, 2, b.T)
+    room = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    ws = room[16:16 + need].zero_()
+
+    def moved(t):
+        n = 16 // t.element_size()
+        x = torch.zeros(t.numel() + n, dtype=t.dtype, device="cuda")[n:].view(t.shape)
+        return x.copy_(t)
+
+    b.q, b.gate = moved(b.q), moved(b.gate)
+    n = 16 // want.element_size()
+    back = torch.full((want.numel() + 2 * n,), 7.0, dtype=odt, device="cuda")
+    out = back[n:-n].view(want.shape)
+    for t in (ws, b.q, b.gate, out):
+        assert t.data_ptr() % 32 == 16
+    for _ in range(2):
+        run(b, odt, out=out, ws=ws)
+        assert torch.equal(out, want)
+    assert torch.all(room[:16] == 0x5a) and torch.all(room[16 + need:] == 0x5a)
+    assert torch.all(back[:n] == 7.0) and torch.all(back[-n:] == 7.0)
+
+
+def test_two_dtypes_share_a_workspace_in_turn():
+    """A workspace that is large enough serves calls of any dims one after another."""
+    a, b = R.Batch([70, 3], [9000, 200], 4, 1, 256, 16, BF, seed=52), R.Batch([40], [3000], 6, 3, 64, 11, F32, seed=53)
+    kinds = [(a, BF), (b, F32), (a, F32), (b, F32), (a, BF)]
+    need = max(gdn.gdn_attn_chunk_workspace_bytes(gdn.make_attn_dims(x.Hq, x.Hkv, x.d, x.dt, o), 1, 1) for x, o in kinds)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for x, o in kinds:
+        assert torch.equal(run(x, o, ws=ws), run(x, o))
