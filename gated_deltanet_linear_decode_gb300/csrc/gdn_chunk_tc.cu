@@ -36,6 +36,7 @@
 #include <cuda.h>
 
 #include "gdn_chunk.cuh"
+#include "gdn_chunk_strays.h"
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -91,7 +92,8 @@ struct Smem {
         } way;
     };
     uint32_t tmem;
-    int last, stop, strays;           // stop: a softmax warp has seen abort; strays: some were found; never taken back
+    int last, stop;                   // stop: a softmax warp has seen abort
+    Strays strays;
     volatile int abort;
 };
 static_assert(sizeof(Smem) <= kRest, "fits");
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 6; ++i) tc::mbar_init(sm.v_told + i, 1);
         tc::mbar_init(&sm.drained, 1);
         tc::mbar_init(&sm.never, 1);
-        sm.strays = 0;
+        sm.strays.clear();
         sm.abort = sm.stop = (smem_u32(smem) & 1023) != 0;   // the swizzle goes by address bits 7-9
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");   // the barriers are there before asynchronous arrivals on them
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cta_tok = static_cast<int>(rank) * cta_tokens, tok = cta_tok + in;   // of the unit's
         auto wait = [&](uint64_t* bar, uint32_t parity) { wait_for(bar, parity, &sm.abort); };
         int g = 0;           // tile number
-        uint32_t told = 0;   // phases of v_told
+        uint32_t told = 0;   // phases of v_told; bit 31: the number of parts with tiles before this one, mod 2
         // acc = acc * f + tile's O, of which `at` has 64 columns
         auto add_o = [&](float (&acc)[S::kF32 ? 64 : 1], uint32_t at, int tile, float f) {
             wait(sm.pv_done + tile % NS, (tile / NS) & 1);
@@ -866,8 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             else *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
                         }
                         if (found) {
-                            sm.strays = 1;
-                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(smem_u32(&sm.strays), rank ^ 1)), "r"(1) : "memory");
+                            volatile int* const mark = sm.strays.mark(told >> 31);
+                            *mark = 1;
+                            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(smem_u32(const_cast<int*>(mark)), rank ^ 1)), "r"(1) : "memory");
                             asm volatile("fence.acq_rel.cluster;" ::: "memory");
                         }
                         tc::fence_proxy_async();
@@ -917,6 +920,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (p.test_stall && warp == 3) long_wait(smem_u32(&sm.never), 0, &sm.abort, 256);
             if (sm.abort) sm.stop = 1;   // told before the barrier, behind which all look
+            if (((g - 1) & 1) == half && (threadIdx.x & 127) == 0) sm.strays.take_over(told >> 31, any);   // by the group that had the last tile
+            told ^= static_cast<uint32_t>(any) << 31;
             // the sum relative to the last tile's base, which the group of that tile has
             sm.sum[half][row] = l;
             sm.base[half][row] = m;
@@ -962,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (half == 0 && row < here) parts.ml[place * kRows + rank * 128 + row] = make_float2(m, sum);
-                    if (sm.strays) {
+                    if (sm.strays.now) {
                         sync_softmax();
                         add_strays<S>(p, c, tok0, cta_tok, here, part);
                     }
@@ -1104,7 +1109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             finish(i, gt[0]);
                         }
                     }
-                    if (whole && sm.strays) {
+                    if (whole && sm.strays.now) {
                         sync_softmax();
                         add_strays<S>(p, c, tok0, cta_tok, here, nullptr);
                     }
