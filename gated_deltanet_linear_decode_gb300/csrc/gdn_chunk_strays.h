@@ -4,8 +4,9 @@
 //
 // A finder marks the part in both CTAs, its own and by a remote store, before it arrives for the tile's product.  At a part's end a
 // thread that has waited for the part's last product -- behind which both CTAs' finders are -- takes the mark over into `now`, before a
-// barrier of the CTA's softmax warps.  Behind that barrier all of them go by `now`, which nobody else writes: the marks are the other CTA's
-// too, and it may be at the next part already, so warps that looked at them would not all see the same.
+// barrier of the CTA's softmax warps.  Behind that barrier all of them go by `now`, which no other CTA writes (whoever joins the parts
+// of a unit sets it where any of them had some): the marks are the other CTA's too, and it may be at the next part already, so
+// warps that looked at them would not all see the same.
 //
 // It is never further than that: the next part's last product is behind this CTA's weights for it, and so behind the barrier that ends
 // this part.  So there are two marks, by the parity of the parts with tiles (between parts without one the CTAs are not held

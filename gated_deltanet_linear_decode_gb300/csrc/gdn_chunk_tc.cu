@@ -51,6 +51,8 @@ constexpr int kDrainLimit = 1 << 14;   // polls for what is in flight at the end
 constexpr int kDrainCycles = 1 << 17;  // and a time for it after a give-up
 constexpr int kMinShare = 512;        // keys of a worker, at least
 constexpr int kJoin = 8;              // parts that are joined at a time, of units with many of them
+constexpr unsigned kStrayPart = 1 << 16;   // in a counter of parts
+static_assert(kMaxWorkers < static_cast<int>(kStrayPart), "parts of a unit");
 constexpr float kSlack = 8.0f;   // how far a score may pass its row's base
 constexpr int kRows = 256, kKeys = 128, kThreads = 384, kSoft = 256;
 constexpr int kRest = 3 * 1024;   // bytes of shared memory beside queries, keys and values
@@ -92,7 +94,7 @@ struct Smem {
         } way;
     };
     uint32_t tmem;
-    int last, stop;                   // stop: a softmax warp has seen abort
+    int last, stop;                   // last: this CTA finishes the part's rows; stop: a softmax warp has seen abort
     Strays strays;
     volatile int abort;
 };
@@ -289,10 +291,12 @@ __device__ __forceinline__ uint32_t part_at(int row, int ch) { return static_cas
 // All softmax warps.
 __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 9, %0;" ::"n"(kSoft) : "memory"); }
 
-// The strays of a unit's late keys (gdn_attn.cuh; those that its first row does not see) are added to the rows that see them,
-// in out or in the part at `part`: this CTA's rows, whose first token is the unit's token cta_tok.  A call, for the size of the code around it.
+// The strays of a unit's late keys (gdn_attn.cuh; those that its first row does not see) are added to the results of the rows that
+// see them: this CTA's rows, whose first token is the unit's token cta_tok.  By whoever finishes the rows, behind the join of a unit's
+// parts, and not to a part: its weight in the join may be zero, in a row that sees none of its keys or far larger scores
+// elsewhere, and would make NaN of an infinity.  A call, for the size of the code around it.
 template <class S>
-__device__ __noinline__ void add_strays(const ChunkParams& p, const Part& c, int tok0, int cta_tok, int rows, float* part) {
+__device__ __noinline__ void add_strays(const ChunkParams& p, const Part& c, int tok0, int cta_tok, int rows) {
     constexpr int DV = S::DV;
     const int hk = c.hk / S::kSlices, ch0 = c.hk % S::kSlices * DV;
 #pragma unroll 1
@@ -312,12 +316,7 @@ __device__ __noinline__ void add_strays(const ChunkParams& p, const Part& c, int
             y.w += isfinite(v.w) ? 0.f : v.w;
         }
         if (y.x == 0.f && y.y == 0.f && y.z == 0.f && y.w == 0.f) continue;
-        if (!part) {
-            put<bf16, S::D, true>(p, !S::kF32, static_cast<long long>(c.r.row0) + tok0 + tok, h, ch0 + ch, y);
-        } else {
-            float4* const at = reinterpret_cast<float4*>(part + part_at(row, ch));
-            *at = make_float4(at->x + y.x, at->y + y.y, at->z + y.z, at->w + y.w);
-        }
+        put<bf16, S::D, true>(p, !S::kF32, static_cast<long long>(c.r.row0) + tok0 + tok, h, ch0 + ch, y);
     }
 }
 
@@ -920,7 +919,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (p.test_stall && warp == 3) long_wait(smem_u32(&sm.never), 0, &sm.abort, 256);
             if (sm.abort) sm.stop = 1;   // told before the barrier, behind which all look
-            if (((g - 1) & 1) == half && (threadIdx.x & 127) == 0) sm.strays.take_over(told >> 31, any);   // by the group that had the last tile
+            if (((g - 1) & 1) == half && (threadIdx.x & 127) == 0) {   // by the group that had the last tile
+                sm.strays.take_over(told >> 31, any);
+                sm.last = whole;
+            }
             told ^= static_cast<uint32_t>(any) << 31;
             // the sum relative to the last tile's base, which the group of that tile has
             sm.sum[half][row] = l;
@@ -967,10 +969,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (half == 0 && row < here) parts.ml[place * kRows + rank * 128 + row] = make_float2(m, sum);
-                    if (sm.strays.now) {
-                        sync_softmax();
-                        add_strays<S>(p, c, tok0, cta_tok, here, part);
-                    }
                     // the worker that arrives last joins this CTA's rows of all parts; of many parts with many rows the last of each kJoin
                     // joins those first, for one CTA reads no more than some 70 bytes a ns
                     const long long first = c.at + ln.cost;
@@ -985,10 +983,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int these = first_time ? min(kJoin, n - from) : (n + step - 1) / step;
                         sync_softmax();
                         if (threadIdx.x == 0) {
+                            // counts the parts, and those with strays above them; zero again behind the last one
                             unsigned old;
                             int* const counter = parts.counters + (first_time ? kMaxWorkers + 4 * (w0 + from) + 2 * (from == 0) : 2 * w0) + rank;
-                            asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(these - 1) : "memory");
-                            sm.last = old == static_cast<unsigned>(these - 1);
+                            asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(sm.strays.now ? kStrayPart + 1 : 1) : "memory");
+                            sm.last = old % kStrayPart == static_cast<unsigned>(these - 1);
+                            if (sm.last) {
+                                *counter = 0;
+                                if (old >= kStrayPart) sm.strays.now = 1;
+                            }
                         }
                         sync_softmax();
                         if (!sm.last) break;
@@ -1109,10 +1112,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             finish(i, gt[0]);
                         }
                     }
-                    if (whole && sm.strays.now) {
-                        sync_softmax();
-                        add_strays<S>(p, c, tok0, cta_tok, here, nullptr);
-                    }
+                }
+                if (sm.strays.now && sm.last) {
+                    sync_softmax();
+                    add_strays<S>(p, c, tok0, cta_tok, here);
                 }
                 tc::fence_before_sync();
             }

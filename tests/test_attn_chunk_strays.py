@@ -58,3 +58,56 @@ def test_split_units_with_strays(dt, odt, d, G, new, lens, gate):
         assert torch.all(~torch.isfinite(got[hit]))
         same = (got == clean) | hit
         assert torch.all(same), torch.argwhere(~same)[:5].tolist()
+
+
+def late_borders(b, d, odt):
+    """(sequence, kv head, key): keys of a unit that some of its rows do not see, at which another worker's part begins (csrc/gdn_chunk_plan.h;
+    one unit a sequence and kv head, a worker is a pair of SMs)."""
+    G, heads = b.Hq // b.Hkv, b.Hkv * (d // 64 if odt == F32 else 1)
+    cost, workers = 768 if d == 256 else 512, torch.cuda.get_device_properties(0).multi_processor_count // 2
+    at = [0]
+    for n in b.len_list:
+        at += [at[-1] + (cost + n) * (h + 1) for h in range(heads)]
+    total = at[-1]
+    W = max(1, min(workers, total // 512))
+    out = set()
+    for s, (new, n) in enumerate(zip(b.new, b.len_list)):
+        assert new <= 2 * (128 // G)
+        for h in range(heads):
+            first = at[s * heads + h] + cost
+            owner = lambda t: ((first + 128 * t + 1) * W - 1) // total
+            for t in range((n - new + 1) // 128 + 1, (n - 1) // 128 + 1):
+                if owner(t) != owner(t - 1):
+                    out.add((s, h // (heads // b.Hkv), 128 * t))
+    return sorted(out)
+
+
+@pytest.mark.parametrize("dt,odt,peak", [(BF, BF, False), (BF, F32, False), (F32, F32, False), (BF, BF, True), (BF, F32, True)])
+@pytest.mark.parametrize("d,G,Hkv,new,lens", [(256, 1, 3, [256] * 12, [700] * 12), (128, 1, 6, [250] * 12, [900, 1100, 2000] * 4),
+                                              (64, 1, 2, [256] * 20, [1000] * 20), (128, 2, 8, [128] * 9, [1000 + 37 * i for i in range(9)])])
+def test_strays_on_both_sides_of_a_border_between_workers(dt, odt, d, G, Hkv, new, lens, peak):
+    """Rows that see an infinity in the one worker's part and no key in the other's get that infinity, whatever the other's tokens hold;
+    over a bf16 cache also where a score of another part leaves the part of the infinity no weight (peak)."""
+    b = R.Batch(new, lens, G * Hkv, Hkv, d, 16, dt, gate=True, seed=25)
+    if peak:
+        b.q[:, ::d] = 40.0   # the first key's score: 40 * 40 / sqrt(d), at least 100 above the others
+        for s in range(len(new)):
+            b.k[int(b.table[s, 0]), 0, :, 0] = 40.0
+    clean = run(b, odt).clone().view(b.T, -1, d)
+    assert torch.all(torch.isfinite(clean))
+    borders = late_borders(b, d, odt)
+    assert len(borders) > 0
+    want = torch.zeros(b.T, b.Hq, d, device="cuda")
+    for s, h, j in borders:
+        for key, ch, x in ((j - 1, 5, math.inf), (j, 6, -math.inf), (j, d - 1, math.nan), (j + 1, 5, math.inf)):
+            if key < lens[s]:
+                hit = plant(b, [(s, key, h, ch, x)])
+                want[hit] += x
+    for _ in range(3):
+        got = run(b, odt).view(b.T, -1, d)
+        hit = want != 0   # (a NaN is)
+        same = (got == clean) | hit
+        assert torch.all(same), torch.argwhere(~same)[:5].tolist()
+        assert torch.all(torch.isnan(got[hit]) == torch.isnan(want[hit]))
+        inf = hit & ~torch.isnan(want)
+        assert inf.any() and torch.all(got[inf].float() == want[inf])
