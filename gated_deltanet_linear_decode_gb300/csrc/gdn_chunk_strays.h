@@ -23,14 +23,23 @@ namespace gdn {
 namespace chunk {
 
 struct Strays {
-    volatile int found[2];   // by the number of the part, among those with tiles, mod 2
+    volatile int found[2];
+    volatile int part;       // which of them is this part's: the number of parts with tiles before it, mod 2
     volatile int now;        // this part has some
 
-    GDN_HD void clear() { found[0] = found[1] = now = 0; }
-    GDN_HD volatile int* mark(unsigned parts) { return found + (parts & 1); }
-    GDN_HD void take_over(unsigned parts, bool tiles) {
-        now = tiles ? *mark(parts) : 0;
-        if (tiles) *mark(parts) = 0;
+    GDN_HD void clear() {
+        found[0] = 0;
+        found[1] = 0;
+        part = 0;
+        now = 0;
+    }
+    GDN_HD volatile int* mark() { return found + part; }   // and the same place in the other CTA
+    GDN_HD void take_over(bool tiles) {
+        now = 0;
+        if (!tiles) return;
+        now = found[part];
+        found[part] = 0;
+        part = part ^ 1;
     }
 };
 

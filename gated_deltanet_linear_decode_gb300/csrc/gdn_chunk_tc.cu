@@ -294,29 +294,42 @@ __device__ __forceinline__ void sync_softmax() { asm volatile("bar.sync 9, %0;" 
 // The strays of a unit's late keys (gdn_attn.cuh; those that its first row does not see) are added to the results of the rows that
 // see them: this CTA's rows, whose first token is the unit's token cta_tok.  By whoever finishes the rows, behind the join of a unit's
 // parts, and not to a part: its weight in the join may be zero, in a row that sees none of its keys or far larger scores
-// elsewhere, and would make NaN of an infinity.  A call, for the size of the code around it.
+// elsewhere, and would make NaN of an infinity.  A thread has 4 channels of a run of consecutive tokens: of the keys before the run it
+// needs the sum, then a token sees one key more than the token before.  Loads of several keys go out together: each is a table entry, then a
+// value.  (8,192 tokens, 4/4 heads of 256, 116 us; with one NaN token, in the last unit of each head, 206, and 2,147 where each row's keys
+// were walked one after another; with NaN in all tokens 594 and 10,418.)  A call, for the size of the code around it.
 template <class S>
 __device__ __noinline__ void add_strays(const ChunkParams& p, const Part& c, int tok0, int cta_tok, int rows) {
-    constexpr int DV = S::DV;
-    const int hk = c.hk / S::kSlices, ch0 = c.hk % S::kSlices * DV;
+    constexpr int DV = S::DV, kQuads = DV / 4, kRuns = kSoft / kQuads, kAt = 4;
+    const int hk = c.hk / S::kSlices, ch = c.hk % S::kSlices * DV + static_cast<int>(threadIdx.x) % kQuads * 4;
+    const int tokens = rows / p.G, each = (tokens + kRuns - 1) / kRuns;
+    const int first = static_cast<int>(threadIdx.x) / kQuads * each, last = min(tokens, first + each);
+    if (first >= last) return;
+    const int seen = c.r.len - c.r.n + tok0;   // the last key that the unit's first token sees; below 0: none
+    const int from = max(0, seen + 1), mine = seen + cta_tok;
+    auto strays_of = [&](int j) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int k = j / p.cache.page_size, page = p.block_table[static_cast<size_t>(c.b) * p.max_pages + k];
+        if (page >= 0 && page < p.cache.num_pages)
+            v = StateIO<bf16>::ld(static_cast<const bf16*>(p.cache.v) + page * p.cache.page_stride +
+                                  (j - k * p.cache.page_size) * p.cache.token_stride + hk * p.cache.head_stride + ch);
+        return make_float4(isfinite(v.x) ? 0.f : v.x, isfinite(v.y) ? 0.f : v.y, isfinite(v.z) ? 0.f : v.z, isfinite(v.w) ? 0.f : v.w);
+    };
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](float4 v) { y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w); };
+#pragma unroll 8
+    for (int j = from; j < mine + first; ++j) add(strays_of(j));
 #pragma unroll 1
-    for (int i = threadIdx.x; i < rows * (DV / 4); i += kSoft) {
-        const int row = i / (DV / 4), ch = i % (DV / 4) * 4, in = row / p.G, tok = cta_tok + in, h = hk * p.G + row - in * p.G;
-        const int off = c.r.len - c.r.n;
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = first; i0 < last; i0 += kAt) {
+        float4 v[kAt];
+#pragma unroll
+        for (int u = 0; u < kAt; ++u) v[u] = i0 + u < last && mine + i0 + u >= from ? strays_of(mine + i0 + u) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-        for (int j = max(0, off + tok0 + 1); j <= off + tok0 + tok; ++j) {
-            const int k = j / p.cache.page_size, page = p.block_table[static_cast<size_t>(c.b) * p.max_pages + k];
-            if (page < 0 || page >= p.cache.num_pages) continue;
-            const float4 v = StateIO<bf16>::ld(static_cast<const bf16*>(p.cache.v) + page * p.cache.page_stride +
-                                               (j - k * p.cache.page_size) * p.cache.token_stride + hk * p.cache.head_stride + ch0 + ch);
-            y.x += isfinite(v.x) ? 0.f : v.x;
-            y.y += isfinite(v.y) ? 0.f : v.y;
-            y.z += isfinite(v.z) ? 0.f : v.z;
-            y.w += isfinite(v.w) ? 0.f : v.w;
+        for (int u = 0; u < kAt && i0 + u < last; ++u) {
+            add(u == 0 ? v[0] : u == 1 ? v[1] : u == 2 ? v[2] : v[3]);
+            if (y.x == 0.f && y.y == 0.f && y.z == 0.f && y.w == 0.f) continue;
+            for (int g = 0; g < p.G; ++g) put<bf16, S::D, true>(p, !S::kF32, static_cast<long long>(c.r.row0) + tok0 + cta_tok + i0 + u, hk * p.G + g, ch, y);
         }
-        if (y.x == 0.f && y.y == 0.f && y.z == 0.f && y.w == 0.f) continue;
-        put<bf16, S::D, true>(p, !S::kF32, static_cast<long long>(c.r.row0) + tok0 + tok, h, ch0 + ch, y);
     }
 }
 
@@ -664,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int cta_tok = static_cast<int>(rank) * cta_tokens, tok = cta_tok + in;   // of the unit's
         auto wait = [&](uint64_t* bar, uint32_t parity) { wait_for(bar, parity, &sm.abort); };
         int g = 0;           // tile number
-        uint32_t told = 0;   // phases of v_told; bit 31: the number of parts with tiles before this one, mod 2
+        uint32_t told = 0;   // phases of v_told
         // acc = acc * f + tile's O, of which `at` has 64 columns
         auto add_o = [&](float (&acc)[S::kF32 ? 64 : 1], uint32_t at, int tile, float f) {
             wait(sm.pv_done + tile % NS, (tile / NS) & 1);
@@ -867,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             else *reinterpret_cast<uint4*>(at) = make_uint4(0, 0, 0, 0);
                         }
                         if (found) {
-                            volatile int* const mark = sm.strays.mark(told >> 31);
+                            volatile int* const mark = sm.strays.mark();
                             *mark = 1;
                             asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(smem_u32(const_cast<int*>(mark)), rank ^ 1)), "r"(1) : "memory");
                             asm volatile("fence.acq_rel.cluster;" ::: "memory");
@@ -920,10 +933,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (p.test_stall && warp == 3) long_wait(smem_u32(&sm.never), 0, &sm.abort, 256);
             if (sm.abort) sm.stop = 1;   // told before the barrier, behind which all look
             if (((g - 1) & 1) == half && (threadIdx.x & 127) == 0) {   // by the group that had the last tile
-                sm.strays.take_over(told >> 31, any);
+                sm.strays.take_over(any);
                 sm.last = whole;
             }
-            told ^= static_cast<uint32_t>(any) << 31;
             // the sum relative to the last tile's base, which the group of that tile has
             sm.sum[half][row] = l;
             sm.base[half][row] = m;

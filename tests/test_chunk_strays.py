@@ -53,7 +53,6 @@ struct World {
 
 Task warp(World& w, int cta, int half, int id) {
     auto& bar = w.bar[cta];
-    unsigned told = 0;
     int g = 0;
 #define SYNC do { const int ph = bar.phase; if (++bar.n == 2 * kWarps) { bar.n = 0; ++bar.phase; } UNTIL(bar.phase != ph); } while (0)
     for (size_t i = 0; i < w.parts.size(); ++i) {
@@ -67,10 +66,11 @@ Task warp(World& w, int cta, int half, int id) {
             if (!w.f32) w.given[cta][id][g] = 1;
             STEP;
             if ((pt.finders[t] >> (4 * cta + id)) & 1) {
-                *w.cta[cta].mark(told >> 31) = 1;
+                volatile int* const mark = w.cta[cta].mark();
+                *mark = 1;
                 w.ever[cta] = true;
                 STEP;
-                *w.cta[cta ^ 1].mark(told >> 31) = 1;
+                *(w.cta[cta ^ 1].found + (mark - w.cta[cta].found)) = 1;   // the same place in the other CTA
                 w.ever[cta ^ 1] = true;
                 STEP;
             }
@@ -81,8 +81,7 @@ Task warp(World& w, int cta, int half, int id) {
         const int mine = w.f32 ? ((g - 1 - half) & 1 ? g - 2 : g - 1) : g - 1;
         if (any && mine >= g0) UNTIL(w.pv_done[mine]);
         STEP;
-        if (((g - 1) & 1) == half && id == 0) w.cta[cta].take_over(told >> 31, any);
-        told ^= static_cast<unsigned>(any) << 31;
+        if (((g - 1) & 1) == half && id == 0) w.cta[cta].take_over(any);
         STEP;
         SYNC;
         STEP;
