@@ -9,9 +9,11 @@
 //
 // Strays.  A key that a row does not see has the weight 0 in it, which keeps its value out only if that is finite.  Of the keys
 // that some rows of a block see and others do not -- the last K - 1 of a sequence -- the values are looked at before
-// the products; an infinite or NaN element is zeroed in shared memory, and added to the rows that see its key, from the
-// cache, at the group's end.  (Three tokens, 24 rows, 64 ragged sequences: 107.7 us, 105.5 without; looked at by the computing
-// warps 111, whose registers do not suffice for it.  One token has no such keys and a kernel without all this.)
+// the products; an infinite or NaN element is zeroed in shared memory, and added, from the cache, to the results of the rows that see
+// its key, by the CTA that finishes them: not to a part, whose weight in the join may be zero (a row that sees none of
+// its keys, far larger scores elsewhere) and would make NaN of an infinity.  (Three tokens, 24 rows, 64 ragged sequences: 107.7
+// us, 105.5 without; looked at by the computing warps 111, whose registers do not suffice for it.  One token has no such
+// keys and a kernel without all this.)
 //
 // What bounds it: the cache's bytes.  A bf16 key and value of head size d are 4 d bytes for 4 R d operations: the stream is the
 // time up to 16 rows (64 ragged sequences of 0.54 GB, heads of 256, floor 80 us: 8 rows 94 us, 16 rows 96); with more the
@@ -56,6 +58,9 @@ constexpr int kMaxCtas = 256;
 constexpr int kFanOne = 16, kMaxFan = 32;         // parts joined at once: all of up to kFanOne, at most kMaxFan
 constexpr size_t kCounterBytes = 3 * kMaxCtas * 4;   // at the start of the workspace
 static_assert(kMaxCtas / 12 < kMaxFan, "parts of the second step");
+constexpr unsigned kStrayPart = 1 << 16;          // in a counter of parts
+static_assert(kMaxCtas < static_cast<int>(kStrayPart), "parts of a group");
+constexpr int kFinished = 1, kStrays = 2;         // what join_group leaves
 
 // Shape of a kernel: Ta cache type, D head size, NT blocks of 8 rows a warp holds, RG row groups, KG key
 // groups, PIECES bf16 parts of a softmax weight (bf16 only), FR rows a warp holds (fp32; NT is 1).
@@ -454,15 +459,17 @@ __device__ __forceinline__ bool my_share(const AttnParams& p, int row_blocks, Pl
 // the first one's lies in either of that CTA's two places.  Up to kFanOne parts are joined by the CTA that arrives
 // last; of more, `fan` neighbours each are joined that way into the first one's place, and the results of those
 // again: few parts for one CTA to read, and no CTA waits.  What is joined with what, and in which order, does not
-// depend on who arrives last.
+// depend on who arrives last.  `strays`: this CTA has found some, of this part or another.  *flag_s is then kFinished where this CTA
+// has written the results, and kStrays besides where the CTA of any part has found some.
 template <class S>
 __device__ __forceinline__ void join_group(const AttnParams& p, bool out_bf16, const Split& sp, const Share& sh, const Cursor& cc,
-                                           long long g_first, long long g_last, int rows, float* join_s, int* flag_s) {
+                                           long long g_first, long long g_last, int rows, float* join_s, const int* strays, int* flag_s) {
     const int c0 = static_cast<int>(quot((g_first + 1) * sh.ctas - 1, sh.total)), c1 = static_cast<int>(quot(g_last * sh.ctas - 1, sh.total));
     const int n = c1 - c0 + 1, fan = n <= kFanOne ? kFanOne : n <= 64 ? 8 : 12;
     const int k0 = (static_cast<int>(blockIdx.x) - c0) / fan * fan;   // this CTA's neighbours are k0..
     const int part0 = 2 * c0 + (quot(sh.total * c0, sh.ctas) >= g_first - S::kGroupCost ? 0 : 1);   // no tile of the group before in that CTA
     auto place = [&](int k) { return k == 0 ? part0 : 2 * (c0 + k); };
+    if (threadIdx.x == 0) *flag_s = *strays ? kStrays : 0;
 #pragma unroll 1
     for (int level = 0; level < 2; ++level) {
         const int from = level == 0 ? k0 : 0, stride = level == 0 ? 1 : fan;
@@ -472,14 +479,16 @@ __device__ __forceinline__ void join_group(const AttnParams& p, bool out_bf16, c
         sync_computing<S>();   // this CTA's part is written
         if (threadIdx.x == 0) {
             int* const counter = level == 0 ? sp.counters + place(k0) : sp.counters + 2 * kMaxCtas + c0;
-            // releases what the CTA wrote, acquires what the others did; counts to count - 1 and back to zero, ready
-            // for the next call
+            // releases what the CTA wrote, acquires what the others did; counts the parts, and above them those with strays; the
+            // last one leaves zero for the next call
             unsigned old;
-            asm volatile("atom.acq_rel.gpu.global.inc.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(count - 1) : "memory");
-            *flag_s = old == static_cast<unsigned>(count - 1);
+            asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(counter), "r"(*flag_s & kStrays ? kStrayPart + 1 : 1) : "memory");
+            const bool is_last = old % kStrayPart == static_cast<unsigned>(count - 1);
+            if (is_last) *counter = 0;
+            *flag_s = (*flag_s & kStrays) | (old >= kStrayPart ? kStrays : 0) | (is_last ? kFinished : 0);
         }
         sync_computing<S>();
-        if (!*flag_s) return;
+        if (!(*flag_s & kFinished)) return;
         join_parts<S>(p, out_bf16, sp, rows, cc.b, cc.hk, cc.rb * S::kRows, join_s, count, final, place(k0),
                       [&](int k) { return static_cast<size_t>(place(from + k * stride)) * S::kRows; });
         if (final) return;
@@ -1004,22 +1013,16 @@ __global__ void __launch_bounds__(S::kAll, 1) attn_decode_kernel(const AttnParam
             }
             sync_computing<S>();
         }
-        if (kTokens && strays_s) {   // of this group, or of one before it in this CTA
+        if (!whole) join_group<S>(p, out_bf16, sp, sh, cc, g_first, g_last, rows, join_s, &strays_s, &flag_s);
+        if (kTokens && (whole ? strays_s : flag_s == (kFinished | kStrays))) {   // of this group, or of another in one of its CTAs
 #pragma unroll 1
             for (int i = threadIdx.x; i < rows * (D / 4); i += S::kThreads) {
                 const int row = i / (D / 4), c = i % (D / 4) * 4;
                 const float4 x = strays_of<Ta>(p, cc.b, cc.hk, cc.len, cc.rb * S::kRows + row, c);
                 if (x.x == 0.f && x.y == 0.f && x.z == 0.f && x.w == 0.f) continue;
-                if (whole) {
-                    put<Ta, D, true>(p, out_bf16, cc.b, cc.hk, cc.rb * S::kRows + row, c, x);
-                } else {
-                    float4* const at = reinterpret_cast<float4*>(sp.o + (static_cast<size_t>(part) * S::kRows + row) * D + c);
-                    *at = make_float4(at->x + x.x, at->y + x.y, at->z + x.z, at->w + x.w);
-                }
+                put<Ta, D, true>(p, out_bf16, cc.b, cc.hk, cc.rb * S::kRows + row, c, x);
             }
         }
-        if (whole) return;
-        join_group<S>(p, out_bf16, sp, sh, cc, g_first, g_last, rows, join_s, &flag_s);
     };
 
     // ---------------------------------------------------------------- the walk (one copy of each part: the code is fetched
