@@ -15,24 +15,41 @@ inline int sm_count() {
     return sms;
 }
 
-// cluster > 1: thread-block clusters of that many CTAs.
+// The attributes of a launch; cluster > 1: thread-block clusters of that many CTAs.
+struct LaunchConfig {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2];
+    LaunchConfig(int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t stream) {
+        cfg.gridDim = grid;
+        cfg.blockDim = block;
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = cluster > 1 ? 2 : 1;
+    }
+    LaunchConfig(const LaunchConfig&) = delete;
+};
+
 template <typename... P, typename... A>
 cudaError_t launch_dependent_cluster(void (*kernel)(P...), int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    const LaunchConfig c(cluster, grid, block, smem, stream);
+    return cudaLaunchKernelEx(&c.cfg, kernel, static_cast<P>(args)...);
+}
+
+// How many such clusters run at a time; 0 where none does, or the runtime does not say.
+template <typename... P>
+int clusters_at_once(void (*kernel)(P...), int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t stream) {
+    const LaunchConfig c(cluster, grid, block, smem, stream);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &c.cfg) == cudaSuccess) return n;
+    cudaGetLastError();   // (not an error of the call)
+    return 0;
 }
 
 template <typename... P, typename... A>

@@ -6,6 +6,7 @@
 #include "gdn.h"
 #include "gdn_attn_internal.h"
 #include "gdn_books.cuh"
+#include "gdn_cluster_size.h"
 #include "gdn_common.cuh"
 #include "gdn_launch.h"
 
@@ -504,8 +505,9 @@ __global__ void __launch_bounds__(kBookThreads, 1) kv_compact_kernel(const KvCom
     });
 }
 
-// One cluster of `ctas` CTAs (more than 8 have to be allowed) with `words` words of shared memory, most of them `most` (the kernel's limit, the same by every call:
-// another thread's call may come between it and the launch).
+// One cluster of `ctas` CTAs (more than 8 have to be allowed, and 8 are taken where the device or a part of it has no room for more) with
+// `words` words of shared memory, most of them `most` (the kernel's limit, the same by every call: another thread's call may come
+// between it and the launch).
 template <typename P>
 cudaError_t launch_books(void (*kernel)(P), const P& p, int ctas, size_t words, size_t most, cudaStream_t stream) {
     const size_t smem = words * 4;
@@ -516,6 +518,7 @@ cudaError_t launch_books(void (*kernel)(P), const P& p, int ctas, size_t words, 
     if (ctas > 8) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
+        ctas = cluster_that_fits(ctas, [&](int n) { return clusters_at_once(kernel, n, dim3(n), dim3(kBookThreads), smem, stream); });
     }
     return launch_dependent_cluster(kernel, ctas, dim3(ctas), dim3(kBookThreads), smem, stream, p);
 }
