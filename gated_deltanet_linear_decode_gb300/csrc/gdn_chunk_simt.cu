@@ -1,5 +1,6 @@
 // gdn_chunk_simt.cu -- gdn_attn_chunk in fp32 on the CUDA cores: fp32 caches, and bf16 ones that have no tensor map (strides that
-// none can have; with fp32 results pages of an odd number of tokens).
+// none can have; with fp32 results pages of an odd number of tokens: 4 x 1,024 tokens behind 1,024, 16/2 heads of 256, 2,690
+// us, on the tensor cores with pages of 16 422).
 //
 // Bound by the products: 2 d operations a row and key for the scores and as many for the result, of which an SM has 128 multiply-adds
 // a cycle.  9 ragged sequences of up to 301 tokens behind 1,500, 6/3 heads of 64, take 77 us (23 TFLOP/s), 1,281 tokens with 32/4

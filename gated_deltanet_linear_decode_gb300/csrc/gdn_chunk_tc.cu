@@ -17,9 +17,10 @@
 //   9     one thread of the first CTA: issues the products
 //
 // Bound by the products where units are long: 8,192 tokens, 24/4 heads of 256, 539 us, 1.53 PFLOP/s, 80% of what a large matrix product
-// reaches; a tile of 128 keys takes some 2,400 cycles.  Elsewhere by a part's begin and end: 8 ragged prompts of up to 4,096
-// tokens, 64/8 heads of 128, 1,151 us, 1.03 PFLOP/s; tiles take 0.82 us each, the rest of a part 5 us.  And where calls are small by
-// a chain of latencies: 37 tokens behind 740, 16/2 heads of 256, 26 us.
+// reaches (in a run of 20; after half a second of them the power limit has the clock at 1.85 GHz, and they take 577, 1.43
+// PFLOP/s); a tile of 128 keys takes some 2,400 cycles.  Elsewhere by a part's begin and end: 8 ragged prompts of up to 4,096
+// tokens, 64/8 heads of 128, 1,161 us, 1.02 PFLOP/s; tiles take 0.82 us each, the rest of a part 5 us.  And where calls are small by
+// a chain of latencies: 37 tokens behind 740, 16/2 heads of 256, 27 us.
 //
 // S has two or three places, as the tensor memory allows, so that the softmax of tiles runs beside the products of others.  The
 // weights take the place of scores that have been read; the S that comes into their place waits for the product with them.
@@ -32,7 +33,7 @@
 // over many tiles in tensor memory would be cut at every product (2^-24 or so of it, always towards zero: 1e-4 after 32,768 keys).
 // So a unit has 64 channels of the values -- a head of 256 is four units, which compute the same weights -- and a tile's O is
 // its own; a thread adds it to its row's 64 sums in registers, each group those of its tiles, relative to a base of its own.
-// (Heads of 64, 64 tokens each of 16 sequences of up to 4,096: 41 us; in fp32 on the CUDA cores 186.)
+// (Heads of 64, 64 tokens each of 16 sequences of up to 4,096: 42 us; in fp32 on the CUDA cores 186.)
 #include <cuda.h>
 
 #include "gdn_chunk.cuh"
@@ -231,7 +232,8 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // Where pages are a multiple of 8 tokens and follow one another, or the heads of one do, the map is (64 channels, 8 tokens, block,
 // group of 8, page and head) and a box is all the blocks of as many tokens as always lie in one page.  (A copy takes its thread
 // 150 cycles: pages of 16 by boxes of 8 keys, or 16 tokens' one block, were bound by that.)  Otherwise it is (64 channels, token,
-// block, head, page) and a box one block of 1 to 8 tokens.
+// block, head, page) and a box one block of 1 to 8 tokens, which the copies then bound: 4 x 1,024 tokens behind 1,024, bf16 results, heads
+// of 256, 128, 64: pages of 16 106, 121, 106 us, of 100 (boxes of 4) 171, 196, 158, of 1 and 5 (boxes of 1) 469, 488, 456.
 struct Boxes {
     int tokens;        // of a box
     int whole;         // the first kind of map

@@ -387,8 +387,9 @@ __global__ void __launch_bounds__(kBookThreads, 1) kv_release_kernel(const KvRel
 // The number of a page among those in use by ballots: a warp walks a run of pages, 32 at a time, and prefix sums over the
 // warps' totals give each its start.  With `used` known, the r-th page from the top of those at `used` and above goes to the
 // r-th place from the bottom that is not in use: each finds its own r, and writes itself into the pair of that number.
-// Bound by the latency of its phases (five cluster barriers): 64 sequences of up to 1,024 pages in a cache half of it free take 22 us,
-// of which the memory would need 0.2; 8 of up to 32 pages 8 us, one CTA.
+// Bound by the latency of its phases, some 4 us each of the larger of these: page_refs is zeroed, counted up, read twice and written,
+// each time through L2 and behind a cluster barrier.  64 sequences of up to 1,024 pages in a cache half of it free take 23 us, of
+// which the memory would need 0.2; 8 of up to 32 pages 8.6 us, one CTA.
 __global__ void __launch_bounds__(kBookThreads, 1) kv_compact_kernel(const KvCompactParams p) {
     extern __shared__ int smem[];
     int* const held_s = smem;   // [B + 1] entries before each sequence

@@ -61,9 +61,9 @@ typedef struct {
     int32_t act_dtype;  /* gdn_dtype of q, k, v, gate and the cache             */
     int32_t out_dtype;  /* gdn_dtype of the attention's out                     */
     uint32_t flags;     /* 0, or GDN_FLAG_TEST_STALL (gdn.h; in gdn_attn_decode,
-                           and in gdn_attn_chunk over a bf16 cache whose pages
-                           hold an even number of tokens, one warp of a CTA
-                           waits while the others go on)                        */
+                           and in gdn_attn_chunk where it runs on the tensor
+                           cores, one warp of a CTA waits while the others go
+                           on)                                                  */
 } gdn_attn_dims;
 
 /*
@@ -225,8 +225,12 @@ size_t gdn_attn_chunk_workspace_bytes(const gdn_attn_dims* dims, int32_t B, int3
  * from run to run.
  * A bf16 result's softmax weights are rounded to bf16 before the product with
  * the values (2^-8 of a weight at most, beside the result's own rounding);
- * an fp32 result's are not.  A bf16 cache is read through the tensor cores, an
- * fp32 one is worked on by the CUDA cores.
+ * an fp32 result's are not.
+ * A bf16 cache is worked on by the tensor cores, an fp32 one by the CUDA cores;
+ * so is a bf16 cache with an fp32 result where pages hold an odd number of
+ * tokens, and one of strides that no tensor map takes (40 bits of bytes).  Pages
+ * of a multiple of 8 tokens are read fastest; of other numbers 1.1 to 1.6 times
+ * as long for multiples of 4, over 4 times for odd ones.
  */
 gdn_status gdn_attn_chunk(const gdn_attn_dims* dims, const gdn_kv_cache* cache, int32_t B, int32_t T,
                           int32_t max_pages, const void* q, int64_t ldq, const void* gate, int64_t ldg,
